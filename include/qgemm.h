@@ -97,6 +97,14 @@ const char *qgemm_status_str(int status);
 #define QGEMM_X_ROW 0
 #define QGEMM_X_FRAG 1
 
+/* activations of the linear layer and of the mixture-of-experts layer; GELU
+ * is v * Phi(v), GELU_TANH its tanh approximation */
+#define QGEMM_ACT_NONE 0
+#define QGEMM_ACT_RELU 1
+#define QGEMM_ACT_SILU 2
+#define QGEMM_ACT_GELU 3
+#define QGEMM_ACT_GELU_TANH 4
+
 /* ---- packed layout (what the packers write and the kernels read) --------
  *
  * Output columns are grouped in panels of 16; Np = ceil(N/16).  Columns past
@@ -337,6 +345,49 @@ int qgemm_select_rung_xf(int format, int64_t M, int64_t N, int64_t K, int dtype,
 #define QGEMM_NOALLOC_SCRATCH_BYTES (16 << 20)
 int qgemm_gemm_xf_noalloc(int format, int rung, const void *Xf, const void *Wpacked, void *Y, int64_t M, int64_t N,
                           int64_t K, int64_t group_size, int has_zp, int dtype, void *stream);
+
+/* ---- linear layer: bias, activation, gating and residual in the epilogue ----
+ * The product with what a layer does next applied to the fp32 accumulators
+ * before the one rounding into Y (the dequant-scratch post, "The two passes
+ * hiding inside one matmul": a pass over memory that the kernel already holds
+ * in registers is the one to remove):
+ *   gated = 0:  Y = RN_t( act(X.W + bias) + residual )
+ *   gated = 1:  Y = RN_t( act(X.Wg + bias_g) * (X.Wu + bias_u) + residual )
+ * With gated = 1, Wpacked is one packed weight of 2N columns, the gate's
+ * columns 0..N-1 and then the up projection's N..2N-1 (for the k-quants the
+ * concatenation of the two packings), bias has 2N elements in that order, and
+ * N must be a multiple of 16.
+ * X is row-major (x_layout QGEMM_X_ROW) or the fragment-major copy
+ * (QGEMM_X_FRAG).  Y is row-major [M][N], or with y_layout QGEMM_X_FRAG the
+ * fragment-major layout of an M x N matrix (qgemm_xf_bytes(M, N) bytes, rows
+ * past M written as zeros), ready to be the next product's X; N must then be
+ * a multiple of 128.  bias (N or 2N elements) and residual (row-major [M][N])
+ * have the activations' type, are 16-byte aligned device memory and may each
+ * be NULL.  Y may be the residual itself when Y is row-major; any other
+ * overlap of Y with an input is not allowed.
+ * Every step after the product is binary32; an infinity or NaN in bias,
+ * residual or an accumulator goes through the formula as IEEE arithmetic has
+ * it (SiLU of -infinity is NaN, as -infinity * 0 is).  With no bias, no
+ * residual, act NONE and gated 0, Y (row-major) has the bits of
+ * qgemm_gemm_rung / qgemm_gemm_xf on the same rung.
+ * rung as in qgemm_gemm_rung, from the same M-ladder over the packed columns
+ * (2N when gated); the gated form has no rung that splits K across
+ * workgroups: the ladder picks the next best, and forcing one is
+ * QGEMM_ERR_FORMAT.  Launches, errors and the workspace as there, plus
+ * QGEMM_ERR_FORMAT for an unknown layout or activation and QGEMM_ERR_SHAPE for
+ * an N that gated or y_layout does not allow; M = 0 is a no-op.
+ *
+ * qgemm_linear_workspace_bytes: the workspace such a call needs (0 for most),
+ *   as qgemm_workspace_bytes.
+ * qgemm_linear_select_rung: the ladder's choice for such a call in the eight
+ *   integers of qgemm_select_rung. */
+int qgemm_linear(int format, int rung, int x_layout, const void *X, const void *Wpacked, const void *bias,
+                 const void *residual, void *Y, int y_layout, int64_t M, int64_t N, int64_t K, int64_t group_size,
+                 int has_zp, int act, int gated, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t qgemm_linear_workspace_bytes(int format, int rung, int x_layout, int64_t M, int64_t N, int64_t K, int gated,
+                                    int dtype);
+int qgemm_linear_select_rung(int format, int x_layout, int64_t M, int64_t N, int64_t K, int gated, int dtype,
+                             int32_t *info8);
 
 /* ---- logical dequant --------------------------------------------------------
  * Writes the unpacked weights as logical Wout[K][N] (row-major, dtype

@@ -16,6 +16,8 @@ Functions keep the C names without the ``qgemm_`` prefix:
   :func:`gemm_rung`;
 * fragment-major activations: :func:`xf_bytes`, :func:`x_to_xf`,
   :func:`gemm_xf`, :func:`select_rung_xf`;
+* the linear layer, the product with bias, activation, gating and residual in
+  its epilogue: :func:`linear`, :func:`linear_xf`, :func:`linear_select_rung`;
 * the staged dequant :func:`dequant` and the M-ladder queries
   :func:`select_rung`, :func:`rung_info`, :func:`rung_name`, :func:`num_rungs`;
 * the split rungs' workspace size :func:`workspace_bytes` (the C library
@@ -40,6 +42,9 @@ FMT_W4A16 = 2
 FORMATS = {"q4k": FMT_Q4K, "q6k": FMT_Q6K, "w4a16": FMT_W4A16}
 X_ROW = 0
 X_FRAG = 1
+
+#: activations of the linear and the mixture-of-experts layer
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 #: status codes of include/qgemm.h
 STATUS = {0: "QGEMM_OK", -1: "QGEMM_ERR_NULL", -2: "QGEMM_ERR_SHAPE", -3: "QGEMM_ERR_DTYPE",
@@ -93,6 +98,10 @@ SIGNATURES = {
     "qgemm_gemm_xf": (_INT, [_INT, _INT, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _INT, _INT, _VP, _SZ, _VP]),
     "qgemm_select_rung_xf": (_INT, [_INT, _I64, _I64, _I64, _INT, _VP]),
     "qgemm_gemm_xf_noalloc": (_INT, [_INT, _INT, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _INT, _INT, _VP]),
+    "qgemm_linear": (_INT, [_INT, _INT, _INT, _VP, _VP, _VP, _VP, _VP, _INT, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _INT,
+                            _VP, _SZ, _VP]),
+    "qgemm_linear_workspace_bytes": (_SZ, [_INT, _INT, _INT, _I64, _I64, _I64, _INT, _INT]),
+    "qgemm_linear_select_rung": (_INT, [_INT, _INT, _I64, _I64, _I64, _INT, _INT, _VP]),
     "qgemm_gguf_header": (_INT, [_VP, _SZ, _VP, _VP, _VP, _VP, _VP]),
     "qgemm_gguf_tensor_info": (_INT, [_VP, _SZ, _I64, _VP, _SZ, _VP, _VP, _VP, _VP, _VP]),
     "qgemm_gguf_find_kv": (_INT, [_VP, _SZ, ctypes.c_char_p, _VP, _VP, _VP]),
@@ -447,6 +456,109 @@ def gemm_xf(fmt, xf, wp, M: int, N: int, K: int, group: int = 0, has_zp: bool = 
     return out
 
 
+# ---- linear layer -----------------------------------------------------------
+
+def _act_code(act) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _like(t, name, shape, ref, dtype=None):
+    """Pointer of a contiguous tensor of `shape` on ref's device, of ref's
+    dtype or `dtype`; None stays None."""
+    if t is None:
+        return None
+    want = ref.dtype if dtype is None else dtype
+    if tuple(t.shape) != shape or t.dtype != want:
+        raise ValueError(f"{name} must be a {want} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != ref.device:
+        raise ValueError(f"{name} is on {t.device}, the activations are on {ref.device}")
+    return _dev(t, name)
+
+
+class _on_device:
+    """The tensor's device as the current one for the call (the library
+    launches on the current device), restored afterwards."""
+
+    def __init__(self, t):
+        cuda = _torch().cuda
+        self.ctx = None if cuda.current_device() == t.device.index else cuda.device(t.device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout, stream,
+            workspace):
+    torch = _torch()
+    f = FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+    code = _dtype_code(x)
+    ac = _act_code(act)
+    nt = 2 * N if gated else N
+    if out_layout not in (X_ROW, X_FRAG):
+        raise ValueError("out_layout must be X_ROW or X_FRAG")
+    _check_wp(f, wp, nt, K, group, has_zp)
+    if wp.device != x.device:
+        raise ValueError(f"wp is on {wp.device}, the activations are on {x.device}")
+    if out_layout == X_FRAG:
+        n = xf_bytes(M, N) // 2
+        if n == 0 and M > 0:
+            raise QGemmError("qgemm_linear", -2)
+        shape = (n,)
+    else:
+        shape = (M, N)
+    bp = _like(bias, "bias", (nt,), x)
+    rp = _like(residual, "residual", (M, N), x)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        op = ctypes.c_void_p(out.data_ptr())
+    else:
+        op = _like(out, "out", shape, x)
+        if out_layout == X_FRAG and rp is not None and op.value == rp.value:
+            raise ValueError("a fragment-major out cannot be the residual")
+    xp, wpp = _dev(x, "x"), _dev(wp, "wp")
+    need = int(lib().qgemm_linear_workspace_bytes(f, rung, layout, M, N, K, int(bool(gated)), code))
+    with _on_device(x):
+        ws, wsb, _keep = _workspace(need, workspace, x.device)
+        st = lib().qgemm_linear(f, rung, layout, xp, wpp, bp, rp, op, out_layout, M, N, K, group, int(bool(has_zp)), ac,
+                                int(bool(gated)), code, ws, wsb, _stream(stream))
+    _check("qgemm_linear", st)
+    return out
+
+
+def linear(fmt, x, wp, N: int, bias=None, residual=None, act: str = "none", gated: bool = False, group: int = 0,
+           has_zp: bool = False, rung: int = -1, out=None, out_layout: int = X_ROW, stream=None, workspace=None):
+    """Y = act(X . dequant(W) + bias) + residual in one launch, X row-major
+    [M, K]; with ``gated``, wp holds 2N columns (gate, then up) and
+    Y = act(X . Wg + bias_g) * (X . Wu + bias_u) + residual.
+
+    ``act`` is a key of :data:`ACTS`; bias [N] ([2N] when gated) and residual
+    [M, N] have x's dtype; ``out`` may be the residual.  ``out_layout`` X_FRAG
+    returns the fragment-major copy of Y (what :func:`x_to_xf` would make of
+    it), the input of the next :func:`linear_xf` or :func:`gemm_xf`."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    return _linear(fmt, X_ROW, x, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout, stream,
+                   workspace)
+
+
+def linear_xf(fmt, xf, wp, M: int, N: int, K: int, bias=None, residual=None, act: str = "none", gated: bool = False,
+              group: int = 0, has_zp: bool = False, rung: int = -1, out=None, out_layout: int = X_ROW, stream=None,
+              workspace=None):
+    """:func:`linear` with X given as its fragment-major copy `xf`."""
+    if xf.numel() < xf_bytes(M, K) // 2:
+        raise ValueError("xf is smaller than the fragment-major copy of an M x K matrix")
+    return _linear(fmt, X_FRAG, xf, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout,
+                   stream, workspace)
+
+
 #: bytes of the library's fixed device array behind gemm_xf_noalloc
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -709,6 +821,18 @@ def select_rung_xf(fmt, M: int, N: int, K: int, dtype: int = F16) -> dict:
     f = FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
     info = np.zeros(8, np.int32)
     _check("qgemm_select_rung_xf", lib().qgemm_select_rung_xf(f, M, N, K, dtype, _np_ptr(info)))
+    d = dict(zip(_INFO_KEYS, (int(v) for v in info)))
+    d["name"] = rung_name(d["rung"])
+    return d
+
+
+def linear_select_rung(fmt, M: int, N: int, K: int, gated: bool = False, dtype: int = F16, layout: int = X_ROW) -> dict:
+    """The rung :func:`linear` (or, with layout X_FRAG, :func:`linear_xf`)
+    picks; columns and tiles count the packed columns (2N when gated)."""
+    f = FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+    info = np.zeros(8, np.int32)
+    _check("qgemm_linear_select_rung", lib().qgemm_linear_select_rung(f, layout, M, N, K, int(bool(gated)), dtype,
+                                                                      _np_ptr(info)))
     d = dict(zip(_INFO_KEYS, (int(v) for v in info)))
     d["name"] = rung_name(d["rung"])
     return d

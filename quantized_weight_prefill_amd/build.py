@@ -3,8 +3,8 @@ measurement-aid library libqprobe.so beside it.
 
 The library is the product: the fused-dequant kernels, the packers and the C
 ABI of include/qgemm.h.  The kernels are split into translation units (one
-per format x dtype x activation layout for the fp16/bf16 path, one per
-format x dtype for the int8 path) that compile in parallel into
+per format x dtype x activation layout for the fp16/bf16 path, one more per
+epilogue for the linear layer, one per format x dtype for the int8 path) that compile in parallel into
 ``_build/`` and link into one shared object.
 Run `python -m quantized_weight_prefill_amd.build`.
 """
@@ -23,6 +23,7 @@ ARCH = "gfx950"
 FORMATS = (0, 1, 2)  # QGEMM_FMT_Q4K, _Q6K, _W4A16
 DTYPES = (0, 1)      # QGEMM_F16, QGEMM_BF16
 LAYOUTS = (0, 1)     # row-major, fragment-major activations
+EPILOGUES = (1, 2)   # the linear layer's: plain, gated
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
@@ -48,7 +49,10 @@ def units():
     for f in FORMATS:
         for d in DTYPES:
             for x in LAYOUTS:
-                out.append((f"inst_fp_{f}{d}{x}", "inst_fp.hip", [f"-DQG_FMT={f}", f"-DQG_DT={d}", f"-DQG_XL={x}"]))
+                defs = [f"-DQG_FMT={f}", f"-DQG_DT={d}", f"-DQG_XL={x}"]
+                out.append((f"inst_fp_{f}{d}{x}", "inst_fp.hip", defs))
+                for e in EPILOGUES:
+                    out.append((f"inst_lin_{f}{d}{x}{e}", "inst_lin.hip", [*defs, f"-DQG_EPI={e}"]))
             out.append((f"inst_i8_{f}{d}", "inst_i8.hip", [f"-DQG_FMT={f}", f"-DQG_DT={d}"]))
     return out
 

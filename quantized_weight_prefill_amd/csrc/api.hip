@@ -55,8 +55,10 @@ int pick_kw(long long groups, int nch, bool stream, int pn)
 
 // QGEMM_OK, QGEMM_ERR_FORMAT for an unknown rung, or QGEMM_ERR_SHAPE when
 // the grid would exceed what one launch can address (2^31-1 workgroups and
-// 2^32-1 work-items along x, 65535 workgroups along y).
-int make_plan(int rung, long long M, long long N, long long K, Plan &pl)
+// 2^32-1 work-items along x, 65535 workgroups along y).  pairs: the linear
+// layer's gated form, whose direct kernels take panels in gate/up pairs (N,
+// the packed columns, is then a multiple of 32).
+int make_plan(int rung, long long M, long long N, long long K, Plan &pl, bool pairs = false)
 {
     const long long np = (N + 15) / 16;
     const int nch = (int)(K / kChunk);
@@ -68,7 +70,7 @@ int make_plan(int rung, long long M, long long N, long long K, Plan &pl)
     case RUNG_WIDE: {
         if (rung == RUNG_SMALL_M) {
             pl.rb = M <= 16 ? 1 : M <= 32 ? 2 : M <= 48 ? 3 : 4;
-            pl.pn = 1;
+            pl.pn = pairs ? 2 : 1;
         } else if (rung == RUNG_SKINNY_N) {
             pl.rb = 1;
             pl.pn = np >= 4 ? 4 : (int)np;
@@ -484,19 +486,25 @@ Args make_args(int fmt, const void *X, const void *W, void *Y, long long M, long
     }
     return a;
 }
-template <int XL>
-hipError_t launch_xl(int fmt, int dtype, const Plan &pl, const Args &a, hipStream_t s)
+
+template <int FMT, int XL, int EPI>
+hipError_t launch_dt(int dtype, const Plan &pl, const Args &a, hipStream_t s)
 {
-    if (fmt == FMT_Q4K)
-        return dtype == DT_F16 ? launch_fd<FMT_Q4K, DT_F16, XL>(pl, a, s) : launch_fd<FMT_Q4K, DT_BF16, XL>(pl, a, s);
-    if (fmt == FMT_Q6K)
-        return dtype == DT_F16 ? launch_fd<FMT_Q6K, DT_F16, XL>(pl, a, s) : launch_fd<FMT_Q6K, DT_BF16, XL>(pl, a, s);
-    return dtype == DT_F16 ? launch_fd<FMT_W4, DT_F16, XL>(pl, a, s) : launch_fd<FMT_W4, DT_BF16, XL>(pl, a, s);
+    return dtype == DT_F16 ? launch_fd<FMT, DT_F16, XL, EPI>(pl, a, s) : launch_fd<FMT, DT_BF16, XL, EPI>(pl, a, s);
 }
 
+template <int XL, int EPI>
+hipError_t launch_xl(int fmt, int dtype, const Plan &pl, const Args &a, hipStream_t s)
+{
+    if (fmt == FMT_Q4K) return launch_dt<FMT_Q4K, XL, EPI>(dtype, pl, a, s);
+    if (fmt == FMT_Q6K) return launch_dt<FMT_Q6K, XL, EPI>(dtype, pl, a, s);
+    return launch_dt<FMT_W4, XL, EPI>(dtype, pl, a, s);
+}
+
+template <int EPI = EP_NONE>
 hipError_t launch(int fmt, int dtype, int xl, const Plan &pl, const Args &a, hipStream_t s)
 {
-    return xl == X_FRAG ? launch_xl<X_FRAG>(fmt, dtype, pl, a, s) : launch_xl<X_ROW>(fmt, dtype, pl, a, s);
+    return xl == X_FRAG ? launch_xl<X_FRAG, EPI>(fmt, dtype, pl, a, s) : launch_xl<X_ROW, EPI>(fmt, dtype, pl, a, s);
 }
 
 // Bytes of the split rungs' partial sums: S slices of 4-byte sums (fp32 or
@@ -564,6 +572,73 @@ int gemm(int fmt, int rung, const void *X, const void *W, void *Y, long long M, 
     a.kw = pl.kw;
     if (need > 0) return gemm_split(fmt, dtype, xl, pl, a, ws, (hipStream_t)stream);
     return launch_status(launch(fmt, dtype, xl, pl, a, (hipStream_t)stream), kRungNames[pl.rung]);
+}
+
+// ---------------------------------------------------------------------------
+// Linear layer: the rungs of the GEMM with the epilogue on the accumulators.
+// ---------------------------------------------------------------------------
+
+bool known_act(int act) { return act >= QGEMM_ACT_NONE && act <= QGEMM_ACT_GELU_TANH; }
+
+// The plan over the packed columns (2N when gated), by the same ladder: the
+// epilogue adds the same few loads and stores per output to every rung.  The
+// gated form has no rung that splits K across workgroups (its partial sums
+// would pair columns of two tiles): where the ladder picks one, the best of
+// the others serves.
+int linear_plan(int fmt, int rung, int xl, long long M, long long N, long long K, long long group, int gated, int dtype,
+                Plan &pl)
+{
+    if (fmt == FMT_W4 && group == 0) return QGEMM_ERR_FORMAT;
+    if (xl != X_ROW && xl != X_FRAG) return QGEMM_ERR_FORMAT;
+    if (gated && (N > INT32_MAX / 2 || N % 16 != 0)) return QGEMM_ERR_SHAPE;
+    const long long nt = gated ? 2 * N : N, m = M > 0 ? M : 1;
+    const int st = check_shape(fmt, M, nt, K, group);
+    if (st != QGEMM_OK) return st;
+    if (dtype != DT_F16 && dtype != DT_BF16) return QGEMM_ERR_DTYPE;
+    if (rung < -1 || rung >= RUNG_COUNT) return QGEMM_ERR_FORMAT;
+    int r = rung < 0 ? select_rung(fmt, m, nt, K, xl, dtype) : rung;
+    if (gated && (r == RUNG_M64_SK || r == RUNG_M768N64_SK)) {
+        if (rung >= 0) return QGEMM_ERR_FORMAT;
+        r = r == RUNG_M64_SK ? round_model_rung(fmt, m, nt, K, xl, dtype) : large_tile_xf(fmt, m, nt, K);
+        if (r < 0) r = RUNG_M64_K4;
+    }
+    return make_plan(r, m, nt, K, pl, gated != 0);
+}
+
+int linear(int fmt, int rung, int xl, const void *X, const void *W, const void *bias, const void *res, void *Y, int yl,
+           long long M, long long N, long long K, long long group, int has_zp, int act, int gated, int dtype, void *ws,
+           size_t ws_bytes, void *stream)
+{
+    Plan pl;
+    const int st = linear_plan(fmt, rung, xl, M, N, K, group, gated, dtype, pl);
+    if (st != QGEMM_OK) return st;
+    if (!known_act(act) || (yl != X_ROW && yl != X_FRAG)) return QGEMM_ERR_FORMAT;
+    if (yl == X_FRAG && N % kChunk != 0) return QGEMM_ERR_SHAPE;
+    if (M == 0) return QGEMM_OK;
+    if (!X || !W || !Y) return QGEMM_ERR_NULL;
+    if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || !aligned16(bias) || !aligned16(res)) return QGEMM_ERR_ALIGN;
+    Args a = make_args(fmt, X, W, Y, M, gated ? 2 * N : N, K, group, has_zp);
+    a.N = (int)N;
+    a.kw = pl.kw;
+    a.bias = (const uint16_t *)bias;
+    a.res = (const uint16_t *)res;
+    a.act = act;
+    a.y_frag = yl == X_FRAG;
+    const hipStream_t s = (hipStream_t)stream;
+    if (gated) return launch_status(launch<EP_GATED>(fmt, dtype, xl, pl, a, s), kRungNames[pl.rung]);
+    const size_t need = split_ws_bytes(pl, M, N);
+    if (need == 0) return launch_status(launch<EP_LIN>(fmt, dtype, xl, pl, a, s), kRungNames[pl.rung]);
+    // K split across workgroups: partial sums to the workspace, then one
+    // launch that adds the slices in order and runs the epilogue
+    if (!ws || ws_bytes < need) return QGEMM_ERR_SIZE;
+    if (!aligned16(ws)) return QGEMM_ERR_ALIGN;
+    if (!launch_fits((((M + 31) / 32 * 32) * ((N + 3) / 4) + 255) / 256, 256)) return QGEMM_ERR_SHAPE;
+    a.part = (float *)ws;
+    a.pstride = (M * N + 3) & ~3LL;
+    a.split = pl.split;
+    hipError_t e = launch(fmt, dtype, xl, pl, a, s);  // the product's kernel: its partial sums know no epilogue
+    if (e == hipSuccess) e = launch_splitk_reduce_ep(dtype, a, s);
+    return launch_status(e, kRungNames[pl.rung]);
 }
 
 long long packed_bytes(int fmt, long long N, long long K, long long group, int has_zp)
@@ -1006,6 +1081,33 @@ int qgemm_gemm_xf(int format, int rung, const void *Xf, const void *W, void *Y, 
 {
     return gemm(format, rung, Xf, W, Y, M, N, K, format == FMT_W4 ? group_size : 0, has_zp, dtype, workspace,
                 workspace_bytes, stream, X_FRAG);
+}
+
+int qgemm_linear(int format, int rung, int x_layout, const void *X, const void *Wpacked, const void *bias,
+                 const void *residual, void *Y, int y_layout, int64_t M, int64_t N, int64_t K, int64_t group_size,
+                 int has_zp, int act, int gated, int dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return linear(format, rung, x_layout, X, Wpacked, bias, residual, Y, y_layout, M, N, K,
+                  format == FMT_W4 ? group_size : 0, has_zp, act, gated, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t qgemm_linear_workspace_bytes(int format, int rung, int x_layout, int64_t M, int64_t N, int64_t K, int gated,
+                                    int dtype)
+{
+    Plan pl;
+    if (linear_plan(format, rung, x_layout, M, N, K, format == FMT_W4 ? 128 : 0, gated, dtype, pl) != QGEMM_OK) return 0;
+    return M > 0 ? split_ws_bytes(pl, M, N) : 0;
+}
+
+int qgemm_linear_select_rung(int format, int x_layout, int64_t M, int64_t N, int64_t K, int gated, int dtype,
+                             int32_t *info8)
+{
+    if (!info8) return QGEMM_ERR_NULL;
+    Plan pl;
+    const int st = linear_plan(format, -1, x_layout, M, N, K, format == FMT_W4 ? 128 : 0, gated, dtype, pl);
+    if (st != QGEMM_OK) return st;
+    fill_info(pl, info8);
+    return QGEMM_OK;
 }
 
 int qgemm_dequant(int format, const void *W, void *Wout, int64_t N, int64_t K, int64_t group_size, int has_zp,

@@ -80,7 +80,30 @@ struct Args {
     float *part;                 // K split across workgroups: fp32 partial sums, one slice after another
     long long pstride;           // elements from one slice to the next
     int split;                   // number of slices
+    const uint16_t *bias, *res;  // linear layer: bias of the packed columns, residual [M][N] (each may be NULL)
+    int act;                     // linear layer: QGEMM_ACT_*
+    int y_frag;                  // linear layer: Y in the fragment-major layout
 };
+
+// Epilogues of the GEMM kernels: the product alone, the linear layer's
+// bias / activation / residual, and its gated form, whose packed weight holds
+// the gate's columns and then the up projection's (a.np panels in all, half
+// of them gate): tile panels 2i and 2i+1 are then gate panel i and up panel i,
+// so that the two values that meet in one output sit in one lane.
+enum { EP_NONE = 0, EP_LIN = 1, EP_GATED = 2 };
+
+// The packed panel behind tile panel p (clamped to the last one: computed
+// and discarded).
+template <int EPI>
+__device__ __forceinline__ int packed_panel(const Args &a, int p)
+{
+    if constexpr (EPI == EP_GATED) {
+        const int h = a.np >> 1, i = min(p >> 1, h - 1);
+        return (p & 1) ? h + i : i;
+    } else {
+        return p < a.np ? p : a.np - 1;
+    }
+}
 
 // Activation layouts.  X_ROW: X[m][k] at m*K + k.  X_FRAG (fragment-major):
 // 32-row blocks one after the other, each a sequence of 128-wide K chunks;

@@ -5,6 +5,7 @@
 #pragma once
 
 #include "common.h"
+#include "epilogue.h"
 #include "plan.h"
 
 namespace qg {
@@ -21,10 +22,12 @@ namespace qg {
 // x = panel groups of PN panels, y = row groups of 16*RB rows.
 // ---------------------------------------------------------------------------
 // One workgroup: rows m0 .. m0+16*RB-1 (those below a.M) of panels p0 ..
-// p0+PN-1; a.kw waves split K and reduce through LDS.
-template <int FMT, int DT, int RB, int PN, int XL>
+// p0+PN-1; a.kw waves split K and reduce through LDS.  EPI: the epilogue
+// (EP_GATED takes panels in gate/up pairs, so PN is even).
+template <int FMT, int DT, int RB, int PN, int XL, int EPI = EP_NONE>
 __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
 {
+    static_assert(EPI != EP_GATED || PN % 2 == 0, "gate and up panels come in pairs");
     using XA = XLay<XL>;
     extern __shared__ f32x4 red[];  // [kw][PN*RB][64]
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -47,10 +50,7 @@ __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
     }
     RunSrc<FMT> src[PN];
 #pragma unroll
-    for (int pn = 0; pn < PN; pn++) {
-        const int p = p0 + pn;
-        src[pn].init(a, p < a.np ? p : a.np - 1, g, col);
-    }
+    for (int pn = 0; pn < PN; pn++) src[pn].init(a, packed_panel<EPI>(a, p0 + pn), g, col);
 
     RunRaw<FMT> raw[PN];
     u32x4 xf[RB][4];
@@ -87,11 +87,21 @@ __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
                 for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[pn][i], xc[rb][i], acc[pn][rb]);
     }
 
+    constexpr int PS = EPI == EP_GATED ? 2 : 1;  // tile panels behind one output panel
+    // the fragment-major Y's zero rows past the last row group
+    const bool tail = EPI != EP_NONE && a.y_frag && m0 + 16 * RB >= a.M && m0 + 16 * RB < y_rows(a);
     if (a.kw == 1) {
 #pragma unroll
-        for (int pn = 0; pn < PN; pn++)
+        for (int pn = 0; pn < PN; pn += PS) {
+            const int nb = 16 * (p0 + pn);
 #pragma unroll
-            for (int rb = 0; rb < RB; rb++) store_block<DT>(a, acc[pn][rb], m0 + 16 * rb, 16 * (p0 + pn), lane);
+            for (int rb = 0; rb < RB; rb++) {
+                if constexpr (EPI == EP_NONE) store_block<DT>(a, acc[pn][rb], m0 + 16 * rb, nb, lane);
+                else store_block_ep<DT, EPI>(a, acc[pn][rb], acc[pn + PS - 1][rb], m0 + 16 * rb, nb, lane);
+            }
+            if constexpr (EPI != EP_NONE)
+                if (tail) store_block_ep<DT, EPI>(a, acc[pn][0], acc[pn][0], m0 + 16 * RB, nb, lane);
+        }
         return;
     }
 #pragma unroll
@@ -99,18 +109,28 @@ __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) red[(w * PN * RB + pn * RB + rb) * 64 + lane] = acc[pn][rb];
     __syncthreads();
-    for (int blk = w; blk < PN * RB; blk += a.kw) {
-        f32x4 s = red[blk * 64 + lane];
-        for (int ww = 1; ww < a.kw; ww++) s += red[(ww * PN * RB + blk) * 64 + lane];
-        const int pn = blk / RB, rb = blk % RB;
-        store_block<DT>(a, s, m0 + 16 * rb, 16 * (p0 + pn), lane);
+    for (int blk = w; blk < PN / PS * RB; blk += a.kw) {
+        const int pn = PS * (blk / RB), rb = blk % RB, b0 = pn * RB + rb;
+        f32x4 s = red[b0 * 64 + lane];
+        for (int ww = 1; ww < a.kw; ww++) s += red[(ww * PN * RB + b0) * 64 + lane];
+        if constexpr (EPI == EP_NONE) {
+            store_block<DT>(a, s, m0 + 16 * rb, 16 * (p0 + pn), lane);
+        } else {
+            f32x4 u = s;
+            if constexpr (EPI == EP_GATED) {
+                u = red[(b0 + RB) * 64 + lane];
+                for (int ww = 1; ww < a.kw; ww++) u += red[(ww * PN * RB + b0 + RB) * 64 + lane];
+            }
+            store_block_ep<DT, EPI>(a, s, u, m0 + 16 * rb, 16 * (p0 + pn), lane);
+            if (tail && rb == 0) store_block_ep<DT, EPI>(a, s, u, m0 + 16 * RB, 16 * (p0 + pn), lane);
+        }
     }
 }
 
-template <int FMT, int DT, int RB, int PN, int XL>
+template <int FMT, int DT, int RB, int PN, int XL, int EPI = EP_NONE>
 __global__ void __launch_bounds__(512) k_direct(Args a)
 {
-    direct_body<FMT, DT, RB, PN, XL>(a, blockIdx.x * PN, blockIdx.y * (16 * RB));
+    direct_body<FMT, DT, RB, PN, XL, EPI>(a, blockIdx.x * PN, blockIdx.y * (16 * RB));
 }
 
 // ---------------------------------------------------------------------------
@@ -136,7 +156,7 @@ __global__ void __launch_bounds__(512) k_direct(Args a)
 // grouped tile order (below): its L2 then serves both the shared weight
 // panels and the shared activation rows.
 // ---------------------------------------------------------------------------
-template <int FMT, int DT, int WM, int WPB, int NWM, int NWN, int XL>
+template <int FMT, int DT, int WM, int WPB, int NWM, int NWN, int XL, int EPI = EP_NONE>
 __global__ void __launch_bounds__(64 * NWM * NWN) k_stream(Args a)
 {
     using XA = XLay<XL>;
@@ -177,8 +197,7 @@ __global__ void __launch_bounds__(64 * NWM * NWN) k_stream(Args a)
 #pragma unroll
     for (int s = 0; s < UPT; s++) {
         const int u = tid + NTG * s;
-        const int p = p0 + (u >> 6);
-        src[s].init(a, p < a.np ? p : a.np - 1, (u >> 4) & 3, u & 15);
+        src[s].init(a, packed_panel<EPI>(a, p0 + (u >> 6)), (u >> 4) & 3, u & 15);
     }
 
     // prologue: chunk 0 unpacked into LDS buffer 0, chunk 1 raw in
@@ -272,11 +291,15 @@ __global__ void __launch_bounds__(64 * NWM * NWN) k_stream(Args a)
         chunk(c + 1, 1, raw2, raw);
     }
     if (c < c_hi) chunk(c, 0, raw, raw2);
+    constexpr int PS = EPI == EP_GATED ? 2 : 1;  // tile panels behind one output panel
 #pragma unroll
-    for (int pb = 0; pb < WPB; pb++)
+    for (int pb = 0; pb < WPB; pb += PS)
 #pragma unroll
-        for (int rb = 0; rb < RBW; rb++)
-            store_block<DT>(a, acc[pb][rb], m0 + 16 * rb, 16 * (p0 + wn * WPB + pb), lane);
+        for (int rb = 0; rb < RBW; rb++) {
+            const int nb = 16 * (p0 + wn * WPB + pb);
+            if constexpr (EPI == EP_NONE) store_block<DT>(a, acc[pb][rb], m0 + 16 * rb, nb, lane);
+            else store_block_ep<DT, EPI>(a, acc[pb][rb], acc[pb + PS - 1][rb], m0 + 16 * rb, nb, lane);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -295,7 +318,7 @@ __global__ void __launch_bounds__(64 * NWM * NWN) k_stream(Args a)
 // ---------------------------------------------------------------------------
 // One workgroup's pass over K chunks [c_lo, c_hi) of one tile: wave (wm, wn)
 // adds its WM x (16*WPB) block of X[rows m0..][:] * W[:][panels p0..] into acc.
-template <int FMT, int DT, int WM, int WPB, int NWM, int NWN, int XL, int D = 8, int LA = 1>
+template <int FMT, int DT, int WM, int WPB, int NWM, int NWN, int XL, int D = 8, int LA = 1, int EPI = EP_NONE>
 struct Stream32 {
     using XA = XLay<XL>;
     static constexpr int NTG = 64 * NWM * NWN;  // threads of one K group
@@ -335,8 +358,7 @@ struct Stream32 {
         // a tile has fewer runs than threads); the others shadow a real run
         // (loads stay in bounds) and never store it
         const int u0 = tid + NTG * s, u = u0 < RUNS ? u0 : u0 % RUNS, pl = u >> 6, col = u & 15;
-        const int p = p0 + pl;
-        src[s].init(a, p < a.np ? p : a.np - 1, (u >> 4) & 3, col);
+        src[s].init(a, packed_panel<EPI>(a, p0 + pl), (u >> 4) & 3, col);
         slot_cp[s] = pl >> 1;
         slot_lane[s] = 16 * (pl & 1) + col;
     }
@@ -435,11 +457,11 @@ struct Stream32 {
     }
 };
 
-template <int FMT, int DT, int WM, int WPB, int NWM, int NWN, int KS, int XL, int D = 8, int LA = 1>
+template <int FMT, int DT, int WM, int WPB, int NWM, int NWN, int KS, int XL, int D = 8, int LA = 1, int EPI = EP_NONE>
 __global__ void __launch_bounds__(64 * NWM * NWN * KS) __attribute__((amdgpu_waves_per_eu(2)))
 k_stream32(Args a)
 {
-    using S = Stream32<FMT, DT, WM, WPB, NWM, NWN, XL, D, LA>;
+    using S = Stream32<FMT, DT, WM, WPB, NWM, NWN, XL, D, LA, EPI>;
     constexpr int CBW = S::CBW, RBW = S::RBW, PB = S::PB, BM = S::BM;
     // f32x16 partial sums one K group hands over: one per (wave, block, lane)
     constexpr int NACC = NWM * NWN * CBW * RBW * 64;
@@ -488,6 +510,10 @@ k_stream32(Args a)
 #pragma unroll
                 for (int rb = 0; rb < RBW; rb++)
                     acc[cb][rb] += red[(g - 1) * NACC + ((w * CBW + cb) * RBW + rb) * 64 + lane];
+    }
+    if constexpr (EPI != EP_NONE) {
+        store_wave32_ep<DT, EPI, CBW, RBW>(a, acc, m0, 16 * p0 + 32 * wn * CBW, lane);
+        return;
     }
 #pragma unroll
     for (int cb = 0; cb < CBW; cb++)
@@ -773,82 +799,130 @@ __global__ void __launch_bounds__(256) k_splitk_reduce(const float *part, uint16
     }
 }
 
-template <int FMT, int DT, int RB, int PN, int XL>
+// k_splitk_reduce with the linear layer's epilogue: four consecutive columns of
+// one row per thread, rows up to y_rows (the fragment-major layout's zeros).
+template <int DT>
+__global__ void __launch_bounds__(256) k_splitk_reduce_ep(Args a)
+{
+    const int nq = (a.N + 3) >> 2;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int m = (int)(i / nq), n0 = 4 * (int)(i % nq);
+    if (m >= y_rows(a)) return;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4];
+    if (m < a.M) {
+        const float *p = a.part + (long long)m * a.N + n0;
+        for (int s = 0; s < a.split; s++, p += a.pstride) {
+            if ((a.N & 3) == 0) {
+                const f32x4 t = *(const f32x4 *)p;
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[j] += t[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (n0 + j < a.N) v[j] += p[j];
+            }
+        }
+    }
+    finish_quad<DT, EP_LIN>(a, m, n0, v, u, quad_in<EP_LIN>(a, m, n0));
+}
+
+template <int FMT, int DT, int RB, int PN, int XL, int EPI>
 hipError_t launch_direct_rp(const Plan &pl, const Args &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_direct<FMT, DT, RB, PN, XL>), pl.grid, dim3(64 * pl.kw), pl.lds, s, a);
+    hipLaunchKernelGGL((k_direct<FMT, DT, RB, PN, XL, EPI>), pl.grid, dim3(64 * pl.kw), pl.lds, s, a);
     return hipGetLastError();
 }
 
-template <int FMT, int DT, int XL>
+template <int FMT, int DT, int XL, int EPI>
 hipError_t launch_direct(const Plan &pl, const Args &a, hipStream_t s)
 {
+    if constexpr (EPI == EP_GATED) {  // gate and up panels in pairs
+        if (pl.pn == 2) {
+            switch (pl.rb) {
+            case 1: return launch_direct_rp<FMT, DT, 1, 2, XL, EPI>(pl, a, s);
+            case 2: return launch_direct_rp<FMT, DT, 2, 2, XL, EPI>(pl, a, s);
+            case 3: return launch_direct_rp<FMT, DT, 3, 2, XL, EPI>(pl, a, s);
+            default: return launch_direct_rp<FMT, DT, 4, 2, XL, EPI>(pl, a, s);
+            }
+        }
+        switch (pl.rb) {
+        case 1: return launch_direct_rp<FMT, DT, 1, 4, XL, EPI>(pl, a, s);
+        case 2: return launch_direct_rp<FMT, DT, 2, 4, XL, EPI>(pl, a, s);
+        default: return launch_direct_rp<FMT, DT, 3, 4, XL, EPI>(pl, a, s);
+        }
+    } else {
     if (pl.pn == 1) {
         switch (pl.rb) {
-        case 1: return launch_direct_rp<FMT, DT, 1, 1, XL>(pl, a, s);
-        case 2: return launch_direct_rp<FMT, DT, 2, 1, XL>(pl, a, s);
-        case 3: return launch_direct_rp<FMT, DT, 3, 1, XL>(pl, a, s);
-        default: return launch_direct_rp<FMT, DT, 4, 1, XL>(pl, a, s);
+        case 1: return launch_direct_rp<FMT, DT, 1, 1, XL, EPI>(pl, a, s);
+        case 2: return launch_direct_rp<FMT, DT, 2, 1, XL, EPI>(pl, a, s);
+        case 3: return launch_direct_rp<FMT, DT, 3, 1, XL, EPI>(pl, a, s);
+        default: return launch_direct_rp<FMT, DT, 4, 1, XL, EPI>(pl, a, s);
         }
     }
     if (pl.rb > 1)
-        return pl.rb == 2 ? launch_direct_rp<FMT, DT, 2, 4, XL>(pl, a, s) : launch_direct_rp<FMT, DT, 3, 4, XL>(pl, a, s);
+        return pl.rb == 2 ? launch_direct_rp<FMT, DT, 2, 4, XL, EPI>(pl, a, s) : launch_direct_rp<FMT, DT, 3, 4, XL, EPI>(pl, a, s);
     switch (pl.pn) {
-    case 2: return launch_direct_rp<FMT, DT, 1, 2, XL>(pl, a, s);
-    case 3: return launch_direct_rp<FMT, DT, 1, 3, XL>(pl, a, s);
-    default: return launch_direct_rp<FMT, DT, 1, 4, XL>(pl, a, s);
+    case 2: return launch_direct_rp<FMT, DT, 1, 2, XL, EPI>(pl, a, s);
+    case 3: return launch_direct_rp<FMT, DT, 1, 3, XL, EPI>(pl, a, s);
+    default: return launch_direct_rp<FMT, DT, 1, 4, XL, EPI>(pl, a, s);
+    }
     }
 }
 
-template <int FMT, int DT, int XL>
+// EPI: EP_NONE for the products, EP_LIN and EP_GATED for the linear layer
+// (whose calls of the tiles that split K across workgroups launch the
+// product's kernel and put the epilogue into the reduction).
+template <int FMT, int DT, int XL, int EPI>
 hipError_t launch_fd(const Plan &pl, const Args &a, hipStream_t s)
 {
     const bool even = (a.K / kChunk) % 2 == 0;  // an odd chunk count is not split
     switch (pl.rung) {
     case RUNG_M16_256:
-        hipLaunchKernelGGL((k_stream<FMT, DT, 32, 8, 8, 1, XL>), pl.grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((k_stream<FMT, DT, 32, 8, 8, 1, XL, EPI>), pl.grid, dim3(512), 0, s, a);
         return hipGetLastError();
     case RUNG_M128:
-        hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 8, 4, 1, 1, XL>), pl.grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 8, 4, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(256), 0, s, a);
         return hipGetLastError();
     case RUNG_M128_K2:
         if (even)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 8, 4, 1, 2, XL>), pl.grid, dim3(512), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 8, 4, 1, 2, XL, 8, 1, EPI>), pl.grid, dim3(512), 0, s, a);
         else
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 8, 4, 1, 1, XL>), pl.grid, dim3(256), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 8, 4, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(256), 0, s, a);
         return hipGetLastError();
     case RUNG_M128N160:
-        hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 10, 4, 1, 1, XL>), pl.grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 10, 4, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(256), 0, s, a);
         return hipGetLastError();
     case RUNG_M352N96:
-        hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 6, 11, 1, 1, XL>), pl.grid, dim3(704), 0, s, a);
+        hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 6, 11, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(704), 0, s, a);
         return hipGetLastError();
     case RUNG_M768N96:
-        hipLaunchKernelGGL((k_stream32<FMT, DT, 96, 6, 8, 1, 1, XL, 1, 1>), pl.grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((k_stream32<FMT, DT, 96, 6, 8, 1, 1, XL, 1, 1, EPI>), pl.grid, dim3(512), 0, s, a);
         return hipGetLastError();
     case RUNG_M512N128:
-        hipLaunchKernelGGL((k_stream32<FMT, DT, 64, 8, 8, 1, 1, XL, 2, 1>), pl.grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((k_stream32<FMT, DT, 64, 8, 8, 1, 1, XL, 2, 1, EPI>), pl.grid, dim3(512), 0, s, a);
         return hipGetLastError();
     case RUNG_M512N96:
-        hipLaunchKernelGGL((k_stream32<FMT, DT, 64, 6, 8, 1, 1, XL, 4, 1>), pl.grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((k_stream32<FMT, DT, 64, 6, 8, 1, 1, XL, 4, 1, EPI>), pl.grid, dim3(512), 0, s, a);
         return hipGetLastError();
     case RUNG_M192N96_K2:
         if (even)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 6, 6, 1, 2, XL>), pl.grid, dim3(768), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 6, 6, 1, 2, XL, 8, 1, EPI>), pl.grid, dim3(768), 0, s, a);
         else
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 6, 6, 1, 1, XL>), pl.grid, dim3(384), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 6, 6, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(384), 0, s, a);
         return hipGetLastError();
     case RUNG_M192N64_K2:
         if (even)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 6, 1, 2, XL>), pl.grid, dim3(768), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 6, 1, 2, XL, 8, 1, EPI>), pl.grid, dim3(768), 0, s, a);
         else
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 6, 1, 1, XL>), pl.grid, dim3(384), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 6, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(384), 0, s, a);
         return hipGetLastError();
     case RUNG_M768N64_SK:
-        hipLaunchKernelGGL((k_stream32_sk<FMT, DT, 96, 4, 8, 1, 1, XL, 2, 1>), pl.grid, dim3(512), 0, s, a);
+        if constexpr (EPI != EP_NONE) return hipErrorInvalidValue;  // the product's; the linear layer adds its epilogue in the reduction
+        else hipLaunchKernelGGL((k_stream32_sk<FMT, DT, 96, 4, 8, 1, 1, XL, 2, 1>), pl.grid, dim3(512), 0, s, a);
         return hipGetLastError();
     case RUNG_M64_SK:
-        if (pl.kw == 4)
+        if constexpr (EPI != EP_NONE) return hipErrorInvalidValue;  // the product's; the linear layer adds its epilogue in the reduction
+        else if (pl.kw == 4)
             hipLaunchKernelGGL((k_stream32_sk<FMT, DT, 32, 4, 2, 1, 4, XL>), pl.grid, dim3(512), 0, s, a);
         else if (pl.kw == 2)
             hipLaunchKernelGGL((k_stream32_sk<FMT, DT, 32, 4, 2, 1, 2, XL>), pl.grid, dim3(256), 0, s, a);
@@ -857,38 +931,38 @@ hipError_t launch_fd(const Plan &pl, const Args &a, hipStream_t s)
         return hipGetLastError();
     case RUNG_M64_K4:
         if ((a.K / kChunk) % 4 == 0)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 2, 1, 4, XL>), pl.grid, dim3(512), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 2, 1, 4, XL, 8, 1, EPI>), pl.grid, dim3(512), 0, s, a);
         else if (even)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 2, 1, 2, XL>), pl.grid, dim3(256), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 2, 1, 2, XL, 8, 1, EPI>), pl.grid, dim3(256), 0, s, a);
         else
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 2, 1, 1, XL>), pl.grid, dim3(128), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 2, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(128), 0, s, a);
         return hipGetLastError();
     case RUNG_M64N32_K4:
         if ((a.K / kChunk) % 4 == 0)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 2, 1, 4, XL>), pl.grid, dim3(512), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 2, 1, 4, XL, 8, 1, EPI>), pl.grid, dim3(512), 0, s, a);
         else if (even)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 2, 1, 2, XL>), pl.grid, dim3(256), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 2, 1, 2, XL, 8, 1, EPI>), pl.grid, dim3(256), 0, s, a);
         else
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 2, 1, 1, XL>), pl.grid, dim3(128), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 2, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(128), 0, s, a);
         return hipGetLastError();
     case RUNG_M128N64_K2:
         if (even)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 4, 1, 2, XL>), pl.grid, dim3(512), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 4, 1, 2, XL, 8, 1, EPI>), pl.grid, dim3(512), 0, s, a);
         else
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 4, 1, 1, XL>), pl.grid, dim3(256), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 4, 4, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(256), 0, s, a);
         return hipGetLastError();
     case RUNG_M96N32_K4:
         if ((a.K / kChunk) % 4 == 0)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 3, 1, 4, XL>), pl.grid, dim3(768), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 3, 1, 4, XL, 8, 1, EPI>), pl.grid, dim3(768), 0, s, a);
         else if (even)
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 3, 1, 2, XL>), pl.grid, dim3(384), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 3, 1, 2, XL, 8, 1, EPI>), pl.grid, dim3(384), 0, s, a);
         else
-            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 3, 1, 1, XL>), pl.grid, dim3(192), 0, s, a);
+            hipLaunchKernelGGL((k_stream32<FMT, DT, 32, 2, 3, 1, 1, XL, 8, 1, EPI>), pl.grid, dim3(192), 0, s, a);
         return hipGetLastError();
     default:
         break;
     }
-    return launch_direct<FMT, DT, XL>(pl, a, s);
+    return launch_direct<FMT, DT, XL, EPI>(pl, a, s);
 }
 
 }  // namespace qg

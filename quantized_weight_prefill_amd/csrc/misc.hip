@@ -96,6 +96,15 @@ hipError_t launch_splitk_reduce(int dtype, const float *part, uint16_t *Y, long 
     return hipGetLastError();
 }
 
+hipError_t launch_splitk_reduce_ep(int dtype, const Args &a, hipStream_t s)
+{
+    const long long quads = (long long)(a.y_frag ? (a.M + 31) / 32 * 32 : a.M) * ((a.N + 3) / 4);
+    const dim3 grid((unsigned)((quads + 255) / 256));
+    if (dtype == DT_F16) hipLaunchKernelGGL((k_splitk_reduce_ep<DT_F16>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_splitk_reduce_ep<DT_BF16>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_dequant(int fmt, int dtype, const Args &a, uint16_t *o, hipStream_t s)
 {
     const long long total = (long long)a.np * (a.K / kChunk) * 64;

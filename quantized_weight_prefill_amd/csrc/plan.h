@@ -63,13 +63,15 @@ struct Plan {
 };
 
 // fp16/bf16 path, one instantiation per (format, dtype, activation layout)
-// in inst_fp.hip: the direct and streaming rungs of a Plan.
-template <int FMT, int DT, int XL>
+// in inst_fp.hip (the products) and per epilogue in inst_lin.hip (the linear
+// layer): the direct and streaming rungs of a Plan.
+template <int FMT, int DT, int XL, int EPI = EP_NONE>
 hipError_t launch_fd(const Plan &pl, const Args &a, hipStream_t s);
 
 // misc.hip
 hipError_t launch_splitk_reduce(int dtype, const float *part, uint16_t *Y, long long MN, long long stride, int S,
                                 hipStream_t s);
+hipError_t launch_splitk_reduce_ep(int dtype, const Args &a, hipStream_t s);
 hipError_t launch_dequant(int fmt, int dtype, const Args &a, uint16_t *out, hipStream_t s);
 hipError_t launch_x_to_xf(const uint16_t *X, uint16_t *Xf, int M, int K, hipStream_t s);
 hipError_t launch_staged(int fmt, int dtype, const Args &a, uint8_t *scratch, const Plan &pl, hipStream_t s);

@@ -87,6 +87,7 @@ const char *qgemm_status_str(int status);
 /* ---- enumerations -------------------------------------------------------- */
 #define QGEMM_F16 0
 #define QGEMM_BF16 1
+#define QGEMM_F32 2 /* routing logits only */
 
 #define QGEMM_FMT_Q4K 0
 #define QGEMM_FMT_Q6K 1
@@ -450,6 +451,82 @@ int qgemm_grouped(int format, const void *X, const void *Wpacked, void *Y, const
 int qgemm_grouped_xf(int format, const void *Xf, const void *Wpacked, void *Y, const int32_t *offsets, int64_t E,
                      int64_t T, int64_t N, int64_t K, int64_t group_size, int has_zp, int dtype, void *stream);
 int qgemm_grouped_plan(int64_t T, int64_t E, int64_t N, int64_t K, int32_t *info8);
+
+/* ---- mixture-of-experts routing ---------------------------------------------
+ * What decides which rows the per-expert products run on (the
+ * batched-prefill post, "What this did not solve": group the tokens by
+ * expert, so that each expert's weights serve all its tokens).  A pair is a
+ * token and one of its chosen experts, numbered p = t * top_k + j.
+ *
+ * qgemm_moe_route: logits [T][E] (row-major; logit_type QGEMM_F16, QGEMM_BF16
+ *   or QGEMM_F32) -> ids [T][top_k] (int32), the experts of the top_k largest
+ *   logits in falling order, equal logits by the lower index first, and
+ *   weights [T][top_k] (float):
+ *     QGEMM_SCORE_SOFTMAX  exp(l_e - max) / sum over all E of exp(l - max)
+ *     QGEMM_SCORE_SIGMOID  1 / (1 + exp(-l_e))
+ *   with renorm divided by the sum over the token's chosen experts, then
+ *   multiplied by scale.  A NaN logit counts as -infinity, +infinity as the
+ *   largest finite float; a token whose logits are all -infinity, or whose
+ *   chosen scores add up to 0 under renorm, gets weights 0.  The choice
+ *   compares the logits themselves (no rounded score), so it is exact.
+ *   Then the grouping of qgemm_moe_group below.  One launch on `stream` up to
+ *   64 tokens and 1024 pairs, else two.
+ * qgemm_moe_group: ids [T][top_k] -> offsets [E+1] and rows [T*top_k]
+ *   (int32): rows holds the pairs grouped by expert, in pair order within an
+ *   expert, expert e's at offsets[e] .. offsets[e+1]-1.  An id outside [0, E)
+ *   is a dropped pair (an expert of another device, a padded token): it is in
+ *   no group, and rows[offsets[E] ..] are -1.  One launch.
+ *   offsets is what qgemm_grouped takes, with X's row i the token
+ *   rows[i] / top_k.
+ * All buffers are device memory and the caller's; logits and ids 16-byte
+ * aligned, the others 4-byte; no buffer may overlap another.  The order of
+ * rows does not depend on timing.  E is 1 .. QGEMM_MOE_MAX_EXPERTS, top_k 1 ..
+ * 64 (and at most E in qgemm_moe_route), T * top_k below 2^31 - 1024.  T = 0
+ * writes nothing in qgemm_moe_route; qgemm_moe_group then writes zeros to
+ * offsets.  Errors: QGEMM_ERR_SHAPE, _DTYPE (logit_type), _FORMAT (score),
+ * _NULL, _ALIGN, _HIP. */
+#define QGEMM_SCORE_SOFTMAX 0
+#define QGEMM_SCORE_SIGMOID 1
+#define QGEMM_MOE_MAX_EXPERTS 1024
+int qgemm_moe_route(const void *logits, int logit_type, int64_t T, int64_t E, int64_t top_k, int score, int renorm,
+                    float scale, int32_t *ids, float *weights, int32_t *offsets, int32_t *rows, void *stream);
+int qgemm_moe_group(const int32_t *ids, int64_t T, int64_t E, int64_t top_k, int32_t *offsets, int32_t *rows,
+                    void *stream);
+
+/* ---- a mixture-of-experts layer for a few tokens ------------------------------
+ * Both products of every chosen expert and the weighted sum, in two launches
+ * (the batched-prefill post, "What this did not solve"; with a few rows per
+ * expert the layer is a stream of the active experts' packed weights, the
+ * dequant-scratch post's 0.5625 bytes per Q4_K weight, "The two passes hiding
+ * inside one matmul"):
+ *   h[p] = RN_t( act(x_t . Wg_e) * (x_t . Wu_e) )            p = t*top_k + j, e its expert
+ *   Y[t] = RN_t( residual[t] + sum_j weights[t][j] * (h[p] . Wd_e) )
+ * X [T][hidden], Y and residual (may be NULL) [T][hidden], all row-major of
+ * type dtype.  Wup: E packed weights of 2*inter columns over K = hidden (the
+ * gate's columns, then the up projection's), format_up; Wdown: E packed
+ * weights of hidden columns over K = inter, format_down; one expert after
+ * another.  group_size and has_zp hold for each of the two that is W4A16.
+ * weights [T][top_k], offsets [E+1] and rows [T*top_k] as qgemm_moe_route and
+ * qgemm_moe_group write them; a dropped pair adds nothing, and a token whose
+ * pairs are all dropped gets its residual (or 0).  The kernels clamp offsets
+ * and rows into range, so any contents stay inside the buffers (bad ones only
+ * give wrong rows).  h goes through `workspace` (device, 16-byte aligned, at
+ * least qgemm_moe_workspace_bytes, whose contents the call needs not and
+ * leaves behind); everything else stays in fp32 up to Y's one rounding, the
+ * sum over j in rising j.  Y may be the residual or X itself when X is not
+ * needed afterwards; any other overlap is not allowed.
+ * T * top_k is at most QGEMM_MOE_MAX_PAIRS (above it the grouped products
+ * above are the path); inter is a multiple of format_down's K step, hidden of
+ * format_up's.  T = 0 is a no-op.  Errors as qgemm_grouped, plus
+ * QGEMM_ERR_FORMAT for an unknown activation and QGEMM_ERR_SIZE for a
+ * workspace too small.
+ * qgemm_moe_workspace_bytes: 2 * T * top_k * inter, 0 for illegal sizes. */
+#define QGEMM_MOE_MAX_PAIRS 1024
+int qgemm_moe(int format_up, int format_down, const void *X, const void *Wup, const void *Wdown, const float *weights,
+              const int32_t *offsets, const int32_t *rows, const void *residual, void *Y, int64_t T, int64_t top_k,
+              int64_t E, int64_t hidden, int64_t inter, int64_t group_size, int has_zp, int act, int dtype,
+              void *workspace, size_t workspace_bytes, void *stream);
+size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t inter);
 
 /* The staged arm (the dequant-scratch post, "The two passes hiding inside
  * one matmul": unpack to a 16-bit scratch, then a GEMM that reads it), kept

@@ -18,6 +18,8 @@ Functions keep the C names without the ``qgemm_`` prefix:
   :func:`gemm_xf`, :func:`select_rung_xf`;
 * the linear layer, the product with bias, activation, gating and residual in
   its epilogue: :func:`linear`, :func:`linear_xf`, :func:`linear_select_rung`;
+* mixture of experts: the routing :func:`moe_route`, :func:`moe_group` and
+  the whole layer for a few tokens :func:`moe`;
 * the staged dequant :func:`dequant` and the M-ladder queries
   :func:`select_rung`, :func:`rung_info`, :func:`rung_name`, :func:`num_rungs`;
 * the split rungs' workspace size :func:`workspace_bytes` (the C library
@@ -45,6 +47,12 @@ X_FRAG = 1
 
 #: activations of the linear and the mixture-of-experts layer
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+#: scores of the mixture-of-experts routing
+SCORES = {"softmax": 0, "sigmoid": 1}
+#: bounds of the routing and of the few-token layer (include/qgemm.h)
+MOE_MAX_EXPERTS = 1024
+MOE_MAX_PAIRS = 1024
 
 #: status codes of include/qgemm.h
 STATUS = {0: "QGEMM_OK", -1: "QGEMM_ERR_NULL", -2: "QGEMM_ERR_SHAPE", -3: "QGEMM_ERR_DTYPE",
@@ -102,6 +110,11 @@ SIGNATURES = {
                             _VP, _SZ, _VP]),
     "qgemm_linear_workspace_bytes": (_SZ, [_INT, _INT, _INT, _I64, _I64, _I64, _INT, _INT]),
     "qgemm_linear_select_rung": (_INT, [_INT, _INT, _I64, _I64, _I64, _INT, _INT, _VP]),
+    "qgemm_moe_route": (_INT, [_VP, _INT, _I64, _I64, _I64, _INT, _INT, ctypes.c_float, _VP, _VP, _VP, _VP, _VP]),
+    "qgemm_moe_group": (_INT, [_VP, _I64, _I64, _I64, _VP, _VP, _VP]),
+    "qgemm_moe": (_INT, [_INT, _INT, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _INT,
+                         _INT, _INT, _VP, _SZ, _VP]),
+    "qgemm_moe_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "qgemm_gguf_header": (_INT, [_VP, _SZ, _VP, _VP, _VP, _VP, _VP]),
     "qgemm_gguf_tensor_info": (_INT, [_VP, _SZ, _I64, _VP, _SZ, _VP, _VP, _VP, _VP, _VP]),
     "qgemm_gguf_find_kv": (_INT, [_VP, _SZ, ctypes.c_char_p, _VP, _VP, _VP]),
@@ -464,34 +477,55 @@ def _act_code(act) -> int:
     return ACTS[act]
 
 
-def _like(t, name, shape, ref, dtype=None):
-    """Pointer of a contiguous tensor of `shape` on ref's device, of ref's
-    dtype or `dtype`; None stays None."""
-    if t is None:
-        return None
-    want = ref.dtype if dtype is None else dtype
-    if tuple(t.shape) != shape or t.dtype != want:
-        raise ValueError(f"{name} must be a {want} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != ref.device:
-        raise ValueError(f"{name} is on {t.device}, the activations are on {ref.device}")
-    return _dev(t, name)
+def _sized(t, name, shape, dtype):
+    """t, when given, has this shape and dtype."""
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
-class _on_device:
-    """The tensor's device as the current one for the call (the library
-    launches on the current device), restored afterwards."""
+def _together(ref, **tensors):
+    """The given tensors are contiguous and on ref's device, a GPU."""
+    if not ref.is_cuda:
+        raise ValueError("the activations must be a device tensor")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, not on the activations' device {ref.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
-    def __init__(self, t):
-        cuda = _torch().cuda
-        self.ctx = None if cuda.current_device() == t.device.index else cuda.device(t.device)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _scratch(need: int, workspace, device, stream):
+    """(pointer, bytes, tensor to keep) of the caller's workspace, or of one
+    from torch's allocator, which is told of a stream that is not its own."""
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the activations' device")
+    elif need:
+        torch = _torch()
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device=device))
+    else:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _call(fn, device, stream, args):
+    """lib().fn(*args, stream) with `device` as the current one (the library
+    launches there), on `stream` or the device's current stream."""
+    cuda = _torch().cuda
+    if cuda.current_device() != device.index:
+        with cuda.device(device):
+            return _call(fn, device, stream, args)
+    if stream is None:
+        stream = cuda.current_stream().cuda_stream
+    _check(fn, getattr(lib(), fn)(*args, stream))
 
 
 def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout, stream,
@@ -504,31 +538,25 @@ def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_
     if out_layout not in (X_ROW, X_FRAG):
         raise ValueError("out_layout must be X_ROW or X_FRAG")
     _check_wp(f, wp, nt, K, group, has_zp)
-    if wp.device != x.device:
-        raise ValueError(f"wp is on {wp.device}, the activations are on {x.device}")
+    shape = (M, N)
     if out_layout == X_FRAG:
-        n = xf_bytes(M, N) // 2
-        if n == 0 and M > 0:
+        shape = (xf_bytes(M, N) // 2,)
+        if shape == (0,) and M > 0:
             raise QGemmError("qgemm_linear", -2)
-        shape = (n,)
-    else:
-        shape = (M, N)
-    bp = _like(bias, "bias", (nt,), x)
-    rp = _like(residual, "residual", (M, N), x)
+    _sized(bias, "bias", (nt,), x.dtype)
+    _sized(residual, "residual", (M, N), x.dtype)
+    _sized(out, "out", shape, x.dtype)
+    _together(x, x=x, wp=wp, bias=bias, residual=residual, out=out)
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=x.device)
-        op = ctypes.c_void_p(out.data_ptr())
-    else:
-        op = _like(out, "out", shape, x)
-        if out_layout == X_FRAG and rp is not None and op.value == rp.value:
-            raise ValueError("a fragment-major out cannot be the residual")
-    xp, wpp = _dev(x, "x"), _dev(wp, "wp")
-    need = int(lib().qgemm_linear_workspace_bytes(f, rung, layout, M, N, K, int(bool(gated)), code))
-    with _on_device(x):
-        ws, wsb, _keep = _workspace(need, workspace, x.device)
-        st = lib().qgemm_linear(f, rung, layout, xp, wpp, bp, rp, op, out_layout, M, N, K, group, int(bool(has_zp)), ac,
-                                int(bool(gated)), code, ws, wsb, _stream(stream))
-    _check("qgemm_linear", st)
+    elif out_layout == X_FRAG and residual is not None and out.data_ptr() == residual.data_ptr():
+        raise ValueError("a fragment-major out cannot be the residual")
+    gated, has_zp = int(bool(gated)), int(bool(has_zp))
+    need = lib().qgemm_linear_workspace_bytes(f, rung, layout, M, N, K, gated, code)
+    ws, wsb, _keep = _scratch(need, workspace, x.device, stream)
+    _call("qgemm_linear", x.device, stream,
+          (f, rung, layout, x.data_ptr(), wp.data_ptr(), _ptr(bias), _ptr(residual), out.data_ptr(), out_layout, M, N, K,
+           group, has_zp, ac, gated, code, ws, wsb))
     return out
 
 
@@ -763,6 +791,103 @@ def grouped_xf(fmt, xf, wp, T: int, N: int, K: int, offsets, E: int, group: int 
     st = lib().qgemm_grouped_xf(f, _dev(xf, "xf"), _dev(wp, "wp"), _dev(out, "out"), _dev(offsets, "offsets"), E, T, N,
                                 K, group, int(bool(has_zp)), _dtype_code(xf), _stream(stream))
     _check("qgemm_grouped_xf", st)
+    return out
+
+
+# ---- mixture of experts -------------------------------------------------------
+
+def moe_route(logits, top_k: int, score: str = "softmax", renorm: bool = True, scale: float = 1.0, stream=None):
+    """Each token's top_k experts from its router logits [T, E] (float16,
+    bfloat16 or float32): (ids [T, top_k] int32, weights [T, top_k] float32,
+    offsets [E+1] int32, rows [T*top_k] int32), the last two as
+    :func:`moe_group` makes them.
+
+    Experts come in falling order of their logits, equal ones by index.  The
+    weights are the softmax over all E logits or the sigmoid of each, with
+    ``renorm`` divided by their sum over the token's choice, times ``scale``."""
+    torch = _torch()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
+    lt = 2 if logits.dtype == torch.float32 else _dtype_code(logits)
+    T, E = logits.shape
+    _together(logits, logits=logits)
+    if not 1 <= top_k <= min(E, 64):
+        raise QGemmError("qgemm_moe_route", -2)
+    P = T * top_k
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    new = torch.empty if T else torch.zeros  # no tokens: every offset is 0
+    offsets = new((E + 1,), dtype=torch.int32, device=logits.device)
+    rows = torch.empty((P,), dtype=torch.int32, device=logits.device)
+    _call("qgemm_moe_route", logits.device, stream,
+          (logits.data_ptr(), lt, T, E, top_k, SCORES[score], int(bool(renorm)), scale, ids.data_ptr(),
+           weights.data_ptr(), offsets.data_ptr(), rows.data_ptr()))
+    return ids, weights, offsets, rows
+
+
+def moe_group(ids, E: int, stream=None):
+    """The token-expert pairs p = t*top_k + j of ids [T, top_k] (int32) grouped
+    by expert: (offsets [E+1], rows [T*top_k]), rows in pair order within an
+    expert.  Ids outside [0, E) are dropped pairs: in no group, rows -1 at
+    the end."""
+    torch = _torch()
+    if ids.dim() != 2 or ids.dtype != torch.int32:
+        raise ValueError("ids must be an int32 tensor [T, top_k]")
+    T, k = ids.shape
+    _together(ids, ids=ids)
+    offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=ids.device)
+    rows = torch.empty((T * k,), dtype=torch.int32, device=ids.device)
+    _call("qgemm_moe_group", ids.device, stream, (ids.data_ptr(), T, E, k, offsets.data_ptr(), rows.data_ptr()))
+    return offsets, rows
+
+
+def moe_workspace_bytes(T: int, top_k: int, inter: int) -> int:
+    return int(lib().qgemm_moe_workspace_bytes(T, top_k, inter))
+
+
+def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, group: int = 0, has_zp: bool = False,
+        act: str = "silu", residual=None, out=None, stream=None, workspace=None):
+    """A mixture-of-experts layer for a few tokens (at most MOE_MAX_PAIRS
+    token-expert pairs), two launches: for each token t of x [T, H] and each of
+    its experts e, h = act(x Wg_e) * (x Wu_e), and
+    Y[t] = residual[t] + sum_j weights[t][j] * (h Wd_e).
+
+    w_up: E packed weights of 2*inter columns over K = H (gate, then up);
+    w_down: E packed weights of H columns over K = inter; weights [T, top_k]
+    float32, offsets [E+1] and rows [T*top_k] from :func:`moe_route` or
+    :func:`moe_group`.  ``out`` may be the residual."""
+    torch = _torch()
+    if x.dim() != 2 or weights.dim() != 2:
+        raise ValueError("x must be [T, H] and weights [T, top_k]")
+    fu = FORMATS[fmt_up] if isinstance(fmt_up, str) else int(fmt_up)
+    fd = FORMATS[fmt_down] if isinstance(fmt_down, str) else int(fmt_down)
+    T, H = x.shape
+    k = weights.shape[1]
+    E = offsets.numel() - 1
+    code = _dtype_code(x)
+    ac = _act_code(act)
+    if E < 1 or k < 1:
+        raise ValueError("offsets must hold E+1 entries and weights at least one column")
+    _sized(weights, "weights", (T, k), torch.float32)
+    _sized(offsets, "offsets", (E + 1,), torch.int32)
+    _sized(rows, "rows", (T * k,), torch.int32)
+    _sized(residual, "residual", (T, H), x.dtype)
+    _sized(out, "out", (T, H), x.dtype)
+    _check_wp(fu, w_up, 2 * inter, H, group, has_zp, experts=E)
+    _check_wp(fd, w_down, H, inter, group, has_zp, experts=E)
+    _together(x, x=x, w_up=w_up, w_down=w_down, weights=weights, offsets=offsets, rows=rows, residual=residual, out=out)
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    need = lib().qgemm_moe_workspace_bytes(T, k, inter)
+    if need == 0 and T > 0:
+        raise QGemmError("qgemm_moe", -2)
+    ws, wsb, _keep = _scratch(need, workspace, x.device, stream)
+    _call("qgemm_moe", x.device, stream,
+          (fu, fd, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
+           rows.data_ptr(), _ptr(residual), out.data_ptr(), T, k, E, H, inter, group, int(bool(has_zp)), ac, code, ws,
+           wsb))
     return out
 
 

@@ -4,7 +4,8 @@ measurement-aid library libqprobe.so beside it.
 The library is the product: the fused-dequant kernels, the packers and the C
 ABI of include/qgemm.h.  The kernels are split into translation units (one
 per format x dtype x activation layout for the fp16/bf16 path, one more per
-epilogue for the linear layer, one per format x dtype for the int8 path) that compile in parallel into
+epilogue for the linear layer, one per format x dtype for the int8 path, one
+per format for the mixture-of-experts layer) that compile in parallel into
 ``_build/`` and link into one shared object.
 Run `python -m quantized_weight_prefill_amd.build`.
 """
@@ -45,8 +46,9 @@ def units():
     """(object name, source, extra flags) of every translation unit."""
     out = [("api", "api.hip", []), ("misc", "misc.hip", []), ("misc_grouped", "misc_grouped.hip", []),
            ("misc_i8", "misc_i8.hip", []), ("pack", "pack.cpp", []),
-           ("noalloc", "noalloc.hip", []), ("gguf", "gguf.cpp", [])]
+           ("noalloc", "noalloc.hip", []), ("gguf", "gguf.cpp", []), ("moe_route", "moe_route.hip", [])]
     for f in FORMATS:
+        out.append((f"inst_moe_{f}", "inst_moe.hip", [f"-DQG_FMT={f}"]))
         for d in DTYPES:
             for x in LAYOUTS:
                 defs = [f"-DQG_FMT={f}", f"-DQG_DT={d}", f"-DQG_XL={x}"]

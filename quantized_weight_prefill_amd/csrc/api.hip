@@ -714,6 +714,91 @@ int grouped(int fmt, const void *X, const void *W, void *Y, const int32_t *offs,
     return launch_status(launch_grouped(fmt, dtype, xl, pl, a, (hipStream_t)stream), "grouped");
 }
 
+// ---------------------------------------------------------------------------
+// Mixture-of-experts routing and few-token layer.
+// ---------------------------------------------------------------------------
+
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+int moe_route_shape(long long T, long long E, long long k)
+{
+    if (T < 0 || E < 1 || E > QGEMM_MOE_MAX_EXPERTS || k < 1 || k > 64) return QGEMM_ERR_SHAPE;
+    return T > (INT32_MAX - 1024) / k ? QGEMM_ERR_SHAPE : QGEMM_OK;
+}
+
+hipError_t launch_up(int fmt, int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s)
+{
+    if (fmt == FMT_Q4K) return launch_moe_up<FMT_Q4K>(dtype, rb, grid, m, s);
+    return fmt == FMT_Q6K ? launch_moe_up<FMT_Q6K>(dtype, rb, grid, m, s) : launch_moe_up<FMT_W4>(dtype, rb, grid, m, s);
+}
+
+hipError_t launch_down(int fmt, int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
+{
+    if (fmt == FMT_Q4K) return launch_moe_down<FMT_Q4K>(dtype, grid, m, s);
+    return fmt == FMT_Q6K ? launch_moe_down<FMT_Q6K>(dtype, grid, m, s) : launch_moe_down<FMT_W4>(dtype, grid, m, s);
+}
+
+int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const float *wts, const int32_t *offs,
+        const int32_t *rows, const void *res, void *Y, long long T, long long k, long long E, long long H, long long I,
+        long long group, int has_zp, int act, int dtype, void *ws, size_t ws_bytes, void *stream)
+{
+    if ((fu == FMT_W4 || fd == FMT_W4) && group == 0) return QGEMM_ERR_FORMAT;
+    if (I < 1 || I > INT32_MAX / 2) return QGEMM_ERR_SHAPE;
+    int st = check_shape(fu, T, 2 * I, H, fu == FMT_W4 ? group : 0);
+    if (st == QGEMM_OK) st = check_shape(fd, T, H, I, fd == FMT_W4 ? group : 0);
+    if (st != QGEMM_OK) return st;
+    if (dtype != DT_F16 && dtype != DT_BF16) return QGEMM_ERR_DTYPE;
+    if (!known_act(act)) return QGEMM_ERR_FORMAT;
+    if (k < 1 || E < 1 || E > INT32_MAX / 2 || T > QGEMM_MOE_MAX_PAIRS || k > QGEMM_MOE_MAX_PAIRS ||
+        T * k > QGEMM_MOE_MAX_PAIRS)
+        return QGEMM_ERR_SHAPE;
+    if (T == 0) return QGEMM_OK;
+    if (!X || !Wu || !Wd || !wts || !offs || !rows || !Y) return QGEMM_ERR_NULL;
+    const long long su = packed_bytes(fu, 2 * I, H, group, has_zp), sd = packed_bytes(fd, H, I, group, has_zp);
+    if (!aligned16(X) || !aligned16(Wu) || !aligned16(Wd) || !aligned16(res) || !aligned16(Y) || !aligned4(wts) ||
+        !aligned4(offs) || !aligned4(rows))  // an expert's packed size is whole 16-byte pieces: H and I fill whole panels
+        return QGEMM_ERR_ALIGN;
+    if (!ws || ws_bytes < qgemm_moe_workspace_bytes(T, k, I)) return QGEMM_ERR_SIZE;
+    if (!aligned16(ws)) return QGEMM_ERR_ALIGN;
+    if (!launch_fits(I / 16, 512) || !launch_fits((H + 15) / 16, 1024)) return QGEMM_ERR_SHAPE;
+    const long long P = T * k;
+    MoeArgs m{};
+    m.rows = rows;
+    m.wts = wts;
+    m.H = (uint16_t *)ws;
+    m.T = (int)T;
+    m.top_k = (int)k;
+    m.inter = (int)I;
+
+    // gate and up: rows per tile by the experts' mean count; eight waves
+    // split K while each keeps two chunks
+    const long long avg = (P + E - 1) / E;
+    const int rb = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
+    m.g = make_args(fu, X, Wu, nullptr, P, 2 * I, H, group, has_zp);
+    m.g.offs = offs;
+    m.g.E = (int)E;
+    m.g.wstride = su;
+    m.g.act = act;
+    const int nch = (int)(H / kChunk);
+    m.g.kw = 8;
+    while (m.g.kw > 1 && nch < 2 * m.g.kw) m.g.kw /= 2;
+    const dim3 gu((unsigned)(I / 16), (unsigned)std::min(P, (P + 16 * rb - 1) / (16 * rb) + E), 1);
+    hipError_t e = launch_up(fu, dtype, rb, gu, m, (hipStream_t)stream);
+    if (e != hipSuccess) return launch_status(e, "moe up");
+
+    // down: K in parts while the row tiles alone leave waves of a workgroup idle
+    m.g = make_args(fd, nullptr, Wd, Y, P, H, I, group, has_zp);
+    m.g.offs = offs;
+    m.g.E = (int)E;
+    m.g.wstride = sd;
+    m.g.res = (const uint16_t *)res;
+    const long long tiles = std::min(P, (P + 15) / 16 + E);
+    m.parts = 1;
+    while (tiles * 2 * m.parts <= 16 && I / kChunk >= 2 * m.parts) m.parts *= 2;
+    e = launch_down(fd, dtype, dim3((unsigned)((H + 15) / 16), 1, 1), m, (hipStream_t)stream);
+    return launch_status(e, "moe down");
+}
+
 size_t staged_scratch_bytes(long long N, long long K)
 {
     if (N < 1 || K < 1 || K % kChunk != 0 || N > INT32_MAX || K > INT32_MAX) return 0;
@@ -868,8 +953,6 @@ hipError_t launch_i8_dt(int fmt, const Plan &pl, const Args &a, hipStream_t s)
     if (fmt == FMT_Q6K) return launch_i8_fd<FMT_Q6K, DT>(pl, a, s);
     return launch_i8_fd<FMT_W4, DT>(pl, a, s);
 }
-
-bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
 int i8_gemm_plan(int fmt, int rung, long long M, long long N, long long K, long long group, int dtype, Plan &pl)
 {
@@ -1145,6 +1228,50 @@ int qgemm_grouped_xf(int format, const void *Xf, const void *Wpacked, void *Y, c
 {
     return grouped(format, Xf, Wpacked, Y, offsets, E, T, N, K, format == FMT_W4 ? group_size : 0, has_zp, dtype, stream,
                    X_FRAG);
+}
+
+int qgemm_moe_route(const void *logits, int logit_type, int64_t T, int64_t E, int64_t top_k, int score, int renorm,
+                    float scale, int32_t *ids, float *weights, int32_t *offsets, int32_t *rows, void *stream)
+{
+    const int st = moe_route_shape(T, E, top_k);
+    if (st != QGEMM_OK) return st;
+    if (top_k > E) return QGEMM_ERR_SHAPE;
+    if (logit_type != QGEMM_F16 && logit_type != QGEMM_BF16 && logit_type != QGEMM_F32) return QGEMM_ERR_DTYPE;
+    if (score != QGEMM_SCORE_SOFTMAX && score != QGEMM_SCORE_SIGMOID) return QGEMM_ERR_FORMAT;
+    if (T == 0) return QGEMM_OK;
+    if (!logits || !ids || !weights || !offsets || !rows) return QGEMM_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(ids) || !aligned4(weights) || !aligned4(offsets) || !aligned4(rows))
+        return QGEMM_ERR_ALIGN;
+    return launch_status(launch_moe_route(logit_type, logits, (int)T, (int)E, (int)top_k, score, renorm, scale, ids,
+                                          weights, offsets, rows, (hipStream_t)stream),
+                         "moe route");
+}
+
+int qgemm_moe_group(const int32_t *ids, int64_t T, int64_t E, int64_t top_k, int32_t *offsets, int32_t *rows,
+                    void *stream)
+{
+    const int st = moe_route_shape(T, E, top_k);
+    if (st != QGEMM_OK) return st;
+    if (!offsets || (T > 0 && (!ids || !rows))) return QGEMM_ERR_NULL;
+    if (!aligned16(ids) || !aligned4(offsets) || !aligned4(rows)) return QGEMM_ERR_ALIGN;
+    return launch_status(launch_moe_group(ids, (int)(T * top_k), (int)E, offsets, rows, (hipStream_t)stream), "moe group");
+}
+
+int qgemm_moe(int format_up, int format_down, const void *X, const void *Wup, const void *Wdown, const float *weights,
+              const int32_t *offsets, const int32_t *rows, const void *residual, void *Y, int64_t T, int64_t top_k,
+              int64_t E, int64_t hidden, int64_t inter, int64_t group_size, int has_zp, int act, int dtype,
+              void *workspace, size_t workspace_bytes, void *stream)
+{
+    return moe(format_up, format_down, X, Wup, Wdown, weights, offsets, rows, residual, Y, T, top_k, E, hidden, inter,
+               group_size, has_zp, act, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t inter)
+{
+    if (T < 0 || top_k < 1 || T > QGEMM_MOE_MAX_PAIRS || top_k > QGEMM_MOE_MAX_PAIRS || T * top_k > QGEMM_MOE_MAX_PAIRS ||
+        inter < 1 || inter > INT32_MAX / 2)
+        return 0;
+    return 2 * (size_t)(T * top_k) * (size_t)inter;
 }
 
 int qgemm_grouped_plan(int64_t T, int64_t E, int64_t N, int64_t K, int32_t *info8)

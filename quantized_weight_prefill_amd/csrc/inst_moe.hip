@@ -1,0 +1,42 @@
+// inst_moe.hip -- the few-token mixture-of-experts kernels of one weight
+// format; the build compiles this file once per format with QG_FMT defined.
+#include "kernels_moe.h"
+
+#if !defined(QG_FMT)
+#error "inst_moe.hip is compiled with -DQG_FMT=<format>"
+#endif
+
+namespace qg {
+
+template <int FMT, int DT>
+hipError_t launch_up_dt(int rb, dim3 grid, const MoeArgs &m, hipStream_t s)
+{
+    const dim3 block(64 * m.g.kw);
+    const size_t lds = (size_t)m.g.kw * 2 * rb * 64 * sizeof(f32x4);
+    if (rb == 1) hipLaunchKernelGGL((k_moe_up<FMT, DT, 1, 2>), grid, block, lds, s, m);
+    else if (rb == 2) hipLaunchKernelGGL((k_moe_up<FMT, DT, 2, 2>), grid, block, lds, s, m);
+    else if (rb == 4) hipLaunchKernelGGL((k_moe_up<FMT, DT, 4, 1>), grid, block, lds, s, m);
+    else return hipErrorInvalidValue;
+    return hipGetLastError();
+}
+
+template <int FMT>
+hipError_t launch_moe_up(int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s)
+{
+    return dtype == DT_F16 ? launch_up_dt<FMT, DT_F16>(rb, grid, m, s) : launch_up_dt<FMT, DT_BF16>(rb, grid, m, s);
+}
+
+template <int FMT>
+hipError_t launch_moe_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
+{
+    const dim3 block(64 * kMoeDownWaves);
+    const size_t lds = moe_down_lds(m.g.M, m.g.E, m.parts);
+    if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16, 3>), grid, block, lds, s, m);
+    else hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16, 3>), grid, block, lds, s, m);
+    return hipGetLastError();
+}
+
+template hipError_t launch_moe_up<QG_FMT>(int, int, dim3, const MoeArgs &, hipStream_t);
+template hipError_t launch_moe_down<QG_FMT>(int, dim3, const MoeArgs &, hipStream_t);
+
+}  // namespace qg

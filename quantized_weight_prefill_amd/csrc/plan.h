@@ -84,6 +84,25 @@ enum GroupedKernel {
 // (X_ROW or X_FRAG)
 hipError_t launch_grouped(int fmt, int dtype, int xl, const Plan &pl, const Args &a, hipStream_t s);
 
+// Few-token mixture-of-experts layer (kernels_moe.h), one instantiation per
+// weight format in inst_moe.hip.
+struct MoeArgs {
+    Args g;              // weights, K, panels, group; offs, E, wstride; M = pairs
+    const int *rows;     // [pairs]
+    const float *wts;    // [T][top_k]
+    uint16_t *H;         // hidden [pairs][inter] (row i of the sorted order)
+    int T, top_k, inter;
+    int parts;           // k_moe_down: K parts per row tile
+};
+template <int FMT>
+hipError_t launch_moe_up(int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s);
+template <int FMT>
+hipError_t launch_moe_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s);
+// moe_route.hip
+hipError_t launch_moe_route(int logit_type, const void *logits, int T, int E, int k, int score, int renorm, float scale,
+                            int *ids, float *weights, int *offsets, int *rows, hipStream_t s);
+hipError_t launch_moe_group(const int *ids, int P, int E, int *offsets, int *rows, hipStream_t s);
+
 // api.hip: the checked fp16/bf16 GEMM of qgemm_gemm_rung (layout X_ROW) and
 // qgemm_gemm_xf (X_FRAG) with an explicit workspace, and the workspace it
 // needs; for the entry points that bring their own workspace (noalloc.hip).

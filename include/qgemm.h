@@ -510,23 +510,24 @@ int qgemm_moe_group(const int32_t *ids, int64_t T, int64_t E, int64_t top_k, int
  * qgemm_moe_group write them; a dropped pair adds nothing, and a token whose
  * pairs are all dropped gets its residual (or 0).  The kernels clamp offsets
  * and rows into range, so any contents stay inside the buffers (bad ones only
- * give wrong rows).  h goes through `workspace` (device, 16-byte aligned, at
- * least qgemm_moe_workspace_bytes, whose contents the call needs not and
- * leaves behind); everything else stays in fp32 up to Y's one rounding, the
- * sum over j in rising j.  Y may be the residual or X itself when X is not
+ * give wrong rows).  h and the partial sums of Y go through `workspace`
+ * (device, 16-byte aligned, at least qgemm_moe_workspace_bytes, of any
+ * contents, which the call overwrites); everything after h stays in fp32 up to
+ * Y's one rounding, in an order that depends on the sizes alone.  Y may be the residual or X itself when X is not
  * needed afterwards; any other overlap is not allowed.
  * T * top_k is at most QGEMM_MOE_MAX_PAIRS (above it the grouped products
  * above are the path); inter is a multiple of format_down's K step, hidden of
  * format_up's.  T = 0 is a no-op.  Errors as qgemm_grouped, plus
  * QGEMM_ERR_FORMAT for an unknown activation and QGEMM_ERR_SIZE for a
  * workspace too small.
- * qgemm_moe_workspace_bytes: 2 * T * top_k * inter, 0 for illegal sizes. */
+ * qgemm_moe_workspace_bytes: what such a call needs, 0 for sizes that no call
+ *   with T > 0 takes. */
 #define QGEMM_MOE_MAX_PAIRS 1024
 int qgemm_moe(int format_up, int format_down, const void *X, const void *Wup, const void *Wdown, const float *weights,
               const int32_t *offsets, const int32_t *rows, const void *residual, void *Y, int64_t T, int64_t top_k,
               int64_t E, int64_t hidden, int64_t inter, int64_t group_size, int has_zp, int act, int dtype,
               void *workspace, size_t workspace_bytes, void *stream);
-size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t inter);
+size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64_t inter);
 
 /* The staged arm (the dequant-scratch post, "The two passes hiding inside
  * one matmul": unpack to a 16-bit scratch, then a GEMM that reads it), kept

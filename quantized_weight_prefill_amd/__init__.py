@@ -29,6 +29,7 @@ Functions keep the C names without the ``qgemm_`` prefix:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -114,7 +115,7 @@ SIGNATURES = {
     "qgemm_moe_group": (_INT, [_VP, _I64, _I64, _I64, _VP, _VP, _VP]),
     "qgemm_moe": (_INT, [_INT, _INT, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _INT,
                          _INT, _INT, _VP, _SZ, _VP]),
-    "qgemm_moe_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "qgemm_moe_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
     "qgemm_gguf_header": (_INT, [_VP, _SZ, _VP, _VP, _VP, _VP, _VP]),
     "qgemm_gguf_tensor_info": (_INT, [_VP, _SZ, _I64, _VP, _SZ, _VP, _VP, _VP, _VP, _VP]),
     "qgemm_gguf_find_kv": (_INT, [_VP, _SZ, ctypes.c_char_p, _VP, _VP, _VP]),
@@ -477,27 +478,52 @@ def _act_code(act) -> int:
     return ACTS[act]
 
 
-def _sized(t, name, shape, dtype):
-    """t, when given, has this shape and dtype."""
-    if t is not None and (t.shape != shape or t.dtype != dtype):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+# A call of these layers at decode sizes takes a few microseconds on the GPU, so
+# their checks are kept to plain attribute reads, and the pure size queries of
+# the library (functions of the sizes alone) are remembered.
 
-
-def _together(ref, **tensors):
-    """The given tensors are contiguous and on ref's device, a GPU."""
+def _refuse(ref, named):
+    """Say what is wrong with the first of `named` ((name, tensor, shape, dtype),
+    shape and dtype None where any will do) that is not a contiguous tensor of
+    its shape and dtype on the device of `ref`, a GPU."""
+    for name, t, shape, dtype in named:
+        if t is not None and shape is not None and (t.shape != shape or t.dtype != dtype):
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if not ref.is_cuda:
-        raise ValueError("the activations must be a device tensor")
-    for name, t in tensors.items():
+        raise ValueError(f"{named[0][0]} must be a device tensor")
+    for name, t, _, _ in named:
         if t is None:
             continue
         if t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on the activations' device {ref.device}")
+            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {ref.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _checked(ref, *named):
+    """Raise unless every tensor of `named` is as :func:`_refuse` says."""
+    dev = ref.device
+    for _, t, shape, dtype in named:
+        if t is not None and ((shape is not None and (t.shape != shape or t.dtype != dtype)) or t.device != dev
+                              or not t.is_contiguous()):
+            _refuse(ref, named)
+    if not ref.is_cuda:
+        _refuse(ref, named)
+    return dev
+
+
+@functools.lru_cache(maxsize=4096)
+def _packed_need(f: int, N: int, K: int, group: int, has_zp: bool) -> int:
+    return packed_bytes(f, N, K, group if group else 128, has_zp)
+
+
+def _check_packed(name, f, wp, N, K, group, has_zp, experts=1):
+    need = _packed_need(f, N, K, group, bool(has_zp)) * experts
+    if need == 0:
+        raise QGemmError("packed_bytes", -2)
+    have = wp.numel() * wp.element_size()
+    if have < need:
+        raise ValueError(f"{name} holds {have} bytes, the packed weight needs {need}")
 
 
 def _scratch(need: int, workspace, device, stream):
@@ -506,57 +532,63 @@ def _scratch(need: int, workspace, device, stream):
     if workspace is not None:
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the activations' device")
-    elif need:
-        torch = _torch()
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=device))
-    else:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if not need:
         return None, 0, None
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    torch = _torch()
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream, device=device))
+    return ws.data_ptr(), need, ws
 
 
-def _call(fn, device, stream, args):
+def _call(fn, device, stream, *args):
     """lib().fn(*args, stream) with `device` as the current one (the library
     launches there), on `stream` or the device's current stream."""
-    cuda = _torch().cuda
-    if cuda.current_device() != device.index:
-        with cuda.device(device):
-            return _call(fn, device, stream, args)
+    torch = _torch()
+    index = device.index
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
     if stream is None:
-        stream = cuda.current_stream().cuda_stream
-    _check(fn, getattr(lib(), fn)(*args, stream))
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    st = getattr(_lib or lib(), fn)(*args, stream)
+    if st != 0:
+        raise QGemmError(fn, st)
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_need(f, rung, layout, M, N, K, gated, code) -> int:
+    return int(lib().qgemm_linear_workspace_bytes(f, rung, layout, M, N, K, gated, code))
 
 
 def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout, stream,
             workspace):
-    torch = _torch()
     f = FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+    dt = x.dtype
     code = _dtype_code(x)
     ac = _act_code(act)
+    gated, has_zp = (1 if gated else 0), (1 if has_zp else 0)
     nt = 2 * N if gated else N
-    if out_layout not in (X_ROW, X_FRAG):
-        raise ValueError("out_layout must be X_ROW or X_FRAG")
-    _check_wp(f, wp, nt, K, group, has_zp)
-    shape = (M, N)
-    if out_layout == X_FRAG:
+    if out_layout == X_ROW:
+        shape = (M, N)
+    elif out_layout == X_FRAG:
         shape = (xf_bytes(M, N) // 2,)
         if shape == (0,) and M > 0:
             raise QGemmError("qgemm_linear", -2)
-    _sized(bias, "bias", (nt,), x.dtype)
-    _sized(residual, "residual", (M, N), x.dtype)
-    _sized(out, "out", shape, x.dtype)
-    _together(x, x=x, wp=wp, bias=bias, residual=residual, out=out)
+    else:
+        raise ValueError("out_layout must be X_ROW or X_FRAG")
+    _check_packed("wp", f, wp, nt, K, group, has_zp)
+    dev = _checked(x, ("x", x, None, None), ("wp", wp, None, None), ("bias", bias, (nt,), dt),
+                   ("residual", residual, (M, N), dt), ("out", out, shape, dt))
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _torch().empty(shape, dtype=dt, device=dev)
     elif out_layout == X_FRAG and residual is not None and out.data_ptr() == residual.data_ptr():
         raise ValueError("a fragment-major out cannot be the residual")
-    gated, has_zp = int(bool(gated)), int(bool(has_zp))
-    need = lib().qgemm_linear_workspace_bytes(f, rung, layout, M, N, K, gated, code)
-    ws, wsb, _keep = _scratch(need, workspace, x.device, stream)
-    _call("qgemm_linear", x.device, stream,
-          (f, rung, layout, x.data_ptr(), wp.data_ptr(), _ptr(bias), _ptr(residual), out.data_ptr(), out_layout, M, N, K,
-           group, has_zp, ac, gated, code, ws, wsb))
+    ws, wsb, _keep = _scratch(_linear_need(f, rung, layout, M, N, K, gated, code), workspace, dev, stream)
+    _call("qgemm_linear", dev, stream, f, rung, layout, x.data_ptr(), wp.data_ptr(),
+          None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(),
+          out_layout, M, N, K, group, has_zp, ac, gated, code, ws, wsb)
     return out
 
 
@@ -812,18 +844,16 @@ def moe_route(logits, top_k: int, score: str = "softmax", renorm: bool = True, s
         raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
     lt = 2 if logits.dtype == torch.float32 else _dtype_code(logits)
     T, E = logits.shape
-    _together(logits, logits=logits)
+    dev = _checked(logits, ("logits", logits, None, None))
     if not 1 <= top_k <= min(E, 64):
         raise QGemmError("qgemm_moe_route", -2)
-    P = T * top_k
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     new = torch.empty if T else torch.zeros  # no tokens: every offset is 0
-    offsets = new((E + 1,), dtype=torch.int32, device=logits.device)
-    rows = torch.empty((P,), dtype=torch.int32, device=logits.device)
-    _call("qgemm_moe_route", logits.device, stream,
-          (logits.data_ptr(), lt, T, E, top_k, SCORES[score], int(bool(renorm)), scale, ids.data_ptr(),
-           weights.data_ptr(), offsets.data_ptr(), rows.data_ptr()))
+    offsets = new(E + 1, dtype=torch.int32, device=dev)
+    rows = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+    _call("qgemm_moe_route", dev, stream, logits.data_ptr(), lt, T, E, top_k, SCORES[score], 1 if renorm else 0, scale,
+          ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr())
     return ids, weights, offsets, rows
 
 
@@ -836,15 +866,16 @@ def moe_group(ids, E: int, stream=None):
     if ids.dim() != 2 or ids.dtype != torch.int32:
         raise ValueError("ids must be an int32 tensor [T, top_k]")
     T, k = ids.shape
-    _together(ids, ids=ids)
-    offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=ids.device)
-    rows = torch.empty((T * k,), dtype=torch.int32, device=ids.device)
-    _call("qgemm_moe_group", ids.device, stream, (ids.data_ptr(), T, E, k, offsets.data_ptr(), rows.data_ptr()))
+    dev = _checked(ids, ("ids", ids, None, None))
+    offsets = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
+    rows = torch.empty(T * k, dtype=torch.int32, device=dev)
+    _call("qgemm_moe_group", dev, stream, ids.data_ptr(), T, E, k, offsets.data_ptr(), rows.data_ptr())
     return offsets, rows
 
 
-def moe_workspace_bytes(T: int, top_k: int, inter: int) -> int:
-    return int(lib().qgemm_moe_workspace_bytes(T, top_k, inter))
+def moe_workspace_bytes(T: int, top_k: int, hidden: int, inter: int) -> int:
+    """Bytes of the workspace a :func:`moe` call of these sizes needs."""
+    return int(lib().qgemm_moe_workspace_bytes(T, top_k, hidden, inter))
 
 
 def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, group: int = 0, has_zp: bool = False,
@@ -870,24 +901,21 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
     ac = _act_code(act)
     if E < 1 or k < 1:
         raise ValueError("offsets must hold E+1 entries and weights at least one column")
-    _sized(weights, "weights", (T, k), torch.float32)
-    _sized(offsets, "offsets", (E + 1,), torch.int32)
-    _sized(rows, "rows", (T * k,), torch.int32)
-    _sized(residual, "residual", (T, H), x.dtype)
-    _sized(out, "out", (T, H), x.dtype)
-    _check_wp(fu, w_up, 2 * inter, H, group, has_zp, experts=E)
-    _check_wp(fd, w_down, H, inter, group, has_zp, experts=E)
-    _together(x, x=x, w_up=w_up, w_down=w_down, weights=weights, offsets=offsets, rows=rows, residual=residual, out=out)
-    if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
-    need = lib().qgemm_moe_workspace_bytes(T, k, inter)
+    _check_packed("w_up", fu, w_up, 2 * inter, H, group, has_zp, E)
+    _check_packed("w_down", fd, w_down, H, inter, group, has_zp, E)
+    i32 = torch.int32
+    dev = _checked(x, ("x", x, None, None), ("w_up", w_up, None, None), ("w_down", w_down, None, None),
+                   ("weights", weights, (T, k), torch.float32), ("offsets", offsets, (E + 1,), i32),
+                   ("rows", rows, (T * k,), i32), ("residual", residual, (T, H), x.dtype), ("out", out, (T, H), x.dtype))
+    need = lib().qgemm_moe_workspace_bytes(T, k, H, inter)
     if need == 0 and T > 0:
         raise QGemmError("qgemm_moe", -2)
-    ws, wsb, _keep = _scratch(need, workspace, x.device, stream)
-    _call("qgemm_moe", x.device, stream,
-          (fu, fd, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-           rows.data_ptr(), _ptr(residual), out.data_ptr(), T, k, E, H, inter, group, int(bool(has_zp)), ac, code, ws,
-           wsb))
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+    ws, wsb, _keep = _scratch(need, workspace, dev, stream)
+    _call("qgemm_moe", dev, stream, fu, fd, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), weights.data_ptr(),
+          offsets.data_ptr(), rows.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), T, k, E,
+          H, inter, group, 1 if has_zp else 0, ac, code, ws, wsb)
     return out
 
 

@@ -726,16 +726,25 @@ int moe_route_shape(long long T, long long E, long long k)
     return T > (INT32_MAX - 1024) / k ? QGEMM_ERR_SHAPE : QGEMM_OK;
 }
 
-hipError_t launch_up(int fmt, int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s)
+hipError_t launch_up(int fmt, int dtype, int rb, int waves, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
-    if (fmt == FMT_Q4K) return launch_moe_up<FMT_Q4K>(dtype, rb, grid, m, s);
-    return fmt == FMT_Q6K ? launch_moe_up<FMT_Q6K>(dtype, rb, grid, m, s) : launch_moe_up<FMT_W4>(dtype, rb, grid, m, s);
+    if (fmt == FMT_Q4K) return launch_moe_up<FMT_Q4K>(dtype, rb, waves, grid, m, s);
+    return fmt == FMT_Q6K ? launch_moe_up<FMT_Q6K>(dtype, rb, waves, grid, m, s)
+                          : launch_moe_up<FMT_W4>(dtype, rb, waves, grid, m, s);
 }
 
 hipError_t launch_down(int fmt, int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
     if (fmt == FMT_Q4K) return launch_moe_down<FMT_Q4K>(dtype, grid, m, s);
     return fmt == FMT_Q6K ? launch_moe_down<FMT_Q6K>(dtype, grid, m, s) : launch_moe_down<FMT_W4>(dtype, grid, m, s);
+}
+
+// Workgroups of the down product that share a 16-column panel of Y: two
+// workgroups of eight waves for each CU.
+int moe_split(long long H)
+{
+    const long long panels = (H + 15) / 16;
+    return (int)std::min(8LL, std::max(1LL, 2 * kCUs / panels));
 }
 
 int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const float *wts, const int32_t *offs,
@@ -758,9 +767,9 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     if (!aligned16(X) || !aligned16(Wu) || !aligned16(Wd) || !aligned16(res) || !aligned16(Y) || !aligned4(wts) ||
         !aligned4(offs) || !aligned4(rows))  // an expert's packed size is whole 16-byte pieces: H and I fill whole panels
         return QGEMM_ERR_ALIGN;
-    if (!ws || ws_bytes < qgemm_moe_workspace_bytes(T, k, I)) return QGEMM_ERR_SIZE;
+    if (!ws || ws_bytes < qgemm_moe_workspace_bytes(T, k, H, I)) return QGEMM_ERR_SIZE;
     if (!aligned16(ws)) return QGEMM_ERR_ALIGN;
-    if (!launch_fits(I / 16, 512) || !launch_fits((H + 15) / 16, 1024)) return QGEMM_ERR_SHAPE;
+    if (!launch_fits(I / 16, 512) || !launch_fits((H + 15) / 16 * 8, 512)) return QGEMM_ERR_SHAPE;
     const long long P = T * k;
     MoeArgs m{};
     m.rows = rows;
@@ -770,8 +779,15 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.top_k = (int)k;
     m.inter = (int)I;
 
-    // gate and up: rows per tile by the experts' mean count; eight waves
-    // split K while each keeps two chunks
+    const long long tiles = std::min(P, (P + 15) / 16 + E);  // a bound on the 16-row tiles
+    m.panels = (int)((H + 15) / 16);
+    m.split = moe_split(H);
+    m.partial = (float *)(m.H + P * I);
+    m.arrived = (int *)(m.partial + (long long)m.panels * m.split * T * 16);
+
+    // gate and up: rows per tile by the experts' mean count; K split over
+    // waves while the grid holds fewer than 4096 of them and each keeps two
+    // chunks
     const long long avg = (P + E - 1) / E;
     const int rb = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
     m.g = make_args(fu, X, Wu, nullptr, P, 2 * I, H, group, has_zp);
@@ -780,22 +796,24 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.g.wstride = su;
     m.g.act = act;
     const int nch = (int)(H / kChunk);
-    m.g.kw = 8;
-    while (m.g.kw > 1 && nch < 2 * m.g.kw) m.g.kw /= 2;
-    const dim3 gu((unsigned)(I / 16), (unsigned)std::min(P, (P + 16 * rb - 1) / (16 * rb) + E), 1);
-    hipError_t e = launch_up(fu, dtype, rb, gu, m, (hipStream_t)stream);
+    const long long slots = std::min(P, (P + 16 * rb - 1) / (16 * rb) + E);
+    m.g.kw = 1;
+    while (m.g.kw < 8 && slots * (I / 16) * m.g.kw < 4096 && nch >= 4 * m.g.kw) m.g.kw *= 2;
+    const int waves = std::max(4, m.g.kw), per = waves / m.g.kw;
+    const dim3 gu((unsigned)((I / 16 + per - 1) / per), (unsigned)slots, 1);
+    hipError_t e = launch_up(fu, dtype, rb, waves, gu, m, (hipStream_t)stream);
     if (e != hipSuccess) return launch_status(e, "moe up");
 
-    // down: K in parts while the row tiles alone leave waves of a workgroup idle
+    // down: K in parts while the row tiles alone leave waves idle
     m.g = make_args(fd, nullptr, Wd, Y, P, H, I, group, has_zp);
     m.g.offs = offs;
     m.g.E = (int)E;
     m.g.wstride = sd;
     m.g.res = (const uint16_t *)res;
-    const long long tiles = std::min(P, (P + 15) / 16 + E);
     m.parts = 1;
-    while (tiles * 2 * m.parts <= 16 && I / kChunk >= 2 * m.parts) m.parts *= 2;
-    e = launch_down(fd, dtype, dim3((unsigned)((H + 15) / 16), 1, 1), m, (hipStream_t)stream);
+    while (m.parts < 8 && tiles * m.parts < 8 * m.split && I / kChunk >= 2 * m.parts && 2 * m.parts * P <= 1024)
+        m.parts *= 2;
+    e = launch_down(fd, dtype, dim3((unsigned)(m.panels * m.split), 1, 1), m, (hipStream_t)stream);
     return launch_status(e, "moe down");
 }
 
@@ -1266,12 +1284,17 @@ int qgemm_moe(int format_up, int format_down, const void *X, const void *Wup, co
                group_size, has_zp, act, dtype, workspace, workspace_bytes, stream);
 }
 
-size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t inter)
+// h [pairs][inter], the panels' partial sums and their arrival counters; inter
+// and hidden are multiples of 128 in every legal call, so each part starts
+// 16-byte aligned.
+size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64_t inter)
 {
-    if (T < 0 || top_k < 1 || T > QGEMM_MOE_MAX_PAIRS || top_k > QGEMM_MOE_MAX_PAIRS || T * top_k > QGEMM_MOE_MAX_PAIRS ||
-        inter < 1 || inter > INT32_MAX / 2)
+    if (T < 1 || top_k < 1 || T > QGEMM_MOE_MAX_PAIRS || top_k > QGEMM_MOE_MAX_PAIRS || T * top_k > QGEMM_MOE_MAX_PAIRS ||
+        inter < kChunk || inter > INT32_MAX / 2 || inter % kChunk != 0 || hidden < kChunk || hidden > INT32_MAX ||
+        hidden % kChunk != 0)
         return 0;
-    return 2 * (size_t)(T * top_k) * (size_t)inter;
+    return 2 * (size_t)(T * top_k) * (size_t)inter + 4 * (size_t)moe_split(hidden) * (size_t)(T * hidden) +
+           4 * (size_t)(hidden / 16);
 }
 
 int qgemm_grouped_plan(int64_t T, int64_t E, int64_t N, int64_t K, int32_t *info8)

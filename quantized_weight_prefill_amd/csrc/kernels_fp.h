@@ -10,6 +10,72 @@
 
 namespace qg {
 
+// acc[PN][RB] += X rows . panels over chunks [cb, ce) of one wave, D chunks of
+// weights and DX of activations in flight ahead of the one being multiplied
+// (DX divides D; the activations come from L2, whose latency is a fraction of
+// the memory's).  cb and ce are the same in every lane.  The steady state has
+// no branch, so that a wait counts only the loads it needs; each output's
+// MFMAs run in chunk order whatever D.
+template <int FMT, int DT, int RB, int PN, int XL, int D, int DX>
+__device__ __forceinline__ void stream_chunks(const RunSrc<FMT> (&src)[PN], const uint16_t *const (&xrow)[RB], int cb,
+                                              int ce, f32x4 (&acc)[PN][RB])
+{
+    using XA = XLay<XL>;
+    static_assert(D % DX == 0, "the rings turn together");
+    RunRaw<FMT> raw[D][PN];
+    u32x4 xf[DX][RB][4];
+    auto fetch_w = [&](int c, int d) {
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) src[pn].load(c, raw[d][pn]);
+    };
+    auto fetch_x = [&](int c, int d) {
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) xf[d][rb][i] = *(const u32x4 *)(xrow[rb] + XA::chunk(c) + XA::off(8 * i));
+    };
+    // chunk c from slot d; its slots refilled with chunks c + D and c + DX
+    auto step = [&](int c, int d, bool more_w, bool more_x) {
+        const int dx = d % DX;
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) {
+            u32x4 wf[4];
+            unpack_run<FMT, DT>(raw[d][pn], src[pn], c, wf);
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[i], xf[dx][rb][i], acc[pn][rb]);
+        }
+        if (more_w) fetch_w(c + D, d);
+        if (more_x) fetch_x(c + DX, dx);
+        __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where they are next needed
+    };
+#pragma unroll
+    for (int d = 0; d < D; d++)
+        if (cb + d < ce) {
+            fetch_w(cb + d, d);
+            if (d < DX) fetch_x(cb + d, d);
+        }
+    int c = cb;
+    for (; c + 2 * D <= ce; c += D)
+#pragma unroll
+        for (int d = 0; d < D; d++) step(c + d, d, true, true);
+#pragma unroll
+    for (int d = 0; d < D; d++)
+        if (c + d < ce) step(c + d, d, c + d + D < ce, c + d + DX < ce);
+    c += D;
+#pragma unroll
+    for (int d = 0; d + 1 < D; d++)
+        if (c + d < ce) step(c + d, d, false, c + d + DX < ce);
+}
+
+// Depths of the rings above by what one chunk takes in registers.
+template <int RB, int PN>
+struct Depth {
+    static constexpr int W = PN == 1 ? 4 : PN == 2 ? 3 : 2;
+    static constexpr int X = RB > 2 ? 1 : PN == 1 ? 2 : 1;
+};
+
 // ---------------------------------------------------------------------------
 // Direct kernel: decode-adjacent M and skinny N.
 //
@@ -30,7 +96,8 @@ __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
     static_assert(EPI != EP_GATED || PN % 2 == 0, "gate and up panels come in pairs");
     using XA = XLay<XL>;
     extern __shared__ f32x4 red[];  // [kw][PN*RB][64]
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int w = EPI == EP_NONE ? threadIdx.x >> 6 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int nch = a.K / kChunk;
     const int cb = (int)((long long)nch * w / a.kw), ce = (int)((long long)nch * (w + 1) / a.kw);
@@ -52,6 +119,10 @@ __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
 #pragma unroll
     for (int pn = 0; pn < PN; pn++) src[pn].init(a, packed_panel<EPI>(a, p0 + pn), g, col);
 
+    if constexpr (EPI != EP_NONE) {
+        // the linear layer: the same MFMAs in the same order, more chunks in flight
+        stream_chunks<FMT, DT, RB, PN, XL, Depth<RB, PN>::W, Depth<RB, PN>::X>(src, xrow, cb, ce, acc);
+    } else {
     RunRaw<FMT> raw[PN];
     u32x4 xf[RB][4];
     if (cb < ce) {
@@ -85,6 +156,7 @@ __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
             for (int pn = 0; pn < PN; pn++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[pn][i], xc[rb][i], acc[pn][rb]);
+    }
     }
 
     constexpr int PS = EPI == EP_GATED ? 2 : 1;  // tile panels behind one output panel

@@ -1,6 +1,6 @@
 // kernels_moe.h -- a mixture-of-experts layer for a few tokens, two launches:
 //
-//   h[i]  = RN_t( act(x_t . Wg_e) * (x_t . Wu_e) )          k_moe_up
+//   h[i]  = RN_t( act(x_t . Wg_e) * (x_t . Wu_e) )            k_moe_up
 //   Y[t]  = RN_t( r[t] + sum_j w[t][j] * (h[i(t,j)] . Wd_e) ) k_moe_down
 //
 // for the pairs i of tokens t and experts e in the order of `rows` (grouped by
@@ -9,14 +9,17 @@
 // With a few rows per expert the layer is a stream of the active experts'
 // packed weights: both kernels exist to keep that stream as deep as the
 // memory's latency asks, and to read each weight once.
-//   * k_moe_up: a workgroup owns one gate panel, the up panel of the same
-//     outputs and one row tile of one expert; its waves split K.  It gathers
-//     x by the pair's token, so no gathered copy is made.
-//   * k_moe_down: a workgroup of 16 waves owns one 16-column panel of Y for
-//     all tokens; its waves take the experts' row tiles in turn (and split K
-//     when there are few), leave each pair's 16 outputs in LDS in fp32, and
-//     the workgroup then adds them per token in slot order with the routing
-//     weights: no atomics, no partial sums in memory, and a fixed order.
+//   * k_moe_up: a wave owns one gate panel, the up panel of the same outputs,
+//     one row tile of one expert and a share of K; the kw waves of a share
+//     add up through LDS.  It gathers x by the pair's token, so no gathered
+//     copy is made.
+//   * k_moe_down: a workgroup owns one 16-column panel of Y for all tokens and
+//     every split-th row tile of the experts; its waves take those in turn
+//     (in parts of K when they are few), leave each pair's 16 outputs in LDS
+//     in fp32, and the workgroup adds them per token in slot order with the
+//     routing weights.  With split > 1 the panel's workgroups leave those
+//     sums in memory, and the last of them to arrive adds them in order: no
+//     floating-point atomics, and a result that does not depend on timing.
 // h is rounded to the operand type because the second product's MFMA takes
 // it so; the sum over a token's experts stays in fp32 until the one store.
 #pragma once
@@ -28,53 +31,122 @@
 
 namespace qg {
 
-constexpr int kMoeDownWaves = 16;
+constexpr int kMoeUpWaves = 4;    // k_moe_up: waves per workgroup while K is not split further
+constexpr int kMoeDownWaves = 8;
 
 inline size_t moe_down_lds(long long pairs, long long E, int parts)
 {
     const long long slots = std::min(pairs, (pairs + 15) / 16 + E);
-    return (size_t)(parts * pairs * 64 + slots * 12 + pairs);
+    return (size_t)(parts * pairs * 64 + slots * 12 + pairs * 5);
 }
 
-// acc[PN][RB] += X rows . panels over chunks [cb, ce), with up to D chunks of
-// weights and activations in flight ahead of the one being multiplied.
-template <int FMT, int DT, int RB, int PN, int D>
-__device__ __forceinline__ void stream_chunks(const RunSrc<FMT> (&src)[PN], const uint16_t *const (&xrow)[RB], int cb,
-                                              int ce, f32x4 (&acc)[PN][RB])
+// Inclusive scans over the wave in DPP steps: row shifts inside rows of 16
+// lanes, then the row broadcasts into the rows that lack them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_from(int x, int identity)
 {
-    RunRaw<FMT> raw[D][PN];
-    u32x4 xf[D][RB][4];
-    auto fetch = [&](int c, int d) {
+    return __builtin_amdgcn_update_dpp(identity, x, CTRL, ROWS, 0xF, false);
+}
+
+__device__ __forceinline__ int wave_scan_add(int x)
+{
+    x += dpp_from<0x111, 0xF>(x, 0);  // row_shr:1
+    x += dpp_from<0x112, 0xF>(x, 0);  // row_shr:2
+    x += dpp_from<0x114, 0xF>(x, 0);  // row_shr:4
+    x += dpp_from<0x118, 0xF>(x, 0);  // row_shr:8
+    x += dpp_from<0x142, 0xA>(x, 0);  // row_bcast:15 into rows 1 and 3
+    x += dpp_from<0x143, 0xC>(x, 0);  // row_bcast:31 into rows 2 and 3
+    return x;
+}
+
+__device__ __forceinline__ int wave_scan_max(int x)
+{
+    x = max(x, dpp_from<0x111, 0xF>(x, INT_MIN));
+    x = max(x, dpp_from<0x112, 0xF>(x, INT_MIN));
+    x = max(x, dpp_from<0x114, 0xF>(x, INT_MIN));
+    x = max(x, dpp_from<0x118, 0xF>(x, INT_MIN));
+    x = max(x, dpp_from<0x142, 0xA>(x, INT_MIN));
+    x = max(x, dpp_from<0x143, 0xC>(x, INT_MIN));
+    return x;
+}
+
+// The experts' row tiles of `rows_per` rows, in expert order, 64 experts at a
+// time, a lane per expert: visit(lane's expert, its first row, its end, its
+// tile count, the tiles before it) until it returns true.  Offsets are
+// clamped into [0, P] and made non-decreasing as the grouped GEMM does, so
+// any contents stay inside the buffers.  Returns the tiles visited over.
+template <class F>
+__device__ __forceinline__ int visit_tiles(const Args &a, int rows_per, int lane, F visit)
+{
+    constexpr int G = 4;  // groups of 64 experts whose offsets are loaded together
+    int qc = max(0, a.offs[0]), base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64 * G) {
+        int q[G];
 #pragma unroll
-        for (int pn = 0; pn < PN; pn++) src[pn].load(c, raw[d][pn]);
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) xf[d][rb][i] = *(const u32x4 *)(xrow[rb] + (long long)kChunk * c + 8 * i);
-    };
-#pragma unroll
-    for (int d = 0; d < D; d++)
-        if (cb + d < ce) fetch(cb + d, d);
-    for (int c = cb; c < ce; c += D) {
-#pragma unroll
-        for (int d = 0; d < D; d++) {
-            if (c + d >= ce) break;
-            u32x4 wf[PN][4];
-#pragma unroll
-            for (int pn = 0; pn < PN; pn++) unpack_run<FMT, DT>(raw[d][pn], src[pn], c + d, wf[pn]);
-            u32x4 xc[RB][4];
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) xc[rb][i] = xf[d][rb][i];
-            if (c + d + D < ce) fetch(c + d + D, d);
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-                for (int pn = 0; pn < PN; pn++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[pn][i], xc[rb][i], acc[pn][rb]);
+        for (int i = 0; i < G; i++) {
+            const int e = e0 + 64 * i + lane;
+            q[i] = e < a.E ? a.offs[e + 1] : INT_MIN;
         }
+#pragma unroll
+        for (int i = 0; i < G; i++) {
+            const int e = e0 + 64 * i + lane;
+            if (e0 + 64 * i >= a.E) break;
+            const int qi = max(wave_scan_max(q[i]), qc);                                 // max(0, offs[0..e+1])
+            const int qp = __builtin_amdgcn_update_dpp(qc, qi, 0x138, 0xF, 0xF, false);  // wave_shr:1, lane 0 keeps qc
+            const int lo = min(qp, a.M), hi = min(qi, a.M);
+            const int nb = e < a.E ? (hi - lo + rows_per - 1) / rows_per : 0;
+            const int incl = wave_scan_add(nb);
+            if (visit(e, lo, hi, nb, base + incl - nb)) return base;
+            base += __builtin_amdgcn_readlane(incl, 63);
+            qc = __builtin_amdgcn_readlane(qi, 63);
+        }
+    }
+    return base;
+}
+
+// Row tile j: expert e, rows [lo, hi) of the expert, tile t of it; false when
+// j is past the last tile.  The same answer in every lane.
+__device__ __forceinline__ bool find_moe_tile(const Args &a, int j, int rows_per, int lane, int &e_out, int &lo_out,
+                                              int &hi_out, int &t_out)
+{
+    bool found = false;
+    visit_tiles(a, rows_per, lane, [&](int e, int lo, int hi, int nb, int before) {
+        const unsigned long long hit = __ballot(j >= before && j < before + nb);
+        if (hit == 0ull) return false;
+        const int l = __builtin_amdgcn_readfirstlane(__ffsll((long long)hit) - 1);
+        e_out = __builtin_amdgcn_readlane(e, l);
+        lo_out = __builtin_amdgcn_readlane(lo, l);
+        hi_out = __builtin_amdgcn_readlane(hi, l);
+        t_out = j - __builtin_amdgcn_readlane(before, l);
+        found = true;
+        return true;
+    });
+    return found;
+}
+
+// Four floats written to, or read from, the device's point of coherence (past
+// the L2 of the XCD): how workgroups on different XCDs hand over sums inside
+// one kernel.  Agent-scope atomics do that by themselves; a release fence
+// would write back the XCD's whole L2, once per wave (measured: 105 instead
+// of 10 us for the down product of one token).
+__device__ __forceinline__ void store_agent(float *p, const float (&v)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const unsigned long long x = (unsigned long long)__builtin_bit_cast(uint32_t, v[2 * i]) |
+                                     (unsigned long long)__builtin_bit_cast(uint32_t, v[2 * i + 1]) << 32;
+        __hip_atomic_store((unsigned long long *)p + i, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+
+__device__ __forceinline__ void load_agent(const float *p, float (&v)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const unsigned long long x =
+            __hip_atomic_load((const unsigned long long *)p + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        v[2 * i] = __builtin_bit_cast(float, (uint32_t)x);
+        v[2 * i + 1] = __builtin_bit_cast(float, (uint32_t)(x >> 32));
     }
 }
 
@@ -85,23 +157,28 @@ __device__ __forceinline__ int pair_at(const MoeArgs &m, int i)
     return (int)min((unsigned)m.rows[i], (unsigned)(m.g.M - 1));
 }
 
-// Grid: x = gate panels (inter/16), y = row-tile slots of 16*RB rows;
-// 64*kw threads, kw waves splitting K.
-template <int FMT, int DT, int RB, int D>
+// Grid: x = groups of nw/kw gate panels (inter/16 in all), y = row-tile slots
+// of 16*RB rows; nw waves, of which kw split the K of one panel.
+template <int FMT, int DT, int RB>
 __global__ void __launch_bounds__(512) k_moe_up(MoeArgs m)
 {
-    extern __shared__ f32x4 red[];  // [kw][2*RB][64]
+    extern __shared__ f32x4 red[];  // [nw][2*RB][64]
     const Args &a = m.g;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    if (blockIdx.x == 0 && blockIdx.y == 0)  // the counters of k_moe_down, which runs after this launch
+        for (int i = threadIdx.x; i < m.panels; i += blockDim.x) m.arrived[i] = 0;
     int e, lo, hi, t;
     // the same answer in every wave: the whole workgroup leaves together
-    if (!find_group_tile(a, blockIdx.y, 16 * RB, lane, e, lo, hi, t)) return;
+    if (!find_moe_tile(a, blockIdx.y, 16 * RB, lane, e, lo, hi, t)) return;
+    const int per = (blockDim.x >> 6) / a.kw, share = w % a.kw;
+    const int pairs = a.np >> 1, p = min((int)blockIdx.x * per + w / a.kw, pairs - 1);  // past the end: computed and discarded
     Args b = a;
     b.W = a.W + (long long)e * a.wstride;
     const int m0 = lo + t * 16 * RB;
     RunSrc<FMT> src[2];
-    src[0].init(b, blockIdx.x, g, col);
-    src[1].init(b, (a.np >> 1) + blockIdx.x, g, col);
+    src[0].init(b, p, g, col);
+    src[1].init(b, pairs + p, g, col);
     const uint16_t *xrow[RB];
 #pragma unroll
     for (int rb = 0; rb < RB; rb++) {
@@ -114,106 +191,171 @@ __global__ void __launch_bounds__(512) k_moe_up(MoeArgs m)
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) acc[pn][rb] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int nch = a.K / kChunk;
-    const int cb = (int)((long long)nch * w / a.kw), ce = (int)((long long)nch * (w + 1) / a.kw);
-    stream_chunks<FMT, DT, RB, 2, D>(src, xrow, cb, ce, acc);
+    const int cb = (int)((long long)nch * share / a.kw), ce = (int)((long long)nch * (share + 1) / a.kw);
+    stream_chunks<FMT, DT, RB, 2, X_ROW, Depth<RB, 2>::W, Depth<RB, 2>::X>(src, xrow, cb, ce, acc);
+    if (a.kw > 1) {
 #pragma unroll
-    for (int pn = 0; pn < 2; pn++)
+        for (int pn = 0; pn < 2; pn++)
 #pragma unroll
-        for (int rb = 0; rb < RB; rb++) red[(w * 2 * RB + pn * RB + rb) * 64 + lane] = acc[pn][rb];
-    __syncthreads();
-    for (int rb = w; rb < RB; rb += a.kw) {
-        f32x4 vg = red[rb * 64 + lane], vu = red[(RB + rb) * 64 + lane];
-        for (int ww = 1; ww < a.kw; ww++) {
-            vg += red[(ww * 2 * RB + rb) * 64 + lane];
-            vu += red[(ww * 2 * RB + RB + rb) * 64 + lane];
-        }
-        float v[4] = {vg[0], vg[1], vg[2], vg[3]};
+            for (int rb = 0; rb < RB; rb++) red[(w * 2 * RB + pn * RB + rb) * 64 + lane] = acc[pn][rb];
+        __syncthreads();
+        if (share != 0) return;
+        for (int ww = 1; ww < a.kw; ww++)
+#pragma unroll
+            for (int pn = 0; pn < 2; pn++)
+#pragma unroll
+                for (int rb = 0; rb < RB; rb++) acc[pn][rb] += red[((w + ww) * 2 * RB + pn * RB + rb) * 64 + lane];
+    }
+    if ((int)blockIdx.x * per + w / a.kw >= pairs) return;
+#pragma unroll
+    for (int rb = 0; rb < RB; rb++) {
+        float v[4] = {acc[0][rb][0], acc[0][rb][1], acc[0][rb][2], acc[0][rb][3]};
         act_apply(a.act, v);
+        const f32x4 u = acc[1][rb];
         const int i = m0 + 16 * rb + col;
         if (i < hi) {
             u32x2 o;
-            o[0] = pack_out<DT>(v[0] * vu[0], v[1] * vu[1]);
-            o[1] = pack_out<DT>(v[2] * vu[2], v[3] * vu[3]);
-            *(u32x2 *)(m.H + (long long)i * m.inter + 16 * blockIdx.x + 4 * g) = o;
+            o[0] = pack_out<DT>(v[0] * u[0], v[1] * u[1]);
+            o[1] = pack_out<DT>(v[2] * u[2], v[3] * u[3]);
+            *(u32x2 *)(m.H + (long long)i * m.inter + 16 * p + 4 * g) = o;
         }
     }
 }
 
-// Grid: x = panels of Y; 16 waves.  Dynamic LDS (moe_down_lds): parts * pairs
-// * 16 floats, the row tiles (expert, first row, end of the expert's rows),
-// and a flag per pair that some expert has computed it: a pair that no expert
-// here serves adds nothing, whatever its weight holds.
+// Grid: x = panels of Y times split.  Dynamic LDS (moe_down_lds): parts *
+// pairs * 16 floats, the row tiles (expert, first row, end of the expert's
+// rows), the sorted pairs, and a flag per pair that some expert has computed
+// it: a pair that no expert here serves adds nothing, whatever its weight
+// holds.
+//
+// A wave's work is one sequence of 128-wide chunks over its units (row tile,
+// part of K), with D chunks of weights in flight across the units' borders:
+// `front` walks the sequence where the loads are, `back` where the MFMAs are.
 template <int FMT, int DT, int D>
-__global__ void __launch_bounds__(64 * kMoeDownWaves) k_moe_down(MoeArgs m)
+__global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
 {
     extern __shared__ float sums[];  // [parts][pairs][16]
-    __shared__ int s_tiles;
+    __shared__ int s_tiles, s_last;
     const Args &a = m.g;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, g = lane >> 4;
     const int P = a.M, span = P * 16;
+    const int panel = blockIdx.x / m.split, slice = blockIdx.x - panel * m.split;
     int *tile_e = (int *)(sums + (size_t)m.parts * span);
     const int slots = min(P, (P + 15) / 16 + a.E);  // a bound on the row tiles
     int *tile_lo = tile_e + slots, *tile_hi = tile_lo + slots;
-    uint8_t *served = (uint8_t *)(tile_hi + slots);
-    for (int i = tid; i < P; i += 64 * kMoeDownWaves) served[i] = 0;
-    if (w == 0) {  // the row tiles, 64 experts at a time: a lane per expert, as find_group_tile clamps the offsets
-        int qc = max(0, a.offs[0]), base = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 64) {
-            const int e = e0 + lane;
-            const bool live = e < a.E;
-            int q = live ? a.offs[e + 1] : INT_MIN;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int u = __shfl_up(q, d, 64);
-                if (lane >= d) q = max(q, u);
-            }
-            q = max(q, qc);
-            int qprev = __shfl_up(q, 1, 64);
-            if (lane == 0) qprev = qc;
-            const int lo = min(qprev, P), hi = min(q, P);
-            const int nb = live ? (hi - lo + 15) / 16 : 0;
-            int incl = nb;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int u = __shfl_up(incl, d, 64);
-                if (lane >= d) incl += u;
-            }
+    int *pair_of = tile_hi + slots;
+    uint8_t *served = (uint8_t *)(pair_of + P);
+    for (int i = tid; i < P; i += 64 * kMoeDownWaves) {
+        pair_of[i] = pair_at(m, i);
+        served[i] = 0;
+    }
+    if (w == 0) {
+        const int n = visit_tiles(a, 16, lane, [&](int e, int lo, int hi, int nb, int before) {
             for (int j = 0; j < nb; j++) {
-                const int at = base + incl - nb + j;
-                tile_e[at] = e;
-                tile_lo[at] = lo + 16 * j;
-                tile_hi[at] = hi;
+                tile_e[before + j] = e;
+                tile_lo[before + j] = lo + 16 * j;
+                tile_hi[before + j] = hi;
             }
-            base += __shfl(incl, 63, 64);
-            qc = __shfl(q, 63, 64);
-        }
-        if (lane == 0) s_tiles = base;
+            return false;
+        });
+        if (lane == 0) s_tiles = n;
     }
     __syncthreads();
-    const int nch = a.K / kChunk, units = s_tiles * m.parts;
-    for (int u = w; u < units; u += kMoeDownWaves) {
-        const int tile = u / m.parts, part = u - tile * m.parts;
-        const int lo = tile_lo[tile], hi = tile_hi[tile];
+    const int nch = a.K / kChunk, tiles = __builtin_amdgcn_readfirstlane(s_tiles);
+    // this workgroup's units: tiles slice, slice + split, ..., each in `parts` parts of K
+    const int units = (tiles > slice ? (tiles - slice + m.split - 1) / m.split : 0) * m.parts;
+
+    struct Cursor {
+        int u, c, ce;  // unit, next chunk, end of the unit's chunks
+        int lo, hi;
+    };
+    auto open = [&](Cursor &q) {  // the unit's rows and chunks
+        const int tile = slice + m.split * (q.u / m.parts), part = q.u % m.parts;
+        q.lo = __builtin_amdgcn_readfirstlane(tile_lo[tile]);
+        q.hi = __builtin_amdgcn_readfirstlane(tile_hi[tile]);
+        q.c = nch * part / m.parts;
+        q.ce = nch * (part + 1) / m.parts;
+        return __builtin_amdgcn_readfirstlane(tile_e[tile]);
+    };
+    RunSrc<FMT> src;      // at the front cursor's expert
+    const uint16_t *xrow; // at the front cursor's rows
+    auto aim = [&](Cursor &q) {
+        const int e = open(q);
         Args b = a;
-        b.W = a.W + (long long)tile_e[tile] * a.wstride;
-        RunSrc<FMT> src[1];
-        src[0].init(b, blockIdx.x, g, col);
-        const int i = lo + col;
-        const uint16_t *xrow[1] = {m.H + (long long)min(i, hi - 1) * a.K + 32 * g};
-        const int pair = i < hi ? pair_at(m, i) : 0;
-        f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
-        stream_chunks<FMT, DT, 1, 1, D>(src, xrow, (int)((long long)nch * part / m.parts),
-                                        (int)((long long)nch * (part + 1) / m.parts), acc);
-        if (i < hi) {
-            *(f32x4 *)(sums + (size_t)part * span + pair * 16 + 4 * g) = acc[0][0];
-            if (part == 0 && g == 0) served[pair] = 1;
+        b.W = a.W + (long long)e * a.wstride;
+        src.init(b, panel, g, col);
+        xrow = m.H + (long long)min(q.lo + col, q.hi - 1) * a.K + 32 * g;
+    };
+    if (w < units) {
+        RunRaw<FMT> raw[D];
+        u32x4 xf[D][4];
+        Cursor front{w, 0, 0, 0, 0}, back{w, 0, 0, 0, 0};
+        aim(front);
+        open(back);
+        int total = 0;  // chunks of this wave's sequence
+        if (m.parts == 1) {
+            total = (units - w + kMoeDownWaves - 1) / kMoeDownWaves * nch;
+        } else {
+            for (int u = w; u < units; u += kMoeDownWaves)
+                total += nch * (u % m.parts + 1) / m.parts - nch * (u % m.parts) / m.parts;
         }
+        auto fetch = [&](int d) {
+            src.load(front.c, raw[d]);
+#pragma unroll
+            for (int i = 0; i < 4; i++) xf[d][i] = *(const u32x4 *)(xrow + (long long)kChunk * front.c + 8 * i);
+            if (++front.c == front.ce) {
+                front.u += kMoeDownWaves;
+                if (front.u < units) aim(front);
+            }
+        };
+        f32x4 acc{0.f, 0.f, 0.f, 0.f};
+        // the branches below touch LDS only: a load from memory in one would
+        // make the next wait drain the ring
+        auto consume = [&](int d) {
+            u32x4 wf[4];
+            unpack_run<FMT, DT>(raw[d], src, back.c, wf);
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc = mma<DT>(wf[i], xf[d][i], acc);
+            if (++back.c == back.ce) {
+                const int i = back.lo + col;
+                if (i < back.hi) {
+                    const int pair = pair_of[i], part = back.u % m.parts;
+                    *(f32x4 *)(sums + (size_t)part * span + pair * 16 + 4 * g) = acc;
+                    if (part == 0 && g == 0) served[pair] = 1;
+                }
+                acc = f32x4{0.f, 0.f, 0.f, 0.f};
+                back.u += kMoeDownWaves;
+                if (back.u < units) open(back);
+            }
+        };
+#pragma unroll
+        for (int d = 0; d < D; d++)
+            if (d < total) fetch(d);
+        int s = 0;
+        for (; s + 2 * D <= total; s += D)
+#pragma unroll
+            for (int d = 0; d < D; d++) {
+                consume(d);
+                fetch(d);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+        for (int d = 0; d < D; d++)
+            if (s + d < total) {
+                consume(d);
+                if (s + d + D < total) fetch(d);
+            }
+        s += D;
+#pragma unroll
+        for (int d = 0; d + 1 < D; d++)
+            if (s + d < total) consume(d);
     }
     __syncthreads();
-    for (int q = tid; q < m.T * 4; q += 64 * kMoeDownWaves) {
-        const int t = q >> 2, n = 4 * (q & 3), n0 = 16 * blockIdx.x + n;
-        if (n0 >= a.N) continue;
-        float v[4] = {0.f, 0.f, 0.f, 0.f}, un[4];
+
+    // per token: its pairs in slot order, each the sum of its parts
+    auto token_sum = [&](int t, int n, float (&v)[4]) {
+        v[0] = v[1] = v[2] = v[3] = 0.0f;
         for (int j = 0; j < m.top_k; j++) {
             const int p = t * m.top_k + j;
             if (!served[p]) continue;
@@ -223,8 +365,44 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves) k_moe_down(MoeArgs m)
 #pragma unroll
             for (int c = 0; c < 4; c++) v[c] = __builtin_fmaf(wt, s[c], v[c]);
         }
-        Args y = a;  // the store sees T rows
-        y.M = m.T;
+    };
+    Args y = a;  // the store sees T rows
+    y.M = m.T;
+    float un[4];
+    if (m.split == 1) {
+        for (int q = tid; q < m.T * 4; q += 64 * kMoeDownWaves) {
+            const int t = q >> 2, n = 4 * (q & 3), n0 = 16 * panel + n;
+            float v[4];
+            token_sum(t, n, v);
+            finish_quad<DT, EP_LIN>(y, t, n0, v, un, quad_in<EP_LIN>(y, t, n0));
+        }
+        return;
+    }
+    float *mine = m.partial + ((long long)panel * m.split + slice) * m.T * 16;
+    for (int q = tid; q < m.T * 4; q += 64 * kMoeDownWaves) {
+        float v[4];
+        token_sum(q >> 2, 4 * (q & 3), v);
+        store_agent(mine + 4 * q, v);
+    }
+    // every wave's stores have reached the device's point of coherence before
+    // the workgroup's arrival counts there, so the last one to arrive finds
+    // all the others' sums
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0)
+        s_last = __hip_atomic_fetch_add(m.arrived + panel, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == m.split - 1;
+    __syncthreads();
+    if (!s_last) return;
+    const float *all = m.partial + (long long)panel * m.split * m.T * 16;
+    for (int q = tid; q < m.T * 4; q += 64 * kMoeDownWaves) {
+        const int t = q >> 2, n0 = 16 * panel + 4 * (q & 3);
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < m.split; s++) {
+            float x[4];
+            load_agent(all + (long long)s * m.T * 16 + 4 * q, x);
+#pragma unroll
+            for (int c = 0; c < 4; c++) v[c] += x[c];
+        }
         finish_quad<DT, EP_LIN>(y, t, n0, v, un, quad_in<EP_LIN>(y, t, n0));
     }
 }

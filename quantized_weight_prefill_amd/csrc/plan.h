@@ -93,9 +93,13 @@ struct MoeArgs {
     uint16_t *H;         // hidden [pairs][inter] (row i of the sorted order)
     int T, top_k, inter;
     int parts;           // k_moe_down: K parts per row tile
+    int split;           // k_moe_down: workgroups per panel of Y
+    int panels;          // panels of Y
+    float *partial;      // split > 1: [panels][split][T][16]
+    int *arrived;        // split > 1: [panels], zeroed by k_moe_up
 };
 template <int FMT>
-hipError_t launch_moe_up(int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s);
+hipError_t launch_moe_up(int dtype, int rb, int waves, dim3 grid, const MoeArgs &m, hipStream_t s);
 template <int FMT>
 hipError_t launch_moe_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s);
 // moe_route.hip

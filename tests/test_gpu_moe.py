@@ -262,11 +262,12 @@ def test_moe_malformed_grouping_stays_inside():
                        ([3, 2, 12, 1, 0], [-big, 11, 12, 13] * 3), ([big] * 5, list(range(12)))):
         buf = torch.full((T * 256 + 512,), 5.0, dtype=torch.float16, device="cuda")
         out = buf[:T * 256].view(T, 256)
-        ws = torch.full((T * k * 256 + 512,), 5.0, dtype=torch.float16, device="cuda")
+        need = qg.moe_workspace_bytes(T, k, 256, 256) // 2
+        ws = torch.full((need + 512,), 5.0, dtype=torch.float16, device="cuda")
         ex.run(x, w, torch.tensor(offs, dtype=torch.int32, device="cuda"), torch.tensor(rows, dtype=torch.int32, device="cuda"),
-               out=out, workspace=ws[:T * k * 256])
+               out=out, workspace=ws[:need])
         torch.cuda.synchronize()
-        assert bool((buf[T * 256:] == 5.0).all()) and bool((ws[T * k * 256:] == 5.0).all())
+        assert bool((buf[T * 256:] == 5.0).all()) and bool((ws[need:] == 5.0).all())
 
 
 def test_moe_in_place_stream_and_graph():

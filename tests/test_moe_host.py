@@ -56,7 +56,7 @@ def moe(fu=0, fd=1, X=P, Wu=P, Wd=P, w=P, offs=P, rows=P, res=None, Y=P, T=4, k=
     (dict(rows=None), -1), (dict(Y=None), -1),
     (dict(X=M4), -4), (dict(Wu=M4), -4), (dict(Wd=M4), -4), (dict(res=M4), -4), (dict(Y=M4), -4), (dict(w=M2), -4),
     (dict(offs=M2), -4), (dict(rows=M2), -4), (dict(ws=M4), -4),
-    (dict(ws=None), -6), (dict(wsb=4 * 2 * 256 * 2 - 1), -6),
+    (dict(ws=None), -6), (dict(wsb=qg.moe_workspace_bytes(4, 2, 512, 256) - 1), -6),
 ])
 def test_moe_argument_errors(kw, status):
     assert moe(**kw) == status
@@ -68,9 +68,12 @@ def test_empty_batches_launch_nothing():
 
 
 def test_workspace_bytes():
-    assert qg.moe_workspace_bytes(64, 8, 768) == 64 * 8 * 768 * 2
-    assert qg.moe_workspace_bytes(128, 8, 768) == 1024 * 768 * 2
-    for bad in ((129, 8, 768), (-1, 8, 768), (4, 0, 768), (4, 8, 0), (1 << 40, 1 << 40, 768)):
+    """h, and the partial sums and counters of the panels that several
+    workgroups share."""
+    assert qg.moe_workspace_bytes(64, 8, 2048, 768) >= 64 * 8 * 768 * 2
+    assert qg.moe_workspace_bytes(128, 8, 2048, 768) > qg.moe_workspace_bytes(64, 8, 2048, 768)
+    for bad in ((129, 8, 256, 768), (-1, 8, 256, 768), (0, 8, 256, 768), (4, 0, 256, 768), (4, 8, 256, 0),
+                (1 << 40, 1 << 40, 256, 768), (4, 8, 100, 768), (4, 8, 256, 100), (4, 8, 0, 768), (4, 8, 1 << 32, 768)):
         assert qg.moe_workspace_bytes(*bad) == 0
 
 

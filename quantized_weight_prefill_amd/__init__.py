@@ -339,10 +339,16 @@ def gguf_pack(buf: np.ndarray, index: int):
 # device calls
 # ---------------------------------------------------------------------------
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -479,77 +485,79 @@ def _act_code(act) -> int:
 
 
 # A call of these layers at decode sizes takes a few microseconds on the GPU, so
-# their checks are kept to plain attribute reads, and the pure size queries of
-# the library (functions of the sizes alone) are remembered.
+# their checks are plain attribute reads, and the pure size queries of the
+# library (functions of the sizes alone) are remembered.
 
-def _refuse(ref, named):
+def _refuse(named):
     """Say what is wrong with the first of `named` ((name, tensor, shape, dtype),
     shape and dtype None where any will do) that is not a contiguous tensor of
-    its shape and dtype on the device of `ref`, a GPU."""
+    its shape and dtype on the device of the first one, a GPU."""
     for name, t, shape, dtype in named:
         if t is not None and shape is not None and (t.shape != shape or t.dtype != dtype):
             raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    first, ref = named[0][:2]
     if not ref.is_cuda:
-        raise ValueError(f"{named[0][0]} must be a device tensor")
+        raise ValueError(f"{first} must be a device tensor")
     for name, t, _, _ in named:
         if t is None:
             continue
         if t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {ref.device}")
+            raise ValueError(f"{name} is on {t.device}, {first} on {ref.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
 
-def _checked(ref, *named):
-    """Raise unless every tensor of `named` is as :func:`_refuse` says."""
-    dev = ref.device
+def _checked(*named):
+    """The device index that every tensor of `named` is on; raises unless they
+    are as :func:`_refuse` says."""
+    index = named[0][1].get_device()
+    ok = index >= 0
     for _, t, shape, dtype in named:
-        if t is not None and ((shape is not None and (t.shape != shape or t.dtype != dtype)) or t.device != dev
-                              or not t.is_contiguous()):
-            _refuse(ref, named)
-    if not ref.is_cuda:
-        _refuse(ref, named)
-    return dev
+        if t is not None:
+            ok = ok and t.get_device() == index and t.is_contiguous()
+            if shape is not None:
+                ok = ok and t.shape == shape and t.dtype == dtype
+    if not ok:
+        _refuse(named)
+    return index
 
 
 @functools.lru_cache(maxsize=4096)
 def _packed_need(f: int, N: int, K: int, group: int, has_zp: bool) -> int:
-    return packed_bytes(f, N, K, group if group else 128, has_zp)
+    return packed_bytes(f, N, K, group if group else 128, bool(has_zp))
 
 
 def _check_packed(name, f, wp, N, K, group, has_zp, experts=1):
-    need = _packed_need(f, N, K, group, bool(has_zp)) * experts
+    need = _packed_need(f, N, K, group, has_zp) * experts
     if need == 0:
         raise QGemmError("packed_bytes", -2)
-    have = wp.numel() * wp.element_size()
-    if have < need:
-        raise ValueError(f"{name} holds {have} bytes, the packed weight needs {need}")
+    if wp.nbytes < need:
+        raise ValueError(f"{name} holds {wp.nbytes} bytes, the packed weight needs {need}")
 
 
-def _scratch(need: int, workspace, device, stream):
+def _scratch(need: int, workspace, ref, stream):
     """(pointer, bytes, tensor to keep) of the caller's workspace, or of one
     from torch's allocator, which is told of a stream that is not its own."""
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
+        if workspace.device != ref.device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the activations' device")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+        return workspace.data_ptr(), workspace.nbytes, workspace
     if not need:
         return None, 0, None
     torch = _torch()
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    ws = torch.empty(need, dtype=torch.uint8, device=ref.device)
     if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=device))
+        ws.record_stream(torch.cuda.ExternalStream(stream, device=ref.device))
     return ws.data_ptr(), need, ws
 
 
-def _call(fn, device, stream, *args):
-    """lib().fn(*args, stream) with `device` as the current one (the library
-    launches there), on `stream` or the device's current stream."""
+def _call(fn, index, stream, *args):
+    """lib().fn(*args, stream) with device `index` as the current one (the
+    library launches there), on `stream` or the device's current stream."""
     torch = _torch()
-    index = device.index
     if torch._C._cuda_getDevice() != index:
-        with torch.cuda.device(device):
-            return _call(fn, device, stream, *args)
+        with torch.cuda.device(index):
+            return _call(fn, index, stream, *args)
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(index)
     st = getattr(_lib or lib(), fn)(*args, stream)
@@ -579,14 +587,14 @@ def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_
     else:
         raise ValueError("out_layout must be X_ROW or X_FRAG")
     _check_packed("wp", f, wp, nt, K, group, has_zp)
-    dev = _checked(x, ("x", x, None, None), ("wp", wp, None, None), ("bias", bias, (nt,), dt),
-                   ("residual", residual, (M, N), dt), ("out", out, shape, dt))
+    index = _checked(("x", x, None, None), ("wp", wp, None, None), ("bias", bias, (nt,), dt),
+                     ("residual", residual, (M, N), dt), ("out", out, shape, dt))
     if out is None:
-        out = _torch().empty(shape, dtype=dt, device=dev)
+        out = x.new_empty(shape)
     elif out_layout == X_FRAG and residual is not None and out.data_ptr() == residual.data_ptr():
         raise ValueError("a fragment-major out cannot be the residual")
-    ws, wsb, _keep = _scratch(_linear_need(f, rung, layout, M, N, K, gated, code), workspace, dev, stream)
-    _call("qgemm_linear", dev, stream, f, rung, layout, x.data_ptr(), wp.data_ptr(),
+    ws, wsb, _keep = _scratch(_linear_need(f, rung, layout, M, N, K, gated, code), workspace, x, stream)
+    _call("qgemm_linear", index, stream, f, rung, layout, x.data_ptr(), wp.data_ptr(),
           None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(),
           out_layout, M, N, K, group, has_zp, ac, gated, code, ws, wsb)
     return out
@@ -844,17 +852,18 @@ def moe_route(logits, top_k: int, score: str = "softmax", renorm: bool = True, s
         raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
     lt = 2 if logits.dtype == torch.float32 else _dtype_code(logits)
     T, E = logits.shape
-    dev = _checked(logits, ("logits", logits, None, None))
+    index = _checked(("logits", logits, None, None))
     if not 1 <= top_k <= min(E, 64):
         raise QGemmError("qgemm_moe_route", -2)
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    P = T * top_k
+    # one allocation for the four results
     new = torch.empty if T else torch.zeros  # no tokens: every offset is 0
-    offsets = new(E + 1, dtype=torch.int32, device=dev)
-    rows = torch.empty(T * top_k, dtype=torch.int32, device=dev)
-    _call("qgemm_moe_route", dev, stream, logits.data_ptr(), lt, T, E, top_k, SCORES[score], 1 if renorm else 0, scale,
-          ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr())
-    return ids, weights, offsets, rows
+    buf = new(3 * P + E + 1, dtype=torch.int32, device=logits.device)
+    ids, weights, offsets, rows = buf.split_with_sizes((P, P, E + 1, P))
+    p = buf.data_ptr()
+    _call("qgemm_moe_route", index, stream, logits.data_ptr(), lt, T, E, top_k, SCORES[score], 1 if renorm else 0, scale,
+          p, p + 4 * P, p + 8 * P, p + 8 * P + 4 * (E + 1))
+    return ids.view(T, top_k), weights.view(torch.float32).view(T, top_k), offsets, rows
 
 
 def moe_group(ids, E: int, stream=None):
@@ -866,10 +875,10 @@ def moe_group(ids, E: int, stream=None):
     if ids.dim() != 2 or ids.dtype != torch.int32:
         raise ValueError("ids must be an int32 tensor [T, top_k]")
     T, k = ids.shape
-    dev = _checked(ids, ("ids", ids, None, None))
-    offsets = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
-    rows = torch.empty(T * k, dtype=torch.int32, device=dev)
-    _call("qgemm_moe_group", dev, stream, ids.data_ptr(), T, E, k, offsets.data_ptr(), rows.data_ptr())
+    index = _checked(("ids", ids, None, None))
+    offsets = ids.new_empty(max(E, 0) + 1)
+    rows = ids.new_empty(T * k)
+    _call("qgemm_moe_group", index, stream, ids.data_ptr(), T, E, k, offsets.data_ptr(), rows.data_ptr())
     return offsets, rows
 
 
@@ -901,21 +910,22 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
     ac = _act_code(act)
     if E < 1 or k < 1:
         raise ValueError("offsets must hold E+1 entries and weights at least one column")
+    has_zp = 1 if has_zp else 0
     _check_packed("w_up", fu, w_up, 2 * inter, H, group, has_zp, E)
     _check_packed("w_down", fd, w_down, H, inter, group, has_zp, E)
     i32 = torch.int32
-    dev = _checked(x, ("x", x, None, None), ("w_up", w_up, None, None), ("w_down", w_down, None, None),
+    index = _checked(("x", x, None, None), ("w_up", w_up, None, None), ("w_down", w_down, None, None),
                    ("weights", weights, (T, k), torch.float32), ("offsets", offsets, (E + 1,), i32),
                    ("rows", rows, (T * k,), i32), ("residual", residual, (T, H), x.dtype), ("out", out, (T, H), x.dtype))
     need = lib().qgemm_moe_workspace_bytes(T, k, H, inter)
     if need == 0 and T > 0:
         raise QGemmError("qgemm_moe", -2)
     if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=dev)
-    ws, wsb, _keep = _scratch(need, workspace, dev, stream)
-    _call("qgemm_moe", dev, stream, fu, fd, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), weights.data_ptr(),
+        out = torch.empty_like(x)
+    ws, wsb, _keep = _scratch(need, workspace, x, stream)
+    _call("qgemm_moe", index, stream, fu, fd, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), weights.data_ptr(),
           offsets.data_ptr(), rows.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), T, k, E,
-          H, inter, group, 1 if has_zp else 0, ac, code, ws, wsb)
+          H, inter, group, has_zp, ac, code, ws, wsb)
     return out
 
 

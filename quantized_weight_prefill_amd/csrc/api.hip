@@ -726,11 +726,10 @@ int moe_route_shape(long long T, long long E, long long k)
     return T > (INT32_MAX - 1024) / k ? QGEMM_ERR_SHAPE : QGEMM_OK;
 }
 
-hipError_t launch_up(int fmt, int dtype, int rb, int waves, dim3 grid, const MoeArgs &m, hipStream_t s)
+hipError_t launch_up(int fmt, int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
-    if (fmt == FMT_Q4K) return launch_moe_up<FMT_Q4K>(dtype, rb, waves, grid, m, s);
-    return fmt == FMT_Q6K ? launch_moe_up<FMT_Q6K>(dtype, rb, waves, grid, m, s)
-                          : launch_moe_up<FMT_W4>(dtype, rb, waves, grid, m, s);
+    if (fmt == FMT_Q4K) return launch_moe_up<FMT_Q4K>(dtype, rb, grid, m, s);
+    return fmt == FMT_Q6K ? launch_moe_up<FMT_Q6K>(dtype, rb, grid, m, s) : launch_moe_up<FMT_W4>(dtype, rb, grid, m, s);
 }
 
 hipError_t launch_down(int fmt, int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
@@ -739,13 +738,11 @@ hipError_t launch_down(int fmt, int dtype, dim3 grid, const MoeArgs &m, hipStrea
     return fmt == FMT_Q6K ? launch_moe_down<FMT_Q6K>(dtype, grid, m, s) : launch_moe_down<FMT_W4>(dtype, grid, m, s);
 }
 
-// Workgroups of the down product that share a 16-column panel of Y: two
-// workgroups of eight waves for each CU.
-int moe_split(long long H)
-{
-    const long long panels = (H + 15) / 16;
-    return (int)std::min(8LL, std::max(1LL, 2 * kCUs / panels));
-}
+// Workgroups of the down product that share a 16-column panel of Y: one
+// workgroup of sixteen waves for each CU (64 tokens, Q6_K 768 -> 2048: 44.0 us
+// with two, 44.7 with four of eight waves; seven tokens, W4A16 1408 -> 2048:
+// 14.0 with two, 19.6 with one; one token 7.8 against 9.4).
+int moe_split(long long H) { return (int)std::min(8LL, std::max(1LL, (long long)kCUs / ((H + 15) / 16))); }
 
 int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const float *wts, const int32_t *offs,
         const int32_t *rows, const void *res, void *Y, long long T, long long k, long long E, long long H, long long I,
@@ -769,7 +766,8 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
         return QGEMM_ERR_ALIGN;
     if (!ws || ws_bytes < qgemm_moe_workspace_bytes(T, k, H, I)) return QGEMM_ERR_SIZE;
     if (!aligned16(ws)) return QGEMM_ERR_ALIGN;
-    if (!launch_fits(I / 16, 512) || !launch_fits((H + 15) / 16 * 8, 512)) return QGEMM_ERR_SHAPE;
+    if (!launch_fits(I / 16, 64 * kMoeUpWaves) || !launch_fits((H + 15) / 16 * 8, 64 * kMoeDownWaves))
+        return QGEMM_ERR_SHAPE;
     const long long P = T * k;
     MoeArgs m{};
     m.rows = rows;
@@ -786,8 +784,10 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.arrived = (int *)(m.partial + (long long)m.panels * m.split * T * 16);
 
     // gate and up: rows per tile by the experts' mean count; K split over
-    // waves while the grid holds fewer than 4096 of them and each keeps two
-    // chunks
+    // waves while the grid holds fewer than 4096 of them and each keeps four
+    // chunks (one token, Q4_K 2048 -> 768, weights rotating: 7.7 us split four
+    // ways, 8.0 eight, 18 unsplit; seven tokens, W4A16 2048 -> 1408: 17.7 two
+    // ways, 18.6 unsplit)
     const long long avg = (P + E - 1) / E;
     const int rb = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
     m.g = make_args(fu, X, Wu, nullptr, P, 2 * I, H, group, has_zp);
@@ -798,20 +798,21 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     const int nch = (int)(H / kChunk);
     const long long slots = std::min(P, (P + 16 * rb - 1) / (16 * rb) + E);
     m.g.kw = 1;
-    while (m.g.kw < 8 && slots * (I / 16) * m.g.kw < 4096 && nch >= 4 * m.g.kw) m.g.kw *= 2;
-    const int waves = std::max(4, m.g.kw), per = waves / m.g.kw;
+    while (m.g.kw < kMoeUpWaves && slots * (I / 16) * m.g.kw < 4096 && nch >= 8 * m.g.kw) m.g.kw *= 2;
+    const int per = kMoeUpWaves / m.g.kw;  // gate panels per workgroup
     const dim3 gu((unsigned)((I / 16 + per - 1) / per), (unsigned)slots, 1);
-    hipError_t e = launch_up(fu, dtype, rb, waves, gu, m, (hipStream_t)stream);
+    hipError_t e = launch_up(fu, dtype, rb, gu, m, (hipStream_t)stream);
     if (e != hipSuccess) return launch_status(e, "moe up");
 
-    // down: K in parts while the row tiles alone leave waves idle
+    // down: K in parts of at least three chunks while the row tiles alone
+    // leave waves idle
     m.g = make_args(fd, nullptr, Wd, Y, P, H, I, group, has_zp);
     m.g.offs = offs;
     m.g.E = (int)E;
     m.g.wstride = sd;
     m.g.res = (const uint16_t *)res;
     m.parts = 1;
-    while (m.parts < 8 && tiles * m.parts < 8 * m.split && I / kChunk >= 2 * m.parts && 2 * m.parts * P <= 1024)
+    while (tiles * m.parts < kMoeDownWaves * m.split && I / kChunk >= 6 * m.parts && 2 * m.parts * P <= 1024)
         m.parts *= 2;
     e = launch_down(fd, dtype, dim3((unsigned)(m.panels * m.split), 1, 1), m, (hipStream_t)stream);
     return launch_status(e, "moe down");

@@ -90,7 +90,7 @@ struct Depth {
 // One workgroup: rows m0 .. m0+16*RB-1 (those below a.M) of panels p0 ..
 // p0+PN-1; a.kw waves split K and reduce through LDS.  EPI: the epilogue
 // (EP_GATED takes panels in gate/up pairs, so PN is even).
-template <int FMT, int DT, int RB, int PN, int XL, int EPI = EP_NONE>
+template <int FMT, int DT, int RB, int PN, int XL, int EPI = EP_NONE, class DP = Depth<RB, PN>>
 __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
 {
     static_assert(EPI != EP_GATED || PN % 2 == 0, "gate and up panels come in pairs");
@@ -121,7 +121,7 @@ __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
 
     if constexpr (EPI != EP_NONE) {
         // the linear layer: the same MFMAs in the same order, more chunks in flight
-        stream_chunks<FMT, DT, RB, PN, XL, Depth<RB, PN>::W, Depth<RB, PN>::X>(src, xrow, cb, ce, acc);
+        stream_chunks<FMT, DT, RB, PN, XL, DP::W, DP::X>(src, xrow, cb, ce, acc);
     } else {
     RunRaw<FMT> raw[PN];
     u32x4 xf[RB][4];

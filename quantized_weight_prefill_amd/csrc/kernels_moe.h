@@ -31,8 +31,15 @@
 
 namespace qg {
 
-constexpr int kMoeUpWaves = 4;    // k_moe_up: waves per workgroup while K is not split further
-constexpr int kMoeDownWaves = 8;
+// Chunks of weights and activations k_moe_up's waves keep in flight.  Two of
+// each lead or tie at every size measured (64 tokens of 8 of 128 experts,
+// Q4_K 2048 -> 768 pairs, weights rotating: 55.4 us; three of weights and one
+// of activations 57.5, three of both 58-62): more take the registers of the
+// waves that would hide the latency.
+template <int RB>
+struct UpDepth {
+    static constexpr int W = RB > 2 ? 1 : 2, X = RB > 2 ? 1 : 2;
+};
 
 inline size_t moe_down_lds(long long pairs, long long E, int parts)
 {
@@ -159,7 +166,7 @@ __device__ __forceinline__ int pair_at(const MoeArgs &m, int i)
 
 // Grid: x = groups of nw/kw gate panels (inter/16 in all), y = row-tile slots
 // of 16*RB rows; nw waves, of which kw split the K of one panel.
-template <int FMT, int DT, int RB>
+template <int FMT, int DT, int RB, class DP = UpDepth<RB>>
 __global__ void __launch_bounds__(512) k_moe_up(MoeArgs m)
 {
     extern __shared__ f32x4 red[];  // [nw][2*RB][64]
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(512) k_moe_up(MoeArgs m)
         for (int rb = 0; rb < RB; rb++) acc[pn][rb] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int nch = a.K / kChunk;
     const int cb = (int)((long long)nch * share / a.kw), ce = (int)((long long)nch * (share + 1) / a.kw);
-    stream_chunks<FMT, DT, RB, 2, X_ROW, Depth<RB, 2>::W, Depth<RB, 2>::X>(src, xrow, cb, ce, acc);
+    stream_chunks<FMT, DT, RB, 2, X_ROW, DP::W, DP::X>(src, xrow, cb, ce, acc);
     if (a.kw > 1) {
 #pragma unroll
         for (int pn = 0; pn < 2; pn++)
@@ -231,8 +238,8 @@ __global__ void __launch_bounds__(512) k_moe_up(MoeArgs m)
 // A wave's work is one sequence of 128-wide chunks over its units (row tile,
 // part of K), with D chunks of weights in flight across the units' borders:
 // `front` walks the sequence where the loads are, `back` where the MFMAs are.
-template <int FMT, int DT, int D>
-__global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
+template <int FMT, int DT, int D, int NW = kMoeDownWaves>
+__global__ void __launch_bounds__(64 * NW, 4) k_moe_down(MoeArgs m)
 {
     extern __shared__ float sums[];  // [parts][pairs][16]
     __shared__ int s_tiles, s_last;
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
     int *tile_lo = tile_e + slots, *tile_hi = tile_lo + slots;
     int *pair_of = tile_hi + slots;
     uint8_t *served = (uint8_t *)(pair_of + P);
-    for (int i = tid; i < P; i += 64 * kMoeDownWaves) {
+    for (int i = tid; i < P; i += 64 * NW) {
         pair_of[i] = pair_at(m, i);
         served[i] = 0;
     }
@@ -295,9 +302,9 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
         open(back);
         int total = 0;  // chunks of this wave's sequence
         if (m.parts == 1) {
-            total = (units - w + kMoeDownWaves - 1) / kMoeDownWaves * nch;
+            total = (units - w + NW - 1) / NW * nch;
         } else {
-            for (int u = w; u < units; u += kMoeDownWaves)
+            for (int u = w; u < units; u += NW)
                 total += nch * (u % m.parts + 1) / m.parts - nch * (u % m.parts) / m.parts;
         }
         auto fetch = [&](int d) {
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
 #pragma unroll
             for (int i = 0; i < 4; i++) xf[d][i] = *(const u32x4 *)(xrow + (long long)kChunk * front.c + 8 * i);
             if (++front.c == front.ce) {
-                front.u += kMoeDownWaves;
+                front.u += NW;
                 if (front.u < units) aim(front);
             }
         };
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
                     if (part == 0 && g == 0) served[pair] = 1;
                 }
                 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-                back.u += kMoeDownWaves;
+                back.u += NW;
                 if (back.u < units) open(back);
             }
         };
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
     y.M = m.T;
     float un[4];
     if (m.split == 1) {
-        for (int q = tid; q < m.T * 4; q += 64 * kMoeDownWaves) {
+        for (int q = tid; q < m.T * 4; q += 64 * NW) {
             const int t = q >> 2, n = 4 * (q & 3), n0 = 16 * panel + n;
             float v[4];
             token_sum(t, n, v);
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
         return;
     }
     float *mine = m.partial + ((long long)panel * m.split + slice) * m.T * 16;
-    for (int q = tid; q < m.T * 4; q += 64 * kMoeDownWaves) {
+    for (int q = tid; q < m.T * 4; q += 64 * NW) {
         float v[4];
         token_sum(q >> 2, 4 * (q & 3), v);
         store_agent(mine + 4 * q, v);
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
     __syncthreads();
     if (!s_last) return;
     const float *all = m.partial + (long long)panel * m.split * m.T * 16;
-    for (int q = tid; q < m.T * 4; q += 64 * kMoeDownWaves) {
+    for (int q = tid; q < m.T * 4; q += 64 * NW) {
         const int t = q >> 2, n0 = 16 * panel + 4 * (q & 3);
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int s = 0; s < m.split; s++) {

@@ -507,19 +507,8 @@ def _refuse(named):
             raise ValueError(f"{name} must be contiguous")
 
 
-def _checked(*named):
-    """The device index that every tensor of `named` is on; raises unless they
-    are as :func:`_refuse` says."""
-    index = named[0][1].get_device()
-    ok = index >= 0
-    for _, t, shape, dtype in named:
-        if t is not None:
-            ok = ok and t.get_device() == index and t.is_contiguous()
-            if shape is not None:
-                ok = ok and t.shape == shape and t.dtype == dtype
-    if not ok:
-        _refuse(named)
-    return index
+def _fits(t, index, shape, dtype) -> bool:
+    return t.get_device() == index and t.is_contiguous() and t.shape == shape and t.dtype == dtype
 
 
 @functools.lru_cache(maxsize=4096)
@@ -527,8 +516,7 @@ def _packed_need(f: int, N: int, K: int, group: int, has_zp: bool) -> int:
     return packed_bytes(f, N, K, group if group else 128, bool(has_zp))
 
 
-def _check_packed(name, f, wp, N, K, group, has_zp, experts=1):
-    need = _packed_need(f, N, K, group, has_zp) * experts
+def _check_bytes(name, wp, need):
     if need == 0:
         raise QGemmError("packed_bytes", -2)
     if wp.nbytes < need:
@@ -566,18 +554,12 @@ def _call(fn, index, stream, *args):
 
 
 @functools.lru_cache(maxsize=4096)
-def _linear_need(f, rung, layout, M, N, K, gated, code) -> int:
-    return int(lib().qgemm_linear_workspace_bytes(f, rung, layout, M, N, K, gated, code))
-
-
-def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout, stream,
-            workspace):
+def _linear_sizes(fmt, layout, M, N, K, act, gated, group, has_zp, rung, out_layout, code):
+    """What a linear call's arguments say by themselves: (format, activation
+    code, packed bytes, workspace bytes, Y's shape, gated, has_zp)."""
     f = FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
-    dt = x.dtype
-    code = _dtype_code(x)
     ac = _act_code(act)
-    gated, has_zp = (1 if gated else 0), (1 if has_zp else 0)
-    nt = 2 * N if gated else N
+    gated, has_zp = int(bool(gated)), int(bool(has_zp))
     if out_layout == X_ROW:
         shape = (M, N)
     elif out_layout == X_FRAG:
@@ -586,14 +568,30 @@ def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_
             raise QGemmError("qgemm_linear", -2)
     else:
         raise ValueError("out_layout must be X_ROW or X_FRAG")
-    _check_packed("wp", f, wp, nt, K, group, has_zp)
-    index = _checked(("x", x, None, None), ("wp", wp, None, None), ("bias", bias, (nt,), dt),
-                     ("residual", residual, (M, N), dt), ("out", out, shape, dt))
+    packed = _packed_need(f, 2 * N if gated else N, K, group, has_zp)
+    need = int(lib().qgemm_linear_workspace_bytes(f, rung, layout, M, N, K, gated, code))
+    return f, ac, packed, need, shape, gated, has_zp
+
+
+def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout, stream,
+            workspace):
+    dt = x.dtype
+    code = _dtype_code(x)
+    f, ac, packed, need, shape, gated, has_zp = _linear_sizes(fmt, layout, M, N, K, act, gated, group, has_zp, rung,
+                                                              out_layout, code)
+    _check_bytes("wp", wp, packed)
+    index = x.get_device()
+    if (index < 0 or not x.is_contiguous() or wp.get_device() != index or not wp.is_contiguous()
+            or (bias is not None and not _fits(bias, index, (2 * N if gated else N,), dt))
+            or (residual is not None and not _fits(residual, index, (M, N), dt))
+            or (out is not None and not _fits(out, index, shape, dt))):
+        _refuse((("x", x, None, None), ("wp", wp, None, None), ("bias", bias, (2 * N if gated else N,), dt),
+                 ("residual", residual, (M, N), dt), ("out", out, shape, dt)))
     if out is None:
         out = x.new_empty(shape)
     elif out_layout == X_FRAG and residual is not None and out.data_ptr() == residual.data_ptr():
         raise ValueError("a fragment-major out cannot be the residual")
-    ws, wsb, _keep = _scratch(_linear_need(f, rung, layout, M, N, K, gated, code), workspace, x, stream)
+    ws, wsb, _keep = _scratch(need, workspace, x, stream)
     _call("qgemm_linear", index, stream, f, rung, layout, x.data_ptr(), wp.data_ptr(),
           None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(),
           out_layout, M, N, K, group, has_zp, ac, gated, code, ws, wsb)
@@ -852,7 +850,9 @@ def moe_route(logits, top_k: int, score: str = "softmax", renorm: bool = True, s
         raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
     lt = 2 if logits.dtype == torch.float32 else _dtype_code(logits)
     T, E = logits.shape
-    index = _checked(("logits", logits, None, None))
+    index = logits.get_device()
+    if index < 0 or not logits.is_contiguous():
+        _refuse((("logits", logits, None, None),))
     if not 1 <= top_k <= min(E, 64):
         raise QGemmError("qgemm_moe_route", -2)
     P = T * top_k
@@ -875,7 +875,9 @@ def moe_group(ids, E: int, stream=None):
     if ids.dim() != 2 or ids.dtype != torch.int32:
         raise ValueError("ids must be an int32 tensor [T, top_k]")
     T, k = ids.shape
-    index = _checked(("ids", ids, None, None))
+    index = ids.get_device()
+    if index < 0 or not ids.is_contiguous():
+        _refuse((("ids", ids, None, None),))
     offsets = ids.new_empty(max(E, 0) + 1)
     rows = ids.new_empty(T * k)
     _call("qgemm_moe_group", index, stream, ids.data_ptr(), T, E, k, offsets.data_ptr(), rows.data_ptr())
@@ -885,6 +887,19 @@ def moe_group(ids, E: int, stream=None):
 def moe_workspace_bytes(T: int, top_k: int, hidden: int, inter: int) -> int:
     """Bytes of the workspace a :func:`moe` call of these sizes needs."""
     return int(lib().qgemm_moe_workspace_bytes(T, top_k, hidden, inter))
+
+
+@functools.lru_cache(maxsize=4096)
+def _moe_sizes(fmt_up, fmt_down, T, k, E, H, inter, group, has_zp, act):
+    """What a moe call's sizes say by themselves: (formats, activation code,
+    packed bytes of each weight, workspace bytes, has_zp)."""
+    fu = FORMATS[fmt_up] if isinstance(fmt_up, str) else int(fmt_up)
+    fd = FORMATS[fmt_down] if isinstance(fmt_down, str) else int(fmt_down)
+    if E < 1 or k < 1:
+        raise ValueError("offsets must hold E+1 entries and weights at least one column")
+    has_zp = int(bool(has_zp))
+    return (fu, fd, _act_code(act), E * _packed_need(fu, 2 * inter, H, group, has_zp),
+            E * _packed_need(fd, H, inter, group, has_zp), moe_workspace_bytes(T, k, H, inter), has_zp)
 
 
 def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, group: int = 0, has_zp: bool = False,
@@ -898,26 +913,27 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
     w_down: E packed weights of H columns over K = inter; weights [T, top_k]
     float32, offsets [E+1] and rows [T*top_k] from :func:`moe_route` or
     :func:`moe_group`.  ``out`` may be the residual."""
-    torch = _torch()
     if x.dim() != 2 or weights.dim() != 2:
         raise ValueError("x must be [T, H] and weights [T, top_k]")
-    fu = FORMATS[fmt_up] if isinstance(fmt_up, str) else int(fmt_up)
-    fd = FORMATS[fmt_down] if isinstance(fmt_down, str) else int(fmt_down)
+    torch = _torch()
     T, H = x.shape
     k = weights.shape[1]
     E = offsets.numel() - 1
+    dt = x.dtype
     code = _dtype_code(x)
-    ac = _act_code(act)
-    if E < 1 or k < 1:
-        raise ValueError("offsets must hold E+1 entries and weights at least one column")
-    has_zp = 1 if has_zp else 0
-    _check_packed("w_up", fu, w_up, 2 * inter, H, group, has_zp, E)
-    _check_packed("w_down", fd, w_down, H, inter, group, has_zp, E)
-    i32 = torch.int32
-    index = _checked(("x", x, None, None), ("w_up", w_up, None, None), ("w_down", w_down, None, None),
-                   ("weights", weights, (T, k), torch.float32), ("offsets", offsets, (E + 1,), i32),
-                   ("rows", rows, (T * k,), i32), ("residual", residual, (T, H), x.dtype), ("out", out, (T, H), x.dtype))
-    need = lib().qgemm_moe_workspace_bytes(T, k, H, inter)
+    fu, fd, ac, up_bytes, down_bytes, need, has_zp = _moe_sizes(fmt_up, fmt_down, T, k, E, H, inter, group, has_zp, act)
+    index = x.get_device()
+    if (index < 0 or not x.is_contiguous() or not _fits(weights, index, (T, k), torch.float32)
+            or not _fits(offsets, index, (E + 1,), torch.int32) or not _fits(rows, index, (T * k,), torch.int32)
+            or w_up.get_device() != index or not w_up.is_contiguous() or w_down.get_device() != index
+            or not w_down.is_contiguous() or (residual is not None and not _fits(residual, index, (T, H), dt))
+            or (out is not None and not _fits(out, index, (T, H), dt))):
+        i32 = torch.int32
+        _refuse((("x", x, None, None), ("weights", weights, (T, k), torch.float32), ("offsets", offsets, (E + 1,), i32),
+                 ("rows", rows, (T * k,), i32), ("w_up", w_up, None, None), ("w_down", w_down, None, None),
+                 ("residual", residual, (T, H), dt), ("out", out, (T, H), dt)))
+    _check_bytes("w_up", w_up, up_bytes)
+    _check_bytes("w_down", w_down, down_bytes)
     if need == 0 and T > 0:
         raise QGemmError("qgemm_moe", -2)
     if out is None:

@@ -4,77 +4,13 @@
 // launches a Plan's rung.  Included by the instantiation units only.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "epilogue.h"
 #include "plan.h"
 
 namespace qg {
-
-// acc[PN][RB] += X rows . panels over chunks [cb, ce) of one wave, D chunks of
-// weights and DX of activations in flight ahead of the one being multiplied
-// (DX divides D; the activations come from L2, whose latency is a fraction of
-// the memory's).  cb and ce are the same in every lane.  The steady state has
-// no branch, so that a wait counts only the loads it needs; each output's
-// MFMAs run in chunk order whatever D.
-template <int FMT, int DT, int RB, int PN, int XL, int D, int DX>
-__device__ __forceinline__ void stream_chunks(const RunSrc<FMT> (&src)[PN], const uint16_t *const (&xrow)[RB], int cb,
-                                              int ce, f32x4 (&acc)[PN][RB])
-{
-    using XA = XLay<XL>;
-    static_assert(D % DX == 0, "the rings turn together");
-    RunRaw<FMT> raw[D][PN];
-    u32x4 xf[DX][RB][4];
-    auto fetch_w = [&](int c, int d) {
-#pragma unroll
-        for (int pn = 0; pn < PN; pn++) src[pn].load(c, raw[d][pn]);
-    };
-    auto fetch_x = [&](int c, int d) {
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) xf[d][rb][i] = *(const u32x4 *)(xrow[rb] + XA::chunk(c) + XA::off(8 * i));
-    };
-    // chunk c from slot d; its slots refilled with chunks c + D and c + DX
-    auto step = [&](int c, int d, bool more_w, bool more_x) {
-        const int dx = d % DX;
-#pragma unroll
-        for (int pn = 0; pn < PN; pn++) {
-            u32x4 wf[4];
-            unpack_run<FMT, DT>(raw[d][pn], src[pn], c, wf);
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[i], xf[dx][rb][i], acc[pn][rb]);
-        }
-        if (more_w) fetch_w(c + D, d);
-        if (more_x) fetch_x(c + DX, dx);
-        __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where they are next needed
-    };
-#pragma unroll
-    for (int d = 0; d < D; d++)
-        if (cb + d < ce) {
-            fetch_w(cb + d, d);
-            if (d < DX) fetch_x(cb + d, d);
-        }
-    int c = cb;
-    for (; c + 2 * D <= ce; c += D)
-#pragma unroll
-        for (int d = 0; d < D; d++) step(c + d, d, true, true);
-#pragma unroll
-    for (int d = 0; d < D; d++)
-        if (c + d < ce) step(c + d, d, c + d + D < ce, c + d + DX < ce);
-    c += D;
-#pragma unroll
-    for (int d = 0; d + 1 < D; d++)
-        if (c + d < ce) step(c + d, d, false, c + d + DX < ce);
-}
-
-// Depths of the rings above by what one chunk takes in registers.
-template <int RB, int PN>
-struct Depth {
-    static constexpr int W = PN == 1 ? 4 : PN == 2 ? 3 : 2;
-    static constexpr int X = RB > 2 ? 1 : PN == 1 ? 2 : 1;
-};
 
 // ---------------------------------------------------------------------------
 // Direct kernel: decode-adjacent M and skinny N.
@@ -87,78 +23,12 @@ struct Depth {
 // chunk c+1 are in flight while chunk c is unpacked and multiplied.  Grid:
 // x = panel groups of PN panels, y = row groups of 16*RB rows.
 // ---------------------------------------------------------------------------
-// One workgroup: rows m0 .. m0+16*RB-1 (those below a.M) of panels p0 ..
-// p0+PN-1; a.kw waves split K and reduce through LDS.  EPI: the epilogue
-// (EP_GATED takes panels in gate/up pairs, so PN is even).
-template <int FMT, int DT, int RB, int PN, int XL, int EPI = EP_NONE, class DP = Depth<RB, PN>>
-__device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
+// The end of a direct kernel: the kw waves' partial sums added through LDS
+// (red: [kw][PN*RB][64]) in wave order, then the stores.
+template <int DT, int RB, int PN, int EPI>
+__device__ __forceinline__ void direct_finish(const Args &a, const f32x4 (&acc)[PN][RB], f32x4 *red, int w, int lane,
+                                              int p0, int m0)
 {
-    static_assert(EPI != EP_GATED || PN % 2 == 0, "gate and up panels come in pairs");
-    using XA = XLay<XL>;
-    extern __shared__ f32x4 red[];  // [kw][PN*RB][64]
-    const int lane = threadIdx.x & 63;
-    const int w = EPI == EP_NONE ? threadIdx.x >> 6 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, g = lane >> 4;
-    const int nch = a.K / kChunk;
-    const int cb = (int)((long long)nch * w / a.kw), ce = (int)((long long)nch * (w + 1) / a.kw);
-
-    f32x4 acc[PN][RB];
-#pragma unroll
-    for (int pn = 0; pn < PN; pn++)
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++) acc[pn][rb] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const uint16_t *xrow[RB];
-#pragma unroll
-    for (int rb = 0; rb < RB; rb++) {
-        int r = m0 + 16 * rb + col;
-        r = r < a.M ? r : a.M - 1;  // clamped rows are computed and discarded
-        xrow[rb] = XA::row(a, r) + XA::off(32 * g);
-    }
-    RunSrc<FMT> src[PN];
-#pragma unroll
-    for (int pn = 0; pn < PN; pn++) src[pn].init(a, packed_panel<EPI>(a, p0 + pn), g, col);
-
-    if constexpr (EPI != EP_NONE) {
-        // the linear layer: the same MFMAs in the same order, more chunks in flight
-        stream_chunks<FMT, DT, RB, PN, XL, DP::W, DP::X>(src, xrow, cb, ce, acc);
-    } else {
-    RunRaw<FMT> raw[PN];
-    u32x4 xf[RB][4];
-    if (cb < ce) {
-#pragma unroll
-        for (int pn = 0; pn < PN; pn++) src[pn].load(cb, raw[pn]);
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) xf[rb][i] = *(const u32x4 *)(xrow[rb] + XA::chunk(cb) + XA::off(8 * i));
-    }
-    for (int c = cb; c < ce; c++) {
-        u32x4 wf[PN][4];
-#pragma unroll
-        for (int pn = 0; pn < PN; pn++) unpack_run<FMT, DT>(raw[pn], src[pn], c, wf[pn]);
-        u32x4 xc[RB][4];
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) xc[rb][i] = xf[rb][i];
-        if (c + 1 < ce) {  // prefetch chunk c+1 while this one is multiplied
-#pragma unroll
-            for (int pn = 0; pn < PN; pn++) src[pn].load(c + 1, raw[pn]);
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) xf[rb][i] = *(const u32x4 *)(xrow[rb] + XA::chunk(c + 1) + XA::off(8 * i));
-        }
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-            for (int pn = 0; pn < PN; pn++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[pn][i], xc[rb][i], acc[pn][rb]);
-    }
-    }
-
     constexpr int PS = EPI == EP_GATED ? 2 : 1;  // tile panels behind one output panel
     // the fragment-major Y's zero rows past the last row group
     const bool tail = EPI != EP_NONE && a.y_frag && m0 + 16 * RB >= a.M && m0 + 16 * RB < y_rows(a);
@@ -199,10 +69,203 @@ __device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
     }
 }
 
+// One workgroup: rows m0 .. m0+16*RB-1 (those below a.M) of panels p0 ..
+// p0+PN-1; a.kw waves split K and reduce through LDS.  EPI: the epilogue
+// (EP_GATED takes panels in gate/up pairs, so PN is even).
+template <int FMT, int DT, int RB, int PN, int XL, int EPI = EP_NONE>
+__device__ __forceinline__ void direct_body(const Args &a, int p0, int m0)
+{
+    static_assert(EPI != EP_GATED || PN % 2 == 0, "gate and up panels come in pairs");
+    using XA = XLay<XL>;
+    extern __shared__ f32x4 red[];  // [kw][PN*RB][64]
+    const int lane = threadIdx.x & 63;
+    const int w = threadIdx.x >> 6;
+    const int col = lane & 15, g = lane >> 4;
+    const int nch = a.K / kChunk;
+    const int cb = (int)((long long)nch * w / a.kw), ce = (int)((long long)nch * (w + 1) / a.kw);
+
+    f32x4 acc[PN][RB];
+#pragma unroll
+    for (int pn = 0; pn < PN; pn++)
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++) acc[pn][rb] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const uint16_t *xrow[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; rb++) {
+        int r = m0 + 16 * rb + col;
+        r = r < a.M ? r : a.M - 1;  // clamped rows are computed and discarded
+        xrow[rb] = XA::row(a, r) + XA::off(32 * g);
+    }
+    RunSrc<FMT> src[PN];
+#pragma unroll
+    for (int pn = 0; pn < PN; pn++) src[pn].init(a, packed_panel<EPI>(a, p0 + pn), g, col);
+
+    RunRaw<FMT> raw[PN];
+    u32x4 xf[RB][4];
+    if (cb < ce) {
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) src[pn].load(cb, raw[pn]);
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) xf[rb][i] = *(const u32x4 *)(xrow[rb] + XA::chunk(cb) + XA::off(8 * i));
+    }
+    for (int c = cb; c < ce; c++) {
+        u32x4 wf[PN][4];
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) unpack_run<FMT, DT>(raw[pn], src[pn], c, wf[pn]);
+        u32x4 xc[RB][4];
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) xc[rb][i] = xf[rb][i];
+        if (c + 1 < ce) {  // prefetch chunk c+1 while this one is multiplied
+#pragma unroll
+            for (int pn = 0; pn < PN; pn++) src[pn].load(c + 1, raw[pn]);
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) xf[rb][i] = *(const u32x4 *)(xrow[rb] + XA::chunk(c + 1) + XA::off(8 * i));
+        }
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+            for (int pn = 0; pn < PN; pn++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[pn][i], xc[rb][i], acc[pn][rb]);
+    }
+
+    direct_finish<DT, RB, PN, EPI>(a, acc, red, w, lane, p0, m0);
+}
+
+// Raw loads of the chunk pair c0, c0+1 (c0 even) of one lane's runs: the
+// k-quants' block header serves both, so it is loaded once.  second: chunk
+// c0+1 exists (always for the k-quants).
+template <int FMT>
+__device__ __forceinline__ void load_pair(const RunSrc<FMT> &s, int c0, bool second, RunRaw<FMT> (&r)[2])
+{
+    if constexpr (FMT == FMT_Q4K) {
+        s.load(c0, r[0]);
+        r[1].hd = r[0].hd;
+        r[1].codes = *(const u32x4 *)(s.rec + (long long)(c0 >> 1) * kQ4kRec + 1280 + (16 * s.g + s.col) * 16);
+    } else if constexpr (FMT == FMT_Q6K) {
+        const uint8_t *b = s.rec + (long long)(c0 >> 1) * kQ6kRec;
+        s.load(c0, r[0]);
+        r[1].hd = r[0].hd;
+        r[1].d = r[0].d;
+        r[1].codes = *(const u32x4 *)(b + 1312 + (16 * s.g + s.col) * 16);
+        r[1].hi = *(const u32x2 *)(b + 2848 + (16 * s.g + s.col) * 8);
+    } else {
+        s.load(c0, r[0]);
+        s.load(second ? c0 + 1 : c0, r[1]);
+    }
+}
+
+// The direct kernel of the linear layer on row-major X: the MFMAs of
+// direct_body in its order, two chunks per step, and the activations turned
+// into fragments through LDS.  A lane's fragments are 64 consecutive bytes of
+// its row, so loading them straight makes each wave load touch 64 separate
+// 64-byte pieces; here a load reads four rows' 256 contiguous bytes, goes to
+// the wave's own LDS tile (rows 272 bytes apart: 16 lanes' 16-byte reads fall
+// into different banks) and comes back as fragments.  No barrier: a wave's LDS
+// operations keep their order.  Measured (weights rotating, one panel per
+// wave): M = 16, Q6_K 12288 -> 4096 14.1-14.7 against 17.4 us, Q4_K 4096 ->
+// 12288 11.9 against 15.5, Q4_K and W4A16 4096 -> 4096 6.4 against 7.6-7.8;
+// M = 1, W4A16 4096 -> 4096 6.0 against 7.6, Q4_K 5.8 against 6.0.
+// With four panels per wave each straight activation load already serves four
+// weight runs, and staging loses (M = 33, W4A16 4096 -> 4097 12.0 against 10.9
+// us), so those keep direct_body.
+constexpr int kXStride = 272;              // bytes from row to row of the tile
+constexpr int kXTile = 2 * 16 * kXStride;  // two chunks of 16 rows
+
+constexpr bool row_staged(int rb, int pn, int xl, int epi)
+{
+    return epi != EP_NONE && xl == X_ROW && rb == 1 && pn <= 2;
+}
+
+template <int FMT, int DT, int PN, int EPI>
+__device__ __forceinline__ void direct_row_body(const Args &a, int p0, int m0)
+{
+    static_assert(EPI != EP_GATED || PN % 2 == 0, "gate and up panels come in pairs");
+    extern __shared__ f32x4 red[];  // [kw] tiles of kXTile bytes, then [kw][PN][64]
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int nch = a.K / kChunk;
+    const int cb = (int)((long long)nch * w / a.kw), ce = (int)((long long)nch * (w + 1) / a.kw);
+    uint8_t *tile = (uint8_t *)red + w * kXTile;
+    uint8_t *put = tile + g * kXStride + 16 * col;             // row g + 4j, 16 bytes col
+    const uint8_t *get = tile + col * kXStride + 64 * g;       // row col, run g
+
+    f32x4 acc[PN][1];
+#pragma unroll
+    for (int pn = 0; pn < PN; pn++) acc[pn][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint16_t *xrow[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) xrow[j] = a.X + (long long)min(m0 + g + 4 * j, a.M - 1) * a.K + 8 * col;
+    RunSrc<FMT> src[PN];
+#pragma unroll
+    for (int pn = 0; pn < PN; pn++) src[pn].init(a, packed_panel<EPI>(a, p0 + pn), g, col);
+
+    RunRaw<FMT> raw[PN][2];
+    u32x4 xp[2][4];
+    auto fetch = [&](int c0) {
+        const bool second = FMT != FMT_W4 || c0 + 1 < nch;
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) load_pair<FMT>(src[pn], c0, second, raw[pn]);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) xp[h][j] = *(const u32x4 *)(xrow[j] + (long long)kChunk * (second ? c0 + h : c0));
+    };
+    // one chunk pair, its halves H0 and H1; the next pair's loads go out
+    // between the unpack and the MFMAs
+    auto step = [&](int c0, auto h0, auto h1) {
+        constexpr int LO = h0.value ? 0 : 1, HI = h1.value ? 2 : 1;
+        u32x4 wf[PN][2][4];
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++)
+#pragma unroll
+            for (int h = LO; h < HI; h++) unpack_run<FMT, DT>(raw[pn][h], src[pn], c0 + h, wf[pn][h]);
+#pragma unroll
+        for (int h = LO; h < HI; h++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) *(u32x4 *)(put + (16 * h + 4 * j) * kXStride) = xp[h][j];
+        if (c0 + 2 < ce) fetch(c0 + 2);
+        __builtin_amdgcn_wave_barrier();
+        u32x4 xc[2][4];
+#pragma unroll
+        for (int h = LO; h < HI; h++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) xc[h][i] = *(const u32x4 *)(get + 16 * h * kXStride + 16 * i);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int h = LO; h < HI; h++)
+#pragma unroll
+            for (int pn = 0; pn < PN; pn++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[pn][0] = mma<DT>(wf[pn][h][i], xc[h][i], acc[pn][0]);
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    int c0 = cb & ~1;
+    if (cb < ce) fetch(c0);
+    if (cb < ce && c0 < cb) {  // a range that starts on an odd chunk
+        step(c0, no, yes);
+        c0 += 2;
+    }
+    for (; c0 + 2 <= ce; c0 += 2) step(c0, yes, yes);
+    if (c0 < ce) step(c0, yes, no);
+    direct_finish<DT, 1, PN, EPI>(a, acc, red + a.kw * (kXTile / sizeof(f32x4)), w, lane, p0, m0);
+}
+
 template <int FMT, int DT, int RB, int PN, int XL, int EPI = EP_NONE>
 __global__ void __launch_bounds__(512) k_direct(Args a)
 {
-    direct_body<FMT, DT, RB, PN, XL, EPI>(a, blockIdx.x * PN, blockIdx.y * (16 * RB));
+    if constexpr (row_staged(RB, PN, XL, EPI))
+        direct_row_body<FMT, DT, PN, EPI>(a, blockIdx.x * PN, blockIdx.y * 16);
+    else
+        direct_body<FMT, DT, RB, PN, XL, EPI>(a, blockIdx.x * PN, blockIdx.y * (16 * RB));
 }
 
 // ---------------------------------------------------------------------------
@@ -901,7 +964,8 @@ __global__ void __launch_bounds__(256) k_splitk_reduce_ep(Args a)
 template <int FMT, int DT, int RB, int PN, int XL, int EPI>
 hipError_t launch_direct_rp(const Plan &pl, const Args &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_direct<FMT, DT, RB, PN, XL, EPI>), pl.grid, dim3(64 * pl.kw), pl.lds, s, a);
+    const size_t tiles = row_staged(RB, PN, XL, EPI) ? (size_t)pl.kw * kXTile : 0;
+    hipLaunchKernelGGL((k_direct<FMT, DT, RB, PN, XL, EPI>), pl.grid, dim3(64 * pl.kw), pl.lds + tiles, s, a);
     return hipGetLastError();
 }
 

@@ -31,6 +31,65 @@
 
 namespace qg {
 
+// acc[PN][RB] += X rows . panels over chunks [cb, ce) of one wave, D chunks of
+// weights and DX of activations in flight ahead of the one being multiplied
+// (DX divides D; the activations come from L2, whose latency is a fraction of
+// the memory's).  cb and ce are the same in every lane.  The steady state has
+// no branch, so that a wait counts only the loads it needs; each output's
+// MFMAs run in chunk order whatever D.
+template <int FMT, int DT, int RB, int PN, int D, int DX>
+__device__ __forceinline__ void stream_chunks(const RunSrc<FMT> (&src)[PN], const uint16_t *const (&xrow)[RB], int cb,
+                                              int ce, f32x4 (&acc)[PN][RB])
+{
+    using XA = XLay<X_ROW>;
+    static_assert(D % DX == 0, "the rings turn together");
+    RunRaw<FMT> raw[D][PN];
+    u32x4 xf[DX][RB][4];
+    auto fetch_w = [&](int c, int d) {
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) src[pn].load(c, raw[d][pn]);
+    };
+    auto fetch_x = [&](int c, int d) {
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) xf[d][rb][i] = *(const u32x4 *)(xrow[rb] + XA::chunk(c) + XA::off(8 * i));
+    };
+    // chunk c from slot d; its slots refilled with chunks c + D and c + DX
+    auto step = [&](int c, int d, bool more_w, bool more_x) {
+        const int dx = d % DX;
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) {
+            u32x4 wf[4];
+            unpack_run<FMT, DT>(raw[d][pn], src[pn], c, wf);
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[i], xf[dx][rb][i], acc[pn][rb]);
+        }
+        if (more_w) fetch_w(c + D, d);
+        if (more_x) fetch_x(c + DX, dx);
+        __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where they are next needed
+    };
+#pragma unroll
+    for (int d = 0; d < D; d++)
+        if (cb + d < ce) {
+            fetch_w(cb + d, d);
+            if (d < DX) fetch_x(cb + d, d);
+        }
+    int c = cb;
+    for (; c + 2 * D <= ce; c += D)
+#pragma unroll
+        for (int d = 0; d < D; d++) step(c + d, d, true, true);
+#pragma unroll
+    for (int d = 0; d < D; d++)
+        if (c + d < ce) step(c + d, d, c + d + D < ce, c + d + DX < ce);
+    c += D;
+#pragma unroll
+    for (int d = 0; d + 1 < D; d++)
+        if (c + d < ce) step(c + d, d, false, c + d + DX < ce);
+}
+
 // Chunks of weights and activations k_moe_up's waves keep in flight.  Two of
 // each lead or tie at every size measured (64 tokens of 8 of 128 experts,
 // Q4_K 2048 -> 768 pairs, weights rotating: 55.4 us; three of weights and one
@@ -199,7 +258,7 @@ __global__ void __launch_bounds__(512) k_moe_up(MoeArgs m)
         for (int rb = 0; rb < RB; rb++) acc[pn][rb] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int nch = a.K / kChunk;
     const int cb = (int)((long long)nch * share / a.kw), ce = (int)((long long)nch * (share + 1) / a.kw);
-    stream_chunks<FMT, DT, RB, 2, X_ROW, DP::W, DP::X>(src, xrow, cb, ce, acc);
+    stream_chunks<FMT, DT, RB, 2, DP::W, DP::X>(src, xrow, cb, ce, acc);
     if (a.kw > 1) {
 #pragma unroll
         for (int pn = 0; pn < 2; pn++)

@@ -371,10 +371,13 @@ int qgemm_gemm_xf_noalloc(int format, int rung, const void *Xf, const void *Wpac
  * it (SiLU of -infinity is NaN, as -infinity * 0 is).  With no bias, no
  * residual, act NONE and gated 0, Y (row-major) has the bits of
  * qgemm_gemm_rung / qgemm_gemm_xf on the same rung.
- * rung as in qgemm_gemm_rung, from the same M-ladder over the packed columns
- * (2N when gated); the gated form has no rung that splits K across
- * workgroups: the ladder picks the next best, and forcing one is
- * QGEMM_ERR_FORMAT.  Launches, errors and the workspace as there, plus
+ * rung as in qgemm_gemm_rung; -1 takes the M-ladder of X's layout over the
+ * packed columns (2N when gated), save that on row-major X 33..64 rows of a
+ * k-quant over at most 256 panels go to direct-small-m where the products go
+ * to direct-skinny-n (qgemm_linear_select_rung says which).  The gated form
+ * has no rung that splits K across workgroups: -1 picks the next best, and
+ * forcing one is QGEMM_ERR_FORMAT.  Launches, errors and the workspace as
+ * there, plus
  * QGEMM_ERR_FORMAT for an unknown layout or activation and QGEMM_ERR_SHAPE for
  * an N that gated or y_layout does not allow; M = 0 is a no-op.
  *
@@ -481,7 +484,7 @@ int qgemm_grouped_plan(int64_t T, int64_t E, int64_t N, int64_t K, int32_t *info
  * All buffers are device memory and the caller's; logits and ids 16-byte
  * aligned, the others 4-byte; no buffer may overlap another.  The order of
  * rows does not depend on timing.  E is 1 .. QGEMM_MOE_MAX_EXPERTS, top_k 1 ..
- * 64 (and at most E in qgemm_moe_route), T * top_k below 2^31 - 1024.  T = 0
+ * 64 (and at most E in qgemm_moe_route), T * top_k below 2^31 - 4096.  T = 0
  * writes nothing in qgemm_moe_route; qgemm_moe_group then writes zeros to
  * offsets.  Errors: QGEMM_ERR_SHAPE, _DTYPE (logit_type), _FORMAT (score),
  * _NULL, _ALIGN, _HIP. */

@@ -580,8 +580,9 @@ int gemm(int fmt, int rung, const void *X, const void *W, void *Y, long long M, 
 
 bool known_act(int act) { return act >= QGEMM_ACT_NONE && act <= QGEMM_ACT_GELU_TANH; }
 
-// The plan over the packed columns (2N when gated), by the same ladder: the
-// epilogue adds the same few loads and stores per output to every rung.  The
+// The plan over the packed columns (2N when gated), by the products' ladder
+// but for one rule: the epilogue adds the same few loads and stores per output
+// to every rung.  The
 // gated form has no rung that splits K across workgroups (its partial sums
 // would pair columns of two tiles): where the ladder picks one, the best of
 // the others serves.
@@ -597,6 +598,16 @@ int linear_plan(int fmt, int rung, int xl, long long M, long long N, long long K
     if (dtype != DT_F16 && dtype != DT_BF16) return QGEMM_ERR_DTYPE;
     if (rung < -1 || rung >= RUNG_COUNT) return QGEMM_ERR_FORMAT;
     int r = rung < 0 ? select_rung(fmt, m, nt, K, xl, dtype) : rung;
+    // Row-major X, 33..64 rows over at most 256 panels of a k-quant: where the
+    // products take 16-row groups of four panels per wave, the linear layer's
+    // one-panel waves carry all rows, their activations staged through LDS
+    // (weights rotating, Q4_K 4096 -> 4096, 48 rows: 10.5 against 12.3 us, 64
+    // rows 12.1 against 12.4; Q6_K 12288 -> 4096, 48 rows: 25.7 against 33.2,
+    // 64 rows 29.9 against 33.0; W4A16, 48 and 64 rows: 10.6 and 12.6 against
+    // 10.8 and 11.1, so it stays).
+    if (rung < 0 && !gated && xl == X_ROW && r == RUNG_SKINNY_N && fmt != FMT_W4 && m > 32 && m <= 64 && nt > 64 &&
+        (nt + 15) / 16 <= kCUs)
+        r = RUNG_SMALL_M;
     if (gated && (r == RUNG_M64_SK || r == RUNG_M768N64_SK)) {
         if (rung >= 0) return QGEMM_ERR_FORMAT;
         r = r == RUNG_M64_SK ? round_model_rung(fmt, m, nt, K, xl, dtype) : large_tile_xf(fmt, m, nt, K);
@@ -723,7 +734,7 @@ bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 int moe_route_shape(long long T, long long E, long long k)
 {
     if (T < 0 || E < 1 || E > QGEMM_MOE_MAX_EXPERTS || k < 1 || k > 64) return QGEMM_ERR_SHAPE;
-    return T > (INT32_MAX - 1024) / k ? QGEMM_ERR_SHAPE : QGEMM_OK;
+    return T > (INT32_MAX - 4096) / k ? QGEMM_ERR_SHAPE : QGEMM_OK;  // the grouping's indexes run a step past the pairs
 }
 
 hipError_t launch_up(int fmt, int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s)

@@ -4,6 +4,7 @@
 // launches a Plan's rung.  Included by the instantiation units only.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -177,52 +178,59 @@ __device__ __forceinline__ void load_pair(const RunSrc<FMT> &s, int c0, bool sec
 // weight runs, and staging loses (M = 33, W4A16 4096 -> 4097 12.0 against 10.9
 // us), so those keep direct_body.
 constexpr int kXStride = 272;              // bytes from row to row of the tile
-constexpr int kXTile = 2 * 16 * kXStride;  // two chunks of 16 rows
+constexpr int row_tile_bytes(int rb) { return (rb == 1 ? 32 : 16 * rb) * kXStride; }  // a wave's rows of a step
 
 constexpr bool row_staged(int rb, int pn, int xl, int epi)
 {
-    return epi != EP_NONE && xl == X_ROW && rb == 1 && pn <= 2;
+    return epi != EP_NONE && xl == X_ROW && pn <= 2;
 }
 
-template <int FMT, int DT, int PN, int EPI>
+template <int FMT, int DT, int RB, int PN, int EPI>
 __device__ __forceinline__ void direct_row_body(const Args &a, int p0, int m0)
 {
     static_assert(EPI != EP_GATED || PN % 2 == 0, "gate and up panels come in pairs");
-    extern __shared__ f32x4 red[];  // [kw] tiles of kXTile bytes, then [kw][PN][64]
+    constexpr int HP = RB == 1 ? 2 : 1;  // chunks per step
+    extern __shared__ f32x4 red[];       // [kw] tiles; then the partial sums
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int nch = a.K / kChunk;
     const int cb = (int)((long long)nch * w / a.kw), ce = (int)((long long)nch * (w + 1) / a.kw);
-    uint8_t *tile = (uint8_t *)red + w * kXTile;
+    uint8_t *tile = (uint8_t *)red + w * row_tile_bytes(RB);
     uint8_t *put = tile + g * kXStride + 16 * col;             // row g + 4j, 16 bytes col
     const uint8_t *get = tile + col * kXStride + 64 * g;       // row col, run g
 
-    f32x4 acc[PN][1];
+    f32x4 acc[PN][RB];
 #pragma unroll
-    for (int pn = 0; pn < PN; pn++) acc[pn][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint16_t *xrow[4];
+    for (int pn = 0; pn < PN; pn++)
 #pragma unroll
-    for (int j = 0; j < 4; j++) xrow[j] = a.X + (long long)min(m0 + g + 4 * j, a.M - 1) * a.K + 8 * col;
+        for (int rb = 0; rb < RB; rb++) acc[pn][rb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint16_t *xrow[4 * RB];
+#pragma unroll
+    for (int j = 0; j < 4 * RB; j++) xrow[j] = a.X + (long long)min(m0 + g + 4 * j, a.M - 1) * a.K + 8 * col;
     RunSrc<FMT> src[PN];
 #pragma unroll
     for (int pn = 0; pn < PN; pn++) src[pn].init(a, packed_panel<EPI>(a, p0 + pn), g, col);
 
-    RunRaw<FMT> raw[PN][2];
-    u32x4 xp[2][4];
+    RunRaw<FMT> raw[PN][HP];
+    u32x4 xp[HP][4 * RB];
     auto fetch = [&](int c0) {
         const bool second = FMT != FMT_W4 || c0 + 1 < nch;
 #pragma unroll
-        for (int pn = 0; pn < PN; pn++) load_pair<FMT>(src[pn], c0, second, raw[pn]);
+        for (int pn = 0; pn < PN; pn++) {
+            if constexpr (HP == 2) load_pair<FMT>(src[pn], c0, second, raw[pn]);
+            else src[pn].load(c0, raw[pn][0]);
+        }
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+        for (int h = 0; h < HP; h++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) xp[h][j] = *(const u32x4 *)(xrow[j] + (long long)kChunk * (second ? c0 + h : c0));
+            for (int j = 0; j < 4 * RB; j++)
+                xp[h][j] = *(const u32x4 *)(xrow[j] + (long long)kChunk * (second ? c0 + h : c0));
     };
-    // one chunk pair, its halves H0 and H1; the next pair's loads go out
-    // between the unpack and the MFMAs
+    // one step, its chunks H0 and H1 (a pair cut by the wave's range has one);
+    // the next step's loads go out between the unpack and the MFMAs
     auto step = [&](int c0, auto h0, auto h1) {
-        constexpr int LO = h0.value ? 0 : 1, HI = h1.value ? 2 : 1;
-        u32x4 wf[PN][2][4];
+        constexpr int LO = h0.value ? 0 : 1, HI = h1.value ? HP : 1;
+        u32x4 wf[PN][HP][4];
 #pragma unroll
         for (int pn = 0; pn < PN; pn++)
 #pragma unroll
@@ -230,40 +238,54 @@ __device__ __forceinline__ void direct_row_body(const Args &a, int p0, int m0)
 #pragma unroll
         for (int h = LO; h < HI; h++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) *(u32x4 *)(put + (16 * h + 4 * j) * kXStride) = xp[h][j];
-        if (c0 + 2 < ce) fetch(c0 + 2);
+            for (int j = 0; j < 4 * RB; j++) *(u32x4 *)(put + (16 * h + 4 * j) * kXStride) = xp[h][j];
+        if (c0 + HP < ce) fetch(c0 + HP);
         __builtin_amdgcn_wave_barrier();
-        u32x4 xc[2][4];
+        u32x4 xc[HP][RB][4];
 #pragma unroll
         for (int h = LO; h < HI; h++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) xc[h][i] = *(const u32x4 *)(get + 16 * h * kXStride + 16 * i);
+            for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    xc[h][rb][i] = *(const u32x4 *)(get + 16 * (h + rb) * kXStride + 16 * i);
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int h = LO; h < HI; h++)
 #pragma unroll
-            for (int pn = 0; pn < PN; pn++)
+            for (int rb = 0; rb < RB; rb++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) acc[pn][0] = mma<DT>(wf[pn][h][i], xc[h][i], acc[pn][0]);
+                for (int pn = 0; pn < PN; pn++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[pn][h][i], xc[h][rb][i], acc[pn][rb]);
     };
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
-    int c0 = cb & ~1;
+    int c0 = cb & ~(HP - 1);
     if (cb < ce) fetch(c0);
-    if (cb < ce && c0 < cb) {  // a range that starts on an odd chunk
-        step(c0, no, yes);
-        c0 += 2;
+    if constexpr (HP == 2) {
+        if (cb < ce && c0 < cb) {  // a range that starts on an odd chunk
+            step(c0, no, yes);
+            c0 += 2;
+        }
     }
-    for (; c0 + 2 <= ce; c0 += 2) step(c0, yes, yes);
-    if (c0 < ce) step(c0, yes, no);
-    direct_finish<DT, 1, PN, EPI>(a, acc, red + a.kw * (kXTile / sizeof(f32x4)), w, lane, p0, m0);
+    for (; c0 + HP <= ce; c0 += HP) step(c0, yes, yes);
+    if constexpr (HP == 2) {
+        if (c0 < ce) step(c0, yes, no);
+    }
+    if constexpr (RB == 1) {
+        direct_finish<DT, RB, PN, EPI>(a, acc, red + a.kw * (row_tile_bytes(RB) / sizeof(f32x4)), w, lane, p0, m0);
+    } else {
+        __syncthreads();  // the sums take the tiles' place
+        direct_finish<DT, RB, PN, EPI>(a, acc, red, w, lane, p0, m0);
+    }
 }
 
 template <int FMT, int DT, int RB, int PN, int XL, int EPI = EP_NONE>
 __global__ void __launch_bounds__(512) k_direct(Args a)
 {
     if constexpr (row_staged(RB, PN, XL, EPI))
-        direct_row_body<FMT, DT, PN, EPI>(a, blockIdx.x * PN, blockIdx.y * 16);
+        direct_row_body<FMT, DT, RB, PN, EPI>(a, blockIdx.x * PN, blockIdx.y * (16 * RB));
     else
         direct_body<FMT, DT, RB, PN, XL, EPI>(a, blockIdx.x * PN, blockIdx.y * (16 * RB));
 }
@@ -964,8 +986,9 @@ __global__ void __launch_bounds__(256) k_splitk_reduce_ep(Args a)
 template <int FMT, int DT, int RB, int PN, int XL, int EPI>
 hipError_t launch_direct_rp(const Plan &pl, const Args &a, hipStream_t s)
 {
-    const size_t tiles = row_staged(RB, PN, XL, EPI) ? (size_t)pl.kw * kXTile : 0;
-    hipLaunchKernelGGL((k_direct<FMT, DT, RB, PN, XL, EPI>), pl.grid, dim3(64 * pl.kw), pl.lds + tiles, s, a);
+    const size_t tiles = row_staged(RB, PN, XL, EPI) ? (size_t)pl.kw * row_tile_bytes(RB) : 0;
+    hipLaunchKernelGGL((k_direct<FMT, DT, RB, PN, XL, EPI>), pl.grid, dim3(64 * pl.kw),
+                       RB == 1 ? pl.lds + tiles : std::max(pl.lds, tiles), s, a);
     return hipGetLastError();
 }
 

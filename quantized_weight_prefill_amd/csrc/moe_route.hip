@@ -267,37 +267,58 @@ __global__ void __launch_bounds__(256) k_route(RouteArgs a)
 // split the pairs into 16 contiguous ranges; pass one counts, per wave, the
 // pairs of earlier experts and of its own; pass two writes its own pairs in
 // order behind them.  Every workgroup reads all ids twice (from L2): no
-// atomics, no second launch, and the order does not depend on timing.
+// atomics, no second launch, and the order does not depend on timing.  What
+// bounds it is the latency of those reads, so each lane has kGroupAhead of
+// its 16-byte loads in flight.
+constexpr int kGroupAhead = 8;
+
+// ids p .. p+3 of [0, hi) as experts: dropped ones E, past the end E + 1.
+__device__ __forceinline__ void load_ids(const int *ids, int p, int hi, int E, int (&v)[4])
+{
+    if (p + 4 <= hi) {
+        const int4 q = *(const int4 *)(ids + p);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = p + j < hi ? ids[p + j] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        v[j] = (int)min((unsigned)v[j], (unsigned)E);  // negative ids are large unsigned ones
+        if (p + j >= hi) v[j] = E + 1;
+    }
+}
+
 __global__ void __launch_bounds__(1024) k_group_large(const int *ids, int P, int E, int *offsets, int *rows)
 {
     __shared__ int s_less[16], s_own[16];
-    const int x = blockIdx.x, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int x = blockIdx.x, lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // ranges of whole groups of 256 pairs (64 lanes x 4)
     const long long blocks = ((long long)P + 255) / 256;
     const int lo = (int)(blocks * wv / 16) * 256;
     const int hi = (int)min((long long)P, (long long)(blocks * (wv + 1) / 16) * 256);
-    auto load4 = [&](int p, int (&v)[4]) {  // ids p .. p+3, E where there is none
-        if (p + 4 <= hi) {
-            const int4 q = *(const int4 *)(ids + p);
-            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    int less = 0, own = 0;
+    for (int p0 = lo; p0 < hi; p0 += 256 * kGroupAhead) {
+        int v[kGroupAhead][4];
+        const bool whole = hi - p0 >= 256 * kGroupAhead;  // no branch between the loads
+        if (whole) {
+            int4 q[kGroupAhead];
+#pragma unroll
+            for (int u = 0; u < kGroupAhead; u++) q[u] = *(const int4 *)(ids + p0 + 256 * u + 4 * lane);
+#pragma unroll
+            for (int u = 0; u < kGroupAhead; u++) v[u][0] = q[u].x, v[u][1] = q[u].y, v[u][2] = q[u].z, v[u][3] = q[u].w;
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; j++) v[j] = p + j < hi ? ids[p + j] : INT_MIN;
+            for (int u = 0; u < kGroupAhead; u++) load_ids(ids, p0 + 256 * u + 4 * lane, hi, E, v[u]);
         }
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (v[j] != INT_MIN || p + j < hi) v[j] = (v[j] < 0 || v[j] > E) ? E : v[j];
-            else v[j] = E + 1;  // past the end
-    };
-    int less = 0, own = 0;
-    for (int p = lo + 4 * lane; p < hi; p += 256) {
-        int v[4];
-        load4(p, v);
+        for (int u = 0; u < kGroupAhead; u++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            less += v[j] < x;
-            own += v[j] == x;
-        }
+            for (int j = 0; j < 4; j++) {
+                const int e = whole ? (int)min((unsigned)v[u][j], (unsigned)E) : v[u][j];
+                less += e < x;
+                own += e == x;
+            }
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -314,24 +335,40 @@ __global__ void __launch_bounds__(1024) k_group_large(const int *ids, int P, int
     if (threadIdx.x == 0) offsets[x] = pos;
     for (int v = 0; v < wv; v++) pos += s_own[v];
     if (own == 0) return;
-    for (int p0 = lo; p0 < hi; p0 += 256) {
-        const int p = p0 + 4 * lane;
-        int v[4] = {E + 1, E + 1, E + 1, E + 1};
-        if (p < hi) load4(p, v);
-        const unsigned long long before = (1ull << lane) - 1ull;
-        int at = pos, mine = 0;
+    const unsigned long long before = (1ull << lane) - 1ull;
+    auto place = [&](int p, const int (&v)[4]) {  // the wave's next 256 pairs, in pair order
+        unsigned long long b[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) b[j] = __ballot(v[j] == x);
+        if ((b[0] | b[1] | b[2] | b[3]) == 0ull) return;
+        int at = pos;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const unsigned long long b = __ballot(v[j] == x);
-            at += __popcll(b & before);
-            pos += __popcll(b);
+            at += __popcll(b[j] & before);
+            pos += __popcll(b[j]);
         }
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            if (v[j] == x) {
-                rows[at + mine] = x < E ? p + j : -1;
-                mine++;
+            if (v[j] == x) rows[at++] = x < E ? p + j : -1;
+    };
+    for (int p0 = lo; p0 < hi; p0 += 256 * kGroupAhead) {
+        int v[kGroupAhead][4];
+        if (hi - p0 >= 256 * kGroupAhead) {
+            int4 q[kGroupAhead];
+#pragma unroll
+            for (int u = 0; u < kGroupAhead; u++) q[u] = *(const int4 *)(ids + p0 + 256 * u + 4 * lane);
+#pragma unroll
+            for (int u = 0; u < kGroupAhead; u++) {
+                v[u][0] = q[u].x, v[u][1] = q[u].y, v[u][2] = q[u].z, v[u][3] = q[u].w;
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[u][j] = (int)min((unsigned)v[u][j], (unsigned)E);
             }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kGroupAhead; u++) load_ids(ids, p0 + 256 * u + 4 * lane, hi, E, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kGroupAhead; u++) place(p0 + 256 * u + 4 * lane, v[u]);
     }
 }
 

@@ -61,6 +61,7 @@ STATUS = {0: "QGEMM_OK", -1: "QGEMM_ERR_NULL", -2: "QGEMM_ERR_SHAPE", -3: "QGEMM
           -8: "QGEMM_ERR_INPUT"}
 
 _lib = None
+_common_calls = None  # the C++ marshalling of the decode-size calls (csrc/calls.cpp)
 
 
 class QGemmError(RuntimeError):
@@ -145,7 +146,7 @@ def lib():
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing; build it with `python -m quantized_weight_prefill_amd.build`")
-        import torch  # noqa: F401  (binds libamdhip64.so.7 to torch's runtime)
+        import torch  # binds libamdhip64.so.7 to torch's runtime
 
         handle = ctypes.CDLL(LIB_PATH)
         for name, (res, args) in SIGNATURES.items():
@@ -153,7 +154,23 @@ def lib():
             fn.restype = res
             fn.argtypes = args
         _lib = handle
+        from . import _calls as calls  # built beside libqgemm.so, linked to it and to torch
+
+        calls.bind(torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        global _common_calls
+        _common_calls = calls
     return _lib
+
+
+def _common(name, fn, args):
+    """The result of csrc/calls.cpp's `fn`, or None where the call needs the
+    checks that follow."""
+    if _common_calls is None:
+        lib()
+    r = getattr(_common_calls, fn)(*args)
+    if type(r) is int:
+        raise QGemmError(name, r)
+    return r
 
 
 def _check(fn: str, status: int):
@@ -484,9 +501,10 @@ def _act_code(act) -> int:
     return ACTS[act]
 
 
-# A call of these layers at decode sizes takes a few microseconds on the GPU, so
-# their checks are plain attribute reads, and the pure size queries of the
-# library (functions of the sizes alone) are remembered.
+# At decode sizes a call of these layers takes a few microseconds on the GPU, less
+# than checking its arguments here: the common call (the current device and
+# stream, arguments as they should be) goes through csrc/calls.cpp, and what
+# follows serves every other one, or says what is wrong with it.
 
 def _refuse(named):
     """Say what is wrong with the first of `named` ((name, tensor, shape, dtype),
@@ -611,6 +629,11 @@ def linear(fmt, x, wp, N: int, bias=None, residual=None, act: str = "none", gate
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
+    if stream is None and workspace is None:
+        y = _common("qgemm_linear", "linear", (FORMATS.get(fmt, fmt), X_ROW, x, wp, M, N, K, bias, residual,
+                                               ACTS.get(act), gated, group, has_zp, rung, out, out_layout))
+        if y is not None:
+            return y
     return _linear(fmt, X_ROW, x, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout, stream,
                    workspace)
 
@@ -621,6 +644,11 @@ def linear_xf(fmt, xf, wp, M: int, N: int, K: int, bias=None, residual=None, act
     """:func:`linear` with X given as its fragment-major copy `xf`."""
     if xf.numel() < xf_bytes(M, K) // 2:
         raise ValueError("xf is smaller than the fragment-major copy of an M x K matrix")
+    if stream is None and workspace is None:
+        y = _common("qgemm_linear", "linear", (FORMATS.get(fmt, fmt), X_FRAG, xf, wp, M, N, K, bias, residual,
+                                               ACTS.get(act), gated, group, has_zp, rung, out, out_layout))
+        if y is not None:
+            return y
     return _linear(fmt, X_FRAG, xf, wp, M, N, K, bias, residual, act, gated, group, has_zp, rung, out, out_layout,
                    stream, workspace)
 
@@ -843,6 +871,10 @@ def moe_route(logits, top_k: int, score: str = "softmax", renorm: bool = True, s
     Experts come in falling order of their logits, equal ones by index.  The
     weights are the softmax over all E logits or the sigmoid of each, with
     ``renorm`` divided by their sum over the token's choice, times ``scale``."""
+    if stream is None:
+        r = _common("qgemm_moe_route", "moe_route", (logits, top_k, SCORES.get(score), renorm, scale))
+        if r is not None:
+            return r
     torch = _torch()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
@@ -871,6 +903,10 @@ def moe_group(ids, E: int, stream=None):
     by expert: (offsets [E+1], rows [T*top_k]), rows in pair order within an
     expert.  Ids outside [0, E) are dropped pairs: in no group, rows -1 at
     the end."""
+    if stream is None:
+        r = _common("qgemm_moe_group", "moe_group", (ids, E))
+        if r is not None:
+            return r
     torch = _torch()
     if ids.dim() != 2 or ids.dtype != torch.int32:
         raise ValueError("ids must be an int32 tensor [T, top_k]")
@@ -913,6 +949,11 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
     w_down: E packed weights of H columns over K = inter; weights [T, top_k]
     float32, offsets [E+1] and rows [T*top_k] from :func:`moe_route` or
     :func:`moe_group`.  ``out`` may be the residual."""
+    if stream is None and workspace is None:
+        y = _common("qgemm_moe", "moe", (FORMATS.get(fmt_up, fmt_up), FORMATS.get(fmt_down, fmt_down), x, w_up, w_down,
+                                         weights, offsets, rows, inter, group, has_zp, ACTS.get(act), residual, out))
+        if y is not None:
+            return y
     if x.dim() != 2 or weights.dim() != 2:
         raise ValueError("x must be [T, H] and weights [T, top_k]")
     torch = _torch()

@@ -7,6 +7,7 @@ per format x dtype x activation layout for the fp16/bf16 path, one more per
 epilogue for the linear layer, one per format x dtype for the int8 path, one
 per format for the mixture-of-experts layer) that compile in parallel into
 ``_build/`` and link into one shared object.
+The binding's C++ marshalling (csrc/calls.cpp) builds into _calls.so beside it.
 Run `python -m quantized_weight_prefill_amd.build`.
 """
 import concurrent.futures as cf
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqgemm.so")
 PROBE_LIB = os.path.join(PKG, "libqprobe.so")
+CALLS_LIB = os.path.join(PKG, "_calls.so")  # the binding's marshalling of the decode-size calls
 ARCH = "gfx950"
 FORMATS = (0, 1, 2)  # QGEMM_FMT_Q4K, _Q6K, _W4A16
 DTYPES = (0, 1)      # QGEMM_F16, QGEMM_BF16
@@ -59,6 +61,23 @@ def units():
     return out
 
 
+def calls_command(out):
+    """The host compiler's command for the Python module in csrc/calls.cpp,
+    against torch's C++ headers and libqgemm.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in (os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], *cpp_extension.include_paths()):
+        cmd += ["-isystem" if "torch" in d else "-I", d]
+    cmd += [os.path.join(CSRC, "calls.cpp"), "-o", out]
+    for d in cpp_extension.library_paths():
+        cmd += ["-L", d]
+    return cmd + ["-ltorch_python", "-ltorch_cpu", "-lc10", "-L", PKG, "-lqgemm", "-Wl,-rpath,$ORIGIN"]
+
+
 def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -89,6 +108,8 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", f"-Wl,--version-script={vscript}", "-o", LIB + ".tmp",
           *[o for o, _ in cmds]], verbose)
     os.replace(LIB + ".tmp", LIB)
+    _run(calls_command(CALLS_LIB + ".tmp"), verbose)
+    os.replace(CALLS_LIB + ".tmp", CALLS_LIB)
     _run([cc, *COMMON_FLAGS, "-shared", "-o", PROBE_LIB + ".tmp", os.path.join(CSRC, "probe", "qprobe.hip")], verbose)
     os.replace(PROBE_LIB + ".tmp", PROBE_LIB)
     return LIB

@@ -737,10 +737,10 @@ int moe_route_shape(long long T, long long E, long long k)
     return T > (INT32_MAX - 4096) / k ? QGEMM_ERR_SHAPE : QGEMM_OK;  // the grouping's indexes run a step past the pairs
 }
 
-hipError_t launch_up(int fmt, int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s)
+hipError_t launch_up(int fmt, int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
-    if (fmt == FMT_Q4K) return launch_moe_up<FMT_Q4K>(dtype, rb, grid, m, s);
-    return fmt == FMT_Q6K ? launch_moe_up<FMT_Q6K>(dtype, rb, grid, m, s) : launch_moe_up<FMT_W4>(dtype, rb, grid, m, s);
+    if (fmt == FMT_Q4K) return launch_moe_up<FMT_Q4K>(dtype, grid, m, s);
+    return fmt == FMT_Q6K ? launch_moe_up<FMT_Q6K>(dtype, grid, m, s) : launch_moe_up<FMT_W4>(dtype, grid, m, s);
 }
 
 hipError_t launch_down(int fmt, int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
@@ -794,37 +794,32 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.partial = (float *)(m.H + P * I);
     m.arrived = (int *)(m.partial + (long long)m.panels * m.split * T * 16);
 
-    // gate and up: rows per tile by the experts' mean count; K split over
-    // waves while the grid holds fewer than 4096 of them and each keeps four
-    // chunks (one token, Q4_K 2048 -> 768, weights rotating: 7.7 us split four
-    // ways, 8.0 eight, 18 unsplit; seven tokens, W4A16 2048 -> 1408: 17.7 two
-    // ways, 18.6 unsplit)
-    const long long avg = (P + E - 1) / E;
-    const int rb = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
+    // gate and up: K split over waves while the grid holds fewer than 4096 of
+    // them and each keeps four chunks (weights rotating: one token, Q4_K 2048
+    // -> 768, 7.5 us split four ways, 8.1 two, 18 unsplit; seven tokens, W4A16
+    // 2048 -> 1408, 17.3 two ways, 18.6 unsplit, 19.2 four; 96 tokens, 4 of 16
+    // experts, 19.7 four ways, 22.2 unsplit)
     m.g = make_args(fu, X, Wu, nullptr, P, 2 * I, H, group, has_zp);
     m.g.offs = offs;
     m.g.E = (int)E;
     m.g.wstride = su;
     m.g.act = act;
     const int nch = (int)(H / kChunk);
-    const long long slots = std::min(P, (P + 16 * rb - 1) / (16 * rb) + E);
     m.g.kw = 1;
-    while (m.g.kw < kMoeUpWaves && slots * (I / 16) * m.g.kw < 4096 && nch >= 8 * m.g.kw) m.g.kw *= 2;
+    while (m.g.kw < kMoeUpWaves && tiles * (I / 16) * m.g.kw < 4096 && nch >= 8 * m.g.kw) m.g.kw *= 2;
     const int per = kMoeUpWaves / m.g.kw;  // gate panels per workgroup
-    const dim3 gu((unsigned)((I / 16 + per - 1) / per), (unsigned)slots, 1);
-    hipError_t e = launch_up(fu, dtype, rb, gu, m, (hipStream_t)stream);
+    const dim3 gu((unsigned)((I / 16 + per - 1) / per), (unsigned)tiles, 1);
+    hipError_t e = launch_up(fu, dtype, gu, m, (hipStream_t)stream);
     if (e != hipSuccess) return launch_status(e, "moe up");
 
-    // down: K in parts of at least three chunks while the row tiles alone
-    // leave waves idle
+    // down: K in parts (of whole chunk pairs) while the row tiles alone leave
+    // waves idle (one token, Q6_K 768 -> 2048: 7.4 us in three parts, 8.1 whole)
     m.g = make_args(fd, nullptr, Wd, Y, P, H, I, group, has_zp);
     m.g.offs = offs;
     m.g.E = (int)E;
     m.g.wstride = sd;
     m.g.res = (const uint16_t *)res;
-    m.parts = 1;
-    while (tiles * m.parts < kMoeDownWaves * m.split && I / kChunk >= 6 * m.parts && 2 * m.parts * P <= 1024)
-        m.parts *= 2;
+    m.parts = (int)std::max(1LL, std::min({kMoeDownWaves * m.split / tiles, (I / kChunk + 1) / 2, 1024 / P, 8LL}));
     e = launch_down(fd, dtype, dim3((unsigned)(m.panels * m.split), 1, 1), m, (hipStream_t)stream);
     return launch_status(e, "moe down");
 }

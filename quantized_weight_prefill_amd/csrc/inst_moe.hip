@@ -8,22 +8,13 @@
 
 namespace qg {
 
-template <int FMT, int DT>
-hipError_t launch_up_dt(int rb, dim3 grid, const MoeArgs &m, hipStream_t s)
+template <int FMT>
+hipError_t launch_moe_up(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
     const dim3 block(64 * kMoeUpWaves);
-    const size_t lds = m.g.kw > 1 ? (size_t)kMoeUpWaves * 2 * rb * 64 * sizeof(f32x4) : 0;
-    if (rb == 1) hipLaunchKernelGGL((k_moe_up<FMT, DT, 1>), grid, block, lds, s, m);
-    else if (rb == 2) hipLaunchKernelGGL((k_moe_up<FMT, DT, 2>), grid, block, lds, s, m);
-    else if (rb == 4) hipLaunchKernelGGL((k_moe_up<FMT, DT, 4>), grid, block, lds, s, m);
-    else return hipErrorInvalidValue;
+    if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_up<FMT, DT_F16>), grid, block, 0, s, m);
+    else hipLaunchKernelGGL((k_moe_up<FMT, DT_BF16>), grid, block, 0, s, m);
     return hipGetLastError();
-}
-
-template <int FMT>
-hipError_t launch_moe_up(int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s)
-{
-    return dtype == DT_F16 ? launch_up_dt<FMT, DT_F16>(rb, grid, m, s) : launch_up_dt<FMT, DT_BF16>(rb, grid, m, s);
 }
 
 template <int FMT>
@@ -31,12 +22,12 @@ hipError_t launch_moe_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s
 {
     const dim3 block(64 * kMoeDownWaves);
     const size_t lds = moe_down_lds(m.g.M, m.g.E, m.parts);
-    if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16, 2>), grid, block, lds, s, m);
-    else hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16, 2>), grid, block, lds, s, m);
+    if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16>), grid, block, lds, s, m);
+    else hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16>), grid, block, lds, s, m);
     return hipGetLastError();
 }
 
-template hipError_t launch_moe_up<QG_FMT>(int, int, dim3, const MoeArgs &, hipStream_t);
+template hipError_t launch_moe_up<QG_FMT>(int, dim3, const MoeArgs &, hipStream_t);
 template hipError_t launch_moe_down<QG_FMT>(int, dim3, const MoeArgs &, hipStream_t);
 
 }  // namespace qg

@@ -31,75 +31,6 @@
 
 namespace qg {
 
-// acc[PN][RB] += X rows . panels over chunks [cb, ce) of one wave, D chunks of
-// weights and DX of activations in flight ahead of the one being multiplied
-// (DX divides D; the activations come from L2, whose latency is a fraction of
-// the memory's).  cb and ce are the same in every lane.  The steady state has
-// no branch, so that a wait counts only the loads it needs; each output's
-// MFMAs run in chunk order whatever D.
-template <int FMT, int DT, int RB, int PN, int D, int DX>
-__device__ __forceinline__ void stream_chunks(const RunSrc<FMT> (&src)[PN], const uint16_t *const (&xrow)[RB], int cb,
-                                              int ce, f32x4 (&acc)[PN][RB])
-{
-    using XA = XLay<X_ROW>;
-    static_assert(D % DX == 0, "the rings turn together");
-    RunRaw<FMT> raw[D][PN];
-    u32x4 xf[DX][RB][4];
-    auto fetch_w = [&](int c, int d) {
-#pragma unroll
-        for (int pn = 0; pn < PN; pn++) src[pn].load(c, raw[d][pn]);
-    };
-    auto fetch_x = [&](int c, int d) {
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) xf[d][rb][i] = *(const u32x4 *)(xrow[rb] + XA::chunk(c) + XA::off(8 * i));
-    };
-    // chunk c from slot d; its slots refilled with chunks c + D and c + DX
-    auto step = [&](int c, int d, bool more_w, bool more_x) {
-        const int dx = d % DX;
-#pragma unroll
-        for (int pn = 0; pn < PN; pn++) {
-            u32x4 wf[4];
-            unpack_run<FMT, DT>(raw[d][pn], src[pn], c, wf);
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) acc[pn][rb] = mma<DT>(wf[i], xf[dx][rb][i], acc[pn][rb]);
-        }
-        if (more_w) fetch_w(c + D, d);
-        if (more_x) fetch_x(c + DX, dx);
-        __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where they are next needed
-    };
-#pragma unroll
-    for (int d = 0; d < D; d++)
-        if (cb + d < ce) {
-            fetch_w(cb + d, d);
-            if (d < DX) fetch_x(cb + d, d);
-        }
-    int c = cb;
-    for (; c + 2 * D <= ce; c += D)
-#pragma unroll
-        for (int d = 0; d < D; d++) step(c + d, d, true, true);
-#pragma unroll
-    for (int d = 0; d < D; d++)
-        if (c + d < ce) step(c + d, d, c + d + D < ce, c + d + DX < ce);
-    c += D;
-#pragma unroll
-    for (int d = 0; d + 1 < D; d++)
-        if (c + d < ce) step(c + d, d, false, c + d + DX < ce);
-}
-
-// Chunks of weights and activations k_moe_up's waves keep in flight.  Two of
-// each lead or tie at every size measured (64 tokens of 8 of 128 experts,
-// Q4_K 2048 -> 768 pairs, weights rotating: 55.4 us; three of weights and one
-// of activations 57.5, three of both 58-62): more take the registers of the
-// waves that would hide the latency.
-template <int RB>
-struct UpDepth {
-    static constexpr int W = RB > 2 ? 1 : 2, X = RB > 2 ? 1 : 2;
-};
-
 inline size_t moe_down_lds(long long pairs, long long E, int parts)
 {
     const long long slots = std::min(pairs, (pairs + 15) / 16 + E);
@@ -136,13 +67,13 @@ __device__ __forceinline__ int wave_scan_max(int x)
     return x;
 }
 
-// The experts' row tiles of `rows_per` rows, in expert order, 64 experts at a
+// The experts' row tiles of 16 rows, in expert order, 64 experts at a
 // time, a lane per expert: visit(lane's expert, its first row, its end, its
 // tile count, the tiles before it) until it returns true.  Offsets are
 // clamped into [0, P] and made non-decreasing as the grouped GEMM does, so
 // any contents stay inside the buffers.  Returns the tiles visited over.
 template <class F>
-__device__ __forceinline__ int visit_tiles(const Args &a, int rows_per, int lane, F visit)
+__device__ __forceinline__ int visit_tiles(const Args &a, int lane, F visit)
 {
     constexpr int G = 4;  // groups of 64 experts whose offsets are loaded together
     int qc = max(0, a.offs[0]), base = 0;
@@ -160,7 +91,7 @@ __device__ __forceinline__ int visit_tiles(const Args &a, int rows_per, int lane
             const int qi = max(wave_scan_max(q[i]), qc);                                 // max(0, offs[0..e+1])
             const int qp = __builtin_amdgcn_update_dpp(qc, qi, 0x138, 0xF, 0xF, false);  // wave_shr:1, lane 0 keeps qc
             const int lo = min(qp, a.M), hi = min(qi, a.M);
-            const int nb = e < a.E ? (hi - lo + rows_per - 1) / rows_per : 0;
+            const int nb = e < a.E ? (hi - lo + 15) / 16 : 0;
             const int incl = wave_scan_add(nb);
             if (visit(e, lo, hi, nb, base + incl - nb)) return base;
             base += __builtin_amdgcn_readlane(incl, 63);
@@ -172,11 +103,11 @@ __device__ __forceinline__ int visit_tiles(const Args &a, int rows_per, int lane
 
 // Row tile j: expert e, rows [lo, hi) of the expert, tile t of it; false when
 // j is past the last tile.  The same answer in every lane.
-__device__ __forceinline__ bool find_moe_tile(const Args &a, int j, int rows_per, int lane, int &e_out, int &lo_out,
+__device__ __forceinline__ bool find_moe_tile(const Args &a, int j, int lane, int &e_out, int &lo_out,
                                               int &hi_out, int &t_out)
 {
     bool found = false;
-    visit_tiles(a, rows_per, lane, [&](int e, int lo, int hi, int nb, int before) {
+    visit_tiles(a, lane, [&](int e, int lo, int hi, int nb, int before) {
         const unsigned long long hit = __ballot(j >= before && j < before + nb);
         if (hit == 0ull) return false;
         const int l = __builtin_amdgcn_readfirstlane(__ffsll((long long)hit) - 1);
@@ -223,69 +154,109 @@ __device__ __forceinline__ int pair_at(const MoeArgs &m, int i)
     return (int)min((unsigned)m.rows[i], (unsigned)(m.g.M - 1));
 }
 
-// Grid: x = groups of nw/kw gate panels (inter/16 in all), y = row-tile slots
-// of 16*RB rows; nw waves, of which kw split the K of one panel.
-template <int FMT, int DT, int RB, class DP = UpDepth<RB>>
-__global__ void __launch_bounds__(512) k_moe_up(MoeArgs m)
+// Raw bytes and activations of one chunk pair: PN panels, one row per column
+// lane.  The k-quants' block header serves both chunks, so a pair costs one
+// header load; second: the pair's second chunk exists (always for the
+// k-quants; W4A16's K may end on a first one).
+template <int FMT, int PN>
+struct Pair {
+    RunRaw<FMT> raw[PN][2];
+    u32x4 x[2][4];
+
+    __device__ __forceinline__ void load(const RunSrc<FMT> (&src)[PN], const uint16_t *xrow, int p, int nch)
+    {
+        const bool second = FMT != FMT_W4 || 2 * p + 1 < nch;
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) load_pair<FMT>(src[pn], 2 * p, second, raw[pn]);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                x[h][i] = *(const u32x4 *)(xrow + (long long)kChunk * (second ? 2 * p + h : 2 * p) + 8 * i);
+    }
+};
+
+// acc[PN] += the pair's product, one run unpacked at a time; refill() issues
+// the loads that take the pair's place.  Unpacking the whole pair first, so
+// that those loads go out before the MFMAs, or holding two pairs, takes
+// registers from the waves that hide the latency: 64 tokens of 8 of 128
+// experts, Q4_K 2048 -> 768 pairs, weights rotating, 51.4 us so, 56 with two
+// single chunks in flight, 64-66 with either of those.
+template <int FMT, int DT, int PN, class F>
+__device__ __forceinline__ void multiply_pair(const Pair<FMT, PN> &q, const RunSrc<FMT> (&src)[PN], int p, int nch,
+                                              f32x4 (&acc)[PN], F refill)
 {
-    extern __shared__ f32x4 red[];  // [nw][2*RB][64]
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        if (FMT == FMT_W4 && h == 1 && 2 * p + 1 >= nch) continue;
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) {
+            u32x4 wf[4];
+            unpack_run<FMT, DT>(q.raw[pn][h], src[pn], 2 * p + h, wf);
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc[pn] = mma<DT>(wf[i], q.x[h][i], acc[pn]);
+        }
+    }
+    refill();
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where they are next needed
+}
+
+// Grid: x = groups of kMoeUpWaves/kw gate panels (inter/16 in all), y =
+// row-tile slots of 16 rows; kw waves split the K of one panel.  16-row tiles
+// serve many rows per expert too: a tile's second reading of the weights comes
+// from L2, and 32- and 64-row tiles, which unpack less, leave the chip emptier
+// (64 tokens, both of 2 to 8 experts: 13.5-18.1 us against 13.0-17.0 and
+// 17.5-24; 128 tokens, 8 of 16: 37.4 against 35.9 and 35.8).
+template <int FMT, int DT>
+__global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
+{
+    __shared__ f32x4 red[kMoeUpWaves][2][64];
     const Args &a = m.g;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     if (blockIdx.x == 0 && blockIdx.y == 0)  // the counters of k_moe_down, which runs after this launch
-        for (int i = threadIdx.x; i < m.panels; i += blockDim.x) m.arrived[i] = 0;
+        for (int i = threadIdx.x; i < m.panels; i += 64 * kMoeUpWaves) m.arrived[i] = 0;
     int e, lo, hi, t;
     // the same answer in every wave: the whole workgroup leaves together
-    if (!find_moe_tile(a, blockIdx.y, 16 * RB, lane, e, lo, hi, t)) return;
-    const int per = (blockDim.x >> 6) / a.kw, share = w % a.kw;
-    const int pairs = a.np >> 1, p = min((int)blockIdx.x * per + w / a.kw, pairs - 1);  // past the end: computed and discarded
+    if (!find_moe_tile(a, blockIdx.y, lane, e, lo, hi, t)) return;
+    const int share = w % a.kw, pairs = a.np >> 1;
+    const int own = (int)blockIdx.x * (kMoeUpWaves / a.kw) + w / a.kw;
+    const int p = min(own, pairs - 1);  // past the end: computed and discarded
     Args b = a;
     b.W = a.W + (long long)e * a.wstride;
-    const int m0 = lo + t * 16 * RB;
     RunSrc<FMT> src[2];
     src[0].init(b, p, g, col);
     src[1].init(b, pairs + p, g, col);
-    const uint16_t *xrow[RB];
-#pragma unroll
-    for (int rb = 0; rb < RB; rb++) {
-        const int tok = pair_at(m, min(m0 + 16 * rb + col, hi - 1)) / m.top_k;
-        xrow[rb] = a.X + (long long)tok * a.K + 32 * g;
+    const int i = lo + 16 * t + col;
+    const uint16_t *xrow = a.X + (long long)(pair_at(m, min(i, hi - 1)) / m.top_k) * a.K + 32 * g;
+    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const int nch = a.K / kChunk, np2 = (nch + 1) / 2;
+    const int pe = np2 * (share + 1) / a.kw;
+    int q = np2 * share / a.kw;
+    if (q < pe) {
+        Pair<FMT, 2> pr;
+        pr.load(src, xrow, q, nch);
+        for (; q + 1 < pe; q++)
+            multiply_pair<FMT, DT, 2>(pr, src, q, nch, acc, [&] { pr.load(src, xrow, q + 1, nch); });
+        multiply_pair<FMT, DT, 2>(pr, src, q, nch, acc, [] {});
     }
-    f32x4 acc[2][RB];
-#pragma unroll
-    for (int pn = 0; pn < 2; pn++)
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++) acc[pn][rb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int nch = a.K / kChunk;
-    const int cb = (int)((long long)nch * share / a.kw), ce = (int)((long long)nch * (share + 1) / a.kw);
-    stream_chunks<FMT, DT, RB, 2, DP::W, DP::X>(src, xrow, cb, ce, acc);
     if (a.kw > 1) {
-#pragma unroll
-        for (int pn = 0; pn < 2; pn++)
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++) red[(w * 2 * RB + pn * RB + rb) * 64 + lane] = acc[pn][rb];
+        red[w][0][lane] = acc[0];
+        red[w][1][lane] = acc[1];
         __syncthreads();
         if (share != 0) return;
-        for (int ww = 1; ww < a.kw; ww++)
-#pragma unroll
-            for (int pn = 0; pn < 2; pn++)
-#pragma unroll
-                for (int rb = 0; rb < RB; rb++) acc[pn][rb] += red[((w + ww) * 2 * RB + pn * RB + rb) * 64 + lane];
-    }
-    if ((int)blockIdx.x * per + w / a.kw >= pairs) return;
-#pragma unroll
-    for (int rb = 0; rb < RB; rb++) {
-        float v[4] = {acc[0][rb][0], acc[0][rb][1], acc[0][rb][2], acc[0][rb][3]};
-        act_apply(a.act, v);
-        const f32x4 u = acc[1][rb];
-        const int i = m0 + 16 * rb + col;
-        if (i < hi) {
-            u32x2 o;
-            o[0] = pack_out<DT>(v[0] * u[0], v[1] * u[1]);
-            o[1] = pack_out<DT>(v[2] * u[2], v[3] * u[3]);
-            *(u32x2 *)(m.H + (long long)i * m.inter + 16 * p + 4 * g) = o;
+        for (int ww = 1; ww < a.kw; ww++) {
+            acc[0] += red[w + ww][0][lane];
+            acc[1] += red[w + ww][1][lane];
         }
     }
+    if (own >= pairs || i >= hi) return;
+    float v[4] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3]};
+    act_apply(a.act, v);
+    u32x2 o;
+    o[0] = pack_out<DT>(v[0] * acc[1][0], v[1] * acc[1][1]);
+    o[1] = pack_out<DT>(v[2] * acc[1][2], v[3] * acc[1][3]);
+    *(u32x2 *)(m.H + (long long)i * m.inter + 16 * p + 4 * g) = o;
 }
 
 // Grid: x = panels of Y times split.  Dynamic LDS (moe_down_lds): parts *
@@ -294,12 +265,13 @@ __global__ void __launch_bounds__(512) k_moe_up(MoeArgs m)
 // it: a pair that no expert here serves adds nothing, whatever its weight
 // holds.
 //
-// A wave's work is one sequence of 128-wide chunks over its units (row tile,
-// part of K), with D chunks of weights in flight across the units' borders:
-// `front` walks the sequence where the loads are, `back` where the MFMAs are.
-template <int FMT, int DT, int D, int NW = kMoeDownWaves>
-__global__ void __launch_bounds__(64 * NW, 4) k_moe_down(MoeArgs m)
+// A wave's work is one sequence of chunk pairs over its units (row tile, part
+// of K), the next pair's loads in flight across the units' borders: `front`
+// walks the sequence where the loads are, `back` where the MFMAs are.
+template <int FMT, int DT>
+__global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
 {
+    constexpr int NW = kMoeDownWaves;
     extern __shared__ float sums[];  // [parts][pairs][16]
     __shared__ int s_tiles, s_last;
     const Args &a = m.g;
@@ -317,7 +289,7 @@ __global__ void __launch_bounds__(64 * NW, 4) k_moe_down(MoeArgs m)
         served[i] = 0;
     }
     if (w == 0) {
-        const int n = visit_tiles(a, 16, lane, [&](int e, int lo, int hi, int nb, int before) {
+        const int n = visit_tiles(a, lane, [&](int e, int lo, int hi, int nb, int before) {
             for (int j = 0; j < nb; j++) {
                 tile_e[before + j] = e;
                 tile_lo[before + j] = lo + 16 * j;
@@ -328,94 +300,68 @@ __global__ void __launch_bounds__(64 * NW, 4) k_moe_down(MoeArgs m)
         if (lane == 0) s_tiles = n;
     }
     __syncthreads();
-    const int nch = a.K / kChunk, tiles = __builtin_amdgcn_readfirstlane(s_tiles);
+    const int nch = a.K / kChunk, np2 = (nch + 1) / 2, tiles = __builtin_amdgcn_readfirstlane(s_tiles);
     // this workgroup's units: tiles slice, slice + split, ..., each in `parts` parts of K
     const int units = (tiles > slice ? (tiles - slice + m.split - 1) / m.split : 0) * m.parts;
 
     struct Cursor {
-        int u, c, ce;  // unit, next chunk, end of the unit's chunks
+        int u, c, ce;  // unit, next chunk pair, end of the unit's pairs
         int lo, hi;
     };
-    auto open = [&](Cursor &q) {  // the unit's rows and chunks
+    auto open = [&](Cursor &q) {  // the unit's rows and pairs
         const int tile = slice + m.split * (q.u / m.parts), part = q.u % m.parts;
         q.lo = __builtin_amdgcn_readfirstlane(tile_lo[tile]);
         q.hi = __builtin_amdgcn_readfirstlane(tile_hi[tile]);
-        q.c = nch * part / m.parts;
-        q.ce = nch * (part + 1) / m.parts;
+        q.c = np2 * part / m.parts;
+        q.ce = np2 * (part + 1) / m.parts;
         return __builtin_amdgcn_readfirstlane(tile_e[tile]);
     };
-    RunSrc<FMT> src;      // at the front cursor's expert
-    const uint16_t *xrow; // at the front cursor's rows
+    RunSrc<FMT> src[1];       // at the front cursor's expert
+    const uint16_t *xrow;     // at the front cursor's rows
     auto aim = [&](Cursor &q) {
         const int e = open(q);
         Args b = a;
         b.W = a.W + (long long)e * a.wstride;
-        src.init(b, panel, g, col);
+        src[0].init(b, panel, g, col);
         xrow = m.H + (long long)min(q.lo + col, q.hi - 1) * a.K + 32 * g;
     };
     if (w < units) {
-        RunRaw<FMT> raw[D];
-        u32x4 xf[D][4];
+        Pair<FMT, 1> pr;
         Cursor front{w, 0, 0, 0, 0}, back{w, 0, 0, 0, 0};
         aim(front);
         open(back);
-        int total = 0;  // chunks of this wave's sequence
-        if (m.parts == 1) {
-            total = (units - w + NW - 1) / NW * nch;
-        } else {
-            for (int u = w; u < units; u += NW)
-                total += nch * (u % m.parts + 1) / m.parts - nch * (u % m.parts) / m.parts;
-        }
-        auto fetch = [&](int d) {
-            src.load(front.c, raw[d]);
-#pragma unroll
-            for (int i = 0; i < 4; i++) xf[d][i] = *(const u32x4 *)(xrow + (long long)kChunk * front.c + 8 * i);
+        int total = 0;  // pairs of this wave's sequence
+        for (int u = w; u < units; u += NW) total += np2 * (u % m.parts + 1) / m.parts - np2 * (u % m.parts) / m.parts;
+        auto fetch = [&] {
+            pr.load(src, xrow, front.c, nch);
             if (++front.c == front.ce) {
                 front.u += NW;
                 if (front.u < units) aim(front);
             }
         };
-        f32x4 acc{0.f, 0.f, 0.f, 0.f};
-        // the branches below touch LDS only: a load from memory in one would
-        // make the next wait drain the ring
-        auto consume = [&](int d) {
-            u32x4 wf[4];
-            unpack_run<FMT, DT>(raw[d], src, back.c, wf);
-#pragma unroll
-            for (int i = 0; i < 4; i++) acc = mma<DT>(wf[i], xf[d][i], acc);
+        f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+        // the branches here touch LDS only: a load from memory in one would
+        // make the next wait drain what is in flight
+        auto close = [&] {  // the back cursor's pair is multiplied
             if (++back.c == back.ce) {
                 const int i = back.lo + col;
                 if (i < back.hi) {
                     const int pair = pair_of[i], part = back.u % m.parts;
-                    *(f32x4 *)(sums + (size_t)part * span + pair * 16 + 4 * g) = acc;
+                    *(f32x4 *)(sums + (size_t)part * span + pair * 16 + 4 * g) = acc[0];
                     if (part == 0 && g == 0) served[pair] = 1;
                 }
-                acc = f32x4{0.f, 0.f, 0.f, 0.f};
+                acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
                 back.u += NW;
                 if (back.u < units) open(back);
             }
         };
-#pragma unroll
-        for (int d = 0; d < D; d++)
-            if (d < total) fetch(d);
-        int s = 0;
-        for (; s + 2 * D <= total; s += D)
-#pragma unroll
-            for (int d = 0; d < D; d++) {
-                consume(d);
-                fetch(d);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-#pragma unroll
-        for (int d = 0; d < D; d++)
-            if (s + d < total) {
-                consume(d);
-                if (s + d + D < total) fetch(d);
-            }
-        s += D;
-#pragma unroll
-        for (int d = 0; d + 1 < D; d++)
-            if (s + d < total) consume(d);
+        fetch();
+        for (int s = 1; s < total; s++) {
+            multiply_pair<FMT, DT, 1>(pr, src, back.c, nch, acc, fetch);
+            close();
+        }
+        multiply_pair<FMT, DT, 1>(pr, src, back.c, nch, acc, [] {});
+        close();
     }
     __syncthreads();
 

@@ -101,7 +101,7 @@ struct MoeArgs {
 constexpr int kMoeUpWaves = 8;     // waves of a k_moe_up workgroup
 constexpr int kMoeDownWaves = 16;  // of a k_moe_down workgroup: at 128 VGPRs a wave it fills a CU
 template <int FMT>
-hipError_t launch_moe_up(int dtype, int rb, dim3 grid, const MoeArgs &m, hipStream_t s);
+hipError_t launch_moe_up(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s);
 template <int FMT>
 hipError_t launch_moe_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s);
 // moe_route.hip

@@ -15,9 +15,11 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <exception>
 
 #include "qgemm.h"
 
@@ -110,8 +112,8 @@ PyObject *guarded(F body)
     } catch (const Bad &) {
         PyErr_Clear();
         Py_RETURN_NONE;
-    } catch (const std::exception &e) {  // torch's allocator among them
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // torch's own, an allocation that fails among them
+        torch::translate_exception_to_python(std::current_exception());
         return nullptr;
     }
 }
@@ -159,6 +161,7 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n)
 PyObject *tuple_of(std::initializer_list<at::Tensor> ts)
 {
     PyObject *t = PyTuple_New((Py_ssize_t)ts.size());
+    if (!t) return nullptr;
     Py_ssize_t i = 0;
     for (const at::Tensor &v : ts) PyTuple_SET_ITEM(t, i++, THPVariable_Wrap(v));
     return t;

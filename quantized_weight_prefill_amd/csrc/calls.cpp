@@ -14,6 +14,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/ops/as_strided.h>
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -107,6 +109,7 @@ void holds(PyObject *w, size_t need)
 template <class F>
 PyObject *guarded(F body)
 {
+    const at::AutoDispatchBelowADInplaceOrView below;  // nothing here is differentiable
     try {
         return body();
     } catch (const Bad &) {
@@ -181,15 +184,18 @@ PyObject *moe_route(PyObject *, PyObject *const *a, Py_ssize_t n)
         const double scale = PyFloat_AsDouble(a[4]);
         if (T < 1 || k < 1 || k > E || k > 64 || renorm < 0 || (scale == -1.0 && PyErr_Occurred())) throw Bad{};
         void *s = stream_of(index);
-        const auto i32 = l.options().dtype(at::kInt);
-        const at::Tensor ids = at::empty({T, k}, i32), w = at::empty({T, k}, l.options().dtype(at::kFloat));
-        const at::Tensor offs = at::empty({E + 1}, i32), rows = at::empty({T * k}, i32);
+        // one allocation for the three integer results, one for the weights
+        const int64_t P = T * k;
+        const at::Tensor buf = at::empty({2 * P + E + 1}, l.options().dtype(at::kInt));
+        const at::Tensor w = at::empty({T, k}, l.options().dtype(at::kFloat));
+        int *p = buf.data_ptr<int>();
         int st;
         Py_BEGIN_ALLOW_THREADS
-        st = qgemm_moe_route(lp, lt, T, E, k, score, renorm, (float)scale, ids.data_ptr<int>(), w.data_ptr<float>(),
-                             offs.data_ptr<int>(), rows.data_ptr<int>(), s);
+        st = qgemm_moe_route(lp, lt, T, E, k, score, renorm, (float)scale, p, w.data_ptr<float>(), p + 2 * P, p + P, s);
         Py_END_ALLOW_THREADS
-        return st == QGEMM_OK ? tuple_of({ids, w, offs, rows}) : PyLong_FromLong(st);
+        if (st != QGEMM_OK) return PyLong_FromLong(st);
+        return tuple_of({buf.as_strided({T, k}, {k, 1}, 0), w, buf.as_strided({E + 1}, {1}, 2 * P),
+                         buf.as_strided({P}, {1}, P)});
     });
 }
 

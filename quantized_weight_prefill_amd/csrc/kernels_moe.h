@@ -163,11 +163,16 @@ struct Pair {
     RunRaw<FMT> raw[PN][2];
     u32x4 x[2][4];
 
-    __device__ __forceinline__ void load(const RunSrc<FMT> (&src)[PN], const uint16_t *xrow, int p, int nch)
+    __device__ __forceinline__ void load_w(const RunSrc<FMT> (&src)[PN], int p, int nch)
     {
         const bool second = FMT != FMT_W4 || 2 * p + 1 < nch;
 #pragma unroll
         for (int pn = 0; pn < PN; pn++) load_pair<FMT>(src[pn], 2 * p, second, raw[pn]);
+    }
+
+    __device__ __forceinline__ void load_x(const uint16_t *xrow, int p, int nch)
+    {
+        const bool second = FMT != FMT_W4 || 2 * p + 1 < nch;
 #pragma unroll
         for (int h = 0; h < 2; h++)
 #pragma unroll
@@ -228,16 +233,21 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
     src[0].init(b, p, g, col);
     src[1].init(b, pairs + p, g, col);
     const int i = lo + 16 * t + col;
-    const uint16_t *xrow = a.X + (long long)(pair_at(m, min(i, hi - 1)) / m.top_k) * a.K + 32 * g;
     f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     const int nch = a.K / kChunk, np2 = (nch + 1) / 2;
     const int pe = np2 * (share + 1) / a.kw;
     int q = np2 * share / a.kw;
     if (q < pe) {
         Pair<FMT, 2> pr;
-        pr.load(src, xrow, q, nch);
+        pr.load_w(src, q, nch);
+        __builtin_amdgcn_sched_barrier(0);  // the weights' loads go out before the token is known
+        const uint16_t *xrow = a.X + (long long)(pair_at(m, min(i, hi - 1)) / m.top_k) * a.K + 32 * g;
+        pr.load_x(xrow, q, nch);
         for (; q + 1 < pe; q++)
-            multiply_pair<FMT, DT, 2>(pr, src, q, nch, acc, [&] { pr.load(src, xrow, q + 1, nch); });
+            multiply_pair<FMT, DT, 2>(pr, src, q, nch, acc, [&] {
+                pr.load_w(src, q + 1, nch);
+                pr.load_x(xrow, q + 1, nch);
+            });
         multiply_pair<FMT, DT, 2>(pr, src, q, nch, acc, [] {});
     }
     if (a.kw > 1) {
@@ -333,7 +343,8 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
         int total = 0;  // pairs of this wave's sequence
         for (int u = w; u < units; u += NW) total += np2 * (u % m.parts + 1) / m.parts - np2 * (u % m.parts) / m.parts;
         auto fetch = [&] {
-            pr.load(src, xrow, front.c, nch);
+            pr.load_w(src, front.c, nch);
+            pr.load_x(xrow, front.c, nch);
             if (++front.c == front.ce) {
                 front.u += NW;
                 if (front.u < units) aim(front);

@@ -18,19 +18,20 @@ namespace qg {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// v * sigmoid(z): SiLU with z = v; the tanh form of GELU with z = 2 sqrt(2/pi)
-// (v + 0.044715 v^3), since (1 + tanh y) / 2 = sigmoid(2y) -- no cancellation
-// on the negative side.  Relative error about 2^-21 (v_exp_f32 and v_rcp_f32
-// are good to 1 ulp; the exponent's rounding adds |z| 2^-24).
-__device__ __forceinline__ float act_sigmoid(float v, float z)
-{
-    constexpr float kLog2e = 1.4426950408889634f;
-    return v * rcp_fast(1.0f + exp2_fast(-kLog2e * z));
-}
+// v * sigmoid(z), the exponent x = -z log2 e given: SiLU with z = v; the tanh
+// form of GELU with z = 2 sqrt(2/pi) (v + 0.044715 v^3), since (1 + tanh y) / 2
+// = sigmoid(2y) -- no cancellation on the negative side.  Relative error about
+// 2^-21 (v_exp_f32 and v_rcp_f32 are good to 1 ulp; the exponent's rounding
+// adds |z| 2^-24).  The two transcendentals are most of an activation's cost:
+// 12 us of the 196 that W4A16 2048x4096 -> 12288 takes with bias and GELU.
+__device__ __forceinline__ float times_sigmoid(float v, float x) { return v * rcp_fast(1.0f + exp2_fast(x)); }
 
-__device__ __forceinline__ float gelu_tanh_arg(float v)
+__device__ __forceinline__ float act_silu(float v) { return times_sigmoid(v, -1.4426950408889634f * v); }
+
+__device__ __forceinline__ float act_gelu_tanh(float v)
 {
-    return v * __builtin_fmaf(0.07135481282554216f * v, v, 1.5957691216057308f);
+    constexpr float a = -2.3022082f, b = -0.10294324f;  // -log2 e times 2 sqrt(2/pi) and that times 0.044715
+    return times_sigmoid(v, v * __builtin_fmaf(b * v, v, a));
 }
 
 // v * Phi(v) = v erfc(-v/sqrt 2) / 2.  erfc(x) = exp(-x^2) erfcx(x) for x >=
@@ -70,10 +71,10 @@ __device__ __forceinline__ void act_apply(int act, float (&v)[N])
         for (int j = 0; j < N; j++) v[j] = act_gelu(v[j]);
     } else if (act == QGEMM_ACT_GELU_TANH) {
 #pragma unroll
-        for (int j = 0; j < N; j++) v[j] = act_sigmoid(v[j], gelu_tanh_arg(v[j]));
+        for (int j = 0; j < N; j++) v[j] = act_gelu_tanh(v[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < N; j++) v[j] = act_sigmoid(v[j], v[j]);
+        for (int j = 0; j < N; j++) v[j] = act_silu(v[j]);
     }
 }
 
@@ -131,32 +132,36 @@ __device__ __forceinline__ void store_quad(const Args &a, int m, int n0, const f
     }
 }
 
-// What the epilogue reads for one output quad, fetched ahead of the stores
-// (Y may be the residual itself, so a load cannot move above a store by
-// itself).
-struct QuadIn {
-    u32x2 b, b2, r;
+// What the epilogue reads: the bias of an output quad's columns, and the
+// residual of the quad.  Both are fetched ahead of the stores (Y may be the
+// residual itself, so a load cannot move above a store by itself), the bias
+// once for all of a wave's rows.
+struct BiasQuad {
+    u32x2 b, b2;
 };
 
 template <int EPI>
-__device__ __forceinline__ QuadIn quad_in(const Args &a, int m, int n0)
+__device__ __forceinline__ BiasQuad bias_quad(const Args &a, int n0)
 {
-    QuadIn q;
-    q.b = q.b2 = q.r = u32x2{0u, 0u};
-    if (n0 >= a.N) return q;
+    BiasQuad q{{0u, 0u}, {0u, 0u}};
+    if (!a.bias || n0 >= a.N) return q;
     const bool quads = (a.N & 3) == 0;
-    if (a.bias) {
-        q.b = load_quad(a.bias + n0, a.N - n0, quads);
-        if constexpr (EPI == EP_GATED) q.b2 = load_quad(a.bias + a.N + n0, a.N - n0, quads);
-    }
-    if (a.res && m < a.M) q.r = load_quad(a.res + (long long)m * a.N + n0, a.N - n0, quads);
+    q.b = load_quad(a.bias + n0, a.N - n0, quads);
+    if constexpr (EPI == EP_GATED) q.b2 = load_quad(a.bias + a.N + n0, a.N - n0, quads);
     return q;
+}
+
+__device__ __forceinline__ u32x2 res_quad(const Args &a, int m, int n0)
+{
+    if (!a.res || n0 >= a.N || m >= a.M) return u32x2{0u, 0u};
+    return load_quad(a.res + (long long)m * a.N + n0, a.N - n0, (a.N & 3) == 0);
 }
 
 // One output quad: v holds acc (EP_LIN) or the gate's acc with u the up
 // projection's (EP_GATED).
 template <int DT, int EPI>
-__device__ __forceinline__ void finish_quad(const Args &a, int m, int n0, float (&v)[4], float (&u)[4], const QuadIn &q)
+__device__ __forceinline__ void finish_quad(const Args &a, int m, int n0, float (&v)[4], float (&u)[4], const BiasQuad &q,
+                                            u32x2 res)
 {
     if (n0 >= a.N || m >= y_rows(a)) return;
     if (m < a.M) {
@@ -167,7 +172,7 @@ __device__ __forceinline__ void finish_quad(const Args &a, int m, int n0, float 
 #pragma unroll
             for (int j = 0; j < 4; j++) v[j] *= u[j];
         }
-        if (a.res) add_quad<DT>(v, q.r);
+        if (a.res) add_quad<DT>(v, res);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; j++) v[j] = 0.0f;
@@ -190,9 +195,36 @@ template <int DT, int EPI>
 __device__ __forceinline__ void store_block_ep(const Args &a, f32x4 v, f32x4 u, int m_base, int n_base, int lane)
 {
     const int m = m_base + (lane & 15), n0 = out_col<EPI>(n_base) + 4 * (lane >> 4);
-    const QuadIn q = quad_in<EPI>(a, m, n0);
+    const BiasQuad q = bias_quad<EPI>(a, n0);
+    const u32x2 res = res_quad(a, m, n0);
     float g[4] = {v[0], v[1], v[2], v[3]}, w[4] = {u[0], u[1], u[2], u[3]};
-    finish_quad<DT, EPI>(a, m, n0, g, w, q);
+    finish_quad<DT, EPI>(a, m, n0, g, w, q, res);
+}
+
+// A wave's PB x RB accumulators of 16x16, tile panels from column n_base,
+// rows m_base + 16 rb.
+template <int DT, int EPI, int PB, int RB>
+__device__ __forceinline__ void store_wave16_ep(const Args &a, const f32x4 (&acc)[PB][RB], int m_base, int n_base,
+                                                int lane)
+{
+    constexpr int PS = EPI == EP_GATED ? 2 : 1, O = PB / PS;  // output panels
+    const int n = out_col<EPI>(n_base) + 4 * (lane >> 4);
+    BiasQuad bias[O];
+#pragma unroll
+    for (int o = 0; o < O; o++) bias[o] = bias_quad<EPI>(a, n + 16 * o);
+#pragma unroll
+    for (int rb = 0; rb < RB; rb++) {
+        const int m = m_base + 16 * rb + (lane & 15);
+        u32x2 res[O];
+#pragma unroll
+        for (int o = 0; o < O; o++) res[o] = res_quad(a, m, n + 16 * o);
+#pragma unroll
+        for (int o = 0; o < O; o++) {
+            const f32x4 g = acc[PS * o][rb], w = acc[PS * o + PS - 1][rb];
+            float v[4] = {g[0], g[1], g[2], g[3]}, u[4] = {w[0], w[1], w[2], w[3]};
+            finish_quad<DT, EPI>(a, m, n + 16 * o, v, u, bias[o], res[o]);
+        }
+    }
 }
 
 // A wave's CB x RB accumulators of 32x32 (store_block32's layout), rows m_base
@@ -203,27 +235,31 @@ __device__ __forceinline__ void store_wave32_ep(const Args &a, const f32x16 (&ac
                                                 int lane)
 {
     constexpr int Q = EPI == EP_GATED ? 2 : 4;  // output quads per block and lane
+    auto col = [&](int cb, int q) { return out_col<EPI>(n_base + 32 * cb) + 8 * q + 4 * (lane >> 5); };
+    BiasQuad bias[CB][Q];
+#pragma unroll
+    for (int cb = 0; cb < CB; cb++)
+#pragma unroll
+        for (int q = 0; q < Q; q++) bias[cb][q] = bias_quad<EPI>(a, col(cb, q));
 #pragma unroll
     for (int rb = 0; rb < RB; rb++) {
         const int m = m_base + 32 * rb + (lane & 31);
-        QuadIn in[CB][Q];
+        u32x2 res[CB][Q];
 #pragma unroll
         for (int cb = 0; cb < CB; cb++)
 #pragma unroll
-            for (int q = 0; q < Q; q++)
-                in[cb][q] = quad_in<EPI>(a, m, out_col<EPI>(n_base + 32 * cb) + 8 * q + 4 * (lane >> 5));
+            for (int q = 0; q < Q; q++) res[cb][q] = res_quad(a, m, col(cb, q));
 #pragma unroll
         for (int cb = 0; cb < CB; cb++)
 #pragma unroll
             for (int q = 0; q < Q; q++) {
-                const int n0 = out_col<EPI>(n_base + 32 * cb) + 8 * q + 4 * (lane >> 5);
                 float v[4], u[4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     v[j] = acc[cb][rb][4 * q + j];
                     u[j] = EPI == EP_GATED ? acc[cb][rb][4 * (q + 4 - Q) + j] : 0.0f;
                 }
-                finish_quad<DT, EPI>(a, m, n0, v, u, in[cb][q]);
+                finish_quad<DT, EPI>(a, m, col(cb, q), v, u, bias[cb][q], res[cb][q]);
             }
     }
 }

@@ -448,15 +448,15 @@ __global__ void __launch_bounds__(64 * NWM * NWN) k_stream(Args a)
         chunk(c + 1, 1, raw2, raw);
     }
     if (c < c_hi) chunk(c, 0, raw, raw2);
-    constexpr int PS = EPI == EP_GATED ? 2 : 1;  // tile panels behind one output panel
+    if constexpr (EPI != EP_NONE) {
+        store_wave16_ep<DT, EPI, WPB, RBW>(a, acc, m0, 16 * (p0 + wn * WPB), lane);
+        return;
+    }
 #pragma unroll
-    for (int pb = 0; pb < WPB; pb += PS)
+    for (int pb = 0; pb < WPB; pb++)
 #pragma unroll
-        for (int rb = 0; rb < RBW; rb++) {
-            const int nb = 16 * (p0 + wn * WPB + pb);
-            if constexpr (EPI == EP_NONE) store_block<DT>(a, acc[pb][rb], m0 + 16 * rb, nb, lane);
-            else store_block_ep<DT, EPI>(a, acc[pb][rb], acc[pb + PS - 1][rb], m0 + 16 * rb, nb, lane);
-        }
+        for (int rb = 0; rb < RBW; rb++)
+            store_block<DT>(a, acc[pb][rb], m0 + 16 * rb, 16 * (p0 + wn * WPB + pb), lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(256) k_splitk_reduce_ep(Args a)
             }
         }
     }
-    finish_quad<DT, EP_LIN>(a, m, n0, v, u, quad_in<EP_LIN>(a, m, n0));
+    finish_quad<DT, EP_LIN>(a, m, n0, v, u, bias_quad<EP_LIN>(a, n0), res_quad(a, m, n0));
 }
 
 template <int FMT, int DT, int RB, int PN, int XL, int EPI>

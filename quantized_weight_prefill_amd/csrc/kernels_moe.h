@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
             const int t = q >> 2, n = 4 * (q & 3), n0 = 16 * panel + n;
             float v[4];
             token_sum(t, n, v);
-            finish_quad<DT, EP_LIN>(y, t, n0, v, un, quad_in<EP_LIN>(y, t, n0));
+            finish_quad<DT, EP_LIN>(y, t, n0, v, un, BiasQuad{}, res_quad(y, t, n0));
         }
         return;
     }
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
 #pragma unroll
             for (int c = 0; c < 4; c++) v[c] += x[c];
         }
-        finish_quad<DT, EP_LIN>(y, t, n0, v, un, quad_in<EP_LIN>(y, t, n0));
+        finish_quad<DT, EP_LIN>(y, t, n0, v, un, BiasQuad{}, res_quad(y, t, n0));
     }
 }
 

@@ -581,11 +581,10 @@ int gemm(int fmt, int rung, const void *X, const void *W, void *Y, long long M, 
 bool known_act(int act) { return act >= QGEMM_ACT_NONE && act <= QGEMM_ACT_GELU_TANH; }
 
 // The plan over the packed columns (2N when gated), by the products' ladder
-// but for one rule: the epilogue adds the same few loads and stores per output
-// to every rung.  The
-// gated form has no rung that splits K across workgroups (its partial sums
-// would pair columns of two tiles): where the ladder picks one, the best of
-// the others serves.
+// but for the two rules below: the epilogue adds the same few loads and stores
+// per output to every rung.  The gated form has no rung that splits K across
+// workgroups (its partial sums would pair columns of two tiles): where the
+// ladder picks one, the best of the others serves.
 int linear_plan(int fmt, int rung, int xl, long long M, long long N, long long K, long long group, int gated, int dtype,
                 Plan &pl)
 {
@@ -608,6 +607,13 @@ int linear_plan(int fmt, int rung, int xl, long long M, long long N, long long K
     if (rung < 0 && !gated && xl == X_ROW && r == RUNG_SKINNY_N && fmt != FMT_W4 && m > 32 && m <= 64 && nt > 64 &&
         (nt + 15) / 16 <= kCUs)
         r = RUNG_SMALL_M;
+    // Up to four panels: the products give one wave all of them; one panel per
+    // wave spreads the weights over as many CUs, at the price of reading X
+    // once per panel (Q6_K 12288 -> 64: 1 and 16 rows 10.9 against 27.2 and
+    // 28.1 us, 64 rows 20.8 against 28.4; W4A16 4096 -> 64, 64 rows 9.6 against
+    // 10.0; Q6_K 12288 -> 32, 16 rows 10.9 against 16.2, but 33 rows 17.5
+    // against 16.4, so two panels change over at 16 rows).
+    if (rung < 0 && !gated && r == RUNG_SKINNY_N && nt <= 64 && (m <= 16 || (m <= 64 && nt > 32))) r = RUNG_SMALL_M;
     if (gated && (r == RUNG_M64_SK || r == RUNG_M768N64_SK)) {
         if (rung >= 0) return QGEMM_ERR_FORMAT;
         r = r == RUNG_M64_SK ? round_model_rung(fmt, m, nt, K, xl, dtype) : large_tile_xf(fmt, m, nt, K);
@@ -795,10 +801,11 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.arrived = (int *)(m.partial + (long long)m.panels * m.split * T * 16);
 
     // gate and up: K split over waves while the grid holds fewer than 4096 of
-    // them and each keeps four chunks (weights rotating: one token, Q4_K 2048
-    // -> 768, 7.5 us split four ways, 8.1 two, 18 unsplit; seven tokens, W4A16
-    // 2048 -> 1408, 17.3 two ways, 18.6 unsplit, 19.2 four; 96 tokens, 4 of 16
-    // experts, 19.7 four ways, 22.2 unsplit)
+    // them and each keeps a chunk pair (weights rotating: one token, Q4_K 2048
+    // -> 768, 7.5 us split eight ways, 8.1 two, 18 unsplit; Q6_K 2304 -> 256,
+    // 7.0 eight ways, 10.2 four; seven tokens, W4A16 2048 -> 1408, 17.3 two
+    // ways, 18.6 unsplit, 19.2 four; 96 tokens, 4 of 16 experts, 19.7 four
+    // ways, 22.2 unsplit)
     m.g = make_args(fu, X, Wu, nullptr, P, 2 * I, H, group, has_zp);
     m.g.offs = offs;
     m.g.E = (int)E;
@@ -806,7 +813,7 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.g.act = act;
     const int nch = (int)(H / kChunk);
     m.g.kw = 1;
-    while (m.g.kw < kMoeUpWaves && tiles * (I / 16) * m.g.kw < 4096 && nch >= 8 * m.g.kw) m.g.kw *= 2;
+    while (m.g.kw < kMoeUpWaves && tiles * (I / 16) * m.g.kw < 4096 && nch >= 4 * m.g.kw) m.g.kw *= 2;
     const int per = kMoeUpWaves / m.g.kw;  // gate panels per workgroup
     const dim3 gu((unsigned)((I / 16 + per - 1) / per), (unsigned)tiles, 1);
     hipError_t e = launch_up(fu, dtype, gu, m, (hipStream_t)stream);

@@ -420,11 +420,14 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
     for (int q = tid; q < m.T * 4; q += 64 * NW) {
         const int t = q >> 2, n0 = 16 * panel + 4 * (q & 3);
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < m.split; s++) {
-            float x[4];
-            load_agent(all + (long long)s * m.T * 16 + 4 * q, x);
+        for (int s = 0; s < m.split; s += 4) {  // four in flight: each is a trip past the L2
+            float x[4][4];
 #pragma unroll
-            for (int c = 0; c < 4; c++) v[c] += x[c];
+            for (int i = 0; i < 4; i++) load_agent(all + (long long)min(s + i, m.split - 1) * m.T * 16 + 4 * q, x[i]);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int c = 0; c < 4; c++) v[c] = s + i < m.split ? v[c] + x[i][c] : v[c];
         }
         finish_quad<DT, EP_LIN>(y, t, n0, v, un, BiasQuad{}, res_quad(y, t, n0));
     }

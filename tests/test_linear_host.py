@@ -73,6 +73,8 @@ def test_plain_ladder_is_the_products(fmt, layout):
                 if (layout == qg.X_ROW and fmt != "w4a16" and 32 < M <= 64 and 64 < N <= 4096
                         and want["name"] == "direct-skinny-n"):
                     assert got["name"] == "direct-small-m" and got["rows"] >= M  # all rows per wave, one panel
+                elif N <= 64 and (M <= 16 or (M <= 64 and N > 32)):
+                    assert got["name"] == "direct-small-m" and got["cols"] == 16  # a panel per wave, not all of them
                 else:
                     assert got == want
                 g = qg.linear_select_rung(fmt, M, 16 * -(-N // 16), K, True, dt, layout)

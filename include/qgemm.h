@@ -502,8 +502,12 @@ int qgemm_moe_group(const int32_t *ids, int64_t T, int64_t E, int64_t top_k, int
  * expert the layer is a stream of the active experts' packed weights, the
  * dequant-scratch post's 0.5625 bytes per Q4_K weight, "The two passes hiding
  * inside one matmul"):
- *   h[p] = RN_t( act(x_t . Wg_e) * (x_t . Wu_e) )            p = t*top_k + j, e its expert
+ *   h[p] = act(x_t . Wg_e) * (x_t . Wu_e)                    p = t*top_k + j, e its expert
  *   Y[t] = RN_t( residual[t] + sum_j weights[t][j] * (h[p] . Wd_e) )
+ * h is held to the type's precision at least: as RN_t(h), and in the row tiles
+ * of at most eight of an expert's pairs (as at decode sizes) with what
+ * that rounding left beside it, twice the type's bits.  Where |h| is beyond the
+ * type's range it is infinite.
  * X [T][hidden], Y and residual (may be NULL) [T][hidden], all row-major of
  * type dtype.  Wup: E packed weights of 2*inter columns over K = hidden (the
  * gate's columns, then the up projection's), format_up; Wdown: E packed
@@ -516,8 +520,9 @@ int qgemm_moe_group(const int32_t *ids, int64_t T, int64_t E, int64_t top_k, int
  * give wrong rows).  h and the partial sums of Y go through `workspace`
  * (device, 16-byte aligned, at least qgemm_moe_workspace_bytes, of any
  * contents, which the call overwrites); everything after h stays in fp32 up to
- * Y's one rounding, in an order that depends on the sizes alone.  Y may be the residual or X itself when X is not
- * needed afterwards; any other overlap is not allowed.
+ * Y's one rounding, in an order that depends on the sizes and the routing
+ * alone.  Y may be the residual, or X itself when X is not needed afterwards;
+ * any other overlap is not allowed.
  * T * top_k is at most QGEMM_MOE_MAX_PAIRS (above it the grouped products
  * above are the path); inter is a multiple of format_down's K step, hidden of
  * format_up's.  T = 0 is a no-op.  Errors as qgemm_grouped, plus

@@ -749,17 +749,23 @@ hipError_t launch_up(int fmt, int dtype, dim3 grid, const MoeArgs &m, hipStream_
     return fmt == FMT_Q6K ? launch_moe_up<FMT_Q6K>(dtype, grid, m, s) : launch_moe_up<FMT_W4>(dtype, grid, m, s);
 }
 
-hipError_t launch_down(int fmt, int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
+hipError_t launch_down(int fmt, int dtype, int pn, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
-    if (fmt == FMT_Q4K) return launch_moe_down<FMT_Q4K>(dtype, grid, m, s);
-    return fmt == FMT_Q6K ? launch_moe_down<FMT_Q6K>(dtype, grid, m, s) : launch_moe_down<FMT_W4>(dtype, grid, m, s);
+    if (fmt == FMT_Q4K) return launch_moe_down<FMT_Q4K>(dtype, pn, grid, m, s);
+    return fmt == FMT_Q6K ? launch_moe_down<FMT_Q6K>(dtype, pn, grid, m, s)
+                          : launch_moe_down<FMT_W4>(dtype, pn, grid, m, s);
 }
 
-// Workgroups of the down product that share a 16-column panel of Y: one
-// workgroup of sixteen waves for each CU (64 tokens, Q6_K 768 -> 2048: 44.0 us
-// with two, 44.7 with four of eight waves; seven tokens, W4A16 1408 -> 2048:
-// 14.0 with two, 19.6 with one; one token 7.8 against 9.4).
-int moe_split(long long H) { return (int)std::min(8LL, std::max(1LL, (long long)kCUs / ((H + 15) / 16))); }
+// Workgroups of the down product that share a strip of Y (pn 16-column
+// panels): one workgroup of sixteen waves for each CU (64 tokens, Q6_K 768 ->
+// 2048: 44.0 us with two on a panel, 44.7 with four of eight waves; seven
+// tokens, W4A16 1408 -> 2048: 14.0 with two, 19.6 with one; one token 7.8
+// against 9.4).
+int moe_split(long long H, int pn)
+{
+    const long long strips = (H + 16 * pn - 1) / (16 * pn);
+    return (int)std::min(8LL, std::max(1LL, kCUs / strips));
+}
 
 int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const float *wts, const int32_t *offs,
         const int32_t *rows, const void *res, void *Y, long long T, long long k, long long E, long long H, long long I,
@@ -783,7 +789,7 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
         return QGEMM_ERR_ALIGN;
     if (!ws || ws_bytes < qgemm_moe_workspace_bytes(T, k, H, I)) return QGEMM_ERR_SIZE;
     if (!aligned16(ws)) return QGEMM_ERR_ALIGN;
-    if (!launch_fits(I / 16, 64 * kMoeUpWaves) || !launch_fits((H + 15) / 16 * 8, 64 * kMoeDownWaves))
+    if (!launch_fits(I / 16, 64 * kMoeUpWaves) || !launch_fits(H / 16 * 8, 64 * kMoeDownWaves))
         return QGEMM_ERR_SHAPE;
     const long long P = T * k;
     MoeArgs m{};
@@ -794,11 +800,19 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.top_k = (int)k;
     m.inter = (int)I;
 
-    const long long tiles = std::min(P, (P + 15) / 16 + E);  // a bound on the 16-row tiles
-    m.panels = (int)((H + 15) / 16);
-    m.split = moe_split(H);
-    m.partial = (float *)(m.H + P * I);
-    m.arrived = (int *)(m.partial + (long long)m.panels * m.split * T * 16);
+    const long long tiles = moe_tiles(P, E);
+    // two panels per workgroup of the down product where the row tiles give
+    // its waves two each: h is then read once for both panels, by half as many
+    // workgroups, each over half the tiles (128 tokens, 8 of 16 experts, 768 ->
+    // 2048: 26.9 against 34.9 us; 64 tokens, 8 of 128: 49.0 against 54.2); below
+    // that one panel, which spreads the weights over more waves (one token 8.2
+    // against 9.0; 16 tokens, 2 of 8, 1024 -> 4096: 8.8 against 9.8; 256 tokens,
+    // 4 of 8, 1024 -> 1024: 28.7 against 29.9)
+    const int pn = tiles > 2 * kMoeDownWaves * moe_split(H, 1) ? 2 : 1;
+    m.strips = (int)(H / (16 * pn));
+    m.split = moe_split(H, pn);
+    m.partial = (float *)(m.H + 2 * P * I);
+    m.arrived = (int *)(m.partial + (long long)m.split * T * H);
 
     // gate and up: K split over waves while the grid holds fewer than 4096 of
     // them and each keeps a chunk pair (weights rotating: one token, Q4_K 2048
@@ -827,7 +841,7 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.g.wstride = sd;
     m.g.res = (const uint16_t *)res;
     m.parts = (int)std::max(1LL, std::min({kMoeDownWaves * m.split / tiles, (I / kChunk + 1) / 2, 1024 / P, 8LL}));
-    e = launch_down(fd, dtype, dim3((unsigned)(m.panels * m.split), 1, 1), m, (hipStream_t)stream);
+    e = launch_down(fd, dtype, pn, dim3((unsigned)(m.strips * m.split), 1, 1), m, (hipStream_t)stream);
     return launch_status(e, "moe down");
 }
 
@@ -1298,16 +1312,16 @@ int qgemm_moe(int format_up, int format_down, const void *X, const void *Wup, co
                group_size, has_zp, act, dtype, workspace, workspace_bytes, stream);
 }
 
-// h [pairs][inter], the panels' partial sums and their arrival counters; inter
-// and hidden are multiples of 128 in every legal call, so each part starts
-// 16-byte aligned.
+// h [pairs][2][inter], the strips' partial sums (two panels to a strip have the
+// larger split) and their arrival counters; inter and hidden are multiples of
+// 128 in every legal call, so each part starts 16-byte aligned.
 size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64_t inter)
 {
     if (T < 1 || top_k < 1 || T > QGEMM_MOE_MAX_PAIRS || top_k > QGEMM_MOE_MAX_PAIRS || T * top_k > QGEMM_MOE_MAX_PAIRS ||
         inter < kChunk || inter > INT32_MAX / 2 || inter % kChunk != 0 || hidden < kChunk || hidden > INT32_MAX ||
         hidden % kChunk != 0)
         return 0;
-    return 2 * (size_t)(T * top_k) * (size_t)inter + 4 * (size_t)moe_split(hidden) * (size_t)(T * hidden) +
+    return 4 * (size_t)(T * top_k) * (size_t)inter + 4 * (size_t)moe_split(hidden, 2) * (size_t)(T * hidden) +
            4 * (size_t)(hidden / 16);
 }
 

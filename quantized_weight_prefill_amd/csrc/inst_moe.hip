@@ -18,16 +18,18 @@ hipError_t launch_moe_up(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
 }
 
 template <int FMT>
-hipError_t launch_moe_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
+hipError_t launch_moe_down(int dtype, int pn, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
     const dim3 block(64 * kMoeDownWaves);
-    const size_t lds = moe_down_lds(m.g.M, m.g.E, m.parts);
-    if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16>), grid, block, lds, s, m);
-    else hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16>), grid, block, lds, s, m);
+    const size_t lds = moe_down_lds(m.g.M, m.g.E, m.parts, pn);
+    if (dtype == DT_F16 && pn == 1) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16, 1>), grid, block, lds, s, m);
+    else if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16, 2>), grid, block, lds, s, m);
+    else if (pn == 1) hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16, 1>), grid, block, lds, s, m);
+    else hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16, 2>), grid, block, lds, s, m);
     return hipGetLastError();
 }
 
 template hipError_t launch_moe_up<QG_FMT>(int, dim3, const MoeArgs &, hipStream_t);
-template hipError_t launch_moe_down<QG_FMT>(int, dim3, const MoeArgs &, hipStream_t);
+template hipError_t launch_moe_down<QG_FMT>(int, int, dim3, const MoeArgs &, hipStream_t);
 
 }  // namespace qg

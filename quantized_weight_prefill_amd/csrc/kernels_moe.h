@@ -1,6 +1,6 @@
 // kernels_moe.h -- a mixture-of-experts layer for a few tokens, two launches:
 //
-//   h[i]  = RN_t( act(x_t . Wg_e) * (x_t . Wu_e) )            k_moe_up
+//   h[i]  = act(x_t . Wg_e) * (x_t . Wu_e)                    k_moe_up
 //   Y[t]  = RN_t( r[t] + sum_j w[t][j] * (h[i(t,j)] . Wd_e) ) k_moe_down
 //
 // for the pairs i of tokens t and experts e in the order of `rows` (grouped by
@@ -13,15 +13,22 @@
 //     one row tile of one expert and a share of K; the kw waves of a share
 //     add up through LDS.  It gathers x by the pair's token, so no gathered
 //     copy is made.
-//   * k_moe_down: a workgroup owns one 16-column panel of Y for all tokens and
-//     every split-th row tile of the experts; its waves take those in turn
-//     (in parts of K when they are few), leave each pair's 16 outputs in LDS
-//     in fp32, and the workgroup adds them per token in slot order with the
-//     routing weights.  With split > 1 the panel's workgroups leave those
+//   * k_moe_down: a workgroup owns one or two 16-column panels of Y for all
+//     tokens and every split-th row tile of the experts; its waves take those
+//     in turn (in parts of K when they are few), leave each pair's outputs in
+//     LDS in fp32, and the workgroup adds them per token in slot order with
+//     the routing weights.  With split > 1 the panels' workgroups leave those
 //     sums in memory, and the last of them to arrive adds them in order: no
 //     floating-point atomics, and a result that does not depend on timing.
-// h is rounded to the operand type because the second product's MFMA takes
-// it so; the sum over a token's experts stays in fp32 until the one store.
+// h goes to memory as its rounding to the operand type, which the second
+// product's MFMA takes, and as what that rounding left.  A tile of at most
+// eight rows multiplies both, the second in the eight MFMA columns that would
+// be idle: h then has twice the type's bits, and the layer's error is that of
+// Y's rounding alone.  A fuller tile takes the rounding alone: both parts of
+// its rows would double the down product's MFMAs and its reads of h (128
+// tokens, 8 of 16 experts: 34.5 us for the kernel with, 57-59, in either tile
+// height, against 34.5 without).  The sum over a token's experts stays in fp32
+// until the one store.
 #pragma once
 
 #include <algorithm>
@@ -31,10 +38,10 @@
 
 namespace qg {
 
-inline size_t moe_down_lds(long long pairs, long long E, int parts)
+inline size_t moe_down_lds(long long pairs, long long E, int parts, int pn)
 {
-    const long long slots = std::min(pairs, (pairs + 15) / 16 + E);
-    return (size_t)(parts * pairs * 64 + slots * 12 + pairs * 5);
+    const long long slots = moe_tiles(pairs, E);
+    return (size_t)(parts * pairs * 64 * pn + slots * 12 + pairs * 5);
 }
 
 // Inclusive scans over the wave in DPP steps: row shifts inside rows of 16
@@ -154,6 +161,20 @@ __device__ __forceinline__ int pair_at(const MoeArgs &m, int i)
     return (int)min((unsigned)m.rows[i], (unsigned)(m.g.M - 1));
 }
 
+// h goes to memory as two numbers of the operand type: its rounding, and what
+// the rounding left, scaled up so that fp16's subnormals do not cut it short
+// (fp16's remainder is at most 2^-11 of h, bf16's 2^-8: scaled it is no larger
+// than h).  Where h is beyond the type's range the rounding is infinite and
+// nothing is left.
+template <int DT> constexpr float kLowScale = DT == DT_F16 ? 2048.0f : 256.0f;
+
+template <int DT>
+__device__ __forceinline__ float low_part(float v, uint32_t bits16)
+{
+    const float hi = widen16<DT>(bits16);
+    return fabsf(hi) < __builtin_inff() ? (v - hi) * kLowScale<DT> : 0.0f;
+}
+
 // Raw bytes and activations of one chunk pair: PN panels, one row per column
 // lane.  The k-quants' block header serves both chunks, so a pair costs one
 // header load; second: the pair's second chunk exists (always for the
@@ -220,7 +241,7 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     if (blockIdx.x == 0 && blockIdx.y == 0)  // the counters of k_moe_down, which runs after this launch
-        for (int i = threadIdx.x; i < m.panels; i += 64 * kMoeUpWaves) m.arrived[i] = 0;
+        for (int i = threadIdx.x; i < m.strips; i += 64 * kMoeUpWaves) m.arrived[i] = 0;
     int e, lo, hi, t;
     // the same answer in every wave: the whole workgroup leaves together
     if (!find_moe_tile(a, blockIdx.y, lane, e, lo, hi, t)) return;
@@ -263,34 +284,38 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
     if (own >= pairs || i >= hi) return;
     float v[4] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3]};
     act_apply(a.act, v);
-    u32x2 o;
-    o[0] = pack_out<DT>(v[0] * acc[1][0], v[1] * acc[1][1]);
-    o[1] = pack_out<DT>(v[2] * acc[1][2], v[3] * acc[1][3]);
-    *(u32x2 *)(m.H + (long long)i * m.inter + 16 * p + 4 * g) = o;
+#pragma unroll
+    for (int c = 0; c < 4; c++) v[c] *= acc[1][c];
+    uint16_t *h = m.H + 2 * (long long)i * m.inter + 16 * p + 4 * g;
+    const u32x2 o = {pack_out<DT>(v[0], v[1]), pack_out<DT>(v[2], v[3])};
+    *(u32x2 *)h = o;
+#pragma unroll
+    for (int c = 0; c < 4; c++) v[c] = low_part<DT>(v[c], o[c >> 1] >> (16 * (c & 1)));
+    *(u32x2 *)(h + m.inter) = u32x2{pack_out<DT>(v[0], v[1]), pack_out<DT>(v[2], v[3])};
 }
 
-// Grid: x = panels of Y times split.  Dynamic LDS (moe_down_lds): parts *
-// pairs * 16 floats, the row tiles (expert, first row, end of the expert's
-// rows), the sorted pairs, and a flag per pair that some expert has computed
-// it: a pair that no expert here serves adds nothing, whatever its weight
-// holds.
+// Grid: x = strips of Y (PN panels each) times split.  Dynamic LDS
+// (moe_down_lds): parts * pairs * 16 PN floats, the row tiles (expert, first
+// row, end of the expert's rows), the sorted pairs, and a flag per pair that
+// some expert has computed it: a pair that no expert here serves adds nothing,
+// whatever its weight holds.
 //
 // A wave's work is one sequence of chunk pairs over its units (row tile, part
 // of K), the next pair's loads in flight across the units' borders: `front`
 // walks the sequence where the loads are, `back` where the MFMAs are.
-template <int FMT, int DT>
+template <int FMT, int DT, int PN>
 __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
 {
-    constexpr int NW = kMoeDownWaves;
-    extern __shared__ float sums[];  // [parts][pairs][16]
+    constexpr int NW = kMoeDownWaves, CW = 16 * PN, QW = 4 * PN;  // columns and quads of a strip's row
+    extern __shared__ float sums[];  // [parts][pairs][CW]
     __shared__ int s_tiles, s_last;
     const Args &a = m.g;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4;
-    const int P = a.M, span = P * 16;
-    const int panel = blockIdx.x / m.split, slice = blockIdx.x - panel * m.split;
+    const int P = a.M, span = P * CW;
+    const int strip = blockIdx.x / m.split, slice = blockIdx.x - strip * m.split;
     int *tile_e = (int *)(sums + (size_t)m.parts * span);
-    const int slots = min(P, (P + 15) / 16 + a.E);  // a bound on the row tiles
+    const int slots = (int)moe_tiles(P, a.E);
     int *tile_lo = tile_e + slots, *tile_hi = tile_lo + slots;
     int *pair_of = tile_hi + slots;
     uint8_t *served = (uint8_t *)(pair_of + P);
@@ -326,17 +351,20 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
         q.ce = np2 * (part + 1) / m.parts;
         return __builtin_amdgcn_readfirstlane(tile_e[tile]);
     };
-    RunSrc<FMT> src[1];       // at the front cursor's expert
+    RunSrc<FMT> src[PN];      // at the front cursor's expert
     const uint16_t *xrow;     // at the front cursor's rows
     auto aim = [&](Cursor &q) {
         const int e = open(q);
         Args b = a;
         b.W = a.W + (long long)e * a.wstride;
-        src[0].init(b, panel, g, col);
-        xrow = m.H + (long long)min(q.lo + col, q.hi - 1) * a.K + 32 * g;
+#pragma unroll
+        for (int pn = 0; pn < PN; pn++) src[pn].init(b, PN * strip + pn, g, col);
+        const bool few = q.hi - q.lo <= 8;  // columns 8..15 take the low parts of the rows in 0..7
+        const int r = few ? col & 7 : col;
+        xrow = m.H + (2 * (long long)min(q.lo + r, q.hi - 1) + (few ? col >> 3 : 0)) * a.K + 32 * g;
     };
     if (w < units) {
-        Pair<FMT, 1> pr;
+        Pair<FMT, PN> pr;
         Cursor front{w, 0, 0, 0, 0}, back{w, 0, 0, 0, 0};
         aim(front);
         open(back);
@@ -350,28 +378,39 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
                 if (front.u < units) aim(front);
             }
         };
-        f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+        f32x4 acc[PN] = {};
         // the branches here touch LDS only: a load from memory in one would
         // make the next wait drain what is in flight
         auto close = [&] {  // the back cursor's pair is multiplied
             if (++back.c == back.ce) {
                 const int i = back.lo + col;
+                if (back.hi - back.lo <= 8) {
+#pragma unroll
+                    for (int c = 0; c < QW; c++) {
+                        const float y = acc[c >> 2][c & 3];
+                        const int low = dpp_from<0x128, 0xF>(__builtin_bit_cast(int, y), 0);  // row_ror:8
+                        acc[c >> 2][c & 3] = __builtin_fmaf(__builtin_bit_cast(float, low), 1.0f / kLowScale<DT>, y);
+                    }
+                }
                 if (i < back.hi) {
                     const int pair = pair_of[i], part = back.u % m.parts;
-                    *(f32x4 *)(sums + (size_t)part * span + pair * 16 + 4 * g) = acc[0];
+#pragma unroll
+                    for (int pn = 0; pn < PN; pn++)
+                        *(f32x4 *)(sums + (size_t)part * span + pair * CW + 16 * pn + 4 * g) = acc[pn];
                     if (part == 0 && g == 0) served[pair] = 1;
                 }
-                acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int pn = 0; pn < PN; pn++) acc[pn] = f32x4{0.f, 0.f, 0.f, 0.f};
                 back.u += NW;
                 if (back.u < units) open(back);
             }
         };
         fetch();
         for (int s = 1; s < total; s++) {
-            multiply_pair<FMT, DT, 1>(pr, src, back.c, nch, acc, fetch);
+            multiply_pair<FMT, DT, PN>(pr, src, back.c, nch, acc, fetch);
             close();
         }
-        multiply_pair<FMT, DT, 1>(pr, src, back.c, nch, acc, [] {});
+        multiply_pair<FMT, DT, PN>(pr, src, back.c, nch, acc, [] {});
         close();
     }
     __syncthreads();
@@ -382,8 +421,8 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
         for (int j = 0; j < m.top_k; j++) {
             const int p = t * m.top_k + j;
             if (!served[p]) continue;
-            f32x4 s = *(const f32x4 *)(sums + p * 16 + n);
-            for (int k = 1; k < m.parts; k++) s += *(const f32x4 *)(sums + (size_t)k * span + p * 16 + n);
+            f32x4 s = *(const f32x4 *)(sums + p * CW + n);
+            for (int k = 1; k < m.parts; k++) s += *(const f32x4 *)(sums + (size_t)k * span + p * CW + n);
             const float wt = m.wts[p];
 #pragma unroll
             for (int c = 0; c < 4; c++) v[c] = __builtin_fmaf(wt, s[c], v[c]);
@@ -393,18 +432,18 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
     y.M = m.T;
     float un[4];
     if (m.split == 1) {
-        for (int q = tid; q < m.T * 4; q += 64 * NW) {
-            const int t = q >> 2, n = 4 * (q & 3), n0 = 16 * panel + n;
+        for (int q = tid; q < m.T * QW; q += 64 * NW) {
+            const int t = q / QW, n = 4 * (q % QW), n0 = CW * strip + n;
             float v[4];
             token_sum(t, n, v);
             finish_quad<DT, EP_LIN>(y, t, n0, v, un, BiasQuad{}, res_quad(y, t, n0));
         }
         return;
     }
-    float *mine = m.partial + ((long long)panel * m.split + slice) * m.T * 16;
-    for (int q = tid; q < m.T * 4; q += 64 * NW) {
+    float *mine = m.partial + ((long long)strip * m.split + slice) * m.T * CW;
+    for (int q = tid; q < m.T * QW; q += 64 * NW) {
         float v[4];
-        token_sum(q >> 2, 4 * (q & 3), v);
+        token_sum(q / QW, 4 * (q % QW), v);
         store_agent(mine + 4 * q, v);
     }
     // every wave's stores have reached the device's point of coherence before
@@ -413,17 +452,17 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid == 0)
-        s_last = __hip_atomic_fetch_add(m.arrived + panel, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == m.split - 1;
+        s_last = __hip_atomic_fetch_add(m.arrived + strip, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == m.split - 1;
     __syncthreads();
     if (!s_last) return;
-    const float *all = m.partial + (long long)panel * m.split * m.T * 16;
-    for (int q = tid; q < m.T * 4; q += 64 * NW) {
-        const int t = q >> 2, n0 = 16 * panel + 4 * (q & 3);
+    const float *all = m.partial + (long long)strip * m.split * m.T * CW;
+    for (int q = tid; q < m.T * QW; q += 64 * NW) {
+        const int t = q / QW, n0 = CW * strip + 4 * (q % QW);
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int s = 0; s < m.split; s += 4) {  // four in flight: each is a trip past the L2
             float x[4][4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) load_agent(all + (long long)min(s + i, m.split - 1) * m.T * 16 + 4 * q, x[i]);
+            for (int i = 0; i < 4; i++) load_agent(all + (long long)min(s + i, m.split - 1) * m.T * CW + 4 * q, x[i]);
 #pragma unroll
             for (int i = 0; i < 4; i++)
 #pragma unroll

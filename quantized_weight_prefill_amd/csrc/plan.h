@@ -90,20 +90,26 @@ struct MoeArgs {
     Args g;              // weights, K, panels, group; offs, E, wstride; M = pairs
     const int *rows;     // [pairs]
     const float *wts;    // [T][top_k]
-    uint16_t *H;         // hidden [pairs][inter] (row i of the sorted order)
+    uint16_t *H;         // hidden [pairs][2][inter] (row i of the sorted order): rounded, and the rest
     int T, top_k, inter;
     int parts;           // k_moe_down: K parts per row tile
-    int split;           // k_moe_down: workgroups per panel of Y
-    int panels;          // panels of Y
-    float *partial;      // split > 1: [panels][split][T][16]
-    int *arrived;        // split > 1: [panels], zeroed by k_moe_up
+    int strips;          // k_moe_down: strips of Y, of one or two panels
+    int split;           // k_moe_down: workgroups per strip
+    float *partial;      // split > 1: [strips][split][T][columns of a strip]
+    int *arrived;        // split > 1: [strips], zeroed by k_moe_up
 };
 constexpr int kMoeUpWaves = 8;     // waves of a k_moe_up workgroup
 constexpr int kMoeDownWaves = 16;  // of a k_moe_down workgroup: at 128 VGPRs a wave it fills a CU
+// A bound on the experts' 16-row tiles.
+__host__ __device__ inline long long moe_tiles(long long pairs, long long E)
+{
+    const long long n = (pairs + 15) / 16 + E;
+    return pairs < n ? pairs : n;
+}
 template <int FMT>
 hipError_t launch_moe_up(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s);
 template <int FMT>
-hipError_t launch_moe_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s);
+hipError_t launch_moe_down(int dtype, int pn, dim3 grid, const MoeArgs &m, hipStream_t s);
 // moe_route.hip
 hipError_t launch_moe_route(int logit_type, const void *logits, int T, int E, int k, int score, int renorm, float scale,
                             int *ids, float *weights, int *offsets, int *rows, hipStream_t s);

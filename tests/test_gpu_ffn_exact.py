@@ -77,6 +77,34 @@ def test_moe_identity(dtype):
             assert same_bits(from_device(y), W[:T])
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f16", "bf16"])
+def test_moe_hidden_keeps_what_its_rounding_left(dtype):
+    """Gate = up = down = I, so h = x * x and Y = h + residual, with the residual
+    -RN(h): what is left has few bits, and Y is exactly that wherever a row tile
+    holds at most eight pairs (x are whole numbers up to 255: x * x has 16 bits,
+    its rounding 11 or 8, the rest at most 8).  One panel per workgroup of the
+    down product, and (many experts) two."""
+    n = 256
+    f = {k: np.zeros_like(v) for k, v in wide_gap_fields(980, n, n).items()}
+    f["d"][:], f["sc"][:], f["q"][:] = 0x3C00, 1, np.eye(n, dtype=np.uint8)
+    up = qg.pack("q4k", synth.encode("q4k", {k: np.concatenate([v, v]) for k, v in f.items()}), 2 * n, n)
+    down = qg.pack("q4k", synth.encode("q4k", f), n, n)
+    for T, E in ((1, 1), (3, 1), (8, 1), (20, 1), (600, 300)):
+        rng = np.random.default_rng(981 + T)
+        x64 = torch.from_numpy(rng.integers(-255, 256, (T, n)).astype(np.float64))
+        tt = torch.float16 if dtype == qg.F16 else torch.bfloat16
+        h = x64 * x64
+        res = -h.to(tt)
+        left = h + res.double()
+        assert bool((left != 0).any()) and torch.equal(left.to(tt).double(), left)
+        ids = (torch.arange(T, dtype=torch.int32) % E)[:, None].cuda()
+        offs, rows = qg.moe_group(ids, E)
+        y = qg.moe("q4k", "q4k", x64.to(tt).cuda(), bytes_to_device(np.tile(up, E)), bytes_to_device(np.tile(down, E)),
+                   torch.ones((T, 1), device="cuda"), offs, rows, n, act="none", residual=res.cuda())
+        first = 16 if T == 20 else 0  # 20 rows of one expert: a full tile and one of four
+        assert torch.equal(y[first:].cpu().double(), left[first:]), (T, E)
+
+
 def test_calls_with_and_without_the_common_path():
     """A call on an explicit stream, or with the caller's workspace, takes the
     checked Python path: the same bits as the common one, refusals alike."""

@@ -220,6 +220,14 @@ def test_moe_sizes(H, I, fu, fd):
         check_moe(ex, T, k, np.argsort(rng.random((T, E)), 1)[:, :k], "silu", True, 730)
 
 
+@pytest.mark.parametrize("fu,fd,E,H,I,T,k", [("q4k", "w4a16", 31, 4096, 128, 40, 1), ("w4a16", "q6k", 3, 2048, 256, 512, 2)])
+def test_moe_two_panels_per_workgroup(fu, fd, E, H, I, T, k):
+    """Enough row tiles for the down product's waves to take two each: few rows
+    to an expert, and the most pairs a call takes on few experts."""
+    ex = Experts(fu, fd, E, H, I, qg.F16, 755)
+    check_moe(ex, T, k, np.random.default_rng(11).integers(-1, E, (T, k)), "silu", True, 756)
+
+
 def test_moe_skewed_and_dropped():
     """Every pair on one expert (several row tiles), experts without rows, a
     token that chose one expert twice, dropped pairs whose weights are not

@@ -372,12 +372,13 @@ int qgemm_gemm_xf_noalloc(int format, int rung, const void *Xf, const void *Wpac
  * residual, act NONE and gated 0, Y (row-major) has the bits of
  * qgemm_gemm_rung / qgemm_gemm_xf on the same rung.
  * rung as in qgemm_gemm_rung; -1 takes the M-ladder of X's layout over the
- * packed columns (2N when gated), save that on row-major X 33..64 rows of a
- * k-quant over at most 256 panels go to direct-small-m where the products go
- * to direct-skinny-n (qgemm_linear_select_rung says which).  The gated form
- * has no rung that splits K across workgroups: -1 picks the next best, and
- * forcing one is QGEMM_ERR_FORMAT.  Launches, errors and the workspace as
- * there, plus
+ * packed columns (2N when gated), save that where the products go to
+ * direct-skinny-n some calls that are not gated go to direct-small-m
+ * (qgemm_linear_select_rung says which): on row-major X 33..64 rows of a
+ * k-quant over 5..256 panels, and up to 16 rows (three or four panels: up to
+ * 64) over at most four panels.  The gated form has no rung that splits K
+ * across workgroups: -1 picks the next best, and forcing one is
+ * QGEMM_ERR_FORMAT.  Launches, errors and the workspace as there, plus
  * QGEMM_ERR_FORMAT for an unknown layout or activation and QGEMM_ERR_SHAPE for
  * an N that gated or y_layout does not allow; M = 0 is a no-op.
  *
@@ -484,10 +485,10 @@ int qgemm_grouped_plan(int64_t T, int64_t E, int64_t N, int64_t K, int32_t *info
  * All buffers are device memory and the caller's; logits and ids 16-byte
  * aligned, the others 4-byte; no buffer may overlap another.  The order of
  * rows does not depend on timing.  E is 1 .. QGEMM_MOE_MAX_EXPERTS, top_k 1 ..
- * 64 (and at most E in qgemm_moe_route), T * top_k below 2^31 - 4096.  T = 0
- * writes nothing in qgemm_moe_route; qgemm_moe_group then writes zeros to
- * offsets.  Errors: QGEMM_ERR_SHAPE, _DTYPE (logit_type), _FORMAT (score),
- * _NULL, _ALIGN, _HIP. */
+ * 64 (and at most E in qgemm_moe_route), T * top_k below 2^31 - 4096, T at
+ * most 2^26 - 4 in qgemm_moe_route.  T = 0 writes nothing in qgemm_moe_route;
+ * qgemm_moe_group then writes zeros to offsets.  Errors: QGEMM_ERR_SHAPE,
+ * _DTYPE (logit_type), _FORMAT (score), _NULL, _ALIGN, _HIP. */
 #define QGEMM_SCORE_SOFTMAX 0
 #define QGEMM_SCORE_SIGMOID 1
 #define QGEMM_MOE_MAX_EXPERTS 1024
@@ -519,9 +520,10 @@ int qgemm_moe_group(const int32_t *ids, int64_t T, int64_t E, int64_t top_k, int
  * and rows into range, so any contents stay inside the buffers (bad ones only
  * give wrong rows).  h and the partial sums of Y go through `workspace`
  * (device, 16-byte aligned, at least qgemm_moe_workspace_bytes, of any
- * contents, which the call overwrites); everything after h stays in fp32 up to
- * Y's one rounding, in an order that depends on the sizes and the routing
- * alone.  Y may be the residual, or X itself when X is not needed afterwards;
+ * contents, which the call overwrites: calls that may run at the same time, on
+ * two streams or in two graphs, need one each); everything after h stays in
+ * fp32 up to Y's one rounding, in an order that depends on the sizes and the
+ * routing alone.  Y may be the residual, or X itself when X is not needed afterwards;
  * any other overlap is not allowed.
  * T * top_k is at most QGEMM_MOE_MAX_PAIRS (above it the grouped products
  * above are the path); inter is a multiple of format_down's K step, hidden of

@@ -1281,7 +1281,7 @@ int qgemm_moe_route(const void *logits, int logit_type, int64_t T, int64_t E, in
 {
     const int st = moe_route_shape(T, E, top_k);
     if (st != QGEMM_OK) return st;
-    if (top_k > E) return QGEMM_ERR_SHAPE;
+    if (top_k > E || !launch_fits((T + 3) / 4, 256)) return QGEMM_ERR_SHAPE;
     if (logit_type != QGEMM_F16 && logit_type != QGEMM_BF16 && logit_type != QGEMM_F32) return QGEMM_ERR_DTYPE;
     if (score != QGEMM_SCORE_SOFTMAX && score != QGEMM_SCORE_SIGMOID) return QGEMM_ERR_FORMAT;
     if (T == 0) return QGEMM_OK;

@@ -313,6 +313,54 @@ def test_moe_in_place_stream_and_graph():
         assert torch.equal(bits(gy), bits(ex.run(xs, w3, o3, r3, residual=xs))), i
 
 
+def test_layers_side_by_side():
+    """The same calls on two streams at once, then captured into two graphs
+    that replay on two streams at once: each with the workspace that the
+    allocator gave it, each with the bits of the call by itself."""
+    ex = Experts("q4k", "q6k", 8, 512, 256, qg.BF16, 775)
+    rx, rw = synth.streams(776, 2)
+    f = synth.weight_fields("q4k", rw, 512, 4096)
+    wp = bytes_to_device(qg.pack("q4k", synth.encode("q4k", f), 512, 4096))
+    work = []
+    for i, T in enumerate((9, 33)):
+        logits = torch.from_numpy(rx.standard_normal((T, 8)).astype(np.float32)).cuda()
+        x = to_device(synth.activations(rx, T, 512, qg.BF16), qg.BF16)
+        wide = to_device(synth.activations(rx, T, 4096, qg.BF16), qg.BF16) * 0.01
+        _, w, offs, rows = qg.moe_route(logits, 2)
+        work.append((x, w, offs, rows, wide))
+
+    def run(i):
+        x, w, offs, rows, wide = work[i]
+        # the linear layer's rung that splits K across workgroups has a workspace too
+        return ex.run(x, w, offs, rows, residual=x), qg.linear("q4k", wide, wp, 512, act="silu", rung=11)
+
+    assert qg.rung_name(11).endswith("-sk")
+    want = [[bits(t) for t in run(i)] for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(i))
+    torch.cuda.synchronize()
+    assert all(torch.equal(bits(t), u) for i in range(2) for ts in got[i] for t, u in zip(ts, want[i]))
+    graphs, outs = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            outs.append(run(i))
+    for _ in range(4):
+        for t in outs[0] + outs[1]:
+            t.zero_()
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(bits(t), u) for i in range(2) for t, u in zip(outs[i], want[i]))
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------

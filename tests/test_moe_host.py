@@ -20,7 +20,7 @@ def route(logits=P, lt=0, T=4, E=8, k=2, score=0, renorm=1, scale=1.0, ids=P, w=
 
 @pytest.mark.parametrize("kw,status", [
     (dict(T=-1), -2), (dict(E=0), -2), (dict(E=1025), -2), (dict(k=0), -2), (dict(k=9), -2), (dict(k=65, E=100), -2),
-    (dict(T=1 << 31), -2), (dict(T=1 << 30, k=2), -2), (dict(lt=3), -3), (dict(lt=-1), -3), (dict(score=2), -5),
+    (dict(T=1 << 31), -2), (dict(T=1 << 30, k=2), -2), (dict(T=(1 << 26) - 3, k=1), -2), (dict(lt=3), -3), (dict(lt=-1), -3), (dict(score=2), -5),
     (dict(logits=None), -1), (dict(ids=None), -1), (dict(w=None), -1), (dict(offs=None), -1), (dict(rows=None), -1),
     (dict(logits=M4), -4), (dict(ids=M4), -4), (dict(w=M2), -4), (dict(offs=M2), -4), (dict(rows=M2), -4),
 ])

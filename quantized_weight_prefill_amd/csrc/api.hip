@@ -580,8 +580,37 @@ int gemm(int fmt, int rung, const void *X, const void *W, void *Y, long long M, 
 
 bool known_act(int act) { return act >= QGEMM_ACT_NONE && act <= QGEMM_ACT_GELU_TANH; }
 
+// Where the linear layer takes one-panel waves instead of rung r, the choice of
+// the products' ladder (np packed panels).
+//
+// Up to four panels: the products give one wave all of them; one panel per wave
+// spreads the weights over as many CUs, at the price of reading X once per
+// panel (Q6_K 12288 -> 64: 1 and 16 rows 10.9 against 27.2 and 28.1 us, 64 rows
+// 20.8 against 28.4; W4A16 4096 -> 64, 64 rows 9.6 against 10.0; Q6_K 12288 ->
+// 32, 16 rows 10.9 against 16.2, but 33 rows 17.5 against 16.4, so two panels
+// change over at 16 rows).
+//
+// Row-major X, 17..64 rows: the linear layer's one-panel waves carry all rows,
+// their activations staged through LDS.  Weights rotating, K = 4096, against
+// 16-row groups of four panels per wave: 17 and 24 rows, W4A16 -> 4097 10.1 and
+// 10.9 against 11.0 and 11.2, -> 6144 10.9 and 11.6 against 11.2 and 11.3, Q4_K
+// -> 6144 11.3 and 11.9 against 13.0 and 13.1, Q6_K -> 8192 12.1 and 13.1
+// against 14.7 and 14.6; above 32 rows up to one panel per CU, -> 4096, 48 rows,
+// Q4_K 10.5 against 12.3, W4A16 10.6 against 11.4, 64 rows, Q4_K 12.1 against
+// 12.4, W4A16 12.8 against 11.7 (so W4A16 stops at 48).  Against 64x32 tiles, a
+// k-quant, 33 and 48 rows: Q4_K -> 6144 15.8 and 18.3 against 15.4 and 18.7, ->
+// 8192 14.8 and 16.5 against 15.8 and 19.2, Q6_K -> 8192 17.0 and 18.5 against
+// 17.7 and 20.7; W4A16 -> 6144 16.2 and 18.5 against 16.0 and 19.2 stays.
+bool one_panel_pays(int fmt, int r, int xl, long long m, long long np)
+{
+    if (np <= 4) return r == RUNG_SKINNY_N && (m <= 16 || (m <= 64 && np > 2));
+    if (xl != X_ROW || m <= 16 || np > 2 * kCUs) return false;
+    if (r == RUNG_SKINNY_N) return m <= 32 || (np <= kCUs && m <= (fmt == FMT_W4 ? 48 : 64));
+    return r == RUNG_M64N32_K4 && fmt != FMT_W4 && m > 32 && m <= 48;
+}
+
 // The plan over the packed columns (2N when gated), by the products' ladder
-// but for the two rules below: the epilogue adds the same few loads and stores
+// but for one_panel_pays: the epilogue adds the same few loads and stores
 // per output to every rung.  The gated form has no rung that splits K across
 // workgroups (its partial sums would pair columns of two tiles): where the
 // ladder picks one, the best of the others serves.
@@ -597,23 +626,7 @@ int linear_plan(int fmt, int rung, int xl, long long M, long long N, long long K
     if (dtype != DT_F16 && dtype != DT_BF16) return QGEMM_ERR_DTYPE;
     if (rung < -1 || rung >= RUNG_COUNT) return QGEMM_ERR_FORMAT;
     int r = rung < 0 ? select_rung(fmt, m, nt, K, xl, dtype) : rung;
-    // Row-major X, 33..64 rows over at most 256 panels of a k-quant: where the
-    // products take 16-row groups of four panels per wave, the linear layer's
-    // one-panel waves carry all rows, their activations staged through LDS
-    // (weights rotating, Q4_K 4096 -> 4096, 48 rows: 10.5 against 12.3 us, 64
-    // rows 12.1 against 12.4; Q6_K 12288 -> 4096, 48 rows: 25.7 against 33.2,
-    // 64 rows 29.9 against 33.0; W4A16, 48 and 64 rows: 10.6 and 12.6 against
-    // 10.8 and 11.1, so it stays).
-    if (rung < 0 && !gated && xl == X_ROW && r == RUNG_SKINNY_N && fmt != FMT_W4 && m > 32 && m <= 64 && nt > 64 &&
-        (nt + 15) / 16 <= kCUs)
-        r = RUNG_SMALL_M;
-    // Up to four panels: the products give one wave all of them; one panel per
-    // wave spreads the weights over as many CUs, at the price of reading X
-    // once per panel (Q6_K 12288 -> 64: 1 and 16 rows 10.9 against 27.2 and
-    // 28.1 us, 64 rows 20.8 against 28.4; W4A16 4096 -> 64, 64 rows 9.6 against
-    // 10.0; Q6_K 12288 -> 32, 16 rows 10.9 against 16.2, but 33 rows 17.5
-    // against 16.4, so two panels change over at 16 rows).
-    if (rung < 0 && !gated && r == RUNG_SKINNY_N && nt <= 64 && (m <= 16 || (m <= 64 && nt > 32))) r = RUNG_SMALL_M;
+    if (rung < 0 && !gated && one_panel_pays(fmt, r, xl, m, (nt + 15) / 16)) r = RUNG_SMALL_M;
     if (gated && (r == RUNG_M64_SK || r == RUNG_M768N64_SK)) {
         if (rung >= 0) return QGEMM_ERR_FORMAT;
         r = r == RUNG_M64_SK ? round_model_rung(fmt, m, nt, K, xl, dtype) : large_tile_xf(fmt, m, nt, K);

@@ -816,15 +816,18 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     const long long tiles = moe_tiles(P, E);
     // two panels per workgroup of the down product where the row tiles give
     // its waves two each: h is then read once for both panels, by half as many
-    // workgroups, each over half the tiles (128 tokens, 8 of 16 experts, 768 ->
-    // 2048: 26.9 against 34.9 us; 64 tokens, 8 of 128: 49.0 against 54.2); below
-    // that one panel, which spreads the weights over more waves (one token 8.2
-    // against 9.0; 16 tokens, 2 of 8, 1024 -> 4096: 8.8 against 9.8; 256 tokens,
-    // 4 of 8, 1024 -> 1024: 28.7 against 29.9)
+    // workgroups, each over half the tiles (64 tokens, 8 of 128 experts, 768 ->
+    // 2048: 47.3 against 56.0 us; 128 tokens, 8 of 16: 27.8 against 32.2; 128
+    // tokens, 4 of 32, 1024 -> 4096: 46.6 against 52.6); below that one panel,
+    // which spreads the weights over more waves (one token 8.2 against 9.0; 16
+    // tokens, 2 of 8, 1024 -> 4096: 8.8 against 9.8; 256 tokens, 4 of 8, 1024 ->
+    // 1024: 30.8 against 33.3)
     const int pn = tiles > 2 * kMoeDownWaves * moe_split(H, 1) ? 2 : 1;
     m.strips = (int)(H / (16 * pn));
     m.split = moe_split(H, pn);
-    m.partial = (float *)(m.H + 2 * P * I);
+    m.plane = (P + 15) / 16 * 16 * I;
+    m.blocked = P > 4 * E;  // full row tiles are likely: hidden_at
+    m.partial = (float *)(m.H + 2 * m.plane);
     m.arrived = (int *)(m.partial + (long long)m.split * T * H);
 
     // gate and up: K split over waves while the grid holds fewer than 4096 of
@@ -1325,7 +1328,7 @@ int qgemm_moe(int format_up, int format_down, const void *X, const void *Wup, co
                group_size, has_zp, act, dtype, workspace, workspace_bytes, stream);
 }
 
-// h [pairs][2][inter], the strips' partial sums (two panels to a strip have the
+// h (two planes of whole 16-row blocks), the strips' partial sums (two panels to a strip have the
 // larger split) and their arrival counters; inter and hidden are multiples of
 // 128 in every legal call, so each part starts 16-byte aligned.
 size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64_t inter)
@@ -1334,7 +1337,7 @@ size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64
         inter < kChunk || inter > INT32_MAX / 2 || inter % kChunk != 0 || hidden < kChunk || hidden > INT32_MAX ||
         hidden % kChunk != 0)
         return 0;
-    return 4 * (size_t)(T * top_k) * (size_t)inter + 4 * (size_t)moe_split(hidden, 2) * (size_t)(T * hidden) +
+    return 4 * (size_t)((T * top_k + 15) / 16 * 16) * (size_t)inter + 4 * (size_t)moe_split(hidden, 2) * (size_t)(T * hidden) +
            4 * (size_t)(hidden / 16);
 }
 

@@ -17,15 +17,22 @@ hipError_t launch_moe_up(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
     return hipGetLastError();
 }
 
+template <int FMT, int PN, bool BLOCKED>
+void launch_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
+{
+    const dim3 block(64 * kMoeDownWaves);
+    const size_t lds = moe_down_lds(m.g.M, m.g.E, m.parts, PN);
+    if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16, PN, BLOCKED>), grid, block, lds, s, m);
+    else hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16, PN, BLOCKED>), grid, block, lds, s, m);
+}
+
 template <int FMT>
 hipError_t launch_moe_down(int dtype, int pn, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
-    const dim3 block(64 * kMoeDownWaves);
-    const size_t lds = moe_down_lds(m.g.M, m.g.E, m.parts, pn);
-    if (dtype == DT_F16 && pn == 1) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16, 1>), grid, block, lds, s, m);
-    else if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16, 2>), grid, block, lds, s, m);
-    else if (pn == 1) hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16, 1>), grid, block, lds, s, m);
-    else hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16, 2>), grid, block, lds, s, m);
+    if (pn == 1 && !m.blocked) launch_down<FMT, 1, false>(dtype, grid, m, s);
+    else if (pn == 1) launch_down<FMT, 1, true>(dtype, grid, m, s);
+    else if (!m.blocked) launch_down<FMT, 2, false>(dtype, grid, m, s);
+    else launch_down<FMT, 2, true>(dtype, grid, m, s);
     return hipGetLastError();
 }
 

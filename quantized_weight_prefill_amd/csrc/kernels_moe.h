@@ -20,15 +20,12 @@
 //     the routing weights.  With split > 1 the panels' workgroups leave those
 //     sums in memory, and the last of them to arrive adds them in order: no
 //     floating-point atomics, and a result that does not depend on timing.
-// h goes to memory as its rounding to the operand type, which the second
-// product's MFMA takes, and as what that rounding left.  A tile of at most
-// eight rows multiplies both, the second in the eight MFMA columns that would
-// be idle: h then has twice the type's bits, and the layer's error is that of
-// Y's rounding alone.  A fuller tile takes the rounding alone: both parts of
-// its rows would double the down product's MFMAs and its reads of h (128
-// tokens, 8 of 16 experts: 34.5 us for the kernel with, 57-59, in either tile
-// height, against 34.5 without).  The sum over a token's experts stays in fp32
-// until the one store.
+// h goes to memory as its rounding to the operand type and what that rounding
+// left, and the second product takes both, so h has twice the type's bits and
+// the layer's error is that of Y's one rounding: with a few rows to a tile in
+// the MFMA columns that would be idle, for free, with full tiles as a second
+// MFMA on the same unpacked weights.  The sum over a token's experts stays in
+// fp32 until the one store.
 #pragma once
 
 #include <algorithm>
@@ -175,6 +172,23 @@ __device__ __forceinline__ float low_part(float v, uint32_t bits16)
     return fabsf(hi) < __builtin_inff() ? (v - hi) * kLowScale<DT> : 0.0f;
 }
 
+// Element k (a multiple of 4) of sorted row i in a plane of the hidden matrix.
+// Plain, for at most four pairs per expert: row-major.  BLOCKED, above: blocks
+// of 16 rows, a chunk of 128 after the other, and inside a chunk the rows'
+// 16-byte pieces (k = 32 g + 8 i .. + 8) ordered by i, g and row, so that the 16
+// lanes of a k_moe_down load that hold one g read 256 consecutive bytes, not 16
+// pieces of as many rows.  The down product of 256 tokens, 4 of 8 experts, 1024
+// -> 1024, h rounded only: 22.4 against 28.9 us; with a few rows in a tile the
+// blocks touch twice the cache lines, and 64 tokens, 8 of 128 experts, take 97
+// against 94 for the whole layer.
+template <bool BLOCKED>
+__device__ __forceinline__ long long hidden_at(int inter, int i, int k)
+{
+    if (!BLOCKED) return (long long)i * inter + k;
+    return ((long long)(i >> 4) * (inter >> 7) + (k >> 7)) * 2048 + ((k >> 3 & 3) * 4 + (k >> 5 & 3)) * 128 +
+           (i & 15) * 8 + (k & 7);
+}
+
 // Raw bytes and activations of one chunk pair: PN panels, one row per column
 // lane.  The k-quants' block header serves both chunks, so a pair costs one
 // header load; second: the pair's second chunk exists (always for the
@@ -202,25 +216,30 @@ struct Pair {
     }
 };
 
-// acc[PN] += the pair's product, one run unpacked at a time; refill() issues
-// the loads that take the pair's place.  Unpacking the whole pair first, so
-// that those loads go out before the MFMAs, or holding two pairs, takes
+// acc[n] += the pair's product with the n-th of NX activation operands, one run
+// unpacked at a time.  acts(h, x) gives the activations of chunk h; refill()
+// issues the loads that take the pair's place.  Unpacking the whole pair first,
+// so that those loads go out before the MFMAs, or holding two pairs, takes
 // registers from the waves that hide the latency: 64 tokens of 8 of 128
 // experts, Q4_K 2048 -> 768 pairs, weights rotating, 51.4 us so, 56 with two
 // single chunks in flight, 64-66 with either of those.
-template <int FMT, int DT, int PN, class F>
+template <int FMT, int DT, int PN, int NX, class X, class F>
 __device__ __forceinline__ void multiply_pair(const Pair<FMT, PN> &q, const RunSrc<FMT> (&src)[PN], int p, int nch,
-                                              f32x4 (&acc)[PN], F refill)
+                                              f32x4 (&acc)[NX][PN], X acts, F refill)
 {
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         if (FMT == FMT_W4 && h == 1 && 2 * p + 1 >= nch) continue;
+        u32x4 x[NX][4];
+        acts(h, x);
 #pragma unroll
         for (int pn = 0; pn < PN; pn++) {
             u32x4 wf[4];
             unpack_run<FMT, DT>(q.raw[pn][h], src[pn], 2 * p + h, wf);
 #pragma unroll
-            for (int i = 0; i < 4; i++) acc[pn] = mma<DT>(wf[i], q.x[h][i], acc[pn]);
+            for (int n = 0; n < NX; n++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[n][pn] = mma<DT>(wf[i], x[n][i], acc[n][pn]);
         }
     }
     refill();
@@ -254,7 +273,7 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
     src[0].init(b, p, g, col);
     src[1].init(b, pairs + p, g, col);
     const int i = lo + 16 * t + col;
-    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    f32x4 acc[1][2] = {};
     const int nch = a.K / kChunk, np2 = (nch + 1) / 2;
     const int pe = np2 * (share + 1) / a.kw;
     int q = np2 * share / a.kw;
@@ -264,34 +283,40 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
         __builtin_amdgcn_sched_barrier(0);  // the weights' loads go out before the token is known
         const uint16_t *xrow = a.X + (long long)(pair_at(m, min(i, hi - 1)) / m.top_k) * a.K + 32 * g;
         pr.load_x(xrow, q, nch);
+        auto acts = [&](int h, u32x4(&x)[1][4]) {
+#pragma unroll
+            for (int k = 0; k < 4; k++) x[0][k] = pr.x[h][k];
+        };
         for (; q + 1 < pe; q++)
-            multiply_pair<FMT, DT, 2>(pr, src, q, nch, acc, [&] {
+            multiply_pair<FMT, DT>(pr, src, q, nch, acc, acts, [&] {
                 pr.load_w(src, q + 1, nch);
                 pr.load_x(xrow, q + 1, nch);
             });
-        multiply_pair<FMT, DT, 2>(pr, src, q, nch, acc, [] {});
+        multiply_pair<FMT, DT>(pr, src, q, nch, acc, acts, [] {});
     }
     if (a.kw > 1) {
-        red[w][0][lane] = acc[0];
-        red[w][1][lane] = acc[1];
+        red[w][0][lane] = acc[0][0];
+        red[w][1][lane] = acc[0][1];
         __syncthreads();
         if (share != 0) return;
         for (int ww = 1; ww < a.kw; ww++) {
-            acc[0] += red[w + ww][0][lane];
-            acc[1] += red[w + ww][1][lane];
+            acc[0][0] += red[w + ww][0][lane];
+            acc[0][1] += red[w + ww][1][lane];
         }
     }
     if (own >= pairs || i >= hi) return;
-    float v[4] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3]};
+    const f32x4 gate = acc[0][0], up = acc[0][1];
+    float v[4] = {gate[0], gate[1], gate[2], gate[3]};
     act_apply(a.act, v);
 #pragma unroll
-    for (int c = 0; c < 4; c++) v[c] *= acc[1][c];
-    uint16_t *h = m.H + 2 * (long long)i * m.inter + 16 * p + 4 * g;
+    for (int c = 0; c < 4; c++) v[c] *= up[c];
+    const int k = 16 * p + 4 * g;
+    uint16_t *h = m.H + (m.blocked ? hidden_at<true>(m.inter, i, k) : hidden_at<false>(m.inter, i, k));
     const u32x2 o = {pack_out<DT>(v[0], v[1]), pack_out<DT>(v[2], v[3])};
     *(u32x2 *)h = o;
 #pragma unroll
     for (int c = 0; c < 4; c++) v[c] = low_part<DT>(v[c], o[c >> 1] >> (16 * (c & 1)));
-    *(u32x2 *)(h + m.inter) = u32x2{pack_out<DT>(v[0], v[1]), pack_out<DT>(v[2], v[3])};
+    *(u32x2 *)(h + m.plane) = u32x2{pack_out<DT>(v[0], v[1]), pack_out<DT>(v[2], v[3])};
 }
 
 // Grid: x = strips of Y (PN panels each) times split.  Dynamic LDS
@@ -303,7 +328,7 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
 // A wave's work is one sequence of chunk pairs over its units (row tile, part
 // of K), the next pair's loads in flight across the units' borders: `front`
 // walks the sequence where the loads are, `back` where the MFMAs are.
-template <int FMT, int DT, int PN>
+template <int FMT, int DT, int PN, bool BLOCKED>
 __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
 {
     constexpr int NW = kMoeDownWaves, CW = 16 * PN, QW = 4 * PN;  // columns and quads of a strip's row
@@ -351,66 +376,90 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
         q.ce = np2 * (part + 1) / m.parts;
         return __builtin_amdgcn_readfirstlane(tile_e[tile]);
     };
-    RunSrc<FMT> src[PN];      // at the front cursor's expert
-    const uint16_t *xrow;     // at the front cursor's rows
+    RunSrc<FMT> src[PN];   // at the front cursor's expert
+    const uint16_t *xrow;  // at the front cursor's rows; BLOCKED: at the back cursor's
+    auto rows_at = [&](const Cursor &q) {
+        const bool few = !BLOCKED && q.hi - q.lo <= 8;  // columns 8..15 take the low parts of the rows in 0..7
+        const int i = min(q.lo + (few ? col & 7 : col), q.hi - 1);
+        xrow = m.H + (few && col > 7 ? m.plane : 0) + hidden_at<BLOCKED>(a.K, i, 32 * g);
+    };
     auto aim = [&](Cursor &q) {
         const int e = open(q);
         Args b = a;
         b.W = a.W + (long long)e * a.wstride;
 #pragma unroll
         for (int pn = 0; pn < PN; pn++) src[pn].init(b, PN * strip + pn, g, col);
-        const bool few = q.hi - q.lo <= 8;  // columns 8..15 take the low parts of the rows in 0..7
-        const int r = few ? col & 7 : col;
-        xrow = m.H + (2 * (long long)min(q.lo + r, q.hi - 1) + (few ? col >> 3 : 0)) * a.K + 32 * g;
+        if (!BLOCKED) rows_at(q);
     };
     if (w < units) {
         Pair<FMT, PN> pr;
         Cursor front{w, 0, 0, 0, 0}, back{w, 0, 0, 0, 0};
         aim(front);
         open(back);
+        if (BLOCKED) rows_at(back);
         int total = 0;  // pairs of this wave's sequence
         for (int u = w; u < units; u += NW) total += np2 * (u % m.parts + 1) / m.parts - np2 * (u % m.parts) / m.parts;
         auto fetch = [&] {
             pr.load_w(src, front.c, nch);
-            pr.load_x(xrow, front.c, nch);
+            if (!BLOCKED) pr.load_x(xrow, front.c, nch);
             if (++front.c == front.ce) {
                 front.u += NW;
                 if (front.u < units) aim(front);
             }
         };
-        f32x4 acc[PN] = {};
+        // BLOCKED: both parts of full rows are loaded when their chunk's turn
+        // comes, under the unpack; ahead of it they would not fit the registers
+        // (128 tokens, 8 of 16 experts: 27.8 us, 36.8 with the roundings ahead)
+        constexpr int NX = BLOCKED ? 2 : 1;
+        auto acts = [&](int h, u32x4(&x)[NX][4]) {
+#pragma unroll
+            for (int n = 0; n < NX; n++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    x[n][i] = BLOCKED ? *(const u32x4 *)(xrow + n * m.plane + 2048LL * (2 * back.c + h) + 512 * i)
+                                      : pr.x[h][i];
+        };
+        f32x4 acc[NX][PN] = {};
         // the branches here touch LDS only: a load from memory in one would
         // make the next wait drain what is in flight
         auto close = [&] {  // the back cursor's pair is multiplied
             if (++back.c == back.ce) {
                 const int i = back.lo + col;
-                if (back.hi - back.lo <= 8) {
+                if constexpr (BLOCKED) {
+#pragma unroll
+                    for (int pn = 0; pn < PN; pn++) acc[0][pn] += acc[1][pn] * (1.0f / kLowScale<DT>);
+                } else if (back.hi - back.lo <= 8) {
 #pragma unroll
                     for (int c = 0; c < QW; c++) {
-                        const float y = acc[c >> 2][c & 3];
+                        const float y = acc[0][c >> 2][c & 3];
                         const int low = dpp_from<0x128, 0xF>(__builtin_bit_cast(int, y), 0);  // row_ror:8
-                        acc[c >> 2][c & 3] = __builtin_fmaf(__builtin_bit_cast(float, low), 1.0f / kLowScale<DT>, y);
+                        acc[0][c >> 2][c & 3] = __builtin_fmaf(__builtin_bit_cast(float, low), 1.0f / kLowScale<DT>, y);
                     }
                 }
                 if (i < back.hi) {
                     const int pair = pair_of[i], part = back.u % m.parts;
 #pragma unroll
                     for (int pn = 0; pn < PN; pn++)
-                        *(f32x4 *)(sums + (size_t)part * span + pair * CW + 16 * pn + 4 * g) = acc[pn];
+                        *(f32x4 *)(sums + (size_t)part * span + pair * CW + 16 * pn + 4 * g) = acc[0][pn];
                     if (part == 0 && g == 0) served[pair] = 1;
                 }
 #pragma unroll
-                for (int pn = 0; pn < PN; pn++) acc[pn] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int n = 0; n < NX; n++)
+#pragma unroll
+                    for (int pn = 0; pn < PN; pn++) acc[n][pn] = f32x4{0.f, 0.f, 0.f, 0.f};
                 back.u += NW;
-                if (back.u < units) open(back);
+                if (back.u < units) {
+                    open(back);
+                    if (BLOCKED) rows_at(back);
+                }
             }
         };
         fetch();
         for (int s = 1; s < total; s++) {
-            multiply_pair<FMT, DT, PN>(pr, src, back.c, nch, acc, fetch);
+            multiply_pair<FMT, DT>(pr, src, back.c, nch, acc, acts, fetch);
             close();
         }
-        multiply_pair<FMT, DT, PN>(pr, src, back.c, nch, acc, [] {});
+        multiply_pair<FMT, DT>(pr, src, back.c, nch, acc, acts, [] {});
         close();
     }
     __syncthreads();

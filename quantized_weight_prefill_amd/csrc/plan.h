@@ -90,7 +90,9 @@ struct MoeArgs {
     Args g;              // weights, K, panels, group; offs, E, wstride; M = pairs
     const int *rows;     // [pairs]
     const float *wts;    // [T][top_k]
-    uint16_t *H;         // hidden [pairs][2][inter] (row i of the sorted order): rounded, and the rest
+    uint16_t *H;         // hidden, two planes (hidden_at): rounded, and the rest
+    long long plane;     // elements of a plane
+    int blocked;         // the planes' layout
     int T, top_k, inter;
     int parts;           // k_moe_down: K parts per row tile
     int strips;          // k_moe_down: strips of Y, of one or two panels

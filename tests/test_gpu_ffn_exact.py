@@ -80,16 +80,17 @@ def test_moe_identity(dtype):
 @pytest.mark.parametrize("dtype", DTYPES, ids=["f16", "bf16"])
 def test_moe_hidden_keeps_what_its_rounding_left(dtype):
     """Gate = up = down = I, so h = x * x and Y = h + residual, with the residual
-    -RN(h): what is left has few bits, and Y is exactly that wherever a row tile
-    holds at most eight pairs (x are whole numbers up to 255: x * x has 16 bits,
-    its rounding 11 or 8, the rest at most 8).  One panel per workgroup of the
-    down product, and (many experts) two."""
+    -RN(h): what is left has few bits, and Y is exactly that (x are whole numbers
+    up to 255: x * x has 16 bits, its rounding 11 or 8, the rest at most 8).  A
+    few pairs per expert and many, with one panel per workgroup of the down
+    product and (many experts) two; then all pairs on one expert of several,
+    where the tile of more than eight rows may keep the rounding alone."""
     n = 256
     f = {k: np.zeros_like(v) for k, v in wide_gap_fields(980, n, n).items()}
     f["d"][:], f["sc"][:], f["q"][:] = 0x3C00, 1, np.eye(n, dtype=np.uint8)
     up = qg.pack("q4k", synth.encode("q4k", {k: np.concatenate([v, v]) for k, v in f.items()}), 2 * n, n)
     down = qg.pack("q4k", synth.encode("q4k", f), n, n)
-    for T, E in ((1, 1), (3, 1), (8, 1), (20, 1), (600, 300)):
+    for T, E, one in ((1, 1, 0), (3, 1, 0), (8, 1, 0), (20, 1, 0), (150, 3, 0), (600, 300, 0), (1024, 200, 0), (20, 8, 1)):
         rng = np.random.default_rng(981 + T)
         x64 = torch.from_numpy(rng.integers(-255, 256, (T, n)).astype(np.float64))
         tt = torch.float16 if dtype == qg.F16 else torch.bfloat16
@@ -97,11 +98,11 @@ def test_moe_hidden_keeps_what_its_rounding_left(dtype):
         res = -h.to(tt)
         left = h + res.double()
         assert bool((left != 0).any()) and torch.equal(left.to(tt).double(), left)
-        ids = (torch.arange(T, dtype=torch.int32) % E)[:, None].cuda()
+        ids = (torch.arange(T, dtype=torch.int32) % E if not one else torch.full((T,), 3, dtype=torch.int32))[:, None].cuda()
         offs, rows = qg.moe_group(ids, E)
         y = qg.moe("q4k", "q4k", x64.to(tt).cuda(), bytes_to_device(np.tile(up, E)), bytes_to_device(np.tile(down, E)),
                    torch.ones((T, 1), device="cuda"), offs, rows, n, act="none", residual=res.cuda())
-        first = 16 if T == 20 else 0  # 20 rows of one expert: a full tile and one of four
+        first = 16 if one else 0
         assert torch.equal(y[first:].cpu().double(), left[first:]), (T, E)
 
 

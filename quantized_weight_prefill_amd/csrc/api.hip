@@ -826,7 +826,7 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.strips = (int)(H / (16 * pn));
     m.split = moe_split(H, pn);
     m.plane = (P + 15) / 16 * 16 * I;
-    m.blocked = P > 4 * E;  // full row tiles are likely: hidden_at
+    m.blocked = P > 4 * E;
     m.partial = (float *)(m.H + 2 * m.plane);
     m.arrived = (int *)(m.partial + (long long)m.split * T * H);
 

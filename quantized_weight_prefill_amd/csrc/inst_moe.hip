@@ -12,8 +12,10 @@ template <int FMT>
 hipError_t launch_moe_up(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
     const dim3 block(64 * kMoeUpWaves);
-    if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_up<FMT, DT_F16>), grid, block, 0, s, m);
-    else hipLaunchKernelGGL((k_moe_up<FMT, DT_BF16>), grid, block, 0, s, m);
+    if (dtype == DT_F16 && !m.blocked) hipLaunchKernelGGL((k_moe_up<FMT, DT_F16, false>), grid, block, 0, s, m);
+    else if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_up<FMT, DT_F16, true>), grid, block, 0, s, m);
+    else if (!m.blocked) hipLaunchKernelGGL((k_moe_up<FMT, DT_BF16, false>), grid, block, 0, s, m);
+    else hipLaunchKernelGGL((k_moe_up<FMT, DT_BF16, true>), grid, block, 0, s, m);
     return hipGetLastError();
 }
 

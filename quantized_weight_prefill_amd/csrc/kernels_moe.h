@@ -24,8 +24,9 @@
 // left, and the second product takes both, so h has twice the type's bits and
 // the layer's error is that of Y's one rounding: with a few rows to a tile in
 // the MFMA columns that would be idle, for free, with full tiles as a second
-// MFMA on the same unpacked weights.  The sum over a token's experts stays in
-// fp32 until the one store.
+// MFMA on the same unpacked weights.  (Where tiles are few rows on average, one
+// of more than eight, a popular expert's, takes the rounding alone.)  The sum
+// over a token's experts stays in fp32 until the one store.
 #pragma once
 
 #include <algorithm>
@@ -252,10 +253,20 @@ __device__ __forceinline__ void multiply_pair(const Pair<FMT, PN> &q, const RunS
 // from L2, and 32- and 64-row tiles, which unpack less, leave the chip emptier
 // (64 tokens, both of 2 to 8 experts: 13.5-18.1 us against 13.0-17.0 and
 // 17.5-24; 128 tokens, 8 of 16: 37.4 against 35.9 and 35.8).
-template <int FMT, int DT>
+//
+// BLOCKED, where full tiles are likely (hidden_at): a load reads 256
+// consecutive bytes of four rows of x, and a tile of the wave's own in LDS turns
+// them into fragments, as the linear layer's row-major kernels do (128 tokens,
+// 8 of 16 experts: 36.0 against 42.3 us; 128, 4 of 32, 4096 -> 1024: 66.4
+// against 79.1).  With a few rows most lanes of a plain load read the same row, which
+// costs little, and the LDS round trip does not pay (64 tokens, 8 of 128: 68.6
+// against 65.2 us; one token 9.3 against 7.8).
+template <int FMT, int DT, bool BLOCKED>
 __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
 {
-    __shared__ f32x4 red[kMoeUpWaves][2][64];
+    constexpr int kTile = BLOCKED ? 32 * kXStride : 2 * 64 * 16;  // a wave's 16 rows of two chunks, later its sums
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kMoeUpWaves * kTile];
+    f32x4(*red)[2][64] = (f32x4(*)[2][64])lds;
     const Args &a = m.g;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
@@ -281,20 +292,44 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
         Pair<FMT, 2> pr;
         pr.load_w(src, q, nch);
         __builtin_amdgcn_sched_barrier(0);  // the weights' loads go out before the token is known
-        const uint16_t *xrow = a.X + (long long)(pair_at(m, min(i, hi - 1)) / m.top_k) * a.K + 32 * g;
-        pr.load_x(xrow, q, nch);
-        auto acts = [&](int h, u32x4(&x)[1][4]) {
+        auto token_row = [&](int r) {  // row r of the tile, the last one for those past the expert's end
+            return a.X + (long long)(pair_at(m, min(lo + 16 * t + r, hi - 1)) / m.top_k) * a.K;
+        };
+        const uint16_t *xrow[4];
 #pragma unroll
-            for (int k = 0; k < 4; k++) x[0][k] = pr.x[h][k];
+        for (int j = 0; j < (BLOCKED ? 4 : 1); j++)
+            xrow[j] = BLOCKED ? token_row(g + 4 * j) + 8 * col : token_row(col) + 32 * g;
+        uint8_t *put = lds + w * kTile + g * kXStride + 16 * col;
+        const uint8_t *get = lds + w * kTile + col * kXStride + 64 * g;
+        auto load_x = [&](int q) {
+            if constexpr (!BLOCKED) return pr.load_x(xrow[0], q, nch);
+            const bool second = FMT != FMT_W4 || 2 * q + 1 < nch;
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    pr.x[h][j] = *(const u32x4 *)(xrow[j] + (long long)kChunk * (second ? 2 * q + h : 2 * q));
+        };
+        load_x(q);
+        auto acts = [&](int h, u32x4(&x)[1][4]) {
+            if constexpr (BLOCKED) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) *(u32x4 *)(put + (16 * h + 4 * j) * kXStride) = pr.x[h][j];
+                __builtin_amdgcn_wave_barrier();
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++) x[0][k] = BLOCKED ? *(const u32x4 *)(get + 16 * h * kXStride + 16 * k) : pr.x[h][k];
+            if constexpr (BLOCKED) __builtin_amdgcn_wave_barrier();
         };
         for (; q + 1 < pe; q++)
             multiply_pair<FMT, DT>(pr, src, q, nch, acc, acts, [&] {
                 pr.load_w(src, q + 1, nch);
-                pr.load_x(xrow, q + 1, nch);
+                load_x(q + 1);
             });
         multiply_pair<FMT, DT>(pr, src, q, nch, acc, acts, [] {});
     }
     if (a.kw > 1) {
+        if (BLOCKED) __syncthreads();  // the sums take the tiles' place
         red[w][0][lane] = acc[0][0];
         red[w][1][lane] = acc[0][1];
         __syncthreads();
@@ -311,7 +346,7 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
 #pragma unroll
     for (int c = 0; c < 4; c++) v[c] *= up[c];
     const int k = 16 * p + 4 * g;
-    uint16_t *h = m.H + (m.blocked ? hidden_at<true>(m.inter, i, k) : hidden_at<false>(m.inter, i, k));
+    uint16_t *h = m.H + hidden_at<BLOCKED>(m.inter, i, k);
     const u32x2 o = {pack_out<DT>(v[0], v[1]), pack_out<DT>(v[2], v[3])};
     *(u32x2 *)h = o;
 #pragma unroll

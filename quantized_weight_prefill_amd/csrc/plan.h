@@ -92,7 +92,7 @@ struct MoeArgs {
     const float *wts;    // [T][top_k]
     uint16_t *H;         // hidden, two planes (hidden_at): rounded, and the rest
     long long plane;     // elements of a plane
-    int blocked;         // the planes' layout
+    int blocked;         // full row tiles are likely: the kernels' BLOCKED form
     int T, top_k, inter;
     int parts;           // k_moe_down: K parts per row tile
     int strips;          // k_moe_down: strips of Y, of one or two panels

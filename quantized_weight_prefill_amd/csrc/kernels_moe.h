@@ -252,7 +252,8 @@ __device__ __forceinline__ void multiply_pair(const Pair<FMT, PN> &q, const RunS
 // serve many rows per expert too: a tile's second reading of the weights comes
 // from L2, and 32- and 64-row tiles, which unpack less, leave the chip emptier
 // (64 tokens, both of 2 to 8 experts: 13.5-18.1 us against 13.0-17.0 and
-// 17.5-24; 128 tokens, 8 of 16: 37.4 against 35.9 and 35.8).
+// 17.5-24; 128 tokens, 8 of 16: 37.4 against 35.9 and 35.8, before the LDS
+// tiles below, 36.0 with them).
 //
 // BLOCKED, where full tiles are likely (hidden_at): a load reads 256
 // consecutive bytes of four rows of x, and a tile of the wave's own in LDS turns

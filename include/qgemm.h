@@ -372,11 +372,11 @@ int qgemm_gemm_xf_noalloc(int format, int rung, const void *Xf, const void *Wpac
  * residual, act NONE and gated 0, Y (row-major) has the bits of
  * qgemm_gemm_rung / qgemm_gemm_xf on the same rung.
  * rung as in qgemm_gemm_rung; -1 takes the M-ladder of X's layout over the
- * packed columns (2N when gated), save that some calls of up to 64 rows that
- * are not gated go to direct-small-m where the products go to direct-skinny-n
- * or mfma32-64x32-k4 (qgemm_linear_select_rung says which).  The gated form has
- * no rung that splits K across workgroups: -1 picks the next best, and forcing
- * one is QGEMM_ERR_FORMAT.  Launches, errors and the workspace as there, plus
+ * packed columns (2N when gated), save that some calls that are not gated go to
+ * direct-small-m where the products go to direct-skinny-n or mfma32-64x32-k4
+ * (qgemm_linear_select_rung says which).  The gated form has no rung that splits
+ * K across workgroups: -1 picks the next best, and forcing one is
+ * QGEMM_ERR_FORMAT.  Launches, errors and the workspace as there, plus
  * QGEMM_ERR_FORMAT for an unknown layout or activation and QGEMM_ERR_SHAPE for
  * an N that gated or y_layout does not allow; M = 0 is a no-op.
  *

@@ -586,26 +586,31 @@ bool known_act(int act) { return act >= QGEMM_ACT_NONE && act <= QGEMM_ACT_GELU_
 // Up to four panels: the products give one wave all of them; one panel per wave
 // spreads the weights over as many CUs, at the price of reading X once per
 // panel (Q6_K 12288 -> 64: 1 and 16 rows 10.9 against 27.2 and 28.1 us, 64 rows
-// 20.8 against 28.4; W4A16 4096 -> 64, 64 rows 9.6 against 10.0; Q6_K 12288 ->
+// 20.8 against 28.4, 1024 rows 24.8 against 28.9; W4A16 4096 -> 64, 64 rows 9.6
+// against 10.0, 1024 rows 10.3 against 10.0, so it stops at 256; Q6_K 12288 ->
 // 32, 16 rows 10.9 against 16.2, but 33 rows 17.5 against 16.4, so two panels
 // change over at 16 rows).
 //
-// Row-major X, 17..64 rows: the linear layer's one-panel waves carry all rows,
-// their activations staged through LDS.  Weights rotating, K = 4096, against
-// 16-row groups of four panels per wave: 17 and 24 rows, W4A16 -> 4097 10.1 and
-// 10.9 against 11.0 and 11.2, -> 6144 10.9 and 11.6 against 11.2 and 11.3, Q4_K
-// -> 6144 11.3 and 11.9 against 13.0 and 13.1, Q6_K -> 8192 12.1 and 13.1
-// against 14.7 and 14.6; above 32 rows up to one panel per CU, -> 4096, 48 rows,
-// Q4_K 10.5 against 12.3, W4A16 10.6 against 11.4, 64 rows, Q4_K 12.1 against
-// 12.4, W4A16 12.8 against 11.7 (so W4A16 stops at 48).  Against 64x32 tiles, a
-// k-quant, 33 and 48 rows: Q4_K -> 6144 15.8 and 18.3 against 15.4 and 18.7, ->
-// 8192 14.8 and 16.5 against 15.8 and 19.2, Q6_K -> 8192 17.0 and 18.5 against
-// 17.7 and 20.7; W4A16 -> 6144 16.2 and 18.5 against 16.0 and 19.2 stays.
+// Row-major X: the linear layer's one-panel waves carry up to 64 rows, their
+// activations staged through LDS.  Against 16-row groups of four panels per wave
+// (weights rotating): 17 and 24 rows, K = 4096, W4A16 -> 4097 10.1 and 10.9
+// against 11.0 and 11.2, -> 6144 10.9 and 11.6 against 11.2 and 11.3, Q4_K ->
+// 6144 11.3 and 11.9 against 13.0 and 13.1, Q6_K -> 8192 12.1 and 13.1 against
+// 14.7 and 14.6; above 32 rows while they are one workgroup per CU at most, Q4_K
+// -> 4096, 48 rows 10.5 against 12.3, 64 rows 12.1 against 12.4, -> 2048, 128
+// rows 11.3 against 13.3, Q6_K -> 1024, 200 rows 11.5 against 13.6, Q4_K 9216 ->
+// 640, 80 and 360 rows 17.9 and 20.0 against 23.5 and 25.2, W4A16 -> 4096, 48
+// rows 10.6 against 11.4, 64 rows 12.8 against 11.7 and 8192 -> 640 no
+// difference (so W4A16 stops at 48).  Against 64x32 tiles, a k-quant, 33 and 48
+// rows, K = 4096: Q4_K -> 6144 15.8 and 18.3 against 15.4 and 18.7, -> 8192 14.8
+// and 16.5 against 15.8 and 19.2, Q6_K -> 8192 17.0 and 18.5 against 17.7 and
+// 20.7; W4A16 -> 6144 16.2 and 18.5 against 16.0 and 19.2 stays.
 bool one_panel_pays(int fmt, int r, int xl, long long m, long long np)
 {
-    if (np <= 4) return r == RUNG_SKINNY_N && (m <= 16 || (m <= 64 && np > 2));
+    const bool one_round = np * ((m + 63) / 64) <= kCUs;
+    if (np <= 4) return r == RUNG_SKINNY_N && (m <= 16 || (np > 2 && one_round && (fmt != FMT_W4 || m <= 256)));
     if (xl != X_ROW || m <= 16 || np > 2 * kCUs) return false;
-    if (r == RUNG_SKINNY_N) return m <= 32 || (np <= kCUs && m <= (fmt == FMT_W4 ? 48 : 64));
+    if (r == RUNG_SKINNY_N) return m <= 32 || (one_round && (fmt != FMT_W4 || m <= 48));
     return r == RUNG_M64N32_K4 && fmt != FMT_W4 && m > 32 && m <= 48;
 }
 

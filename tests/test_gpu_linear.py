@@ -111,6 +111,22 @@ def test_odd_sizes(fmt, M, N, K, dtype):
             assert bool((buf[M * N:] == 7.0).all())
 
 
+@pytest.mark.parametrize("fmt,M,N,K", [("q4k", 98, 640, 1024), ("q6k", 173, 61, 768), ("q4k", 17, 4112, 512), ("q6k", 300, 256, 512),
+                                       ("q4k", 48, 8192, 256), ("w4a16", 47, 1000, 384), ("w4a16", 200, 50, 640)])
+def test_one_panel_waves_through_the_ladder(fmt, M, N, K):
+    """Sizes whose ladder gives each wave one panel where the products share
+    four (in bf16; of 48 x 8192 fp16 has four, too), one row group and several."""
+    assert qg.linear_select_rung(fmt, M, N, K, False, qg.BF16)["name"] == "direct-small-m"
+    assert qg.select_rung(fmt, M, N, K, qg.BF16)["name"] != "direct-small-m"
+    for dtype in (qg.F16, qg.BF16):
+        p = Problem(fmt, M, N, K, dtype, 460)
+        y, d = p.want(True, True, "silu")
+        got = p.run(qg.X_ROW, True, True, "silu")
+        assert_within(got, y, d, dtype, f"{fmt} {M} {N} {K}")
+        if N % 128 == 0:
+            assert torch.equal(bits(p.run(qg.X_ROW, True, True, "silu", out_layout=qg.X_FRAG)), bits(frag(got)))
+
+
 @pytest.mark.parametrize("M", [1, 5, 17, 33, 40, 49, 65, 100])
 @pytest.mark.parametrize("gated", [False, True])
 def test_fragment_major_output_zeroes_its_padding(M, gated):

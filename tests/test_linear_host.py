@@ -67,11 +67,12 @@ def test_split_rungs():
 def test_plain_ladder_is_the_products(fmt, layout):
     sel = qg.select_rung if layout == qg.X_ROW else qg.select_rung_xf
     for M in (1, 7, 16, 17, 33, 48, 64, 65, 130, 400, 658, 2048):
-        for N, K in ((16, 256), (33, 512), (1024, 4096), (4096, 12288), (4128, 4096), (8192, 4096), (12288, 4096)):
+        for N, K in ((16, 256), (33, 512), (640, 9216), (1024, 4096), (4096, 12288), (4128, 4096), (8192, 4096), (12288, 4096)):
             for dt in (qg.F16, qg.BF16):
                 got, want = qg.linear_select_rung(fmt, M, N, K, False, dt, layout), sel(fmt, M, N, K, dt)
                 if got["name"] != want["name"]:  # a panel and all rows per wave, where the products share four panels
-                    assert got["name"] == "direct-small-m" and got["cols"] == 16 and got["rows"] >= min(M, 64) and M <= 64
+                    assert got["name"] == "direct-small-m" and got["cols"] == 16 and got["rows"] >= min(M, 64)
+                    assert M <= 64 or got["tiles_n"] * got["tiles_m"] <= 256
                     assert want["name"] == "direct-skinny-n" or (want["name"] == "mfma32-64x32-k4" and 32 < M <= 48)
                     assert N <= 64 or (layout == qg.X_ROW and M > 16)
                 elif N <= 64 and (M <= 16 or (M <= 64 and N > 32)):

@@ -142,7 +142,7 @@ def lib():
     torch is imported first so that opening libqgemm.so binds it to the HIP
     runtime already in the process: device pointers, streams and kernels then
     all belong to one runtime."""
-    global _lib
+    global _lib, _common_calls
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing; build it with `python -m quantized_weight_prefill_amd.build`")
@@ -153,12 +153,11 @@ def lib():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
-        _lib = handle
         from . import _calls as calls  # built beside libqgemm.so, linked to it and to torch
 
         calls.bind(torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-        global _common_calls
         _common_calls = calls
+        _lib = handle  # last: what sees it set finds the calls, too
     return _lib
 
 

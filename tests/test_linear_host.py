@@ -4,6 +4,9 @@ the gated form never asks for a rung that splits K across workgroups."""
 from __future__ import annotations
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -115,3 +118,17 @@ def test_binding_refusals():
         qg.linear("q4k", x[0], wp, N)
     with pytest.raises(qg.QGemmError):                  # N is no multiple of 128
         qg.linear("q4k", x, wp, N, out_layout=qg.X_FRAG)
+
+
+def test_missing_calls_module_fails_every_time():
+    """Without the C++ calls the library does not load, at the first use or a
+    later one (in a process of its own: here it is loaded)."""
+    code = ("import sys, quantized_weight_prefill_amd as qg\n"
+            "sys.modules['quantized_weight_prefill_amd._calls'] = None\n"
+            "n = 0\n"
+            "for _ in range(2):\n"
+            "    try: qg.lib()\n"
+            "    except ImportError: n += 1\n"
+            "assert n == 2, n\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(qg.__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=300)

@@ -818,7 +818,7 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     m.top_k = (int)k;
     m.inter = (int)I;
 
-    const long long tiles = moe_tiles(P, E);
+    const long long tiles = moe_tiles(P, E, 16);
     // two panels per workgroup of the down product where the row tiles give
     // its waves two each: h is then read once for both panels, by half as many
     // workgroups, each over half the tiles (64 tokens, 8 of 128 experts, 768 ->

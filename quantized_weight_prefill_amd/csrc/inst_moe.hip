@@ -23,7 +23,7 @@ template <int FMT, int PN, bool BLOCKED>
 void launch_down(int dtype, dim3 grid, const MoeArgs &m, hipStream_t s)
 {
     const dim3 block(64 * kMoeDownWaves);
-    const size_t lds = moe_down_lds(m.g.M, m.g.E, m.parts, PN);
+    const size_t lds = moe_down_lds(m.g.M, m.g.E, m.parts, PN, moe_down_rows(BLOCKED));
     if (dtype == DT_F16) hipLaunchKernelGGL((k_moe_down<FMT, DT_F16, PN, BLOCKED>), grid, block, lds, s, m);
     else hipLaunchKernelGGL((k_moe_down<FMT, DT_BF16, PN, BLOCKED>), grid, block, lds, s, m);
 }

@@ -22,11 +22,14 @@
 //     floating-point atomics, and a result that does not depend on timing.
 // h goes to memory as its rounding to the operand type and what that rounding
 // left, and the second product takes both, so h has twice the type's bits and
-// the layer's error is that of Y's one rounding: with a few rows to a tile in
-// the MFMA columns that would be idle, for free, with full tiles as a second
-// MFMA on the same unpacked weights.  (Where tiles are few rows on average, one
-// of more than eight, a popular expert's, takes the rounding alone.)  The sum
-// over a token's experts stays in fp32 until the one store.
+// the layer's error is that of Y's one rounding: with a few rows per expert in
+// the MFMA columns that tiles of eight rows leave idle, with full tiles of
+// sixteen as a second MFMA on the same unpacked weights.  (With a few rows per
+// expert on average a popular one's weights are unpacked once per eight of its
+// rows; against tiles of sixteen with the rounding alone, the whole layer: 64
+// tokens, 8 of 128 experts, 97.0 against 96.4 us, every token with one expert in
+// common 98.7 against 96.0; 32 tokens on one of eight experts 16.4 against 15.0.)
+// The sum over a token's experts stays in fp32 until the one store.
 #pragma once
 
 #include <algorithm>
@@ -36,9 +39,9 @@
 
 namespace qg {
 
-inline size_t moe_down_lds(long long pairs, long long E, int parts, int pn)
+inline size_t moe_down_lds(long long pairs, long long E, int parts, int pn, int rows)
 {
-    const long long slots = moe_tiles(pairs, E);
+    const long long slots = moe_tiles(pairs, E, rows);
     return (size_t)(parts * pairs * 64 * pn + slots * 12 + pairs * 5);
 }
 
@@ -72,12 +75,12 @@ __device__ __forceinline__ int wave_scan_max(int x)
     return x;
 }
 
-// The experts' row tiles of 16 rows, in expert order, 64 experts at a
+// The experts' row tiles of ROWS rows, in expert order, 64 experts at a
 // time, a lane per expert: visit(lane's expert, its first row, its end, its
 // tile count, the tiles before it) until it returns true.  Offsets are
 // clamped into [0, P] and made non-decreasing as the grouped GEMM does, so
 // any contents stay inside the buffers.  Returns the tiles visited over.
-template <class F>
+template <int ROWS, class F>
 __device__ __forceinline__ int visit_tiles(const Args &a, int lane, F visit)
 {
     constexpr int G = 4;  // groups of 64 experts whose offsets are loaded together
@@ -96,7 +99,7 @@ __device__ __forceinline__ int visit_tiles(const Args &a, int lane, F visit)
             const int qi = max(wave_scan_max(q[i]), qc);                                 // max(0, offs[0..e+1])
             const int qp = __builtin_amdgcn_update_dpp(qc, qi, 0x138, 0xF, 0xF, false);  // wave_shr:1, lane 0 keeps qc
             const int lo = min(qp, a.M), hi = min(qi, a.M);
-            const int nb = e < a.E ? (hi - lo + 15) / 16 : 0;
+            const int nb = e < a.E ? (hi - lo + ROWS - 1) / ROWS : 0;
             const int incl = wave_scan_add(nb);
             if (visit(e, lo, hi, nb, base + incl - nb)) return base;
             base += __builtin_amdgcn_readlane(incl, 63);
@@ -106,13 +109,13 @@ __device__ __forceinline__ int visit_tiles(const Args &a, int lane, F visit)
     return base;
 }
 
-// Row tile j: expert e, rows [lo, hi) of the expert, tile t of it; false when
-// j is past the last tile.  The same answer in every lane.
+// Row tile j of 16 rows: expert e, rows [lo, hi) of the expert, tile t of it;
+// false when j is past the last tile.  The same answer in every lane.
 __device__ __forceinline__ bool find_moe_tile(const Args &a, int j, int lane, int &e_out, int &lo_out,
                                               int &hi_out, int &t_out)
 {
     bool found = false;
-    visit_tiles(a, lane, [&](int e, int lo, int hi, int nb, int before) {
+    visit_tiles<16>(a, lane, [&](int e, int lo, int hi, int nb, int before) {
         const unsigned long long hit = __ballot(j >= before && j < before + nb);
         if (hit == 0ull) return false;
         const int l = __builtin_amdgcn_readfirstlane(__ffsll((long long)hit) - 1);
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(64 * kMoeUpWaves) k_moe_up(MoeArgs m)
 
 // Grid: x = strips of Y (PN panels each) times split.  Dynamic LDS
 // (moe_down_lds): parts * pairs * 16 PN floats, the row tiles (expert, first
-// row, end of the expert's rows), the sorted pairs, and a flag per pair that
+// row, end), the sorted pairs, and a flag per pair that
 // some expert has computed it: a pair that no expert here serves adds nothing,
 // whatever its weight holds.
 //
@@ -368,6 +371,7 @@ template <int FMT, int DT, int PN, bool BLOCKED>
 __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
 {
     constexpr int NW = kMoeDownWaves, CW = 16 * PN, QW = 4 * PN;  // columns and quads of a strip's row
+    constexpr int ROWS = moe_down_rows(BLOCKED);
     extern __shared__ float sums[];  // [parts][pairs][CW]
     __shared__ int s_tiles, s_last;
     const Args &a = m.g;
@@ -376,7 +380,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
     const int P = a.M, span = P * CW;
     const int strip = blockIdx.x / m.split, slice = blockIdx.x - strip * m.split;
     int *tile_e = (int *)(sums + (size_t)m.parts * span);
-    const int slots = (int)moe_tiles(P, a.E);
+    const int slots = (int)moe_tiles(P, a.E, ROWS);
     int *tile_lo = tile_e + slots, *tile_hi = tile_lo + slots;
     int *pair_of = tile_hi + slots;
     uint8_t *served = (uint8_t *)(pair_of + P);
@@ -385,11 +389,11 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
         served[i] = 0;
     }
     if (w == 0) {
-        const int n = visit_tiles(a, lane, [&](int e, int lo, int hi, int nb, int before) {
+        const int n = visit_tiles<ROWS>(a, lane, [&](int e, int lo, int hi, int nb, int before) {
             for (int j = 0; j < nb; j++) {
                 tile_e[before + j] = e;
-                tile_lo[before + j] = lo + 16 * j;
-                tile_hi[before + j] = hi;
+                tile_lo[before + j] = lo + ROWS * j;
+                tile_hi[before + j] = min(lo + ROWS * (j + 1), hi);
             }
             return false;
         });
@@ -415,9 +419,9 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
     RunSrc<FMT> src[PN];   // at the front cursor's expert
     const uint16_t *xrow;  // at the front cursor's rows; BLOCKED: at the back cursor's
     auto rows_at = [&](const Cursor &q) {
-        const bool few = !BLOCKED && q.hi - q.lo <= 8;  // columns 8..15 take the low parts of the rows in 0..7
-        const int i = min(q.lo + (few ? col & 7 : col), q.hi - 1);
-        xrow = m.H + (few && col > 7 ? m.plane : 0) + hidden_at<BLOCKED>(a.K, i, 32 * g);
+        const int i = min(q.lo + (col & (ROWS - 1)), q.hi - 1);
+        // plain: columns 8..15 take the low parts of the rows in 0..7
+        xrow = m.H + (!BLOCKED && col > 7 ? m.plane : 0) + hidden_at<BLOCKED>(a.K, i, 32 * g);
     };
     auto aim = [&](Cursor &q) {
         const int e = open(q);
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
                 if constexpr (BLOCKED) {
 #pragma unroll
                     for (int pn = 0; pn < PN; pn++) acc[0][pn] += acc[1][pn] * (1.0f / kLowScale<DT>);
-                } else if (back.hi - back.lo <= 8) {
+                } else {
 #pragma unroll
                     for (int c = 0; c < QW; c++) {
                         const float y = acc[0][c >> 2][c & 3];

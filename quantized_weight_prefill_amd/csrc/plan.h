@@ -102,10 +102,13 @@ struct MoeArgs {
 };
 constexpr int kMoeUpWaves = 8;     // waves of a k_moe_up workgroup
 constexpr int kMoeDownWaves = 16;  // of a k_moe_down workgroup: at 128 VGPRs a wave it fills a CU
-// A bound on the experts' 16-row tiles.
-__host__ __device__ inline long long moe_tiles(long long pairs, long long E)
+// Rows of a k_moe_down tile: sixteen, or eight where the other MFMA columns
+// hold what the rounding of h left of the same rows.
+constexpr int moe_down_rows(bool blocked) { return blocked ? 16 : 8; }
+// A bound on the experts' tiles of `rows` rows.
+__host__ __device__ inline long long moe_tiles(long long pairs, long long E, int rows)
 {
-    const long long n = (pairs + 15) / 16 + E;
+    const long long n = (pairs + rows - 1) / rows + E;
     return pairs < n ? pairs : n;
 }
 template <int FMT>

@@ -504,7 +504,9 @@ int qgemm_moe_group(const int32_t *ids, int64_t T, int64_t E, int64_t top_k, int
  *   h[p] = act(x_t . Wg_e) * (x_t . Wu_e)                    p = t*top_k + j, e its expert
  *   Y[t] = RN_t( residual[t] + sum_j weights[t][j] * (h[p] . Wd_e) )
  * h is held to twice the type's bits, as RN_t(h) and the rounding of what that
- * left.  Where |h| is beyond the type's range it is infinite.
+ * left.  Where |h| is beyond the type's range it is infinite, and a weight that
+ * its rounding made infinite gives infinite outputs of the sign of RN_t(h) (NaN
+ * where RN_t(h) is 0).
  * X [T][hidden], Y and residual (may be NULL) [T][hidden], all row-major of
  * type dtype.  Wup: E packed weights of 2*inter columns over K = hidden (the
  * gate's columns, then the up projection's), format_up; Wdown: E packed

@@ -176,6 +176,16 @@ __device__ __forceinline__ float low_part(float v, uint32_t bits16)
     return fabsf(hi) < __builtin_inff() ? (v - hi) * kLowScale<DT> : 0.0f;
 }
 
+// A sum over RN(h) with the sum over what the rounding left, which is small
+// beside it unless a weight or a product is infinite: there the two meet the
+// same infinity with signs of their own (or 0), and the definition's answer is
+// the rounding's.
+template <int DT>
+__device__ __forceinline__ float join_parts(float hi, float low)
+{
+    return fabsf(low) < __builtin_inff() ? __builtin_fmaf(low, 1.0f / kLowScale<DT>, hi) : hi;
+}
+
 // Element k (a multiple of 4) of sorted row i in a plane of the hidden matrix.
 // Plain, for at most four pairs per expert: row-major.  BLOCKED, above: blocks
 // of 16 rows, a chunk of 128 after the other, and inside a chunk the rows'
@@ -467,13 +477,14 @@ __global__ void __launch_bounds__(64 * kMoeDownWaves, 4) k_moe_down(MoeArgs m)
                 const int i = back.lo + col;
                 if constexpr (BLOCKED) {
 #pragma unroll
-                    for (int pn = 0; pn < PN; pn++) acc[0][pn] += acc[1][pn] * (1.0f / kLowScale<DT>);
+                    for (int c = 0; c < QW; c++)
+                        acc[0][c >> 2][c & 3] = join_parts<DT>(acc[0][c >> 2][c & 3], acc[1][c >> 2][c & 3]);
                 } else {
 #pragma unroll
                     for (int c = 0; c < QW; c++) {
                         const float y = acc[0][c >> 2][c & 3];
                         const int low = dpp_from<0x128, 0xF>(__builtin_bit_cast(int, y), 0);  // row_ror:8
-                        acc[0][c >> 2][c & 3] = __builtin_fmaf(__builtin_bit_cast(float, low), 1.0f / kLowScale<DT>, y);
+                        acc[0][c >> 2][c & 3] = join_parts<DT>(y, __builtin_bit_cast(float, low));
                     }
                 }
                 if (i < back.hi) {

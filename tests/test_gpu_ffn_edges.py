@@ -66,3 +66,45 @@ def test_moe_keeps_both_parts_of_h_whatever_an_experts_share(T, E, share, dtype)
     y = square_layer(x64, popular(T, E, share, rng), E, dtype, eye_fields(n), residual=res.cuda())
     bad = (y != left).any(1).nonzero().flatten().tolist()
     assert not bad, f"{len(bad)} rows differ, first {bad[:8]}"
+
+
+@pytest.mark.parametrize("T,E", [(3, 2), (20, 8), (40, 2), (1024, 300), (1024, 200)])
+def test_moe_infinite_weights(T, E):
+    """A weight beyond fp16's range is an infinity, and an output takes its
+    sign whatever the rounding of h left: few pairs per expert and many, one
+    panel of Y per workgroup and two."""
+    n = 256
+    rng = np.random.default_rng(1300 + T)
+    x64 = torch.from_numpy(rng.integers(1, 256, (T, n)).astype(np.float64))
+    down = eye_fields(n)
+    w = torch.eye(n, dtype=torch.float64)           # [K][N]
+    for col, k in ((5, 7), (130, 200)):             # 2 * 65504 * 1 in one row of the column
+        down["d"][col, 0], down["sc"][col, 0, k // 32] = 0x7BFF, 2
+        down["q"][col] = 0
+        down["q"][col, k] = 1
+        w[:, col] = 0
+        w[k, col] = math.inf
+    down["d"][77, 0], down["dmin"][77, 0] = 0, 0x7BFF  # 0 - 65504 * 2 in a whole sub-block
+    down["m"][77, 0, 3] = 2
+    w[:, 77] = 0
+    w[96:128, 77] = -math.inf
+    h = x64 * x64
+    want = torch.where(torch.isinf(w).any(0), torch.where(w.sum(0) > 0, math.inf, -math.inf), h).to(torch.float16).double()
+    low = h - h.half().double()
+    assert all(bool((low[:, 7].sign() == s).any()) or T < 20 for s in (-1, 0, 1))
+    y = square_layer(x64, popular(T, E, 0.2, rng), E, qg.F16, down)
+    assert torch.equal(y, want), (y != want).nonzero()[:5]
+
+
+def test_moe_products_beyond_binary32():
+    """h * w above the largest float is an infinity in bf16, and what the
+    rounding of h left does not turn it into a NaN."""
+    n, T = 256, 12
+    x64 = torch.full((T, n), 1.0e19, dtype=torch.float64) * (1 + torch.arange(n) / 512.0)
+    x64 = x64.bfloat16().double()
+    down = eye_fields(n)
+    down["sc"][:] = 63
+    for E in (2, 8):
+        y = square_layer(x64, [i % E for i in range(T)], E, qg.BF16, down)
+        assert bool((x64 * x64 < 3.3e38).all()) and bool((x64 * x64 * 63 > 3.5e38).all())
+        assert bool((y == math.inf).all())

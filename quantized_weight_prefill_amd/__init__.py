@@ -30,6 +30,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import numpy as np
@@ -540,6 +541,19 @@ def _check_bytes(name, wp, need):
         raise ValueError(f"{name} holds {wp.nbytes} bytes, the packed weight needs {need}")
 
 
+def _apart(what, t, size, others, same=()):
+    """Refuse `t`, written by the call, when its `size` bytes share memory with
+    another of the call's tensors ((name, tensor, bytes)); it may be one of
+    those named in `same` itself."""
+    if t is None or size == 0:
+        return
+    a = t.data_ptr()
+    for name, o, n in others:
+        b = 0 if o is None or n == 0 else o.data_ptr()
+        if b and a < b + n and b < a + size and not (name in same and a == b):
+            raise ValueError(f"{what} shares memory with {name}")
+
+
 def _scratch(need: int, workspace, ref, stream):
     """(pointer, bytes, tensor to keep) of the caller's workspace, or of one
     from torch's allocator, which is told of a stream that is not its own."""
@@ -604,10 +618,14 @@ def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_
             or (out is not None and not _fits(out, index, shape, dt))):
         _refuse((("x", x, None, None), ("wp", wp, None, None), ("bias", bias, (2 * N if gated else N,), dt),
                  ("residual", residual, (M, N), dt), ("out", out, shape, dt)))
+    if out is not None or workspace is not None:
+        inputs = (("x", x, xf_bytes(M, K) if layout == X_FRAG else 2 * M * K), ("wp", wp, packed),
+                  ("bias", bias, 4 * N if gated else 2 * N), ("residual", residual, 2 * M * N))
+        out_bytes = 2 * math.prod(shape)
+        _apart("out", out, out_bytes, inputs, ("residual",) if out_layout == X_ROW else ())
+        _apart("workspace", workspace, need, (*inputs, ("out", out, out_bytes)))
     if out is None:
         out = x.new_empty(shape)
-    elif out_layout == X_FRAG and residual is not None and out.data_ptr() == residual.data_ptr():
-        raise ValueError("a fragment-major out cannot be the residual")
     ws, wsb, _keep = _scratch(need, workspace, x, stream)
     _call("qgemm_linear", index, stream, f, rung, layout, x.data_ptr(), wp.data_ptr(),
           None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(),
@@ -622,7 +640,8 @@ def linear(fmt, x, wp, N: int, bias=None, residual=None, act: str = "none", gate
     Y = act(X . Wg + bias_g) * (X . Wu + bias_u) + residual.
 
     ``act`` is a key of :data:`ACTS`; bias [N] ([2N] when gated) and residual
-    [M, N] have x's dtype; ``out`` may be the residual.  ``out_layout`` X_FRAG
+    [M, N] have x's dtype; a row-major ``out`` may be the residual, and shares
+    memory with no other argument.  ``out_layout`` X_FRAG
     returns the fragment-major copy of Y (what :func:`x_to_xf` would make of
     it), the input of the next :func:`linear_xf` or :func:`gemm_xf`."""
     if x.dim() != 2:
@@ -947,7 +966,8 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
     w_up: E packed weights of 2*inter columns over K = H (gate, then up);
     w_down: E packed weights of H columns over K = inter; weights [T, top_k]
     float32, offsets [E+1] and rows [T*top_k] from :func:`moe_route` or
-    :func:`moe_group`.  ``out`` may be the residual."""
+    :func:`moe_group`.  ``out`` may be the residual or x, and shares memory with
+    no other argument."""
     if stream is None and workspace is None:
         y = _common("qgemm_moe", "moe", (FORMATS.get(fmt_up, fmt_up), FORMATS.get(fmt_down, fmt_down), x, w_up, w_down,
                                          weights, offsets, rows, inter, group, has_zp, ACTS.get(act), residual, out))
@@ -976,6 +996,12 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
     _check_bytes("w_down", w_down, down_bytes)
     if need == 0 and T > 0:
         raise QGemmError("qgemm_moe", -2)
+    if out is not None or workspace is not None:
+        inputs = (("x", x, 2 * T * H), ("residual", residual, 2 * T * H), ("w_up", w_up, up_bytes),
+                  ("w_down", w_down, down_bytes), ("weights", weights, 4 * T * k), ("offsets", offsets, 4 * (E + 1)),
+                  ("rows", rows, 4 * T * k))
+        _apart("out", out, 2 * T * H, inputs, ("x", "residual"))
+        _apart("workspace", workspace, need, (*inputs, ("out", out, 2 * T * H)))
     if out is None:
         out = torch.empty_like(x)
     ws, wsb, _keep = _scratch(need, workspace, x, stream)

@@ -104,6 +104,14 @@ void holds(PyObject *w, size_t need)
     if (tensor(w).nbytes() < need) throw Bad{};
 }
 
+// The caller's `out` (`bytes` from `y`) shares memory with an input, of n
+// bytes: not a call for here.
+void apart(const void *y, size_t bytes, const void *p, size_t n)
+{
+    const uintptr_t a = (uintptr_t)y, b = (uintptr_t)p;
+    if (p && a < b + n && b < a + bytes) throw Bad{};
+}
+
 // The body of a function: its result, None for an uncommon call, or the
 // library's status when that is not QGEMM_OK.
 template <class F>
@@ -139,13 +147,20 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n)
         const at::ScalarType type = x.scalar_type();
         const void *xp = data(a[2], index), *wp = data(a[3], index);
         const void *bp = data(a[7], index, type, {nt}), *rp = data(a[8], index, type, {M, N});
-        holds(a[3], packed(fmt, nt, K, group, zp));
+        const size_t wb = packed(fmt, nt, K, group, zp);
+        holds(a[3], wb);
         const int64_t flat = (int64_t)(qgemm_xf_bytes(M, N) / 2);
         if (yl != QGEMM_X_ROW && (yl != QGEMM_X_FRAG || flat == 0)) throw Bad{};
         const int64_t rows[2] = {M, N}, frag[1] = {flat};
         const at::IntArrayRef shape = yl == QGEMM_X_ROW ? at::IntArrayRef(rows, 2) : at::IntArrayRef(frag, 1);
         void *yp = data(a[14], index, type, shape);
-        if (yp && yl == QGEMM_X_FRAG && yp == rp) throw Bad{};
+        if (yp) {
+            const size_t yb = tensor(a[14]).nbytes();
+            apart(yp, yb, xp, xl == QGEMM_X_FRAG ? qgemm_xf_bytes(M, K) : (size_t)(2 * M * K));
+            apart(yp, yb, wp, wb);
+            apart(yp, yb, bp, (size_t)(2 * nt));
+            if (yl == QGEMM_X_FRAG || yp != rp) apart(yp, yb, rp, (size_t)(2 * M * N));
+        }
         void *s = stream_of(index);
         const at::Tensor y = yp ? tensor(a[14]) : at::empty(shape, x.options());
         if (!yp) yp = y.data_ptr();
@@ -236,9 +251,20 @@ PyObject *moe(PyObject *, PyObject *const *a, Py_ssize_t n)
         const void *xp = data(a[2], index), *up = data(a[3], index), *dp = data(a[4], index);
         const void *wt = data(a[5], index, at::kFloat, {T, k}), *op = data(a[6], index, at::kInt, {E + 1});
         const void *rp = data(a[7], index, at::kInt, {T * k}), *res = data(a[12], index, x.scalar_type(), {T, H});
-        holds(a[3], (size_t)E * packed(fu, 2 * inter, H, group, zp));
-        holds(a[4], (size_t)E * packed(fd, H, inter, group, zp));
+        const size_t ub = (size_t)E * packed(fu, 2 * inter, H, group, zp), db = (size_t)E * packed(fd, H, inter, group, zp);
+        holds(a[3], ub);
+        holds(a[4], db);
         void *yp = data(a[13], index, x.scalar_type(), {T, H});
+        if (yp) {
+            const size_t yb = (size_t)(2 * T * H);
+            if (yp != xp) apart(yp, yb, xp, yb);
+            if (yp != res) apart(yp, yb, res, yb);
+            apart(yp, yb, up, ub);
+            apart(yp, yb, dp, db);
+            apart(yp, yb, wt, (size_t)(4 * T * k));
+            apart(yp, yb, op, (size_t)(4 * (E + 1)));
+            apart(yp, yb, rp, (size_t)(4 * T * k));
+        }
         const size_t need = qgemm_moe_workspace_bytes(T, k, H, inter);
         if (need == 0) throw Bad{};
         void *s = stream_of(index);

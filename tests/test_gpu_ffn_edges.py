@@ -108,3 +108,69 @@ def test_moe_products_beyond_binary32():
         y = square_layer(x64, [i % E for i in range(T)], E, qg.BF16, down)
         assert bool((x64 * x64 < 3.3e38).all()) and bool((x64 * x64 * 63 > 3.5e38).all())
         assert bool((y == math.inf).all())
+
+
+def test_buffers_that_share_memory_are_refused():
+    """A result that overlaps an input would depend on which workgroup comes
+    first; the residual in place, and the layer's x, are what is allowed."""
+    rng = np.random.default_rng(1400)
+    M, n = 40, 512
+    wp = bytes_to_device(pack(synth.q4k_fields(rng, n, n), n, n))
+    flat = torch.randn(3 * M * n, device="cuda").half()
+    x, res = flat[:M * n].view(M, n), flat[M * n:2 * M * n].view(M, n)
+    shifted = flat[M * n + n:2 * M * n + n].view(M, n)   # the residual from its second row on
+    bias = torch.randn(n, device="cuda").half()
+    with_bias = flat[2 * M * n:].view(M, n)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    split = [r for r in range(qg.num_rungs()) if qg.rung_name(r) == "mfma32-64x64-sk"][0]
+    need = qg.workspace_bytes("q4k", split, M, n, n)
+    xf = qg.x_to_xf(x)
+    before = flat.clone()
+    for kw in (dict(), dict(workspace=ws)):            # the common calls and the others
+        for bad in (dict(out=x), dict(out=x, residual=x), dict(out=shifted, residual=res),
+                    dict(out=with_bias, bias=with_bias[-1])):
+            with pytest.raises(ValueError, match="shares memory"):
+                qg.linear("q4k", x, wp, n, **bad, **kw)
+        with pytest.raises(ValueError, match="shares memory"):
+            qg.linear_xf("q4k", xf, wp, M, n, n, out=xf, out_layout=qg.X_FRAG, **kw)
+        buf = torch.zeros(qg.xf_bytes(M, n) // 2, dtype=torch.float16, device="cuda")
+        with pytest.raises(ValueError, match="shares memory"):
+            qg.linear("q4k", x, wp, n, residual=buf[:M * n].view(M, n), out=buf, out_layout=qg.X_FRAG, **kw)
+    for bad in (flat, wp):
+        with pytest.raises(ValueError, match="workspace shares memory"):
+            qg.linear("q4k", x, wp, n, rung=split, workspace=bad)
+    with pytest.raises(ValueError, match="workspace shares memory"):
+        inside = ws[need - 16:need - 16 + 2 * M * n].view(torch.float16).view(M, n)
+        qg.linear("q4k", x, wp, n, rung=split, out=inside, workspace=ws[:need])
+    assert torch.equal(flat, before)
+    # side by side in one allocation is no overlap
+    y = qg.linear("q4k", x, wp, n, bias=bias, residual=res)
+    assert torch.equal(qg.linear("q4k", x, wp, n, bias=bias, residual=res, out=with_bias), y)
+    assert torch.equal(qg.linear("q4k", x, wp, n, bias=bias, residual=res, out=res), y)
+
+    T, k, E, H, I = 6, 2, 4, 512, 256
+    up = bytes_to_device(np.tile(pack(synth.q4k_fields(rng, 2 * I, H), 2 * I, H), E))
+    down = bytes_to_device(np.tile(pack(synth.q4k_fields(rng, H, I), H, I), E))
+    ids, w, offs, rows = qg.moe_route(torch.randn((T, E), device="cuda"), k)
+    both = (torch.randn((2 * T, H), device="cuda") * 0.01).half()
+    tx, tr = both[:T], both[T:]
+    ws = torch.empty(qg.moe_workspace_bytes(T, k, H, I), dtype=torch.uint8, device="cuda")
+    args = ("q4k", "q4k", tx, up, down, w, offs, rows, I)
+    before = both.clone()
+    for kw in (dict(), dict(workspace=ws)):
+        for out in (both[1:T + 1], *(t[:2 * T * H].view(torch.float16).view(T, H) for t in (up, down))):
+            with pytest.raises(ValueError, match="shares memory"):
+                qg.moe(*args, out=out, **kw)
+        with pytest.raises(ValueError, match="shares memory"):
+            qg.moe(*args, residual=tr, out=both[T - 1:2 * T - 1], **kw)
+    for bad in (up, down):
+        with pytest.raises(ValueError, match="workspace shares memory"):
+            qg.moe(*args, workspace=bad)
+    assert torch.equal(both, before)
+    y = qg.moe(*args, residual=tr)
+    assert torch.equal(qg.moe(*args, residual=tr, out=tx.clone()), y)
+    for kw in (dict(), dict(workspace=ws)):
+        both.copy_(before)
+        assert torch.equal(qg.moe(*args, residual=tr, out=tr, **kw), y)
+        both.copy_(before)
+        assert torch.equal(qg.moe(*args, residual=tr, out=tx, **kw), y)

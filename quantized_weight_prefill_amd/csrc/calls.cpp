@@ -99,6 +99,14 @@ size_t packed(int fmt, int64_t N, int64_t K, int64_t group, int has_zp)
     return n;
 }
 
+// Bytes of E weights of `each`, where they can be counted at all: a product
+// that wraps around would pass for a small one.
+size_t of_experts(int64_t E, size_t each)
+{
+    if (each > SIZE_MAX / (size_t)E) throw Bad{};
+    return (size_t)E * each;
+}
+
 void holds(PyObject *w, size_t need)
 {
     if (tensor(w).nbytes() < need) throw Bad{};
@@ -251,7 +259,8 @@ PyObject *moe(PyObject *, PyObject *const *a, Py_ssize_t n)
         const void *xp = data(a[2], index), *up = data(a[3], index), *dp = data(a[4], index);
         const void *wt = data(a[5], index, at::kFloat, {T, k}), *op = data(a[6], index, at::kInt, {E + 1});
         const void *rp = data(a[7], index, at::kInt, {T * k}), *res = data(a[12], index, x.scalar_type(), {T, H});
-        const size_t ub = (size_t)E * packed(fu, 2 * inter, H, group, zp), db = (size_t)E * packed(fd, H, inter, group, zp);
+        const size_t ub = of_experts(E, packed(fu, 2 * inter, H, group, zp));
+        const size_t db = of_experts(E, packed(fd, H, inter, group, zp));
         holds(a[3], ub);
         holds(a[4], db);
         void *yp = data(a[13], index, x.scalar_type(), {T, H});

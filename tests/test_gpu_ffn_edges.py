@@ -174,3 +174,16 @@ def test_buffers_that_share_memory_are_refused():
         assert torch.equal(qg.moe(*args, residual=tr, out=tr, **kw), y)
         both.copy_(before)
         assert torch.equal(qg.moe(*args, residual=tr, out=tx, **kw), y)
+
+
+def test_moe_weight_bytes_beyond_64_bits():
+    """Experts whose packed bytes add up to a multiple of 2^64: refused by
+    their size, not taken for weights of no bytes."""
+    E, H, I = 1 << 24, 1 << 20, 1 << 26
+    up, down = (qg.packed_bytes("w4a16", n, k, 128) for n, k in ((2 * I, H), (H, I)))
+    assert up > 0 and E * up % 2 ** 64 == 0 and E * down % 2 ** 64 == 0
+    x = torch.zeros((1, H), dtype=torch.float16, device="cuda")
+    w = torch.zeros(1024, dtype=torch.uint8, device="cuda")
+    offs = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="w_up holds 1024 bytes"):
+        qg.moe("w4a16", "w4a16", x, w, w, torch.ones((1, 1), device="cuda"), offs, offs[:1].clone(), I, group=128)

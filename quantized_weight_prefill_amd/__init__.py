@@ -554,9 +554,28 @@ def _apart(what, t, size, others, same=()):
             raise ValueError(f"{what} shares memory with {name}")
 
 
+def _allocate(stream, index, make, returned=True):
+    """The tensors of make(), for a call on `stream`: from that stream's own
+    memory, since a block of the current stream's may still be in use by work
+    queued there.  Those that the call returns are kept for the current
+    stream's later work, too."""
+    if stream is None:
+        return make()
+    cuda = _torch().cuda
+    current = cuda.current_stream(index)
+    if stream == current.cuda_stream:
+        return make()
+    with cuda.stream(cuda.ExternalStream(stream, device=index) if stream else cuda.default_stream(index)):
+        made = make()
+    if returned:
+        for t in made:
+            t.record_stream(current)
+    return made
+
+
 def _scratch(need: int, workspace, ref, stream):
     """(pointer, bytes, tensor to keep) of the caller's workspace, or of one
-    from torch's allocator, which is told of a stream that is not its own."""
+    from torch's allocator."""
     if workspace is not None:
         if workspace.device != ref.device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the activations' device")
@@ -564,9 +583,8 @@ def _scratch(need: int, workspace, ref, stream):
     if not need:
         return None, 0, None
     torch = _torch()
-    ws = torch.empty(need, dtype=torch.uint8, device=ref.device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=ref.device))
+    index = ref.get_device()
+    (ws,) = _allocate(stream, index, lambda: (torch.empty(need, dtype=torch.uint8, device=ref.device),), returned=False)
     return ws.data_ptr(), need, ws
 
 
@@ -625,7 +643,7 @@ def _linear(fmt, layout, x, wp, M, N, K, bias, residual, act, gated, group, has_
         _apart("out", out, out_bytes, inputs, ("residual",) if out_layout == X_ROW else ())
         _apart("workspace", workspace, need, (*inputs, ("out", out, out_bytes)))
     if out is None:
-        out = x.new_empty(shape)
+        (out,) = _allocate(stream, index, lambda: (x.new_empty(shape),))
     ws, wsb, _keep = _scratch(need, workspace, x, stream)
     _call("qgemm_linear", index, stream, f, rung, layout, x.data_ptr(), wp.data_ptr(),
           None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(),
@@ -643,7 +661,9 @@ def linear(fmt, x, wp, N: int, bias=None, residual=None, act: str = "none", gate
     [M, N] have x's dtype; a row-major ``out`` may be the residual, and shares
     memory with no other argument.  ``out_layout`` X_FRAG
     returns the fragment-major copy of Y (what :func:`x_to_xf` would make of
-    it), the input of the next :func:`linear_xf` or :func:`gemm_xf`."""
+    it), the input of the next :func:`linear_xf` or :func:`gemm_xf`.
+    ``stream`` is a raw stream handle (None: the current stream); what the call
+    allocates then belongs to that stream."""
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
@@ -908,7 +928,7 @@ def moe_route(logits, top_k: int, score: str = "softmax", renorm: bool = True, s
     P = T * top_k
     # one allocation for the four results
     new = torch.empty if T else torch.zeros  # no tokens: every offset is 0
-    buf = new(3 * P + E + 1, dtype=torch.int32, device=logits.device)
+    (buf,) = _allocate(stream, index, lambda: (new(3 * P + E + 1, dtype=torch.int32, device=logits.device),))
     ids, weights, offsets, rows = buf.split_with_sizes((P, P, E + 1, P))
     p = buf.data_ptr()
     _call("qgemm_moe_route", index, stream, logits.data_ptr(), lt, T, E, top_k, SCORES[score], 1 if renorm else 0, scale,
@@ -932,8 +952,7 @@ def moe_group(ids, E: int, stream=None):
     index = ids.get_device()
     if index < 0 or not ids.is_contiguous():
         _refuse((("ids", ids, None, None),))
-    offsets = ids.new_empty(max(E, 0) + 1)
-    rows = ids.new_empty(T * k)
+    offsets, rows = _allocate(stream, index, lambda: (ids.new_empty(max(E, 0) + 1), ids.new_empty(T * k)))
     _call("qgemm_moe_group", index, stream, ids.data_ptr(), T, E, k, offsets.data_ptr(), rows.data_ptr())
     return offsets, rows
 
@@ -1003,7 +1022,7 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
         _apart("out", out, 2 * T * H, inputs, ("x", "residual"))
         _apart("workspace", workspace, need, (*inputs, ("out", out, 2 * T * H)))
     if out is None:
-        out = torch.empty_like(x)
+        (out,) = _allocate(stream, index, lambda: (torch.empty_like(x),))
     ws, wsb, _keep = _scratch(need, workspace, x, stream)
     _call("qgemm_moe", index, stream, fu, fd, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), weights.data_ptr(),
           offsets.data_ptr(), rows.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), T, k, E,

@@ -187,3 +187,54 @@ def test_moe_weight_bytes_beyond_64_bits():
     offs = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError, match="w_up holds 1024 bytes"):
         qg.moe("w4a16", "w4a16", x, w, w, torch.ones((1, 1), device="cuda"), offs, offs[:1].clone(), I, group=128)
+
+
+def home_stream(ptr):
+    """The stream whose memory the allocator's block at `ptr` belongs to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= ptr < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("no block of torch's allocator")
+
+
+def test_results_and_workspaces_belong_to_the_calls_stream(monkeypatch):
+    """A call on an explicit stream writes memory of that stream: a block of
+    the current one may still be read by work that was queued there."""
+    rng = np.random.default_rng(1500)
+    T, k, E, n = 12, 2, 4, 512
+    wp = bytes_to_device(pack(synth.q4k_fields(rng, n, n), n, n))
+    up = bytes_to_device(np.tile(pack(synth.q4k_fields(rng, 2 * n, n), 2 * n, n), E))
+    down = bytes_to_device(np.tile(pack(synth.q4k_fields(rng, n, n), n, n), E))
+    x = (torch.randn((T, n), device="cuda") * 0.01).half()
+    logits = torch.randn((T, E), device="cuda")
+    split = [r for r in range(qg.num_rungs()) if qg.rung_name(r) == "mfma32-64x64-sk"][0]
+    spaces = []
+    call = qg._call
+
+    def spy(fn, index, stream, *args):
+        if fn in ("qgemm_linear", "qgemm_moe"):
+            spaces.append(args[-2])
+        return call(fn, index, stream, *args)
+
+    def run(**kw):
+        ids, w, offs, rows = qg.moe_route(logits, k, **kw)
+        o2, r2 = qg.moe_group(ids, E, **kw)
+        return [ids, w, offs, rows, o2, r2, qg.linear("q4k", x, wp, n, rung=split, **kw),
+                qg.linear("q4k", x, wp, n, out_layout=qg.X_FRAG, **kw),
+                qg.moe("q4k", "q4k", x, up, down, w, offs, rows, n, **kw)]
+
+    want = run()
+    monkeypatch.setattr(qg, "_call", spy)
+    side, default = torch.cuda.Stream(), torch.cuda.default_stream()
+    torch.cuda.synchronize()
+    for current, other in ((default, side), (side, default), (default, default), (side, side)):
+        spaces.clear()
+        with torch.cuda.stream(current):
+            got = run(stream=other.cuda_stream)
+            current.wait_stream(other)
+            same = [torch.equal(a, b) for a, b in zip(got, want)]
+        torch.cuda.synchronize()
+        assert all(same), same
+        assert len(spaces) == 3 and spaces[0] and not spaces[1] and spaces[2]
+        for p in [t.data_ptr() for t in got] + [spaces[0], spaces[2]]:
+            assert home_stream(p) == other.cuda_stream

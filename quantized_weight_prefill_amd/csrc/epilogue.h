@@ -20,10 +20,13 @@ __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcp
 
 // v * sigmoid(z), the exponent x = -z log2 e given: SiLU with z = v; the tanh
 // form of GELU with z = 2 sqrt(2/pi) (v + 0.044715 v^3), since (1 + tanh y) / 2
-// = sigmoid(2y) -- no cancellation on the negative side.  Relative error about
-// 2^-21 (v_exp_f32 and v_rcp_f32 are good to 1 ulp; the exponent's rounding
-// adds |z| 2^-24).  The two transcendentals are most of an activation's cost:
-// about 6 us of the 189 that W4A16 2048x4096 -> 12288 takes with bias and GELU.
+// = sigmoid(2y) -- no cancellation on the negative side.  Relative error 2^-21
+// (v_exp_f32 and v_rcp_f32 are good to 1 ulp) and, where z is negative, what the
+// roundings on the way to x make of it, up to 4 |x| 2^-24: 2^-19 for SiLU at v =
+// -30, 2^-17 for GELU at v = -9, far below a rounding to 16 bits.  A result
+// below |v| 2^-125, whose reciprocal has no normal binary32 value, may be 0.
+// The two transcendentals are most of an activation's cost: about 6 us of the
+// 189 that W4A16 2048x4096 -> 12288 takes with bias and GELU.
 __device__ __forceinline__ float times_sigmoid(float v, float x) { return v * rcp_fast(1.0f + exp2_fast(x)); }
 
 __device__ __forceinline__ float act_silu(float v) { return times_sigmoid(v, -1.4426950408889634f * v); }
@@ -37,8 +40,9 @@ __device__ __forceinline__ float act_gelu_tanh(float v)
 // v * Phi(v) = v erfc(-v/sqrt 2) / 2.  erfc(x) = exp(-x^2) erfcx(x) for x >=
 // 0, and erfcx(x) = t P(t) with t = 1/(1 + 0.38 x), P of degree 8: a minimax
 // fit of this file's own (relative error 2.5e-8 over x >= 0, 4e-7 with
-// binary32 coefficients and arithmetic), so the tail keeps its relative
-// accuracy where 1 + erf would cancel.
+// binary32 coefficients and arithmetic), so the tail does not cancel as 1 + erf
+// would.  The roundings of the exponent x = v^2 log2(e) / 2 add up to 4 x 2^-24
+// there: 2^-17 at v = -8, 2^-16 at -12.6; from about -13.2 on results are 0.
 __device__ __forceinline__ float act_gelu(float v)
 {
     constexpr float kLog2e = 1.4426950408889634f;

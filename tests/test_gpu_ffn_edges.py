@@ -11,6 +11,7 @@ import torch
 
 import quantized_weight_prefill_amd as qg
 from quantized_weight_prefill_amd import synth
+from tests.ffn_ref import HALF, SUB, act64
 from tests.helpers import bytes_to_device
 from tests.test_gpu_exact import DTYPES
 
@@ -238,3 +239,38 @@ def test_results_and_workspaces_belong_to_the_calls_stream(monkeypatch):
         assert len(spaces) == 3 and spaces[0] and not spaces[1] and spaces[2]
         for p in [t.data_ptr() for t in got] + [spaces[0], spaces[2]]:
             assert home_stream(p) == other.cuda_stream
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f16", "bf16"])
+def test_activations_relative_accuracy(act, dtype):
+    """act(v) to the bits that its rounding leaves, the negative tail
+    included: with X = 0, v the bias and -RN(act(v)) the residual, Y is what
+    was left, exact in binary32 (the two are within a factor of two).
+
+    Error: exp2 and rcp 2^-23 each, two products 2^-24 each, in all 2^-21;
+    erfc's fit 4e-7 < 2^-21 more.  The exponent x takes at most 5.5 roundings
+    of 2^-24 (GELU: |v| / sqrt 2 and its constant twice, the product with
+    log2 e, its constant, one more product), ln 2 * 5.5 < 4.  Then Y's own
+    rounding."""
+    tt, half, sub = TORCH[dtype], HALF[dtype], SUB[dtype]
+    wide = 60.0 if act == "silu" else 13.5
+    v = torch.cat([torch.linspace(-wide, wide, 4000, dtype=torch.float64), torch.logspace(-3, 0, 48, dtype=torch.float64),
+                   -torch.logspace(-3, 0, 48, dtype=torch.float64)]).to(tt)
+    N, K = v.numel(), 256
+    wp = bytes_to_device(pack(synth.q4k_fields(np.random.default_rng(1600), N, K), N, K))
+    x0 = torch.zeros((1, K), dtype=tt, device="cuda")
+    v64 = v.double()
+    y = act64(v64, act)
+    r = y.to(tt)
+    got = qg.linear("q4k", x0, wp, N, bias=v.cuda(), act=act, residual=-r.cuda()[None])[0].cpu().double()
+    want = y - r.double()
+    order = {"silu": 1.4427 * v64.abs(), "gelu": 0.72135 * v64 ** 2,
+             "gelu_tanh": v64.abs() * (2.3023 + 0.10295 * v64 ** 2)}[act]
+    err = (2.0 ** -21 * (2 if act == "gelu" else 1) + 4 * order * 2.0 ** -24) * y.abs()
+    tail = order > 100                       # below |v| 2^-100; from |v| 2^-125 on it may be 0
+    bad = ((got - want).abs() > err + half * (want.abs() + err) + sub) & ~tail
+    assert not bool(bad.any()), (v64[bad][:4], got[bad][:4], want[bad][:4])
+    plain = qg.linear("q4k", x0, wp, N, bias=v.cuda(), act=act)[0].cpu().double()
+    low = tail & (v64 < 0)
+    assert bool((plain[low].abs() <= y[low].abs() * (1 + 2 * half) + sub).all())

@@ -9,11 +9,12 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import quantized_weight_prefill_amd as qg
 from quantized_weight_prefill_amd import synth
 from tests.ffn_ref import HALF, SUB, act64
-from tests.helpers import bytes_to_device
-from tests.test_gpu_exact import DTYPES
+from tests.helpers import bytes_to_device, from_device, same_bits
+from tests.test_gpu_exact import DTYPES, double_rounded, wide_gap_fields
 
 pytestmark = pytest.mark.gpu
 
@@ -274,3 +275,26 @@ def test_activations_relative_accuracy(act, dtype):
     plain = qg.linear("q4k", x0, wp, N, bias=v.cuda(), act=act)[0].cpu().double()
     low = tail & (v64 < 0)
     assert bool((plain[low].abs() <= y[low].abs() * (1 + 2 * half) + sub).all())
+
+
+@pytest.mark.parametrize("E", [300, 200], ids=["few_per_expert", "many_per_expert"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f16", "bf16"])
+def test_unpack_contract_with_two_panels_per_workgroup(dtype, E):
+    """Identity extraction of the down projection on blocks whose d and dmin
+    are far apart, with more row tiles than two per wave of the down product
+    (1024 pairs over 300 and 200 experts, 256 columns)."""
+    n, T = 256, 1024
+    wide = wide_gap_fields(1700 + dtype, n, n)
+    enc = synth.encode("q4k", wide)
+    W = oracle.dequant("q4k", enc, n, n, dtype)
+    assert int((double_rounded(wide, dtype) != W).sum()) > 0
+    eye = eye_fields(n)
+    ones = {k: v.copy() for k, v in eye.items()}
+    ones["q"][:] = 1
+    up = pack({k: np.concatenate([eye[k], ones[k]]) for k in eye}, 2 * n, n)
+    x = torch.eye(n, dtype=TORCH[dtype], device="cuda").repeat(T // n, 1)
+    ids = torch.from_numpy(np.random.default_rng(1701).integers(0, E, (T, 1)).astype(np.int32)).cuda()
+    offs, rows = qg.moe_group(ids, E)
+    y = qg.moe("q4k", "q4k", x, bytes_to_device(np.tile(up, E)), bytes_to_device(np.tile(qg.pack("q4k", enc, n, n), E)),
+               torch.ones((T, 1), device="cuda"), offs, rows, n, act="none")
+    assert same_bits(from_device(y), np.tile(W, (T // n, 1)))

@@ -775,10 +775,11 @@ hipError_t launch_down(int fmt, int dtype, int pn, dim3 grid, const MoeArgs &m, 
 }
 
 // Workgroups of the down product that share a strip of Y (pn 16-column
-// panels): one workgroup of sixteen waves for each CU (64 tokens, Q6_K 768 ->
-// 2048: 44.0 us with two on a panel, 44.7 with four of eight waves; seven
-// tokens, W4A16 1408 -> 2048: 14.0 with two, 19.6 with one; one token 7.8
-// against 9.4).
+// panels): one workgroup of sixteen waves for each CU.  The down product
+// against half and twice as many (profiler's medians, weights rotating): 64
+// tokens, 8 of 128, Q6_K 768 -> 2048, 50-52 us against 72-75 and 59-62; 128
+// tokens, 8 of 16, 31.0 against 41.6 and 46.5; seven tokens, W4A16 1408 -> 2048,
+// 16.6 against 23.4 and 21.4; one token 8.6 against 9.8 and 13.6.
 int moe_split(long long H, int pn)
 {
     const long long strips = (H + 16 * pn - 1) / (16 * pn);
@@ -821,12 +822,14 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     const long long tiles = moe_tiles(P, E, 16);
     // two panels per workgroup of the down product where the row tiles give
     // its waves two each: h is then read once for both panels, by half as many
-    // workgroups, each over half the tiles (64 tokens, 8 of 128 experts, 768 ->
-    // 2048: 47.3 against 56.0 us; 128 tokens, 8 of 16: 27.8 against 32.2; 128
-    // tokens, 4 of 32, 1024 -> 4096: 46.6 against 52.6); below that one panel,
-    // which spreads the weights over more waves (one token 8.2 against 9.0; 16
-    // tokens, 2 of 8, 1024 -> 4096: 8.8 against 9.8; 256 tokens, 4 of 8, 1024 ->
-    // 1024: 30.8 against 33.3)
+    // workgroups, each over half the tiles (as for moe_split: 64 tokens, 8 of
+    // 128 experts, 768 -> 2048: 50-52 against 58-61 us; 128 tokens, 8 of 16: 31.0
+    // against 38.5; 128 tokens, 4 of 32, 1024 -> 4096: 52.5 against 61-63); below
+    // that one panel, which spreads the weights over more waves (one token
+    // 8.2-8.6 against 9.2-9.5; 16 tokens, 2 of 8, 1024 -> 4096: 9.0 against 10.0;
+    // 256 tokens, 4 of 8, 1024 -> 1024: 30.9 against 33.0; only seven tokens of
+    // W4A16 1408 -> 2048, 16.6 against 15.8, would gain).  The bound is that of
+    // 16-row tiles in both forms of the kernel.
     const int pn = tiles > 2 * kMoeDownWaves * moe_split(H, 1) ? 2 : 1;
     m.strips = (int)(H / (16 * pn));
     m.split = moe_split(H, pn);
@@ -855,7 +858,8 @@ int moe(int fu, int fd, const void *X, const void *Wu, const void *Wd, const flo
     if (e != hipSuccess) return launch_status(e, "moe up");
 
     // down: K in parts (of whole chunk pairs) while the row tiles alone leave
-    // waves idle (one token, Q6_K 768 -> 2048: 7.4 us in three parts, 8.1 whole)
+    // waves idle (one token, Q6_K 768 -> 2048: 7.4 us in three parts, 8.1
+    // whole, back to back)
     m.g = make_args(fd, nullptr, Wd, Y, P, H, I, group, has_zp);
     m.g.offs = offs;
     m.g.E = (int)E;

@@ -298,3 +298,38 @@ def test_unpack_contract_with_two_panels_per_workgroup(dtype, E):
     y = qg.moe("q4k", "q4k", x, bytes_to_device(np.tile(up, E)), bytes_to_device(np.tile(qg.pack("q4k", enc, n, n), E)),
                torch.ones((T, 1), device="cuda"), offs, rows, n, act="none")
     assert same_bits(from_device(y), np.tile(W, (T // n, 1)))
+
+
+def test_explicit_stream_inside_a_capture():
+    """Calls on a stream that joins a capture, captured and replayed on inputs
+    that change: the results of the eager calls, memory of their own."""
+    rng = np.random.default_rng(1800)
+    T, k, E, n = 12, 2, 4, 512
+    wp = bytes_to_device(pack(synth.q4k_fields(rng, n, n), n, n))
+    up = bytes_to_device(np.tile(pack(synth.q4k_fields(rng, 2 * n, n), 2 * n, n), E))
+    down = bytes_to_device(np.tile(pack(synth.q4k_fields(rng, n, n), n, n), E))
+    x0 = (torch.randn((T, n), device="cuda") * 0.01).half()
+    l0 = torch.randn((T, E), device="cuda")
+    x, logits = x0.clone(), l0.clone()
+    split = [r for r in range(qg.num_rungs()) if qg.rung_name(r) == "mfma32-64x64-sk"][0]
+
+    def run(**kw):
+        _, w, offs, rows = qg.moe_route(logits, k, **kw)
+        return (qg.linear("q4k", x, wp, n, rung=split, act="silu", **kw),
+                qg.moe("q4k", "q4k", x, up, down, w, offs, rows, n, residual=x, **kw))
+
+    run()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = run(stream=side.cuda_stream)
+        here.wait_stream(side)
+    for i in range(4):
+        x.copy_(x0.roll(i, 0))
+        logits.copy_(l0.roll(i, 1))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, run())), i

@@ -87,7 +87,7 @@ const char *qgemm_status_str(int status);
 /* ---- enumerations -------------------------------------------------------- */
 #define QGEMM_F16 0
 #define QGEMM_BF16 1
-#define QGEMM_F32 2 /* routing logits only */
+#define QGEMM_F32 2 /* routing logits and qgemm_kv_read only */
 
 #define QGEMM_FMT_Q4K 0
 #define QGEMM_FMT_Q6K 1
@@ -536,6 +536,113 @@ int qgemm_moe(int format_up, int format_down, const void *X, const void *Wup, co
               int64_t E, int64_t hidden, int64_t inter, int64_t group_size, int has_zp, int act, int dtype,
               void *workspace, size_t workspace_bytes, void *stream);
 size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64_t inter);
+
+/* ---- attention: head norms, position rotation, a 4-bit paged cache -----------
+ * What a layer runs between its q/k/v and its output product (the
+ * batched-prefill post, "The two prefill paths": chunked projections, rotation,
+ * KV write and attention in one flow), for one new token of each sequence or
+ * for whole prompts.
+ *
+ * Heads.  Q, K and V rows are given by a pointer and a row stride in elements (a
+ * multiple of 8; the three may be column ranges of one merged product): token
+ * row t holds its heads of head_dim (64 or 128) elements side by side.  dtype is
+ * theirs and the results'.
+ *
+ * Norm and rotation (qgemm_qk_norm_rope; inside qgemm_kv_append for K and Q).
+ *   With eps >= 0 a head x becomes x / sqrt(mean(x^2) + eps) * weight, weight
+ *   [head_dim] float (16-byte aligned) or NULL for ones; with eps < 0 there is no
+ *   norm.  `rope` (device, float, 16-byte aligned; NULL: no rotation) is a table
+ *   [rope_len][rot] of cosines (rot/2) and then sines, rot a multiple of 16 up to
+ *   head_dim; qgemm_rope_table makes it.  The pair (a, b) becomes (a cos - b sin,
+ *   b cos + a sin): dims i and i + rot/2, or 2i and 2i+1 when interleaved; dims
+ *   from rot on stay.  positions [T] (int32, device) says each row's line of the table.
+ *   Computed in 32 bits (64 for what goes into the cache) and rounded once.
+ *   A row whose position is outside the table is a padded one: zeros in Qout
+ *   and Kout, nothing in the cache.
+ *
+ * Cache.  `cache` is `pages` pages of qgemm_kv_page_bytes(kv_heads, head_dim,
+ *   page) bytes (device, 16-byte aligned); page is 16, 32, 64, 128 or 256 tokens.
+ *   tables [S][table_width] (int32, device): the pages of each sequence in order,
+ *   so that its token at place p is in page tables[s][p / page].  Values are held
+ *   in groups of 32 dims of one token's head: minimum = fp16(min), scale =
+ *   fp16((max - minimum) / 15), code = the nearest of 0..15 to (x - minimum) /
+ *   scale, ties to even (0 where scale is 0); a value reads as code * scale +
+ *   minimum.  Magnitudes are held to 32768, NaN becomes 0: what the cache holds is
+ *   finite.  The order of the bytes:
+ *     page    one region per key head, of page/16 tiles of 20*head_dim bytes
+ *     tile    16 tokens: key codes (8*head_dim), key headers (2*head_dim), value
+ *             codes, value headers
+ *     headers [head_dim/32][16 tokens] of (scale, minimum), two fp16
+ *     key codes    lane (h, r), h = 0..3, r = token, at (16*h + r) * head_dim/8: dims
+ *             head_dim/4*h .., words of 8 in pair order (see the packed layout)
+ *     value codes  lane (h, n), n = 0..15, at (16*h + n) * head_dim/8: the E =
+ *             head_dim/16 dims from E*n of tokens 4h .. 4h+3; word w has dims 2w and
+ *             2w+1, dim 2w+b of token 4h+i at bits 4*(2b + i/2) + 16*(i%2)
+ *
+ * Sequences.  lens [S] (int32, device) are their lengths, the new tokens
+ *   included.  offsets [S+1] (int32, device) say which rows are whose: rows
+ *   offsets[s] .. offsets[s+1]-1 are the last places of sequence s, in order; NULL means
+ *   one row each (T = S).  Rows from offsets[S] on belong to no sequence: they
+ *   are not read, and their results stay as they were.  A row whose place is
+ *   negative, beyond the table or in a page that is not in [0, pages) has no
+ *   place in the cache.  The kernels clamp all of these, so any contents stay
+ *   inside the buffers (bad ones only give wrong values); a page must not be
+ *   written by two sequences, or by two calls that may run at the same time.
+ *
+ * qgemm_rope_table: host memory [positions][rot]: the angle of pair i at position
+ *   p is p * scale * base^(-2i/rot), in 64 bits, its cosine and sine rounded to
+ *   float.  Errors: QGEMM_ERR_SHAPE, _NULL.
+ * qgemm_kv_page_bytes: bytes of a page, 0 for sizes that no call takes.
+ * qgemm_qk_norm_rope: the `heads` heads of Q and the `kv_heads` heads of K (either
+ *   may be 0) to Qout and Kout, which may be Q and K themselves (with their
+ *   strides) and overlap nothing else.  positions may be NULL without rope.
+ * qgemm_kv_append: the new tokens' keys, normed and rotated, and their values as
+ *   they are, into the cache at their places; rows without one are left out.
+ *   With Q (may be NULL), the queries too are normed and rotated into Qout (which may be
+ *   Q) in the same launch.  positions NULL: a row's place in its sequence.  Only the new tokens'
+ *   codes and headers are written.  One launch.
+ * qgemm_kv_read: the keys and values of the same rows as the cache holds them, to K
+ *   and V [T][kv_heads][head_dim] of out_type (QGEMM_F16, _BF16 or _F32); zeros
+ *   for a row without a place.  With offsets from 0 to each sequence's whole
+ *   length this reads a cache out.  One launch.
+ * qgemm_kv_attention: Y[t] = sum over the keys that row t sees of softmax(scale *
+ *   q . k) v, for each of `heads` query heads (a multiple of kv_heads, at most 128
+ *   times it; query heads g*j .. g*j+g-1 read key head j), Y [T][heads][head_dim]
+ *   contiguous.  Row t at place p of its sequence sees the places 0 .. p, with
+ *   window > 0 those above p - window; keys without a place are not seen, and a
+ *   row that sees none gets zeros.  The new tokens' keys must be in the cache.
+ *   Statistics and sums in 32 bits; the result does not depend on timing.  max_len (0:
+ *   the table's width) is a bound on the lengths that the split of the work over a
+ *   long cache goes by; longer ones are read all the same.  `workspace`
+ *   (device, 16-byte aligned, of any contents) has at least
+ *   qgemm_kv_attention_workspace_bytes(T, S, heads, kv_heads, head_dim, max_len,
+ *   offsets != NULL) bytes, max_len 0 counted as table_width * page; calls that may run
+ *   at the same time need one each.
+ * T = 0 or S = 0 is a no-op.  Errors of the device calls: QGEMM_ERR_SHAPE,
+ * _DTYPE, _FORMAT (page), _NULL, _ALIGN, _SIZE (workspace), _HIP; all but the
+ * last before any launch. */
+int qgemm_rope_table(int64_t positions, int64_t rot, double base, double scale, float *table);
+size_t qgemm_kv_page_bytes(int64_t kv_heads, int64_t head_dim, int64_t page);
+int qgemm_qk_norm_rope(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const float *q_weight,
+                       const float *k_weight, const float *rope, int64_t rope_len, int64_t rot, int interleaved,
+                       const int32_t *positions, float eps, void *Qout, int64_t qout_stride, void *Kout,
+                       int64_t kout_stride, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int dtype,
+                       void *stream);
+int qgemm_kv_append(void *cache, int64_t pages, int64_t page, const int32_t *tables, int64_t table_width,
+                    const int32_t *lens, const int32_t *offsets, int64_t S, const void *K, int64_t k_stride,
+                    const void *V, int64_t v_stride, const float *k_weight, const float *rope, int64_t rope_len,
+                    int64_t rot, int interleaved, const int32_t *positions, float eps, const void *Q, int64_t q_stride,
+                    const float *q_weight, void *Qout, int64_t qout_stride, int64_t T, int64_t heads, int64_t kv_heads,
+                    int64_t head_dim, int dtype, void *stream);
+int qgemm_kv_read(const void *cache, int64_t pages, int64_t page, const int32_t *tables, int64_t table_width,
+                  const int32_t *lens, const int32_t *offsets, int64_t S, void *K, void *V, int64_t T, int64_t kv_heads,
+                  int64_t head_dim, int out_type, void *stream);
+int qgemm_kv_attention(const void *Q, int64_t q_stride, const void *cache, int64_t pages, int64_t page,
+                       const int32_t *tables, int64_t table_width, const int32_t *lens, const int32_t *offsets, int64_t S,
+                       void *Y, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t window, float scale,
+                       int64_t max_len, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t qgemm_kv_attention_workspace_bytes(int64_t T, int64_t S, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                          int64_t max_len, int ragged);
 
 /* The staged arm (the dequant-scratch post, "The two passes hiding inside
  * one matmul": unpack to a 16-bit scratch, then a GEMM that reads it), kept

@@ -20,6 +20,9 @@ Functions keep the C names without the ``qgemm_`` prefix:
   its epilogue: :func:`linear`, :func:`linear_xf`, :func:`linear_select_rung`;
 * mixture of experts: the routing :func:`moe_route`, :func:`moe_group` and
   the whole layer for a few tokens :func:`moe`;
+* attention between the projections: :func:`qk_norm_rope` with its table
+  :func:`rope_table`, the paged 4-bit cache :func:`kv_cache`, :func:`kv_append`,
+  :func:`kv_read`, and the attention over it :func:`kv_attention`;
 * the staged dequant :func:`dequant` and the M-ladder queries
   :func:`select_rung`, :func:`rung_info`, :func:`rung_name`, :func:`num_rungs`;
 * the split rungs' workspace size :func:`workspace_bytes` (the C library
@@ -118,6 +121,16 @@ SIGNATURES = {
     "qgemm_moe": (_INT, [_INT, _INT, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _INT,
                          _INT, _INT, _VP, _SZ, _VP]),
     "qgemm_moe_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
+    "qgemm_rope_table": (_INT, [_I64, _I64, ctypes.c_double, ctypes.c_double, _VP]),
+    "qgemm_kv_page_bytes": (_SZ, [_I64, _I64, _I64]),
+    "qgemm_qk_norm_rope": (_INT, [_VP, _I64, _VP, _I64, _VP, _VP, _VP, _I64, _I64, _INT, _VP, ctypes.c_float, _VP, _I64,
+                                  _VP, _I64, _I64, _I64, _I64, _I64, _INT, _VP]),
+    "qgemm_kv_append": (_INT, [_VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _I64,
+                               _INT, _VP, ctypes.c_float, _VP, _I64, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _INT, _VP]),
+    "qgemm_kv_read": (_INT, [_VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I64, _I64, _INT, _VP]),
+    "qgemm_kv_attention": (_INT, [_VP, _I64, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _I64, _I64, _I64,
+                                  _I64, ctypes.c_float, _I64, _INT, _VP, _SZ, _VP]),
+    "qgemm_kv_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _INT]),
     "qgemm_gguf_header": (_INT, [_VP, _SZ, _VP, _VP, _VP, _VP, _VP]),
     "qgemm_gguf_tensor_info": (_INT, [_VP, _SZ, _I64, _VP, _SZ, _VP, _VP, _VP, _VP, _VP]),
     "qgemm_gguf_find_kv": (_INT, [_VP, _SZ, ctypes.c_char_p, _VP, _VP, _VP]),
@@ -1027,6 +1040,279 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
     _call("qgemm_moe", index, stream, fu, fd, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), weights.data_ptr(),
           offsets.data_ptr(), rows.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), T, k, E,
           H, inter, group, has_zp, ac, code, ws, wsb)
+    return out
+
+
+# ---- attention ----------------------------------------------------------------
+
+#: tokens of a cache page
+KV_PAGES = (16, 32, 64, 128, 256)
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, scale: float = 1.0) -> np.ndarray:
+    """The rotation's table, float32 [positions, rot] (host): the cosines of the
+    angles position * scale * base**(-2i/rot), i < rot/2, then their sines."""
+    out = np.empty((positions, rot), np.float32)
+    _check("qgemm_rope_table", lib().qgemm_rope_table(positions, rot, base, scale, _np_ptr(out)))
+    return out
+
+
+def kv_page_bytes(kv_heads: int, head_dim: int, page: int) -> int:
+    """Bytes of a cache page of `page` tokens (one of KV_PAGES)."""
+    return int(lib().qgemm_kv_page_bytes(kv_heads, head_dim, page))
+
+
+def kv_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda"):
+    """An empty cache of `pages` pages for keys and values in 4 bits: a uint8
+    tensor [pages, page bytes], its contents undefined until they are appended."""
+    n = kv_page_bytes(kv_heads, head_dim, page)
+    if n == 0:
+        raise QGemmError("qgemm_kv_page_bytes", -2)
+    return _torch().empty((pages, n), dtype=_torch().uint8, device=device)
+
+
+def _heads(name, x, index, code=None):
+    """(pointer, row stride, heads, head_dim) of x [T, heads, head_dim] on device `index`,
+    whose rows hold their heads side by side."""
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, head_dim]")
+    if x.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be on the cache's device" if index >= 0 else f"{name} must be a device tensor")
+    if code is not None and _dtype_code(x) != code:
+        raise ValueError(f"{name} has another dtype")
+    T, h, d = x.shape
+    if x.numel() and ((d > 1 and x.stride(2) != 1) or (h > 1 and x.stride(1) != d)):
+        raise ValueError(f"{name} must hold each row's heads side by side")
+    return x.data_ptr(), x.stride(0) if T > 1 else h * d, h, d
+
+
+def _vector(name, t, n, dtype, index):
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {n} on the call's device")
+    return t.data_ptr()
+
+
+def _turn_args(rope, positions, T, index):
+    """(rope pointer, rows, columns, positions pointer)."""
+    torch = _torch()
+    if rope is None:
+        return None, 0, 0, _vector("positions", positions, (T,), torch.int32, index)
+    if rope.dim() != 2:
+        raise ValueError("rope must be [positions, rot]")
+    return (_vector("rope", rope, tuple(rope.shape), torch.float32, index), rope.shape[0], rope.shape[1],
+            _vector("positions", positions, (T,), torch.int32, index))
+
+
+def _kv_page(cache, kv_heads, D) -> int:
+    """Tokens of a page of `cache` [pages, page bytes]."""
+    if cache.dim() != 2 or cache.dtype != _torch().uint8 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 tensor [pages, page bytes]")
+    per = 20 * D * kv_heads
+    page = cache.shape[1] * 16 // per if per > 0 else 0
+    if page not in KV_PAGES or page * per != cache.shape[1] * 16:
+        raise ValueError(f"a page of {cache.shape[1]} bytes holds no {KV_PAGES} tokens of {kv_heads} heads of {D}")
+    return page
+
+
+def _kv_sequences(tables, lens, offsets, T, index):
+    """(tables pointer, width, lens pointer, offsets pointer, S)."""
+    torch = _torch()
+    if tables.dim() != 2:
+        raise ValueError("tables must be [S, pages of a sequence]")
+    S, width = tables.shape
+    if offsets is None and S != T:
+        raise ValueError(f"without offsets every sequence has one row, got {T} rows for {S} sequences")
+    i32 = torch.int32
+    return (_vector("tables", tables, (S, width), i32, index), width, _vector("lens", lens, (S,), i32, index),
+            _vector("offsets", offsets, (S + 1,), i32, index), S)
+
+
+def _rows(x):
+    """(address, bytes of a row, bytes from row to row, rows) of x [T, heads, head_dim]."""
+    T, h, d = x.shape
+    return x.data_ptr(), 2 * h * d, 2 * (x.stride(0) if T > 1 else h * d), T
+
+
+def _rows_apart(what, t, others):
+    """Refuse `t` [T, heads, head_dim], written by the call, when a row of it shares memory with a
+    row of another ((name, tensor)); the rows of a merged product's parts may interleave."""
+    a, wa, sa, T = _rows(t)
+    for name, o in others:
+        if o is None or T == 0 or o.shape[0] == 0 or wa == 0:
+            continue
+        b, wb, sb, n = _rows(o)
+        if not (a < b + (n - 1) * sb + wb and b < a + (T - 1) * sa + wa):
+            continue
+        if sa == sb and (b - a) % sa >= wa and (a - b) % sa >= wb:
+            continue
+        raise ValueError(f"{what} shares memory with {name}")
+
+
+def _span(x):
+    """Bytes from the first to the last element of x [T, heads, head_dim]."""
+    _, width, step, T = _rows(x)
+    return (T - 1) * step + width if T else 0
+
+
+def qk_norm_rope(q, k, rope=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, interleaved: bool = False,
+                 q_out=None, k_out=None, stream=None):
+    """Queries [T, heads, D] and keys [T, kv_heads, D] (D 64 or 128; k may be
+    None), each head divided by its root mean square and multiplied by its weight
+    (float32 [D], None: ones), then rotated: (q, k) results.
+
+    ``eps`` None leaves the norm out, ``rope`` None the rotation; ``rope`` is a device
+    copy of :func:`rope_table`, ``positions`` int32 [T] its rows (a row outside
+    it gives zeros).  q and k may be column ranges of one merged product;
+    ``q_out`` and ``k_out`` may be q and k themselves."""
+    torch = _torch()
+    index, code = q.get_device(), _dtype_code(q)
+    qp, qs, heads, D = _heads("q", q, index)
+    T = q.shape[0]
+    kp, ks, kv = (None, 0, 0) if k is None else _heads("k", k, index, code)[:3]
+    if k is not None and (k.shape[0] != T or k.shape[2] != D):
+        raise ValueError("k must have q's rows and head size")
+    rp, rl, rot, pp = _turn_args(rope, positions, T, index)
+    if rope is not None and positions is None:
+        raise ValueError("a rotation needs positions")
+    wq, wk = (_vector(n, w, (D,), torch.float32, index) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)))
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    small = (("rope", rope, 4 * rl * rot), ("positions", positions, 4 * T), ("q_weight", q_weight, 4 * D),
+             ("k_weight", k_weight, 4 * D))
+    for name, out, own, src in (("q_out", q_out, "q", q), ("k_out", k_out, "k", k)):
+        if out is None:
+            continue
+        if out.shape != src.shape or out.dtype != src.dtype:
+            raise ValueError(f"{name} must have its input's shape and dtype")
+        _heads(name, out, index, code)
+        in_place = _rows(out) == _rows(src)
+        _rows_apart(name, out, [(n, x) for n, x in (("q", q), ("k", k)) if not (n == own and in_place)]
+                    + ([("k_out", k_out)] if name == "q_out" else []))
+        _apart(name, out, _span(out), small)
+    if q_out is None:
+        (q_out,) = _allocate(stream, index, lambda: (torch.empty((T, heads, D), dtype=q.dtype, device=q.device),))
+    if k is not None and k_out is None:
+        (k_out,) = _allocate(stream, index, lambda: (torch.empty((T, kv, D), dtype=q.dtype, device=q.device),))
+    _call("qgemm_qk_norm_rope", index, stream, qp, qs, kp, ks, wq, wk, rp, rl, rot, int(bool(interleaved)), pp,
+          -1.0 if eps is None else eps, q_out.data_ptr(), q_out.stride(0) if T > 1 else heads * D,
+          None if k is None else k_out.data_ptr(), 0 if k is None else k_out.stride(0) if T > 1 else kv * D, T, heads, kv, D, code)
+    return q_out, k_out
+
+
+def kv_append(cache, k, v, tables, lens, offsets=None, rope=None, positions=None, k_weight=None, eps=None,
+              interleaved: bool = False, q=None, q_weight=None, q_out=None, stream=None):
+    """Append new tokens' keys and values [T, kv_heads, D] to a 4-bit cache
+    (:func:`kv_cache`), the keys normed (``eps`` not None) and rotated (``rope`` not None)
+    on the way as in :func:`qk_norm_rope`; with ``q`` [T, heads, D], the queries too
+    in the same launch: returns their result (None without q).
+
+    tables [S, pages of a sequence], lens [S] (lengths with the new tokens),
+    offsets [S+1] (rows offsets[s] .. offsets[s+1]-1 are the last places of
+    sequence s; None: one row each), all int32.  ``positions`` None takes a row's
+    place in its sequence.  Rows behind offsets[S] stay as they were."""
+    torch = _torch()
+    index, code = cache.get_device(), _dtype_code(k)
+    kp, ks, H, D = _heads("k", k, index)
+    vp, vs, _, _ = _heads("v", v, index, code)
+    T = k.shape[0]
+    if v.shape != k.shape:
+        raise ValueError("v must have k's shape")
+    page = _kv_page(cache, H, D)
+    tp, width, lp, op, S = _kv_sequences(tables, lens, offsets, T, index)
+    rp, rl, rot, pp = _turn_args(rope, positions, T, index)
+    wq, wk = (_vector(n, w, (D,), torch.float32, index) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)))
+    inputs = [("k", k, _span(k)), ("v", v, _span(v)), ("tables", tables, 4 * S * width),
+              ("lens", lens, 4 * S), ("offsets", offsets, 4 * (S + 1)), ("rope", rope, 4 * rl * rot),
+              ("positions", positions, 4 * T), ("k_weight", k_weight, 4 * D), ("q_weight", q_weight, 4 * D)]
+    qp, qs, heads, yp, ys = None, 0, 0, None, 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        qp, qs, heads, dq = _heads("q", q, index, code)
+        if dq != D or q.shape[0] != T:
+            raise ValueError("q must have k's rows and head size")
+        if q_out is None:
+            (q_out,) = _allocate(stream, index, lambda: (torch.empty((T, heads, D), dtype=q.dtype, device=q.device),))
+            ys = heads * D
+        else:
+            if q_out.shape != q.shape or q_out.dtype != q.dtype:
+                raise ValueError("q_out must have q's shape and dtype")
+            _, ys, _, _ = _heads("q_out", q_out, index, code)
+            in_place = _rows(q_out) == _rows(q)
+            _rows_apart("q_out", q_out, (("k", k), ("v", v), ("q", None if in_place else q)))
+            _apart("q_out", q_out, _span(q_out), inputs[2:])
+            inputs.append(("q_out", q_out, _span(q_out)))
+        inputs.append(("q", q, _span(q)))
+        yp = q_out.data_ptr()
+    _apart("cache", cache, cache.numel(), inputs)
+    _call("qgemm_kv_append", index, stream, cache.data_ptr(), cache.shape[0], page, tp, width, lp, op, S, kp, ks, vp, vs, wk,
+          rp, rl, rot, int(bool(interleaved)), pp, -1.0 if eps is None else eps, qp, qs, wq, yp, ys, T, heads, H, D, code)
+    return q_out
+
+
+def kv_read(cache, tables, lens, T: int, kv_heads: int, head_dim: int, offsets=None, dtype=None, stream=None):
+    """The keys and values [T, kv_heads, head_dim] of the rows that lens and
+    offsets name (as in :func:`kv_append`), as the cache holds them; ``dtype``
+    float16, bfloat16 or float32 (the default).  Rows of no sequence and rows
+    without a place in the cache are zeros."""
+    torch = _torch()
+    dtype = torch.float32 if dtype is None else dtype
+    codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: 2}
+    if dtype not in codes:
+        raise TypeError(f"dtype must be float16, bfloat16 or float32, got {dtype}")
+    index = cache.get_device()
+    if index < 0:
+        raise ValueError("cache must be a device tensor")
+    page = _kv_page(cache, kv_heads, head_dim)
+    tp, width, lp, op, S = _kv_sequences(tables, lens, offsets, T, index)
+    new = torch.empty if offsets is None else torch.zeros
+    k, v = _allocate(stream, index, lambda: tuple(new((T, kv_heads, head_dim), dtype=dtype, device=cache.device) for _ in "kv"))
+    _call("qgemm_kv_read", index, stream, cache.data_ptr(), cache.shape[0], page, tp, width, lp, op, S, k.data_ptr(),
+          v.data_ptr(), T, kv_heads, head_dim, codes[dtype])
+    return k, v
+
+
+def kv_attention_workspace_bytes(T: int, S: int, heads: int, kv_heads: int, head_dim: int, max_len: int,
+                                 ragged: bool) -> int:
+    """Bytes of the workspace a :func:`kv_attention` call of these sizes needs;
+    ragged: with offsets."""
+    return int(lib().qgemm_kv_attention_workspace_bytes(T, S, heads, kv_heads, head_dim, max_len, int(bool(ragged))))
+
+
+def kv_attention(q, cache, tables, lens, kv_heads: int, offsets=None, scale=None, window: int = 0, max_len: int = 0,
+                 out=None, stream=None, workspace=None):
+    """Causal attention of queries [T, heads, D] over a 4-bit cache: row t, at place
+    p of its sequence, sees the places up to p (with ``window``, the last `window` of
+    them); [T, heads, D], zeros for a row that sees nothing.
+
+    tables, lens and offsets as in :func:`kv_append`, whose keys and values must
+    already hold the new tokens; query heads j*g .. j*g+g-1 read key head j, g =
+    heads / kv_heads.  ``scale`` defaults to D**-0.5.  ``max_len``, a bound on the
+    lengths (0: the width of the tables), only decides how the work is split.
+    Rows of ``out`` behind offsets[S] stay as they were."""
+    torch = _torch()
+    index, code = cache.get_device(), _dtype_code(q)
+    qp, qs, heads, D = _heads("q", q, index)
+    T = q.shape[0]
+    page = _kv_page(cache, kv_heads, D)
+    tp, width, lp, op, S = _kv_sequences(tables, lens, offsets, T, index)
+    need = kv_attention_workspace_bytes(T, S, heads, kv_heads, D, max_len or width * page, offsets is not None)
+    if out is not None:
+        if not _fits(out, index, q.shape, q.dtype):
+            raise ValueError("out must be a contiguous tensor of q's shape and dtype on its device")
+    if out is not None or workspace is not None:
+        inputs = (("q", q, _span(q)), ("cache", cache, cache.numel()), ("tables", tables, 4 * S * width),
+                  ("lens", lens, 4 * S), ("offsets", offsets, 4 * (S + 1)))
+        _apart("out", out, 2 * T * heads * D, inputs)
+        _apart("workspace", workspace, need, (*inputs, ("out", out, 2 * T * heads * D)))
+    if out is None:
+        (out,) = _allocate(stream, index, lambda: (torch.empty((T, heads, D), dtype=q.dtype, device=q.device),))
+    ws, wsb, _keep = _scratch(need, workspace, q, stream)
+    _call("qgemm_kv_attention", index, stream, qp, qs, cache.data_ptr(), cache.shape[0], page, tp, width, lp, op, S,
+          out.data_ptr(), T, heads, kv_heads, D, window, D ** -0.5 if scale is None else scale, max_len, code, ws, wsb)
     return out
 
 

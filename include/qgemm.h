@@ -565,8 +565,8 @@ size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64
  *   tables [S][table_width] (int32, device): the pages of each sequence in order,
  *   so that its token at place p is in page tables[s][p / page].  Values are held
  *   in groups of 32 dims of one token's head: minimum = fp16(min), scale =
- *   fp16((max - minimum) / 15), code = the nearest of 0..15 to (x - minimum) /
- *   scale, ties to even (0 where scale is 0); a value reads as code * scale +
+ *   fp16((max - minimum) / 15), both rounded to binary32 first, code = the nearest of
+ *   0..15 to (x - minimum) / scale, ties to even (0 where scale is 0); a value reads as code * scale +
  *   minimum.  Magnitudes are held to 32768, NaN becomes 0: what the cache holds is
  *   finite.  The order of the bytes:
  *     page    one region per key head, of page/16 tiles of 20*head_dim bytes

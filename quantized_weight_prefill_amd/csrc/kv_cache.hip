@@ -166,9 +166,19 @@ __device__ __forceinline__ double min32(const double (&x)[E], double sign)
     return sign * m;
 }
 
+// fp16 of a 64-bit value, rounded to binary32 on the way.  The compiler would
+// merge the two conversions into one rounding (in software, and other bits
+// where binary32 lands on a tie); the empty statement keeps them apart.
+__device__ __forceinline__ _Float16 header_of(double x)
+{
+    float f = (float)x;
+    asm("" : "+v"(f));
+    return (_Float16)f;
+}
+
 // The cache's codes of a lane's E dims and the header of their group: minimum =
-// fp16(min), scale = fp16((max - minimum)/15), code = the nearest of 0..15 to
-// (x - minimum)/scale, ties to even.  In 64 bits, where vector arithmetic has
+// fp16(min), scale = fp16((max - minimum)/15), both by way of binary32, code =
+// the nearest of 0..15 to (x - minimum)/scale, ties to even.  In 64 bits, where vector arithmetic has
 // the rate of 32 bits on this GPU: a code then is that of the definition and
 // does not hang on the last bit of a binary32 norm or rotation.  The quotient is
 // a product with the reciprocal and one correction, which makes a tie exact.
@@ -177,8 +187,8 @@ __device__ __forceinline__ uint32_t quantize(double (&x)[E], uint32_t (&code)[E]
 {
 #pragma unroll
     for (int i = 0; i < E; i++) x[i] = x[i] != x[i] ? 0.0 : fmin(fmax(x[i], -(double)kKvMax), (double)kKvMax);
-    const _Float16 m = (_Float16)(float)min32<E>(x, 1.0);
-    const _Float16 s = (_Float16)(float)((min32<E>(x, -1.0) - (double)(float)m) / 15.0);
+    const _Float16 m = header_of(min32<E>(x, 1.0));
+    const _Float16 s = header_of((min32<E>(x, -1.0) - (double)(float)m) / 15.0);
     const double sd = (double)(float)s, md = (double)(float)m, inv = sd > 0.0 ? 1.0 / sd : 0.0;
 #pragma unroll
     for (int i = 0; i < E; i++) {

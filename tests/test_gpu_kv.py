@@ -225,6 +225,22 @@ def test_append_special_values():
         assert k.isfinite().all() and v.isfinite().all() and k.abs().max() <= 32816
 
 
+def test_append_header_rounding():
+    """A minimum that binary32 rounds onto an fp16 tie: rounded twice, as the header says."""
+    D, kv = 64, 1
+    tiny = 2.0 ** -11 + 2.0 ** -31
+    rope = torch.zeros((1, D), device="cuda")
+    rope[:, :D // 2], rope[:, D // 2:] = 1.0, tiny
+    k = torch.zeros((1, kv, D), dtype=F16, device="cuda")
+    k[0, 0, 0], k[0, 0, 1] = -1.0, 1.0      # dim 0 becomes -(1 + tiny), the first group's minimum
+    pool = Pool(1, [1], kv, D, 16)
+    qg.kv_append(pool.cache, k, k, pool.tables, i32([1]), rope=rope, interleaved=True)
+    k64 = R.turn64(k, None, rope, i32([0]), None, True)[0]
+    assert float(k64[0, 0, 0]) == -1.0 - tiny
+    check_tokens(pool, 0, [0], k64, k.double().cpu())
+    assert float(pool.tokens(0, [0])[(0, 0)][2][0]) == -1.0
+
+
 def test_append_places_outside():
     """Positions outside the rotation's table, pages that are none, lengths beyond the table, rows before
     the first place, offsets of any contents: left out, nothing else touched."""

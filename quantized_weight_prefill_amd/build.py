@@ -49,7 +49,8 @@ def units():
     out = [("api", "api.hip", []), ("misc", "misc.hip", []), ("misc_grouped", "misc_grouped.hip", []),
            ("misc_i8", "misc_i8.hip", []), ("pack", "pack.cpp", []),
            ("noalloc", "noalloc.hip", []), ("gguf", "gguf.cpp", []), ("moe_route", "moe_route.hip", []),
-           ("kv_api", "kv_api.hip", []), ("kv_cache", "kv_cache.hip", [])]
+           ("kv_api", "kv_api.hip", []), ("kv_cache", "kv_cache.hip", []),
+           ("kv_attention", "kv_attention.hip", [])]
     for f in FORMATS:
         out.append((f"inst_moe_{f}", "inst_moe.hip", [f"-DQG_FMT={f}"]))
         for d in DTYPES:

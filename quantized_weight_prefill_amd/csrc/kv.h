@@ -82,13 +82,13 @@ __device__ __forceinline__ Seq seq_of(const KvView &v, int s)
 // The sequence that owns slot x: the last one starting at or before x, found by W
 // lanes that probe W places at a time (x is the same in all of them).
 template <int W>
-__device__ __forceinline__ int find_seq(const KvView &v, int x, int per_shift, int extra)
+__device__ __forceinline__ int find_seq(const KvView &v, int x, int per, int extra)
 {
     const int lane = threadIdx.x & (W - 1), shift = (threadIdx.x & 63) & ~(W - 1);
     int lo = 0, span = v.S;
     while (span > 1) {
         const int step = (span + W - 1) / W, s = lo + lane * step;
-        const bool before = s < min(lo + span, v.S) && (row_end(v, s) >> per_shift) + extra * s <= x;
+        const bool before = s < min(lo + span, v.S) && row_end(v, s) / per + extra * s <= x;
         const unsigned long long b = (__ballot(before) >> shift) & (W == 64 ? ~0ull : (1ull << W) - 1ull);
         lo += max(__popcll(b) - 1, 0) * step;
         span = step;
@@ -107,6 +107,29 @@ __device__ __forceinline__ uint8_t *tile_of(const KvView &v, int s, int at, int 
     if ((unsigned)id >= (unsigned)v.pages) return nullptr;
     const int in = (at & ((1 << v.page_shift) - 1)) >> 4, tiles = 1 << (v.page_shift - 4);
     return v.cache + (long long)id * v.page_bytes + (long long)(h * tiles + in) * KvLay<D>::kBytes;
+}
+
+template <int DT>
+__device__ __forceinline__ float of_bits(uint32_t bits16)
+{
+    if constexpr (DT == DT_F16) return f16_to_f32(bits16);
+    else return __builtin_bit_cast(float, bits16 << 16);
+}
+
+// E neighbouring values as 16-bit ones or floats.
+template <int OT, int E>
+__device__ __forceinline__ void store_out(void *base, long long i, const float (&x)[E])
+{
+    if constexpr (OT == QGEMM_F32) {
+#pragma unroll
+        for (int j = 0; j < E / 4; j++)
+            *(f32x4 *)((float *)base + i + 4 * j) = f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+    } else {
+        uint32_t w[E / 2];
+#pragma unroll
+        for (int j = 0; j < E / 2; j++) w[j] = pack_out<OT>(x[2 * j], x[2 * j + 1]);
+        __builtin_memcpy(__builtin_assume_aligned((uint16_t *)base + i, 2 * E), w, 2 * E);
+    }
 }
 
 // Norm and rotation of heads: what qk_norm_rope and kv_append share.
@@ -141,6 +164,9 @@ struct AppendArgs {
     long long kv_blocks;    // workgroups of keys and values; the rest are the queries'
 };
 
+// Partial results of the attention: of one row and query head from one part of
+// the keys, the sums of p*v [D] relative to its own maximum, and (maximum, sum
+// of p, log2 units per unit of the maximum, unused).
 struct AttnArgs {
     KvView v;
     const uint16_t *q;
@@ -149,12 +175,29 @@ struct AttnArgs {
     int heads, group;       // query heads, and of them to a key head
     int window;             // 0: none
     float scale;
+    int few_rows;           // sequences of at most so many rows (tokens * group) are k_attn_few's
+    int few_tiles;          // k_attn_few: row tiles of a sequence
+    int few_splits, few_chunk;    // k_attn_few: workgroups along the keys, keys of each
+    int many_splits, many_chunk;  // k_attn_many's
+    int tile_tokens, slots;       // k_attn_many: tokens of a row tile, row tiles of all sequences (a bound)
+    float *few_sum, *many_sum;    // partial results (null: one split)
+    f32x4 *few_stat, *many_stat;
 };
+
+// The parts of a call's workspace and its launches (kv_attention.hip).
+struct AttnPlan {
+    bool few, many;
+    int few_rows, few_tiles, few_rb;
+    int few_splits, few_chunk, many_splits, many_chunk, tile_tokens, many_waves;
+    long long slots, few_entries, many_entries;  // entries: rows * heads * splits kept
+    size_t bytes;
+};
+AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D, long long max_len, bool ragged);
 
 hipError_t launch_norm_rope(int dtype, int D, const NormRopeArgs &a, hipStream_t s);
 hipError_t launch_kv_append(int dtype, int D, const AppendArgs &a, hipStream_t s);
 // out_type: QGEMM_F16, QGEMM_BF16 or QGEMM_F32
 hipError_t launch_kv_read(int out_type, int D, const KvView &v, void *k, void *val, hipStream_t s);
-hipError_t launch_kv_attention(int dtype, int D, const AttnArgs &a, hipStream_t s);
+hipError_t launch_kv_attention(int dtype, int D, const AttnPlan &pl, AttnArgs a, void *workspace, hipStream_t s);
 
 }  // namespace qg

@@ -72,6 +72,18 @@ int view_of(const void *cache, long long pages, long long page, const int32_t *t
     return QGEMM_OK;
 }
 
+// Sizes of an attention call, S and T checked before; max_len is the bound on the lengths that counts.
+int attention_shape(long long T, long long S, long long heads, long long kv_heads, long long D, long long max_len)
+{
+    int st = head_shape(heads, kv_heads, D);
+    if (st != QGEMM_OK) return st;
+    if (heads < 1 || heads % kv_heads != 0 || heads / kv_heads > 128 || T > INT32_MAX / 2 || S > INT32_MAX / 8 ||
+        max_len < 0 || max_len > INT32_MAX)
+        return QGEMM_ERR_SHAPE;
+    // every launch's work-items along x below 2^32: 16 lanes per row and head, 512 threads per sequence and head
+    return items_fit(T * heads) && items_fit(32 * S * heads) ? QGEMM_OK : QGEMM_ERR_SHAPE;
+}
+
 }  // namespace
 }  // namespace qg
 
@@ -183,8 +195,8 @@ int qgemm_kv_read(const void *cache, int64_t pages, int64_t page, const int32_t 
 size_t qgemm_kv_attention_workspace_bytes(int64_t T, int64_t S, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                           int64_t max_len, int ragged)
 {
-    (void)T, (void)S, (void)heads, (void)kv_heads, (void)head_dim, (void)max_len, (void)ragged;
-    return 0;
+    if (T < 1 || S < 1 || T > INT32_MAX / 2 || S > INT32_MAX / 8 || attention_shape(T, S, heads, kv_heads, head_dim, max_len) != QGEMM_OK) return 0;
+    return plan_attention(T, S, (int)heads, (int)kv_heads, (int)head_dim, max_len, ragged != 0).bytes;
 }
 
 int qgemm_kv_attention(const void *Q, int64_t q_stride, const void *cache, int64_t pages, int64_t page,
@@ -196,17 +208,17 @@ int qgemm_kv_attention(const void *Q, int64_t q_stride, const void *cache, int64
     if (dtype != DT_F16 && dtype != DT_BF16) return QGEMM_ERR_DTYPE;
     int st = head_shape(heads, kv_heads, head_dim);
     if (st != QGEMM_OK) return st;
-    if (heads < 1 || heads % kv_heads != 0 || heads / kv_heads > 128 || window < 0 || max_len < 0 || scale != scale)
-        return QGEMM_ERR_SHAPE;
+    if (window < 0 || max_len < 0 || !std::isfinite(scale)) return QGEMM_ERR_SHAPE;
     if ((st = view_of(cache, pages, page, tables, table_width, lens, offsets, S, T, kv_heads, head_dim, a.v)) != QGEMM_OK)
         return st;
-    if (!items_fit((T + S) * heads)) return QGEMM_ERR_SHAPE;
+    const long long capacity = table_width * page, bound = max_len == 0 || max_len > capacity ? capacity : max_len;
+    if ((st = attention_shape(T, S, heads, kv_heads, head_dim, bound)) != QGEMM_OK) return st;
     if (T == 0 || S == 0) return QGEMM_OK;
     if ((st = rows_of(Q, q_stride, heads, head_dim, false)) != QGEMM_OK) return st;
     if (!Y) return QGEMM_ERR_NULL;
     if (!aligned(Y, 16)) return QGEMM_ERR_ALIGN;
-    if (workspace_bytes < qgemm_kv_attention_workspace_bytes(T, S, heads, kv_heads, head_dim, max_len, offsets != nullptr))
-        return QGEMM_ERR_SIZE;
+    const AttnPlan pl = plan_attention(T, S, (int)heads, (int)kv_heads, (int)head_dim, bound, offsets != nullptr);
+    if (pl.bytes && (!workspace || workspace_bytes < pl.bytes)) return QGEMM_ERR_SIZE;
     if (!aligned(workspace, 16)) return QGEMM_ERR_ALIGN;
     a.q = (const uint16_t *)Q;
     a.q_stride = q_stride;
@@ -215,7 +227,7 @@ int qgemm_kv_attention(const void *Q, int64_t q_stride, const void *cache, int64
     a.group = (int)(heads / kv_heads);
     a.window = (int)(window > INT32_MAX ? 0 : window);
     a.scale = scale;
-    return status_of(launch_kv_attention(dtype, (int)head_dim, a, (hipStream_t)stream), "cache attention");
+    return status_of(launch_kv_attention(dtype, (int)head_dim, pl, a, workspace, (hipStream_t)stream), "cache attention");
 }
 
 }  // extern "C"

@@ -1,0 +1,672 @@
+// kv_attention.hip -- attention over the 4-bit paged cache.
+//
+//   y_i = sum_t p_it v_t / sum_t p_it,  p_it = exp(scale (q_i.k_t) - m_i)
+//
+// Both kernels compute the transposed products: S^T = K Q^T with the keys as
+// the MFMA's A rows, then O^T = V^T P^T.  An accumulator column is then a query
+// row: its running maximum and sum live in the lanes that hold the column, the
+// rescaling of O is one factor per lane, and the registers that S^T leaves
+// are, packed to fp16, the B operand of the second product as they stand (the
+// order of the contraction is free as long as V's registers run over the same
+// tokens, which the cache's layout does).  Nothing of P goes through LDS.
+//
+// Operands are fp16 for both activation types.  Queries in bfloat16 are scaled
+// by a power of two per row, which fp16 then holds exactly but for elements 2^-22
+// of the row's largest; keys and values are code*scale + minimum rounded once to
+// fp16 (v_fma_mix, as the weights of the fp16 GEMMs), probabilities likewise.
+// Products, maxima, sums and O are binary32.
+//
+// The maximum is kept in units of the products, so that the exponent's argument
+// (x - m)*c is at most 0 whatever their size, and is raised only when some row's
+// products pass it by more than 2^kLift: O is then rescaled rarely, and
+// probabilities stay far below fp16's range.
+#include "kv.h"
+
+namespace qg {
+namespace {
+
+constexpr float kLift = 8.0f;
+constexpr float kLog2e = 1.44269504f;
+
+template <int D>
+struct Words {
+    typedef uint32_t W __attribute__((ext_vector_type(D / 32)));  // a lane's codes of 16 tokens
+};
+
+// Eight codes of one key -> eight fp16 values; f is scale*2^24, b the minimum.
+__device__ __forceinline__ u32x4 key_values(uint32_t w, float f, float b)
+{
+    const float f16 = f * 0.0625f;
+    const uint32_t h = w >> 8;
+    return u32x4{dq_pair<DT_F16>(w & 0x000F000Fu, f, b), dq_pair<DT_F16>(w & 0x00F000F0u, f16, b),
+                 dq_pair<DT_F16>(h & 0x000F000Fu, f, b), dq_pair<DT_F16>(h & 0x00F000F0u, f16, b)};
+}
+
+// Two codes of two tokens.
+__device__ __forceinline__ uint32_t two_values(uint32_t t, float f0, float b0, float f1, float b1)
+{
+    const f16x2 h = __builtin_bit_cast(f16x2, t);
+    const f16x2 r = {(_Float16)__builtin_fmaf((float)h.x, f0, b0), (_Float16)__builtin_fmaf((float)h.y, f1, b1)};
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ float head_scale(uint32_t h) { return f16_to_f32(h & 0xFFFFu) * kTwo24; }
+__device__ __forceinline__ float head_min(uint32_t h) { return f16_to_f32(h >> 16); }
+
+// A quad's values: word w of a lane, dims 2w and 2w+1 of four tokens, as two dims
+// of two fp16 pairs.
+struct QuadHead {
+    float f[4], b[4];  // tokens 2 and 3 with their codes four bits up
+};
+
+__device__ __forceinline__ QuadHead quad_head(u32x4 h)
+{
+    QuadHead q;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        q.f[i] = head_scale(h[i]) * (i < 2 ? 1.0f : 0.0625f);
+        q.b[i] = head_min(h[i]);
+    }
+    return q;
+}
+
+__device__ __forceinline__ u32x2 quad_values(uint32_t w, const QuadHead &q)
+{
+    return u32x2{two_values(w & 0x000F000Fu, q.f[0], q.b[0], q.f[1], q.b[1]),
+                 two_values(w & 0x00F000F0u, q.f[2], q.b[2], q.f[3], q.b[3])};
+}
+
+// Headers of tokens that the sequence does not have are cleared: their
+// probability is 0, and 0 times what lies there could be NaN.
+__device__ __forceinline__ u32x4 live_heads(u32x4 h, int from, int len)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++) h[i] = from + i < len ? h[i] : 0u;
+    return h;
+}
+
+// The tile at place t (a multiple of 16) for key head h: its address, and whether
+// the table names a page for it; the address is inside the cache either way.  t is
+// the same in all lanes.
+template <int D>
+__device__ __forceinline__ const uint8_t *wave_tile(const KvView &v, int s, int t, int h, bool &there)
+{
+    const int i = t >> v.page_shift;
+    int id = -1;
+    if (i < v.width) id = v.tables[(long long)s * v.width + i];
+    there = (unsigned)id < (unsigned)v.pages;
+    id = there ? id : 0;
+    const int in = (t & ((1 << v.page_shift) - 1)) >> 4, tiles = 1 << (v.page_shift - 4);
+    return v.cache + (long long)id * v.page_bytes + (long long)(h * tiles + in) * KvLay<D>::kBytes;
+}
+
+// One query row as P pieces of eight dims, `step` dims from one to the next, in
+// fp16; returns log2 units per unit of the products.  The row's lanes are ACROSS
+// lanes apart (a multiple of it up to 64).
+template <int DT, int P, int ACROSS>
+__device__ __forceinline__ float load_query(const uint16_t *x, bool live, int step, float scale, u32x4 (&f)[P])
+{
+    const uint32_t sign = scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int j = 0; j < P; j++) {
+        f[j] = live ? *(const u32x4 *)(x + j * step) : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[j][i] ^= sign;
+    }
+    float c = fabsf(scale) * kLog2e;
+    if constexpr (DT == DT_BF16) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < P; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) mx = max(mx, max(f[j][i] & 0x7FFFu, (f[j][i] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int d = ACROSS; d < 64; d <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d, 64));
+        int e = (int)(mx >> 7);                       // the largest magnitude's exponent
+        e = e == 0xFF || mx == 0 ? 127 + 8 : max(e, 27);  // infinities and NaN as they are
+        const float down = __builtin_bit_cast(float, (uint32_t)(127 + 8 + 127 - e) << 23);
+        c *= __builtin_bit_cast(float, (uint32_t)(max(e - 8, 1)) << 23);
+#pragma unroll
+        for (int j = 0; j < P; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                f[j][i] = pack_out<DT_F16>(of_bits<DT_BF16>(f[j][i] & 0xFFFFu) * down, of_bits<DT_BF16>(f[j][i] >> 16) * down);
+    }
+    return fminf(fmaxf(c, 1.17549435e-38f), 1e37f);  // never 0 or infinite: an exponent's argument is 0 at the maximum, -inf where masked
+}
+
+__device__ __forceinline__ float exp_from(float x, float m, float c) { return __builtin_amdgcn_exp2f((x - m) * c); }
+
+// The new maximum of a row whose products reach mx: by the row alone, whatever
+// made its wave look.
+__device__ __forceinline__ float raised(float mx, float m, float c) { return (mx - m) * c > kLift ? mx : m; }
+
+// Keys that a range of rows sees.
+struct Range {
+    int lo, hi;
+};
+
+__device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0, int rows)
+{
+    const int cap = a.v.width << a.v.page_shift;
+    const int pmin = q.first + row0 / a.group, pmax = q.first + (row0 + rows - 1) / a.group;
+    return Range{a.window ? max(pmin - a.window + 1, 0) : 0, min(pmax + 1, cap)};
+}
+
+// ---------------------------------------------------------------------------
+// A few rows of each sequence (single tokens): a stream of the cache.  A
+// workgroup takes one key head of one sequence, 16*RB rows and a chunk of the
+// keys; its four waves take steps of 32 keys in turn, straight from memory into
+// MFMA registers, and add their results through LDS.
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 4;
+constexpr int kStep = 32;
+
+template <int D>
+struct FewRaw {
+    typename Words<D>::W k[2], v[2];
+    uint32_t kh[2];
+    u32x4 vh[2];
+    bool there[2];
+};
+
+template <int D>
+__device__ __forceinline__ void few_load(const AttnArgs &a, int s, int h, int t, int lane, FewRaw<D> &r)
+{
+    using L = KvLay<D>;
+    using W = typename Words<D>::W;
+    const int n = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint8_t *p = wave_tile<D>(a.v, s, t + 16 * i, h, r.there[i]);
+        r.k[i] = *(const W *)(p + lane * L::kLane);
+        r.kh[i] = *(const uint32_t *)(p + L::kKeyHead + (g * (D / 4) / 32 * 16 + n) * 4);
+        r.v[i] = *(const W *)(p + L::kVal + lane * L::kLane);
+        r.vh[i] = *(const u32x4 *)(p + L::kValHead + (n * L::E / 32 * 16 + 4 * g) * 4);
+    }
+}
+
+template <int DT, int D, int RB>
+__global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
+{
+    using L = KvLay<D>;
+    constexpr int E = L::E, J = D / 32, LD = D + 4;
+    __shared__ __align__(16) float s_o[kFewWaves][16][LD];
+    __shared__ float s_m[kFewWaves][16], s_l[kFewWaves][16], s_c[16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    int b = blockIdx.x;
+    const int rt = b % a.few_tiles;
+    b /= a.few_tiles;
+    const int h = b % a.v.H, s = b / a.v.H, z = blockIdx.y;
+    const Seq q = seq_of(a.v, s);
+    const int all = q.n * a.group, row0 = rt * 16 * RB;
+    if ((a.v.offs && all > a.few_rows) || row0 >= all) return;
+    const int rows = min(all - row0, 16 * RB);
+    const Range keys = seen(a, q, row0, rows);
+    const int from = max(keys.lo & ~(kStep - 1), z * a.few_chunk), to = z + 1 < a.few_splits ? min(keys.hi, (z + 1) * a.few_chunk) : keys.hi;
+
+    u32x4 qf[RB][J];
+    float c[RB], m[RB], l[RB];
+    int place[RB];
+    f32x4 o[RB][E];
+#pragma unroll
+    for (int rb = 0; rb < RB; rb++) {
+        const int r = row0 + 16 * rb + n, token = r / a.group;
+        const bool live = r < all;
+        place[rb] = live ? q.first + token : -1;
+        c[rb] = load_query<DT, J, 16>(a.q + (long long)(q.row + (live ? token : 0)) * a.q_stride +
+                                          (h * a.group + r - token * a.group) * D + g * (D / 4),
+                                      live, 8, a.scale, qf[rb]);
+        m[rb] = -INFINITY;
+        l[rb] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; e++) o[rb][e] = f32x4{0, 0, 0, 0};
+    }
+
+    const int stride = kStep * kFewWaves;
+    const int pmin = q.first + row0 / a.group, pmax_lo = a.window ? q.first + (row0 + rows - 1) / a.group - a.window + 1 : 0;
+    int t = from + wave * kStep;
+    FewRaw<D> next;
+    if (t < to) few_load<D>(a, s, h, t, lane, next);
+    for (; t < to; t += stride) {
+        FewRaw<D> r = next;
+        if (t + stride < to) few_load<D>(a, s, h, t + stride, lane, next);
+        f32x4 x[RB][2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float f = head_scale(r.kh[i]), bm = head_min(r.kh[i]);
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++) x[rb][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                const u32x4 kv = key_values(r.k[i][j], f, bm);
+#pragma unroll
+                for (int rb = 0; rb < RB; rb++) x[rb][i] = mma<DT_F16>(kv, qf[rb][j], x[rb][i]);
+            }
+        }
+        const bool whole = r.there[0] && r.there[1];
+        if (!(whole && t + kStep - 1 <= pmin && t >= pmax_lo)) {
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        const int at = t + 16 * i + 4 * g + u;
+                        const bool ok = r.there[i] && at <= place[rb] && (!a.window || at > place[rb] - a.window);
+                        x[rb][i][u] = ok ? x[rb][i][u] : -INFINITY;
+                    }
+        }
+        if (!whole || t + kStep > q.len) {
+#pragma unroll
+            for (int i = 0; i < 2; i++) r.vh[i] = live_heads(r.vh[i], t + 16 * i + 4 * g, r.there[i] ? q.len : 0);
+        }
+        u32x4 p[RB];
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++) {
+            float mx = fmaxf(fmaxf(fmaxf(x[rb][0][0], x[rb][0][1]), fmaxf(x[rb][0][2], x[rb][0][3])),
+                             fmaxf(fmaxf(x[rb][1][0], x[rb][1][1]), fmaxf(x[rb][1][2], x[rb][1][3])));
+            if (__any((mx - m[rb]) * c[rb] > kLift)) {
+                mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+                mx = raised(fmaxf(mx, __shfl_xor(mx, 32, 64)), m[rb], c[rb]);
+                const float f = m[rb] == -INFINITY ? 0.0f : exp_from(m[rb], mx, c[rb]);
+                m[rb] = mx;
+                l[rb] *= f;
+#pragma unroll
+                for (int e = 0; e < E; e++) o[rb][e] *= f;
+            }
+            const float base = m[rb] == -INFINITY ? 0.0f : m[rb];
+            float pr[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                pr[u] = exp_from(x[rb][u >> 2][u & 3], base, c[rb]);
+                l[rb] += pr[u];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; u++) p[rb][u] = pack_out<DT_F16>(pr[2 * u], pr[2 * u + 1]);
+        }
+        const QuadHead h0 = quad_head(r.vh[0]), h1 = quad_head(r.vh[1]);
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const u32x2 v0 = quad_values(r.v[0][e >> 1] >> (8 * (e & 1)), h0);
+            const u32x2 v1 = quad_values(r.v[1][e >> 1] >> (8 * (e & 1)), h1);
+            const u32x4 v = {v0.x, v0.y, v1.x, v1.y};
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++) o[rb][e] = mma<DT_F16>(v, p[rb], o[rb][e]);
+        }
+    }
+
+#pragma unroll
+    for (int rb = 0; rb < RB; rb++) {
+        if (RB > 1 && 16 * rb >= rows) break;
+        l[rb] += __shfl_xor(l[rb], 16, 64);
+        l[rb] += __shfl_xor(l[rb], 32, 64);
+        if (rb) __syncthreads();
+        // lane: row n, dims E*(4g + i) + e
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int e = 0; e < E; e += 4)
+                *(f32x4 *)&s_o[wave][n][E * (4 * g + i) + e] =
+                    f32x4{o[rb][e][i], o[rb][e + 1][i], o[rb][e + 2][i], o[rb][e + 3][i]};
+        if (g == 0) {
+            s_m[wave][n] = m[rb];
+            s_l[wave][n] = l[rb];
+            if (wave == 0) s_c[n] = c[rb];
+        }
+        __syncthreads();
+        const int rr = threadIdx.x >> 4, dl = threadIdx.x & 15, r = 16 * rb + rr;
+        if (r >= rows) continue;
+        const float cr = s_c[rr];
+        float mx = s_m[0][rr], sum = 0.0f, y[E];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; w++) mx = fmaxf(mx, s_m[w][rr]);
+#pragma unroll
+        for (int e = 0; e < E; e++) y[e] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; w++) {
+            const float f = s_m[w][rr] == -INFINITY ? 0.0f : exp_from(s_m[w][rr], mx, cr);
+            sum += s_l[w][rr] * f;
+#pragma unroll
+            for (int e = 0; e < E; e++) y[e] += s_o[w][rr][E * dl + e] * f;
+        }
+        const int ra = row0 + r, token = ra / a.group;
+        if (a.few_splits == 1) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int e = 0; e < E; e++) y[e] *= inv;
+            store_out<DT, E>(a.y, ((long long)(q.row + token) * a.heads + h * a.group + ra - token * a.group) * D + E * dl, y);
+        } else {
+            const long long entry = ((long long)(s * a.v.H + h) * a.few_rows + ra) * a.few_splits + z;
+            if (sum != 0.0f) store_out<QGEMM_F32, E>(a.few_sum, entry * D + E * dl, y);
+            if (dl == 0) a.few_stat[entry] = f32x4{mx, sum, cr, 0.0f};
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows (prompts): a workgroup takes one key head and 32 rows per wave,
+// row r being token r/group, head r%group of the key head's; tiles of 64 keys are
+// unpacked once into LDS, in fragment order, for all its waves.
+// ---------------------------------------------------------------------------
+constexpr int kKeys = 64;
+
+template <int D>
+struct ManyRaw {
+    typename Words<D>::W w;
+    u32x4 head;
+    bool there;
+};
+
+// Job 0..3: the keys of a tile's 16 tokens; 4..7: their values.
+template <int D>
+__device__ __forceinline__ void many_load(const AttnArgs &a, int s, int h, int kt, int job, int lane, ManyRaw<D> &r)
+{
+    using L = KvLay<D>;
+    using W = typename Words<D>::W;
+    const int n = lane & 15, g = lane >> 4;
+    const uint8_t *p = wave_tile<D>(a.v, s, kt * kKeys + 16 * (job & 3), h, r.there);
+    if (job < 4) {
+        r.w = *(const W *)(p + lane * L::kLane);
+        r.head.x = *(const uint32_t *)(p + L::kKeyHead + (g * (D / 4) / 32 * 16 + n) * 4);
+    } else {
+        r.w = *(const W *)(p + L::kVal + lane * L::kLane);
+        r.head = *(const u32x4 *)(p + L::kValHead + (n * L::E / 32 * 16 + 4 * g) * 4);
+    }
+}
+
+// LDS of one tile of keys and values: keys as [32-key half][8-dim piece][key]
+// of 16 bytes; values as [16 tokens][32-dim block][quad parity][dim row] of 16
+// bytes, two quads of four tokens.  Row d of block b is dim E*(d%16) + 2b + d/16:
+// a wave's stores are then contiguous, and a lane ends with E neighbouring dims.
+template <int D>
+struct ManyLds {
+    uint4 k[2][D / 8][32];
+    uint2 v[4][D / 32][2][32][2];
+    int absent[4];
+};
+
+template <int D>
+__device__ __forceinline__ void many_store(ManyLds<D> &t, const ManyRaw<D> &r, int kt, int job, int len, int lane)
+{
+    constexpr int E = D / 16;
+    const int n = lane & 15, g = lane >> 4, i = job & 3;
+    if (job < 4) {
+        const float f = head_scale(r.head.x), b = head_min(r.head.x);
+#pragma unroll
+        for (int j = 0; j < D / 32; j++) {
+            const u32x4 kv = key_values(r.w[j], f, b);
+            *(u32x4 *)&t.k[i >> 1][(D / 32) * g + j][16 * (i & 1) + n] = kv;
+        }
+        if (lane == 0) t.absent[i] = !r.there;
+    } else {
+        u32x4 hd = r.head;
+        const int at = kt * kKeys + 16 * i;
+        if (!r.there || at + 16 > len) hd = live_heads(hd, at + 4 * g, r.there ? len : 0);
+        const QuadHead q = quad_head(hd);
+#pragma unroll
+        for (int e = 0; e < E; e++)
+            *(u32x2 *)&t.v[i][e >> 1][g & 1][n + 16 * (e & 1)][g >> 1] = quad_values(r.w[e >> 1] >> (8 * (e & 1)), q);
+    }
+}
+
+template <int DT, int D, int NW>
+__global__ void __launch_bounds__(64 * NW) k_attn_many(AttnArgs a)
+{
+    constexpr int E = D / 16, B = D / 32, P = D / 16, JOBS = 8 / NW;
+    __shared__ __align__(16) ManyLds<D> lds[2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 31, g = lane >> 5;
+    // key heads side by side, so that with a multiple of eight of them each XCD's
+    // L2 holds its own; later row tiles, which see more keys, first
+    const int h = blockIdx.x % a.v.H, slot = a.slots - 1 - (int)(blockIdx.x / a.v.H), z = blockIdx.y;
+    const int s = __builtin_amdgcn_readfirstlane(find_seq<64>(a.v, slot, a.tile_tokens, 1));
+    const Seq q = seq_of(a.v, s);
+    const int all = q.n * a.group;
+    const int tile = slot - (row_end(a.v, s) / a.tile_tokens + s), row0 = tile * a.tile_tokens * a.group;
+    if (tile < 0 || row0 >= all || all <= a.few_rows) return;
+    const int rows = min(all - row0, a.tile_tokens * a.group);
+    const Range keys = seen(a, q, row0, rows);
+    const int from = max(keys.lo, z * a.many_chunk), to = z + 1 < a.many_splits ? min(keys.hi, (z + 1) * a.many_chunk) : keys.hi;
+
+    const int w0 = 32 * wave, r = row0 + w0 + n, token = r / a.group;
+    const bool live = w0 + n < rows;
+    const int place = live ? q.first + token : -1;
+    const Range mine = w0 < rows ? seen(a, q, row0 + w0, min(rows - w0, 32)) : Range{0, 0};
+    // keys that every row of the wave sees: [clear_lo, clear_hi]
+    const int clear_hi = q.first + (row0 + w0) / a.group;
+    const int clear_lo = a.window ? q.first + (row0 + min(rows, w0 + 32) - 1) / a.group - a.window + 1 : 0;
+
+    u32x4 qf[P];
+    const float c = load_query<DT, P, 32>(a.q + (long long)(q.row + (live ? token : 0)) * a.q_stride +
+                                              (h * a.group + r - token * a.group) * D + 8 * g,
+                                          live, 16, a.scale, qf);
+    float m = -INFINITY, l = 0.0f;
+    f32x16 o[B];
+#pragma unroll
+    for (int b = 0; b < B; b++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) o[b][i] = 0.0f;
+
+    const int kt0 = from / kKeys, kt1 = to > from ? (to + kKeys - 1) / kKeys : kt0;
+    ManyRaw<D> raw[JOBS];
+    if (kt0 < kt1) {
+#pragma unroll
+        for (int j = 0; j < JOBS; j++) many_load<D>(a, s, h, kt0, wave + j * NW, lane, raw[j]);
+#pragma unroll
+        for (int j = 0; j < JOBS; j++) many_store<D>(lds[0], raw[j], kt0, wave + j * NW, q.len, lane);
+        if (kt0 + 1 < kt1)
+#pragma unroll
+            for (int j = 0; j < JOBS; j++) many_load<D>(a, s, h, kt0 + 1, wave + j * NW, lane, raw[j]);
+    }
+    for (int kt = kt0; kt < kt1; kt++) {
+        __syncthreads();  // this tile is whole, and the other buffer's readers are done
+        const ManyLds<D> &t = lds[(kt - kt0) & 1];
+        if (kt + 1 < kt1) {
+#pragma unroll
+            for (int j = 0; j < JOBS; j++) many_store<D>(lds[(kt - kt0 + 1) & 1], raw[j], kt + 1, wave + j * NW, q.len, lane);
+        }
+        if (kt + 2 < kt1) {
+#pragma unroll
+            for (int j = 0; j < JOBS; j++) many_load<D>(a, s, h, kt + 2, wave + j * NW, lane, raw[j]);
+        }
+        const int k0 = kt * kKeys;
+        if (k0 >= min(mine.hi, to) || k0 + kKeys <= mine.lo) continue;
+        f32x16 x[2];
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) x[b][i] = 0.0f;
+#pragma unroll
+            for (int p = 0; p < P; p++) x[b] = mma32<DT_F16>(*(const u32x4 *)&t.k[b][2 * p + g][n], qf[p], x[b]);
+        }
+        const int4 gone = *(const int4 *)t.absent;
+        const bool some_gone = __builtin_amdgcn_readfirstlane(gone.x | gone.y | gone.z | gone.w) != 0;
+        if (some_gone || k0 + kKeys - 1 > clear_hi || k0 < clear_lo) {
+            const int ab[4] = {gone.x, gone.y, gone.z, gone.w};
+#pragma unroll
+            for (int b = 0; b < 2; b++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int at = k0 + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3);
+                    const bool ok = at <= place && (!a.window || at > place - a.window) && !ab[2 * b + (i >> 3)];
+                    x[b][i] = ok ? x[b][i] : -INFINITY;
+                }
+        }
+        float mx = x[0][0];
+#pragma unroll
+        for (int b = 0; b < 2; b++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) mx = fmaxf(mx, x[b][i]);
+        if (__any((mx - m) * c > kLift)) {
+            mx = raised(fmaxf(mx, __shfl_xor(mx, 32, 64)), m, c);
+            const float f = m == -INFINITY ? 0.0f : exp_from(m, mx, c);
+            m = mx;
+            l *= f;
+#pragma unroll
+            for (int b = 0; b < B; b++) o[b] *= f;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {  // 16 tokens: registers 8*(u%2) .. +7 of half u/2
+            float pr[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                pr[i] = exp_from(x[u >> 1][8 * (u & 1) + i], base, c);
+                l += pr[i];
+            }
+            const u32x4 p = {pack_out<DT_F16>(pr[0], pr[1]), pack_out<DT_F16>(pr[2], pr[3]), pack_out<DT_F16>(pr[4], pr[5]),
+                             pack_out<DT_F16>(pr[6], pr[7])};
+#pragma unroll
+            for (int b = 0; b < B; b++) o[b] = mma32<DT_F16>(*(const u32x4 *)&t.v[u][b][g][n][0], p, o[b]);
+        }
+    }
+    l += __shfl_xor(l, 32, 64);
+    if (!live) return;
+    const long long row = (long long)(q.row + token) * a.heads + h * a.group + r - token * a.group;
+    const long long entry = row * a.many_splits + z;
+    const float inv = a.many_splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        float y[E];
+#pragma unroll
+        for (int b = 0; b < B; b++) {
+            y[2 * b] = o[b][i] * inv;
+            y[2 * b + 1] = o[b][i + 8] * inv;
+        }
+        const int d = E * (8 * (i >> 2) + 4 * g + (i & 3));
+        if (a.many_splits == 1) store_out<DT, E>(a.y, row * D + d, y);
+        else if (l != 0.0f) store_out<QGEMM_F32, E>(a.many_sum, entry * D + d, y);
+    }
+    if (a.many_splits > 1 && g == 0) a.many_stat[entry] = f32x4{m, l, c, 0.0f};
+}
+
+// The parts of a row's keys joined: 16 lanes per row and query head.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) k_attn_join(AttnArgs a)
+{
+    constexpr int E = D / 16;
+    const int item = (int)(blockIdx.x * 16 + (threadIdx.x >> 4)), dl = threadIdx.x & 15;
+    const int row = item / a.heads, head = item - row * a.heads;
+    if (row >= a.v.T) return;
+    const int s = a.v.offs ? find_seq<16>(a.v, row, 1, 0) : row;
+    const Seq q = seq_of(a.v, s);
+    if (row < q.row || row >= q.row + q.n) return;
+    const bool few = !a.v.offs || q.n * a.group <= a.few_rows;
+    const int splits = few ? a.few_splits : a.many_splits;
+    if (splits == 1) return;  // written where it was computed
+    const int h = head / a.group, ra = (row - q.row) * a.group + head - h * a.group;
+    const long long entry = few ? ((long long)(s * a.v.H + h) * a.few_rows + ra) * splits
+                                : ((long long)row * a.heads + head) * splits;
+    const f32x4 *stat = (few ? a.few_stat : a.many_stat) + entry;
+    const float *sums = (few ? a.few_sum : a.many_sum) + entry * D + E * dl;
+    float mx = -INFINITY;
+    for (int z = dl; z < splits; z += 16) mx = fmaxf(mx, stat[z].x);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 16));
+    float y[E], sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; e++) y[e] = 0.0f;
+    for (int z = 0; z < splits; z++) {
+        const f32x4 st = stat[z];
+        if (st.y == 0.0f) continue;  // no keys, and no sums written
+        const float f = exp_from(st.x, mx, st.z);
+        sum += st.y * f;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            const f32x4 v = *(const f32x4 *)(sums + (long long)z * D + e);
+#pragma unroll
+            for (int i = 0; i < 4; i++) y[e + i] += v[i] * f;
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < E; e++) y[e] *= inv;
+    store_out<DT, E>(a.y, ((long long)row * a.heads + head) * D + E * dl, y);
+}
+
+long long ceil_of(long long a, long long b) { return (a + b - 1) / b; }
+
+template <int DT, int D, int RB>
+void run_few(const AttnArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_attn_few<DT, D, RB>), dim3((unsigned)(a.v.S * a.v.H * a.few_tiles), (unsigned)a.few_splits),
+                       dim3(64 * kFewWaves), 0, s, a);
+}
+
+template <int DT, int D, int NW>
+hipError_t run_many(const AttnArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_attn_many<DT, D, NW>), dim3((unsigned)(a.slots * a.v.H), (unsigned)a.many_splits), dim3(64 * NW), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int DT, int D>
+hipError_t run_attention(const AttnPlan &pl, const AttnArgs &a, hipStream_t s)
+{
+    if (pl.few) {
+        if (pl.few_rb == 1) run_few<DT, D, 1>(a, s);
+        else run_few<DT, D, 2>(a, s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (pl.many) {
+        const hipError_t e = pl.many_waves == 8 ? run_many<DT, D, 8>(a, s) : run_many<DT, D, 4>(a, s);
+        if (e != hipSuccess) return e;
+    }
+    if ((pl.few && pl.few_splits > 1) || (pl.many && pl.many_splits > 1))
+        hipLaunchKernelGGL((k_attn_join<DT, D>), dim3((unsigned)ceil_of((long long)a.v.T * a.heads, 16)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D, long long max_len, bool ragged)
+{
+    AttnPlan p{};
+    const int group = heads / kv_heads;
+    // ragged: k_attn_few takes the sequences of at most 32 rows, if there can be any beside one long one
+    p.few = !ragged || S > 1 || T * group <= 32;
+    p.many = ragged && T * group > 32;
+    p.few_rows = !p.few ? 0 : ragged ? 32 : group;
+    p.few_rb = p.few_rows <= 16 ? 1 : 2;
+    p.few_tiles = (int)ceil_of(p.few_rows > 0 ? p.few_rows : 1, 16 * p.few_rb);
+    if (max_len < 1) max_len = 1;
+    // chunks of whole steps for every wave; enough workgroups to fill the CUs
+    const long long step = kStep * kFewWaves, units = S * kv_heads * p.few_tiles;
+    long long chunk = ceil_of(ceil_of(units * max_len, 1536), step) * step;
+    if (ceil_of(max_len, chunk) > 128) chunk = ceil_of(ceil_of(max_len, 128), step) * step;
+    p.few_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
+    p.few_splits = (int)ceil_of(max_len, p.few_chunk);
+    p.few_entries = p.few && p.few_splits > 1 ? S * kv_heads * (long long)p.few_rows * p.few_splits : 0;
+    p.many_waves = 8;
+    p.tile_tokens = 32 * p.many_waves / group;
+    p.slots = T / p.tile_tokens + S;
+    p.many_splits = 1;
+    p.many_chunk = INT32_MAX / 2;
+    p.many_entries = 0;
+    p.bytes = (size_t)(p.few_entries + p.many_entries) * (size_t)(D + 4) * 4;
+    return p;
+}
+
+hipError_t launch_kv_attention(int dtype, int D, const AttnPlan &pl, AttnArgs a, void *workspace, hipStream_t s)
+{
+    a.few_rows = pl.few_rows;
+    a.few_tiles = pl.few_tiles;
+    a.few_splits = pl.few_splits;
+    a.few_chunk = pl.few_chunk;
+    a.many_splits = pl.many_splits;
+    a.many_chunk = pl.many_chunk;
+    a.tile_tokens = pl.tile_tokens;
+    a.slots = (int)pl.slots;
+    float *w = (float *)workspace;
+    a.few_stat = (f32x4 *)w;
+    a.many_stat = a.few_stat + pl.few_entries;
+    a.few_sum = (float *)(a.many_stat + pl.many_entries);
+    a.many_sum = a.few_sum + pl.few_entries * D;
+    if (dtype == DT_F16) return D == 64 ? run_attention<DT_F16, 64>(pl, a, s) : run_attention<DT_F16, 128>(pl, a, s);
+    return D == 64 ? run_attention<DT_BF16, 64>(pl, a, s) : run_attention<DT_BF16, 128>(pl, a, s);
+}
+
+}  // namespace qg

@@ -19,13 +19,6 @@ __device__ __forceinline__ F sum16(F x)
     return x;
 }
 
-template <int DT>
-__device__ __forceinline__ float of_bits(uint32_t bits16)
-{
-    if constexpr (DT == DT_F16) return f16_to_f32(bits16);
-    else return __builtin_bit_cast(float, bits16 << 16);
-}
-
 // E neighbouring elements.
 template <int DT, int E, typename F>
 __device__ __forceinline__ void load_row(const uint16_t *p, F (&x)[E])
@@ -202,7 +195,7 @@ __device__ __forceinline__ uint32_t quantize(double (&x)[E], uint32_t (&code)[E]
 // sequence.
 __device__ __forceinline__ int place_of(const KvView &v, int t, int &s)
 {
-    s = v.offs ? find_seq<16>(v, t, 0, 0) : t;
+    s = v.offs ? find_seq<16>(v, t, 1, 0) : t;
     const Seq q = seq_of(v, s);
     return t >= q.row && t < q.row + q.n ? q.first + t - q.row : INT_MIN;
 }
@@ -215,7 +208,7 @@ __device__ __forceinline__ void append_quad(const AppendArgs &a, int slot, int h
     using L = KvLay<D>;
     constexpr int E = L::E;
     const KvView &v = a.v;
-    const int s = v.offs ? find_seq<16>(v, slot, 2, 2) : slot;
+    const int s = v.offs ? find_seq<16>(v, slot, kQuad, 2) : slot;
     const Seq q = seq_of(v, s);
     const int at0 = ((v.offs ? slot - ((row_end(v, s) >> 2) + 2 * s) : 0) + (q.first >> 2)) * kQuad;
     if (at0 < 0 || at0 >= q.len) return;
@@ -302,20 +295,6 @@ __device__ __forceinline__ void read_token(const uint8_t *tile, int r, int l, fl
     }
 }
 
-template <int OT, int E>
-__device__ __forceinline__ void store_out(void *base, long long i, const float (&x)[E])
-{
-    if constexpr (OT == QGEMM_F32) {
-#pragma unroll
-        for (int j = 0; j < E / 4; j++) *(f32x4 *)((float *)base + i + 4 * j) = f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
-    } else {
-        uint32_t w[E / 2];
-#pragma unroll
-        for (int j = 0; j < E / 2; j++) w[j] = pack_out<OT>(x[2 * j], x[2 * j + 1]);
-        __builtin_memcpy(__builtin_assume_aligned((uint16_t *)base + i, 2 * E), w, 2 * E);
-    }
-}
-
 template <int OT, int D>
 __global__ void __launch_bounds__(256) k_kv_read(KvView v, void *ko, void *vo)
 {
@@ -333,55 +312,6 @@ __global__ void __launch_bounds__(256) k_kv_read(KvView v, void *ko, void *vo)
     const long long o = ((long long)row * v.H + head) * D + E * l;
     store_out<OT, E>(ko, o, k);
     store_out<OT, E>(vo, o, x);
-}
-
-// Attention: four groups of 16 lanes share a query head of one row and take
-// every fourth key.  The maximum is that of the unscaled products, so that the
-// exponent's argument is at most 0 whatever their size (a scaled maximum
-// subtracted in one FMA is off by its rounding, more than the exponential's
-// range for products of 1e30).
-template <int DT, int D>
-__global__ void __launch_bounds__(256) k_attention(AttnArgs a)
-{
-    constexpr int E = D / 16;
-    const int item = (int)(blockIdx.x * 4 + (threadIdx.x >> 6)), l = threadIdx.x & 15, sub = (threadIdx.x >> 4) & 3;
-    const int row = item / a.heads, head = item - row * a.heads;
-    if (row >= a.v.T) return;
-    int s;
-    const int at = place_of(a.v, row, s);
-    if (at == INT_MIN) return;
-    const float c = a.scale * 1.44269504f;
-    float q[E], o[E], m = -INFINITY, n = 0.0f;
-    load_row<DT, E>(a.q + (long long)row * a.q_stride + head * D + E * l, q);
-#pragma unroll
-    for (int i = 0; i < E; i++) o[i] = 0.0f;
-    const int from = a.window ? max(at - a.window + 1, 0) : 0;
-    for (int t = from + sub; t <= at; t += 4) {
-        const uint8_t *tile = tile_of<D>(a.v, s, t, head / a.group);
-        if (!tile) continue;
-        float k[E], x[E], dot = 0.0f;
-        read_token<D>(tile, t & 15, l, k, x);
-#pragma unroll
-        for (int i = 0; i < E; i++) dot = fmaf(q[i], k[i], dot);
-        dot = sum16(dot);
-        const float mx = fmaxf(m, dot), f = __builtin_amdgcn_exp2f((m - mx) * c), p = __builtin_amdgcn_exp2f((dot - mx) * c);
-        m = mx;
-        n = n * f + p;
-#pragma unroll
-        for (int i = 0; i < E; i++) o[i] = o[i] * f + p * x[i];
-    }
-#pragma unroll
-    for (int d = 16; d < 64; d <<= 1) {
-        const float m2 = __shfl_xor(m, d, 64), n2 = __shfl_xor(n, d, 64), mx = fmaxf(m, m2);
-        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - mx) * c), f2 = m2 == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m2 - mx) * c);
-#pragma unroll
-        for (int i = 0; i < E; i++) o[i] = o[i] * f + __shfl_xor(o[i], d, 64) * f2;
-        n = n * f + n2 * f2;
-        m = mx;
-    }
-#pragma unroll
-    for (int i = 0; i < E; i++) o[i] = n == 0.0f ? 0.0f : o[i] / n;
-    if (sub == 0) store_out<DT, E>(a.y, ((long long)row * a.heads + head) * D + E * l, o);
 }
 
 unsigned blocks(long long items, int per) { return (unsigned)((items + per - 1) / per); }
@@ -410,13 +340,6 @@ hipError_t run_read(const KvView &v, void *k, void *val, hipStream_t s)
     return hipGetLastError();
 }
 
-template <int DT, int D>
-hipError_t run_attention(const AttnArgs &a, hipStream_t s)
-{
-    hipLaunchKernelGGL((k_attention<DT, D>), dim3(blocks((long long)a.v.T * a.heads, 4)), dim3(256), 0, s, a);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 #define QG_BY_TYPE(fn, ...)                                                              \
@@ -425,7 +348,6 @@ hipError_t run_attention(const AttnArgs &a, hipStream_t s)
 
 hipError_t launch_norm_rope(int dtype, int D, const NormRopeArgs &a, hipStream_t s) { return QG_BY_TYPE(run_norm_rope, a, s); }
 hipError_t launch_kv_append(int dtype, int D, const AppendArgs &a, hipStream_t s) { return QG_BY_TYPE(run_append, a, s); }
-hipError_t launch_kv_attention(int dtype, int D, const AttnArgs &a, hipStream_t s) { return QG_BY_TYPE(run_attention, a, s); }
 
 hipError_t launch_kv_read(int out_type, int D, const KvView &v, void *k, void *val, hipStream_t s)
 {

@@ -583,7 +583,7 @@ size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64
  *   included.  offsets [S+1] (int32, device) say which rows are whose: rows
  *   offsets[s] .. offsets[s+1]-1 are the last places of sequence s, in order; NULL means
  *   one row each (T = S).  Rows from offsets[S] on belong to no sequence: they
- *   are not read, and their results stay as they were.  A row whose place is
+ *   are not read, and their results stay as they were (qgemm_kv_read: zeros).  A row whose place is
  *   negative, beyond the table or in a page that is not in [0, pages) has no
  *   place in the cache.  The kernels clamp all of these, so any contents stay
  *   inside the buffers (bad ones only give wrong values); a page must not be

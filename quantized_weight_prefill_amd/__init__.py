@@ -1166,6 +1166,10 @@ def qk_norm_rope(q, k, rope=None, positions=None, q_weight=None, k_weight=None, 
     copy of :func:`rope_table`, ``positions`` int32 [T] its rows (a row outside
     it gives zeros).  q and k may be column ranges of one merged product;
     ``q_out`` and ``k_out`` may be q and k themselves."""
+    if stream is None and q_out is None and k_out is None:
+        y = _common("qgemm_qk_norm_rope", "qk_norm_rope", (q, k, rope, positions, q_weight, k_weight, eps, interleaved))
+        if y is not None:
+            return y
     torch = _torch()
     index, code = q.get_device(), _dtype_code(q)
     qp, qs, heads, D = _heads("q", q, index)
@@ -1212,6 +1216,11 @@ def kv_append(cache, k, v, tables, lens, offsets=None, rope=None, positions=None
     offsets [S+1] (rows offsets[s] .. offsets[s+1]-1 are the last places of
     sequence s; None: one row each), all int32.  ``positions`` None takes a row's
     place in its sequence.  Rows behind offsets[S] stay as they were."""
+    if stream is None and q_out is None:
+        y = _common("qgemm_kv_append", "kv_append", (cache, k, v, tables, lens, offsets, rope, positions, k_weight, eps,
+                                                     interleaved, q, q_weight))
+        if y is not None:
+            return None if y is True else y
     torch = _torch()
     index, code = cache.get_device(), _dtype_code(k)
     kp, ks, H, D = _heads("k", k, index)
@@ -1263,13 +1272,16 @@ def kv_read(cache, tables, lens, T: int, kv_heads: int, head_dim: int, offsets=N
     codes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: 2}
     if dtype not in codes:
         raise TypeError(f"dtype must be float16, bfloat16 or float32, got {dtype}")
+    if stream is None:
+        y = _common("qgemm_kv_read", "kv_read", (cache, tables, lens, T, kv_heads, head_dim, offsets, codes[dtype]))
+        if y is not None:
+            return y
     index = cache.get_device()
     if index < 0:
         raise ValueError("cache must be a device tensor")
     page = _kv_page(cache, kv_heads, head_dim)
     tp, width, lp, op, S = _kv_sequences(tables, lens, offsets, T, index)
-    new = torch.empty if offsets is None else torch.zeros
-    k, v = _allocate(stream, index, lambda: tuple(new((T, kv_heads, head_dim), dtype=dtype, device=cache.device) for _ in "kv"))
+    k, v = _allocate(stream, index, lambda: tuple(torch.empty((T, kv_heads, head_dim), dtype=dtype, device=cache.device) for _ in "kv"))
     _call("qgemm_kv_read", index, stream, cache.data_ptr(), cache.shape[0], page, tp, width, lp, op, S, k.data_ptr(),
           v.data_ptr(), T, kv_heads, head_dim, codes[dtype])
     return k, v
@@ -1293,13 +1305,18 @@ def kv_attention(q, cache, tables, lens, kv_heads: int, offsets=None, scale=None
     heads / kv_heads.  ``scale`` defaults to D**-0.5.  ``max_len``, a bound on the
     lengths (0: the width of the tables), only decides how the work is split.
     Rows of ``out`` behind offsets[S] stay as they were."""
+    if stream is None and workspace is None:
+        y = _common("qgemm_kv_attention", "kv_attention", (q, cache, tables, lens, kv_heads, offsets, scale, window, max_len, out))
+        if y is not None:
+            return y
     torch = _torch()
     index, code = cache.get_device(), _dtype_code(q)
     qp, qs, heads, D = _heads("q", q, index)
     T = q.shape[0]
     page = _kv_page(cache, kv_heads, D)
     tp, width, lp, op, S = _kv_sequences(tables, lens, offsets, T, index)
-    need = kv_attention_workspace_bytes(T, S, heads, kv_heads, D, max_len or width * page, offsets is not None)
+    need = kv_attention_workspace_bytes(T, S, heads, kv_heads, D, min(max_len or width * page, width * page),
+                                        offsets is not None)
     if out is not None:
         if not _fits(out, index, q.shape, q.dtype):
             raise ValueError("out must be a contiguous tensor of q's shape and dtype on its device")

@@ -1,5 +1,5 @@
-// calls.cpp -- the binding's calls of the linear and mixture-of-experts
-// layers, marshalled in C++ (the Python module quantized_weight_prefill_amd._calls).
+// calls.cpp -- the binding's calls of the linear, mixture-of-experts and
+// attention layers, marshalled in C++ (the Python module quantized_weight_prefill_amd._calls).
 //
 // At decode sizes these kernels take a few microseconds, and checking and
 // marshalling their arguments in Python took longer than that (13.9 us a call
@@ -20,6 +20,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdint>
 #include <exception>
 
@@ -289,6 +290,225 @@ PyObject *moe(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// Rows of heads [T][heads][head_dim], each row's heads side by side.
+struct Rows {
+    const void *p = nullptr;
+    int64_t T = 0, heads = 0, D = 0, stride = 0;
+    size_t span() const { return (size_t)(2 * ((T - 1) * stride + heads * D)); }
+};
+
+Rows rows(PyObject *o, int index, at::ScalarType type)
+{
+    const at::Tensor &t = tensor(o);
+    if (t.dim() != 3 || !t.is_cuda() || t.get_device() != index || t.scalar_type() != type) throw Bad{};
+    Rows r{nullptr, t.size(0), t.size(1), t.size(2), 0};
+    if (r.T < 1 || r.heads < 1 || r.D < 1 || t.stride(2) != 1 || (r.heads > 1 && t.stride(1) != r.D)) throw Bad{};
+    r.stride = r.T > 1 ? t.stride(0) : r.heads * r.D;
+    r.p = t.data_ptr();
+    return r;
+}
+
+float real(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Bad{};
+    return (float)v;
+}
+
+// The rotation's table and positions, and the norm: what qk_norm_rope and
+// kv_append share.
+struct Turn {
+    const float *rope = nullptr;
+    int64_t lines = 0, rot = 0;
+    const int32_t *positions = nullptr;
+    float eps = -1.0f;
+    int interleaved = 0;
+};
+
+Turn turn(PyObject *rope, PyObject *positions, PyObject *eps, PyObject *interleaved, int64_t T, int index)
+{
+    Turn t;
+    if (rope != Py_None) {
+        const at::Tensor &r = tensor(rope);
+        if (r.dim() != 2 || r.scalar_type() != at::kFloat) throw Bad{};
+        t.rope = (const float *)data(rope, index);
+        t.lines = r.size(0);
+        t.rot = r.size(1);
+    }
+    t.positions = (const int32_t *)data(positions, index, at::kInt, {T});
+    if (eps != Py_None) t.eps = real(eps);
+    t.interleaved = PyObject_IsTrue(interleaved);
+    if (t.interleaved < 0) throw Bad{};
+    return t;
+}
+
+// A cache and its sequences.
+struct Cache {
+    uint8_t *p = nullptr;
+    int64_t pages = 0, page = 0, width = 0, S = 0;
+    const int32_t *tables = nullptr, *lens = nullptr, *offsets = nullptr;
+    size_t bytes = 0;
+};
+
+Cache cache_of(PyObject *cache, PyObject *tables, PyObject *lens, PyObject *offsets, int64_t T, int64_t kv_heads, int64_t D,
+               int index)
+{
+    const at::Tensor &c = tensor(cache), &tb = tensor(tables);
+    if (c.dim() != 2 || c.scalar_type() != at::kByte || tb.dim() != 2 || lens == Py_None || kv_heads < 1) throw Bad{};
+    Cache r;
+    r.p = (uint8_t *)data(cache, index);
+    r.bytes = c.nbytes();
+    r.pages = c.size(0);
+    r.page = c.size(1) * 16 / (20 * kv_heads * D);
+    if (r.page < 1 || qgemm_kv_page_bytes(kv_heads, D, r.page) != (size_t)c.size(1)) throw Bad{};
+    r.S = tb.size(0);
+    r.width = tb.size(1);
+    r.tables = (const int32_t *)data(tables, index, at::kInt, {r.S, r.width});
+    r.lens = (const int32_t *)data(lens, index, at::kInt, {r.S});
+    r.offsets = (const int32_t *)data(offsets, index, at::kInt, {r.S + 1});
+    if (r.S < 1 || (!r.offsets && r.S != T)) throw Bad{};
+    return r;
+}
+
+// qk_norm_rope(q, k, rope, positions, q_weight, k_weight, eps, interleaved)
+PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 8) throw Bad{};
+        const at::Tensor &x = tensor(a[0]);
+        const int index = x.get_device(), dtype = half_type(x);
+        const Rows q = rows(a[0], index, x.scalar_type());
+        Rows k;
+        if (a[1] != Py_None) {
+            k = rows(a[1], index, x.scalar_type());
+            if (k.T != q.T || k.D != q.D) throw Bad{};
+        }
+        const Turn t = turn(a[2], a[3], a[6], a[7], q.T, index);
+        if (t.rope && !t.positions) throw Bad{};
+        const float *wq = (const float *)data(a[4], index, at::kFloat, {q.D});
+        const float *wk = (const float *)data(a[5], index, at::kFloat, {q.D});
+        void *s = stream_of(index);
+        const at::Tensor yq = at::empty({q.T, q.heads, q.D}, x.options());
+        at::Tensor yk;
+        if (k.p) yk = at::empty({k.T, k.heads, k.D}, x.options());
+        int st;
+        Py_BEGIN_ALLOW_THREADS
+        st = qgemm_qk_norm_rope(q.p, q.stride, k.p, k.stride, wq, wk, t.rope, t.lines, t.rot, t.interleaved, t.positions, t.eps,
+                                yq.data_ptr(), q.heads * q.D, k.p ? yk.data_ptr() : nullptr, k.heads * q.D, q.T, q.heads, k.heads,
+                                q.D, dtype, s);
+        Py_END_ALLOW_THREADS
+        if (st != QGEMM_OK) return PyLong_FromLong(st);
+        if (k.p) return tuple_of({yq, yk});
+        PyObject *y = THPVariable_Wrap(yq), *both = y ? PyTuple_Pack(2, y, Py_None) : nullptr;
+        Py_XDECREF(y);
+        return both;
+    });
+}
+
+// kv_append(cache, k, v, tables, lens, offsets, rope, positions, k_weight,
+// eps, interleaved, q, q_weight): the queries' result, or True without any
+PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 13) throw Bad{};
+        const at::Tensor &x = tensor(a[1]);
+        const int index = x.get_device(), dtype = half_type(x);
+        const Rows k = rows(a[1], index, x.scalar_type()), v = rows(a[2], index, x.scalar_type());
+        if (v.T != k.T || v.heads != k.heads || v.D != k.D) throw Bad{};
+        const Cache c = cache_of(a[0], a[3], a[4], a[5], k.T, k.heads, k.D, index);
+        const Turn t = turn(a[6], a[7], a[9], a[10], k.T, index);
+        const float *wk = (const float *)data(a[8], index, at::kFloat, {k.D});
+        const float *wq = (const float *)data(a[12], index, at::kFloat, {k.D});
+        Rows q;
+        if (a[11] != Py_None) {
+            q = rows(a[11], index, x.scalar_type());
+            if (q.T != k.T || q.D != k.D) throw Bad{};
+            apart(c.p, c.bytes, q.p, q.span());
+        }
+        apart(c.p, c.bytes, k.p, k.span());
+        apart(c.p, c.bytes, v.p, v.span());
+        apart(c.p, c.bytes, c.tables, (size_t)(4 * c.S * c.width));
+        apart(c.p, c.bytes, c.lens, (size_t)(4 * c.S));
+        apart(c.p, c.bytes, c.offsets, (size_t)(4 * (c.S + 1)));
+        apart(c.p, c.bytes, t.rope, (size_t)(4 * t.lines * t.rot));
+        apart(c.p, c.bytes, t.positions, (size_t)(4 * k.T));
+        apart(c.p, c.bytes, wk, (size_t)(4 * k.D));
+        apart(c.p, c.bytes, wq, (size_t)(4 * k.D));
+        void *s = stream_of(index);
+        at::Tensor y;
+        if (q.p) y = at::empty({q.T, q.heads, q.D}, x.options());
+        int st;
+        Py_BEGIN_ALLOW_THREADS
+        st = qgemm_kv_append(c.p, c.pages, c.page, c.tables, c.width, c.lens, c.offsets, c.S, k.p, k.stride, v.p, v.stride, wk,
+                             t.rope, t.lines, t.rot, t.interleaved, t.positions, t.eps, q.p, q.stride, wq,
+                             q.p ? y.data_ptr() : nullptr, q.heads * q.D, k.T, q.heads, k.heads, k.D, dtype, s);
+        Py_END_ALLOW_THREADS
+        if (st != QGEMM_OK) return PyLong_FromLong(st);
+        if (q.p) return THPVariable_Wrap(y);
+        Py_RETURN_TRUE;
+    });
+}
+
+// kv_read(cache, tables, lens, T, kv_heads, head_dim, offsets, type)
+PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 8) throw Bad{};
+        const at::Tensor &x = tensor(a[0]);
+        const int index = x.get_device();
+        const int64_t T = integer(a[3]), H = integer(a[4]), D = integer(a[5]), type = integer(a[7]);
+        if (T < 1 || D < 1 || (type != QGEMM_F16 && type != QGEMM_BF16 && type != QGEMM_F32)) throw Bad{};
+        const Cache c = cache_of(a[0], a[1], a[2], a[6], T, H, D, index);
+        void *s = stream_of(index);
+        const at::TensorOptions o = x.options().dtype(type == QGEMM_F16 ? at::kHalf : type == QGEMM_BF16 ? at::kBFloat16 : at::kFloat);
+        const at::Tensor k = at::empty({T, H, D}, o), v = at::empty({T, H, D}, o);
+        int st;
+        Py_BEGIN_ALLOW_THREADS
+        st = qgemm_kv_read(c.p, c.pages, c.page, c.tables, c.width, c.lens, c.offsets, c.S, k.data_ptr(), v.data_ptr(), T, H, D,
+                           (int)type, s);
+        Py_END_ALLOW_THREADS
+        return st == QGEMM_OK ? tuple_of({k, v}) : PyLong_FromLong(st);
+    });
+}
+
+// kv_attention(q, cache, tables, lens, kv_heads, offsets, scale, window,
+// max_len, out)
+PyObject *kv_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        if (n != 10) throw Bad{};
+        const at::Tensor &x = tensor(a[0]);
+        const int index = x.get_device(), dtype = half_type(x);
+        const Rows q = rows(a[0], index, x.scalar_type());
+        const int64_t H = integer(a[4]), window = integer(a[7]), max_len = integer(a[8]);
+        const Cache c = cache_of(a[1], a[2], a[3], a[5], q.T, H, q.D, index);
+        const float scale = a[6] == Py_None ? (float)(1.0 / std::sqrt((double)q.D)) : real(a[6]);
+        const int64_t all = c.width * c.page;
+        if (max_len < 0) throw Bad{};
+        void *yp = data(a[9], index, x.scalar_type(), {q.T, q.heads, q.D});
+        if (yp) {
+            const size_t yb = tensor(a[9]).nbytes();
+            apart(yp, yb, q.p, q.span());
+            apart(yp, yb, c.p, c.bytes);
+            apart(yp, yb, c.tables, (size_t)(4 * c.S * c.width));
+            apart(yp, yb, c.lens, (size_t)(4 * c.S));
+            apart(yp, yb, c.offsets, (size_t)(4 * (c.S + 1)));
+        }
+        void *s = stream_of(index);
+        const at::Tensor y = yp ? tensor(a[9]) : at::empty({q.T, q.heads, q.D}, x.options());
+        const size_t need = qgemm_kv_attention_workspace_bytes(q.T, c.S, q.heads, H, q.D, max_len && max_len < all ? max_len : all,
+                                                               c.offsets != nullptr);
+        at::Tensor ws;
+        if (need) ws = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
+        int st;
+        Py_BEGIN_ALLOW_THREADS
+        st = qgemm_kv_attention(q.p, q.stride, c.p, c.pages, c.page, c.tables, c.width, c.lens, c.offsets, c.S, y.data_ptr(), q.T,
+                                q.heads, H, q.D, window, scale, max_len, dtype, need ? ws.data_ptr() : nullptr, need, s);
+        Py_END_ALLOW_THREADS
+        return wrap_or_status(st, y);
+    });
+}
+
 // bind(current_device, current_stream): torch's queries, as callables
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -309,6 +529,10 @@ PyMethodDef methods[] = {
     {"moe_route", (PyCFunction)(void (*)(void))moe_route, METH_FASTCALL, nullptr},
     {"moe_group", (PyCFunction)(void (*)(void))moe_group, METH_FASTCALL, nullptr},
     {"moe", (PyCFunction)(void (*)(void))moe, METH_FASTCALL, nullptr},
+    {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, nullptr},
+    {"kv_append", (PyCFunction)(void (*)(void))kv_append, METH_FASTCALL, nullptr},
+    {"kv_read", (PyCFunction)(void (*)(void))kv_read, METH_FASTCALL, nullptr},
+    {"kv_attention", (PyCFunction)(void (*)(void))kv_attention, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -161,7 +161,7 @@ struct AppendArgs {
     Heads k, q;             // q.x null: no queries
     const uint16_t *val;
     long long val_stride;
-    long long kv_blocks;    // workgroups of keys and values; the rest are the queries'
+    int value_blocks, key_blocks;  // workgroups of values and of keys; the rest are the queries'
 };
 
 // Partial results of the attention: of one row and query head from one part of

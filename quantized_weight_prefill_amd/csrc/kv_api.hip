@@ -158,7 +158,7 @@ int qgemm_kv_append(void *cache, int64_t pages, int64_t page, const int32_t *tab
     if (st != QGEMM_OK) return st;
     if ((st = view_of(cache, pages, page, tables, table_width, lens, offsets, S, T, kv_heads, head_dim, a.v)) != QGEMM_OK)
         return st;
-    if (!items_fit((T + 8 * S) * (heads + kv_heads))) return QGEMM_ERR_SHAPE;
+    if (!items_fit((2 * T + 8 * S) * (heads + kv_heads))) return QGEMM_ERR_SHAPE;
     if ((st = turn_of(rope, rope_len, rot, interleaved, positions, eps, head_dim, a.t)) != QGEMM_OK) return st;
     if (T == 0 || S == 0) return QGEMM_OK;
     if ((st = rows_of(K, k_stride, kv_heads, head_dim, false)) != QGEMM_OK) return st;

@@ -11,12 +11,29 @@
 namespace qg {
 namespace {
 
+// x of another lane of the row of 16, by DPP (no trip through LDS).
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // lanes ^1, ^2, mirrored in 8, in 16
+
+template <int CTRL>
+__device__ __forceinline__ int dpp(int x) { return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xF, 0xF, false); }
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) { return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, x))); }
+template <int CTRL>
+__device__ __forceinline__ double dpp(double x)
+{
+    const u32x2 v = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(uint32_t)dpp<CTRL>((int)v.x), (uint32_t)dpp<CTRL>((int)v.y)});
+}
+
+// Reductions over the first 4, 8 or 16 lanes' worth of neighbours: each step joins
+// blocks whose lanes already agree, so a mirror serves for a swap.
 template <typename F>
 __device__ __forceinline__ F sum16(F x)
 {
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) x += __shfl_xor(x, d, 16);
-    return x;
+    x += dpp<kSwap1>(x);
+    x += dpp<kSwap2>(x);
+    x += dpp<kHalfMirror>(x);
+    return x + dpp<kMirror>(x);
 }
 
 // E neighbouring elements.
@@ -62,11 +79,8 @@ __device__ __forceinline__ bool turn_head(const TurnArgs &t, const uint16_t *x, 
     if (turned) {
         const float *row = t.rope + (long long)pos * t.rot;
         if (t.interleaved) {
-#pragma unroll
-            for (int i = 0; i < E / 2; i++) {
-                c[i] = row[d0 / 2 + i];
-                s[i] = row[half + d0 / 2 + i];
-            }
+            __builtin_memcpy(c, __builtin_assume_aligned(row + d0 / 2, 2 * E), 2 * E);
+            __builtin_memcpy(s, __builtin_assume_aligned(row + half + d0 / 2, 2 * E), 2 * E);
         } else {
             load_f32<E>(row + (low ? d0 : dp), c);
             load_f32<E>(row + half + (low ? d0 : dp), s);
@@ -147,18 +161,6 @@ __global__ void __launch_bounds__(256) k_norm_rope(NormRopeArgs a)
     else turn_store<DT, D>(a.t, a.k, row, head - a.q.heads, pos, l);
 }
 
-// A group of 32 dims lies in 32/E neighbouring lanes.
-template <int E>
-__device__ __forceinline__ double min32(const double (&x)[E], double sign)
-{
-    double m = sign * x[0];
-#pragma unroll
-    for (int i = 1; i < E; i++) m = fmin(m, sign * x[i]);
-#pragma unroll
-    for (int d = 1; d < 32 / E; d <<= 1) m = fmin(m, __shfl_xor(m, d, 16));
-    return sign * m;
-}
-
 // fp16 of a 64-bit value, rounded to binary32 on the way.  The compiler would
 // merge the two conversions into one rounding (in software, and other bits
 // where binary32 lands on a tie); the empty statement keeps them apart.
@@ -169,25 +171,59 @@ __device__ __forceinline__ _Float16 header_of(double x)
     return (_Float16)f;
 }
 
-// The cache's codes of a lane's E dims and the header of their group: minimum =
-// fp16(min), scale = fp16((max - minimum)/15), both by way of binary32, code =
-// the nearest of 0..15 to (x - minimum)/scale, ties to even.  In 64 bits, where vector arithmetic has
-// the rate of 32 bits on this GPU: a code then is that of the definition and
-// does not hang on the last bit of a binary32 norm or rotation.  The quotient is
-// a product with the reciprocal and one correction, which makes a tie exact.
+// 1/x to about a 64-bit step.
+__device__ __forceinline__ double reciprocal(double x)
+{
+    double r = __builtin_amdgcn_rcp(x);
+    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+    return __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+}
+
+// a/b with r about 1/b: a product and one correction, which makes a quotient that
+// 64 bits hold (a tie between two codes) exact.
+__device__ __forceinline__ double quotient(double a, double b, double r)
+{
+    const double q = a * r;
+    return __builtin_fma(__builtin_fma(-q, b, a), r, q);
+}
+
+// The cache's codes of a lane's E dims and the header of their group of 32, which
+// lies in 32/E neighbouring lanes: minimum = fp16(min), scale = fp16((max -
+// minimum)/15), both by way of binary32, code = the nearest of 0..15 to (x -
+// minimum)/scale, ties to even.  In 64 bits, where vector arithmetic has the
+// rate of 32 bits on this GPU: a code then is that of the definition and does
+// not hang on the last bit of a binary32 norm or rotation.
 template <int E>
 __device__ __forceinline__ uint32_t quantize(double (&x)[E], uint32_t (&code)[E])
 {
+    bool odd = false;
 #pragma unroll
-    for (int i = 0; i < E; i++) x[i] = x[i] != x[i] ? 0.0 : fmin(fmax(x[i], -(double)kKvMax), (double)kKvMax);
-    const _Float16 m = header_of(min32<E>(x, 1.0));
-    const _Float16 s = header_of((min32<E>(x, -1.0) - (double)(float)m) / 15.0);
-    const double sd = (double)(float)s, md = (double)(float)m, inv = sd > 0.0 ? 1.0 / sd : 0.0;
+    for (int i = 0; i < E; i++) odd |= !(fabsf((float)x[i]) <= kKvMax);
+    if (odd) {
 #pragma unroll
-    for (int i = 0; i < E; i++) {
-        const double d = x[i] - md, q0 = d * inv, q = __builtin_fma(__builtin_fma(-q0, sd, d), inv, q0);
-        code[i] = (uint32_t)fmin(fmax(rint(q), 0.0), 15.0);
+        for (int i = 0; i < E; i++) x[i] = x[i] != x[i] ? 0.0 : fmin(fmax(x[i], -(double)kKvMax), (double)kKvMax);
     }
+    float lo = (float)x[0];  // the rounding keeps the order
+    double hi = x[0];
+#pragma unroll
+    for (int i = 1; i < E; i++) {
+        lo = fminf(lo, (float)x[i]);
+        hi = fmax(hi, x[i]);
+    }
+    lo = fminf(lo, dpp<kSwap1>(lo));
+    hi = fmax(hi, dpp<kSwap1>(hi));
+    lo = fminf(lo, dpp<kSwap2>(lo));
+    hi = fmax(hi, dpp<kSwap2>(hi));
+    if constexpr (E == 4) {
+        lo = fminf(lo, dpp<kHalfMirror>(lo));
+        hi = fmax(hi, dpp<kHalfMirror>(hi));
+    }
+    const _Float16 m = (_Float16)lo;
+    const double md = (double)(float)m;
+    const _Float16 s = header_of(quotient(hi - md, 15.0, 1.0 / 15.0));
+    const double sd = (double)(float)s, inv = sd > 0.0 ? reciprocal(sd) : 0.0;
+#pragma unroll
+    for (int i = 0; i < E; i++) code[i] = (uint32_t)(int)fminf(fmaxf((float)rint(quotient(x[i] - md, sd, inv)), 0.0f), 15.0f);
     return (uint32_t)__builtin_bit_cast(uint16_t, s) | ((uint32_t)__builtin_bit_cast(uint16_t, m) << 16);
 }
 
@@ -200,21 +236,48 @@ __device__ __forceinline__ int place_of(const KvView &v, int t, int &s)
     return t >= q.row && t < q.row + q.n ? q.first + t - q.row : INT_MIN;
 }
 
-// Keys and values: 16 lanes take a quad of tokens and one head.  A quad whose
-// tokens are not all new keeps the others' codes.
+// A row's key head into the cache.
 template <int DT, int D>
-__device__ __forceinline__ void append_quad(const AppendArgs &a, int slot, int head, int l)
+__device__ __forceinline__ void append_key(const AppendArgs &a, int row, int head, int l)
+{
+    using L = KvLay<D>;
+    constexpr int E = L::E;
+    int s;
+    const int at = place_of(a.v, row, s);
+    if (at == INT_MIN) return;
+    uint8_t *tile = tile_of<D>(a.v, s, at, head);
+    double x[E];
+    uint32_t code[E], w = 0;
+    const int pos = a.t.positions ? a.t.positions[row] : at;
+    if (!tile || !turn_head<DT, D>(a.t, a.k.x + (long long)row * a.k.stride + head * D, a.k.weight, pos, l, x)) return;
+    const uint32_t header = quantize<E>(x, code);
+    const int r = at & 15, d0 = E * l, h = d0 / (D / 4), j = d0 % (D / 4) / 8;
+#pragma unroll
+    for (int i = 0; i < E; i++) {
+        const int c = (d0 & 4) + i;  // place in the word of 8 (E = 4: half a word)
+        w |= code[i] << (4 * (c >> 1) + 16 * (c & 1));
+    }
+    if constexpr (E == 4) w |= (uint32_t)dpp<kSwap1>((int)w);
+    if (E == 8 || (l & 1) == 0) *(uint32_t *)(tile + (h * 16 + r) * L::kLane + 4 * j) = w;
+    if (d0 % 32 == 0) *(uint32_t *)(tile + L::kKeyHead + (d0 / 32 * 16 + r) * 4) = header;
+}
+
+// Values: 16 lanes take a quad of places, whose codes share words, and one head.
+// A quad whose tokens are not all new keeps the others' codes.
+template <int DT, int D>
+__device__ __forceinline__ void append_values(const AppendArgs &a, int slot, int head, int l)
 {
     using L = KvLay<D>;
     constexpr int E = L::E;
     const KvView &v = a.v;
     const int s = v.offs ? find_seq<16>(v, slot, kQuad, 2) : slot;
     const Seq q = seq_of(v, s);
-    const int at0 = ((v.offs ? slot - ((row_end(v, s) >> 2) + 2 * s) : 0) + (q.first >> 2)) * kQuad;
+    const int at0 = ((v.offs ? slot - (row_end(v, s) / kQuad + 2 * s) : 0) + (q.first >> 2)) * kQuad;
     if (at0 < 0 || at0 >= q.len) return;
     uint8_t *tile = tile_of<D>(v, s, at0, head);
     if (!tile) return;
-    const int quad = (at0 >> 2) & 3, g = E * l / 32, d0 = E * l;
+    const int quad = (at0 >> 2) & 3, d0 = E * l;
+    uint32_t *out = (uint32_t *)(tile + L::kVal + (quad * 16 + l) * L::kLane);
     uint32_t words[E / 2], fresh = 0;
 #pragma unroll
     for (int i = 0; i < E / 2; i++) words[i] = 0;
@@ -222,34 +285,17 @@ __device__ __forceinline__ void append_quad(const AppendArgs &a, int slot, int h
     for (int i = 0; i < kQuad; i++) {
         const int at = at0 + i, row = q.row + at - q.first;
         if (at < q.first || at >= q.len) continue;
+        if (a.t.rope && (unsigned)(a.t.positions ? a.t.positions[row] : at) >= (unsigned)a.t.rope_len) continue;  // a padded row
         double x[E];
         uint32_t code[E];
-        const int pos = a.t.positions ? a.t.positions[row] : at;
-        if (!turn_head<DT, D>(a.t, a.k.x + (long long)row * a.k.stride + head * D, a.k.weight, pos, l, x)) continue;
-        const int r = 4 * quad + i;
-        uint32_t header = quantize<E>(x, code);
-        uint32_t w = 0;
-#pragma unroll
-        for (int j = 0; j < E; j++) {
-            const int c = (d0 & 4) + j;  // place in the word of 8 (E = 4: half a word)
-            w |= code[j] << (4 * (c >> 1) + 16 * (c & 1));
-        }
-        if constexpr (E == 4) w |= (uint32_t)__shfl_xor((int)w, 1, 16);
-        if (E == 8 || (l & 1) == 0) {
-            const int h = d0 / (D / 4), j = d0 % (D / 4) / 8;
-            *(uint32_t *)(tile + (h * 16 + r) * L::kLane + 4 * j) = w;
-        }
-        if (d0 % 32 == 0) *(uint32_t *)(tile + L::kKeyHead + (g * 16 + r) * 4) = header;
-
         load_row<DT, E>(a.val + (long long)row * a.val_stride + head * D + d0, x);
-        header = quantize<E>(x, code);
+        const uint32_t header = quantize<E>(x, code);
 #pragma unroll
         for (int j = 0; j < E; j++) words[j >> 1] |= code[j] << (4 * (2 * (j & 1) + (i >> 1)) + 16 * (i & 1));
         fresh |= 0x0F0Fu << (4 * (i >> 1) + 16 * (i & 1));
-        if (d0 % 32 == 0) *(uint32_t *)(tile + L::kValHead + (g * 16 + r) * 4) = header;
+        if (d0 % 32 == 0) *(uint32_t *)(tile + L::kValHead + (d0 / 32 * 16 + 4 * quad + i) * 4) = header;
     }
     if (fresh == 0) return;
-    uint32_t *out = (uint32_t *)(tile + L::kVal + (quad * 16 + l) * L::kLane);
     if (fresh != 0xFFFFFFFFu) {
 #pragma unroll
         for (int i = 0; i < E / 2; i++) words[i] |= out[i] & ~fresh;
@@ -257,17 +303,25 @@ __device__ __forceinline__ void append_quad(const AppendArgs &a, int slot, int h
     __builtin_memcpy(__builtin_assume_aligned(out, 2 * E), words, 2 * E);
 }
 
+// Workgroups of values (quads, the longest chains, first), of keys and of queries.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) k_kv_append(AppendArgs a)
 {
-    const int l = threadIdx.x & 15;
-    if (blockIdx.x < a.kv_blocks) {
-        const int item = (int)(blockIdx.x * 16 + (threadIdx.x >> 4)), slot = item / a.v.H;
-        const int slots = a.v.offs ? (a.v.T >> 2) + 2 * a.v.S : a.v.S;
-        if (slot < slots) append_quad<DT, D>(a, slot, item - slot * a.v.H, l);
+    const int l = threadIdx.x & 15, sub = threadIdx.x >> 4;
+    int b = blockIdx.x;
+    if (b < a.value_blocks) {
+        const int item = b * 16 + sub, slot = item / a.v.H;
+        const int slots = a.v.offs ? a.v.T / kQuad + 2 * a.v.S : a.v.S;
+        if (slot < slots) append_values<DT, D>(a, slot, item - slot * a.v.H, l);
         return;
     }
-    const int item = (int)((blockIdx.x - a.kv_blocks) * 16 + (threadIdx.x >> 4)), row = item / a.q.heads;
+    b -= a.value_blocks;
+    if (b < a.key_blocks) {
+        const int item = b * 16 + sub, row = item / a.v.H;
+        if (row < a.v.T) append_key<DT, D>(a, row, item - row * a.v.H, l);
+        return;
+    }
+    const int item = (b - a.key_blocks) * 16 + sub, row = item / a.q.heads;
     if (row >= a.v.T) return;
     int s;
     const int at = place_of(a.v, row, s);
@@ -303,8 +357,7 @@ __global__ void __launch_bounds__(256) k_kv_read(KvView v, void *ko, void *vo)
     const int row = item / v.H, head = item - row * v.H;
     if (row >= v.T) return;
     int s;
-    const int at = place_of(v, row, s);
-    if (at == INT_MIN) return;
+    const int at = place_of(v, row, s);  // no place at all is none of the table's
     float k[E], x[E];
 #pragma unroll
     for (int i = 0; i < E; i++) k[i] = x[i] = 0.0f;
@@ -326,10 +379,11 @@ hipError_t run_norm_rope(const NormRopeArgs &a, hipStream_t s)
 template <int DT, int D>
 hipError_t run_append(AppendArgs a, hipStream_t s)
 {
-    const long long slots = a.v.offs ? (a.v.T >> 2) + 2LL * a.v.S : a.v.S;
-    a.kv_blocks = blocks(slots * a.v.H, 16);
+    const long long slots = a.v.offs ? a.v.T / kQuad + 2LL * a.v.S : a.v.S;
+    a.value_blocks = (int)blocks(slots * a.v.H, 16);
+    a.key_blocks = (int)blocks((long long)a.v.T * a.v.H, 16);
     const unsigned qb = a.q.x ? blocks((long long)a.v.T * a.q.heads, 16) : 0;
-    hipLaunchKernelGGL((k_kv_append<DT, D>), dim3((unsigned)a.kv_blocks + qb), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_kv_append<DT, D>), dim3((unsigned)(a.value_blocks + a.key_blocks) + qb), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

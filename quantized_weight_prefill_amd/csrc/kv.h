@@ -164,9 +164,10 @@ struct AppendArgs {
     int value_blocks, key_blocks;  // workgroups of values and of keys; the rest are the queries'
 };
 
-// Partial results of the attention: of one row and query head from one part of
-// the keys, the sums of p*v [D] relative to its own maximum, and (maximum, sum
-// of p, log2 units per unit of the maximum, unused).
+// Partial results of the attention, of one row and query head from one part of
+// the keys: the sums of p*v [D], and (b, sum of p) with p relative to 2^b.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 struct AttnArgs {
     KvView v;
     const uint16_t *q;
@@ -181,7 +182,7 @@ struct AttnArgs {
     int many_splits, many_chunk;  // k_attn_many's
     int tile_tokens, slots;       // k_attn_many: tokens of a row tile, row tiles of all sequences (a bound)
     float *few_sum, *many_sum;    // partial results (null: one split)
-    f32x4 *few_stat, *many_stat;
+    f32x2 *few_stat, *many_stat;
 };
 
 // The parts of a call's workspace and its launches (kv_attention.hip).

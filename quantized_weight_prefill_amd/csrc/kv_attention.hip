@@ -16,16 +16,19 @@
 // fp16 (v_fma_mix, as the weights of the fp16 GEMMs), probabilities likewise.
 // Products, maxima, sums and O are binary32.
 //
-// The maximum is kept in units of the products, so that the exponent's argument
-// (x - m)*c is at most 0 whatever their size, and is raised only when some row's
-// products pass it by more than 2^kLift: O is then rescaled rarely, and
-// probabilities stay far below fp16's range.
+// With x the product and c the scale in log2 units, p = 2^(x*c - b): one FMA and one
+// exponential.  b is an integer, so that a raised b rescales O by an exact power
+// of two; it is raised only when some product passes it by more than kLift, to
+// kRoom below the largest, which keeps the weights that matter far inside fp16's range on
+// both sides.  Beyond |b| = 2^22 the product is rounded before b is taken off: one FMA
+// would leave the rounding error of the largest itself, more than the exponential's range.
 #include "kv.h"
 
 namespace qg {
 namespace {
 
-constexpr float kLift = 8.0f;
+constexpr float kLift = 15.0f, kRoom = 7.0f;  // probabilities reach 2^15, and 2^-14, the least normal fp16, is 2^-21 of the largest at least
+constexpr float kHuge = 4194304.0f;
 constexpr float kLog2e = 1.44269504f;
 
 template <int D>
@@ -85,17 +88,27 @@ __device__ __forceinline__ u32x4 live_heads(u32x4 h, int from, int len)
     return h;
 }
 
-// The tile at place t (a multiple of 16) for key head h: its address, and whether
-// the table names a page for it; the address is inside the cache either way.  t is
-// the same in all lanes.
-template <int D>
-__device__ __forceinline__ const uint8_t *wave_tile(const KvView &v, int s, int t, int h, bool &there)
+// What the table says of place t of sequence s (t and s the same in all lanes: a
+// scalar load, from the constant address space, since nothing writes tables
+// here; behind the table's end, its last entry again).  Not looked at here, so
+// that a load ahead of its use is not waited for.
+__device__ __forceinline__ int entry_of(const KvView &v, int s, int t)
 {
-    const int i = t >> v.page_shift;
-    int id = -1;
-    if (i < v.width) id = v.tables[(long long)s * v.width + i];
-    there = (unsigned)id < (unsigned)v.pages;
-    id = there ? id : 0;
+    typedef const int __attribute__((address_space(4))) *Scalars;
+    return ((Scalars)(uintptr_t)v.tables)[(long long)s * v.width + min(t >> v.page_shift, v.width - 1)];
+}
+
+__device__ __forceinline__ bool names_page(const KvView &v, int entry, int t)
+{
+    return (unsigned)entry < (unsigned)v.pages && (t >> v.page_shift) < v.width;
+}
+
+// The tile at place t for key head h, in the page of that entry (in the first page
+// where it names none: the address is inside the cache either way).
+template <int D>
+__device__ __forceinline__ const uint8_t *tile_at(const KvView &v, int entry, int t, int h)
+{
+    const int id = (unsigned)entry < (unsigned)v.pages ? entry : 0;
     const int in = (t & ((1 << v.page_shift) - 1)) >> 4, tiles = 1 << (v.page_shift - 4);
     return v.cache + (long long)id * v.page_bytes + (long long)(h * tiles + in) * KvLay<D>::kBytes;
 }
@@ -135,11 +148,35 @@ __device__ __forceinline__ float load_query(const uint16_t *x, bool live, int st
     return fminf(fmaxf(c, 1.17549435e-38f), 1e37f);  // never 0 or infinite: an exponent's argument is 0 at the maximum, -inf where masked
 }
 
-__device__ __forceinline__ float exp_from(float x, float m, float c) { return __builtin_amdgcn_exp2f((x - m) * c); }
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The new maximum of a row whose products reach mx: by the row alone, whatever
-// made its wave look.
-__device__ __forceinline__ float raised(float mx, float m, float c) { return (mx - m) * c > kLift ? mx : m; }
+// 2^(x*c - b), and the argument for a wave that holds rows of huge products (see above).
+__device__ __forceinline__ float weight_of(float x, float c, float b) { return exp2_of(__builtin_fmaf(x, c, -b)); }
+
+__device__ __forceinline__ float argument_of_huge(float x, float c, float b)
+{
+    float xc = x * c;
+    asm("" : "+v"(xc));  // not one FMA
+    return fabsf(b) > kHuge ? xc - b : __builtin_fmaf(x, c, -b);
+}
+
+// The b of a row whose largest product is mx: by the row alone, whatever made its
+// wave look.  -inf until the row has seen a key.
+__device__ __forceinline__ float raised(float mx, float b, float c)
+{
+    const float v = mx * c;
+    return v - b > kLift ? ceilf(v) - kRoom : b;
+}
+
+// b as a subtrahend: a row that has seen nothing takes 0, and its products are -inf.
+__device__ __forceinline__ float shift_of(float b) { return b == -INFINITY ? 0.0f : b; }
+__device__ __forceinline__ float rescale_of(float before, float after) { return before == -INFINITY ? 0.0f : exp2_of(before - after); }
+
+// Adds the two probabilities as the second product sees them, rounded.
+__device__ __forceinline__ float add_pair(uint32_t pair, float l)
+{
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), f16x2{(_Float16)1.0f, (_Float16)1.0f}, l, false);
+}
 
 // Keys that a range of rows sees.
 struct Range {
@@ -167,18 +204,25 @@ struct FewRaw {
     typename Words<D>::W k[2], v[2];
     uint32_t kh[2];
     u32x4 vh[2];
-    bool there[2];
+    int entry[2];
 };
 
+__device__ __forceinline__ void few_entries(const AttnArgs &a, int s, int t, int (&entry)[2])
+{
+#pragma unroll
+    for (int i = 0; i < 2; i++) entry[i] = entry_of(a.v, s, t + 16 * i);
+}
+
 template <int D>
-__device__ __forceinline__ void few_load(const AttnArgs &a, int s, int h, int t, int lane, FewRaw<D> &r)
+__device__ __forceinline__ void few_load(const AttnArgs &a, const int (&entry)[2], int h, int t, int lane, FewRaw<D> &r)
 {
     using L = KvLay<D>;
     using W = typename Words<D>::W;
     const int n = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const uint8_t *p = wave_tile<D>(a.v, s, t + 16 * i, h, r.there[i]);
+        r.entry[i] = entry[i];
+        const uint8_t *p = tile_at<D>(a.v, entry[i], t + 16 * i, h);
         r.k[i] = *(const W *)(p + lane * L::kLane);
         r.kh[i] = *(const uint32_t *)(p + L::kKeyHead + (g * (D / 4) / 32 * 16 + n) * 4);
         r.v[i] = *(const W *)(p + L::kVal + lane * L::kLane);
@@ -192,13 +236,10 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
     using L = KvLay<D>;
     constexpr int E = L::E, J = D / 32, LD = D + 4;
     __shared__ __align__(16) float s_o[kFewWaves][16][LD];
-    __shared__ float s_m[kFewWaves][16], s_l[kFewWaves][16], s_c[16];
+    __shared__ float s_b[kFewWaves][16], s_l[kFewWaves][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    int b = blockIdx.x;
-    const int rt = b % a.few_tiles;
-    b /= a.few_tiles;
-    const int h = b % a.v.H, s = b / a.v.H, z = blockIdx.y;
+    const int rt = blockIdx.x % a.few_tiles, sh = blockIdx.x / a.few_tiles, h = sh % a.v.H, s = sh / a.v.H, z = blockIdx.y;
     const Seq q = seq_of(a.v, s);
     const int all = q.n * a.group, row0 = rt * 16 * RB;
     if ((a.v.offs && all > a.few_rows) || row0 >= all) return;
@@ -207,7 +248,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
     const int from = max(keys.lo & ~(kStep - 1), z * a.few_chunk), to = z + 1 < a.few_splits ? min(keys.hi, (z + 1) * a.few_chunk) : keys.hi;
 
     u32x4 qf[RB][J];
-    float c[RB], m[RB], l[RB];
+    float c[RB], b[RB], l[RB];
     int place[RB];
     f32x4 o[RB][E];
 #pragma unroll
@@ -218,7 +259,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
         c[rb] = load_query<DT, J, 16>(a.q + (long long)(q.row + (live ? token : 0)) * a.q_stride +
                                           (h * a.group + r - token * a.group) * D + g * (D / 4),
                                       live, 8, a.scale, qf[rb]);
-        m[rb] = -INFINITY;
+        b[rb] = -INFINITY;
         l[rb] = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; e++) o[rb][e] = f32x4{0, 0, 0, 0};
@@ -228,10 +269,19 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
     const int pmin = q.first + row0 / a.group, pmax_lo = a.window ? q.first + (row0 + rows - 1) / a.group - a.window + 1 : 0;
     int t = from + wave * kStep;
     FewRaw<D> next;
-    if (t < to) few_load<D>(a, s, h, t, lane, next);
+    int ahead[2];
+    bool huge = false;
+    if (t < to) {
+        few_entries(a, s, t, ahead);
+        few_load<D>(a, ahead, h, t, lane, next);
+        few_entries(a, s, t + stride, ahead);
+    }
     for (; t < to; t += stride) {
         FewRaw<D> r = next;
-        if (t + stride < to) few_load<D>(a, s, h, t + stride, lane, next);
+        if (t + stride < to) {
+            few_load<D>(a, ahead, h, t + stride, lane, next);
+            few_entries(a, s, t + 2 * stride, ahead);
+        }
         f32x4 x[RB][2];
 #pragma unroll
         for (int i = 0; i < 2; i++) {
@@ -245,7 +295,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
                 for (int rb = 0; rb < RB; rb++) x[rb][i] = mma<DT_F16>(kv, qf[rb][j], x[rb][i]);
             }
         }
-        const bool whole = r.there[0] && r.there[1];
+        const bool there[2] = {names_page(a.v, r.entry[0], t), names_page(a.v, r.entry[1], t + 16)}, whole = there[0] && there[1];
         if (!(whole && t + kStep - 1 <= pmin && t >= pmax_lo)) {
 #pragma unroll
             for (int rb = 0; rb < RB; rb++)
@@ -254,37 +304,43 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
                         const int at = t + 16 * i + 4 * g + u;
-                        const bool ok = r.there[i] && at <= place[rb] && (!a.window || at > place[rb] - a.window);
+                        const bool ok = there[i] && at <= place[rb] && (!a.window || at > place[rb] - a.window);
                         x[rb][i][u] = ok ? x[rb][i][u] : -INFINITY;
                     }
         }
         if (!whole || t + kStep > q.len) {
 #pragma unroll
-            for (int i = 0; i < 2; i++) r.vh[i] = live_heads(r.vh[i], t + 16 * i + 4 * g, r.there[i] ? q.len : 0);
+            for (int i = 0; i < 2; i++) r.vh[i] = live_heads(r.vh[i], t + 16 * i + 4 * g, there[i] ? q.len : 0);
         }
         u32x4 p[RB];
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
             float mx = fmaxf(fmaxf(fmaxf(x[rb][0][0], x[rb][0][1]), fmaxf(x[rb][0][2], x[rb][0][3])),
                              fmaxf(fmaxf(x[rb][1][0], x[rb][1][1]), fmaxf(x[rb][1][2], x[rb][1][3])));
-            if (__any((mx - m[rb]) * c[rb] > kLift)) {
+            if (__any(mx * c[rb] - b[rb] > kLift)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-                mx = raised(fmaxf(mx, __shfl_xor(mx, 32, 64)), m[rb], c[rb]);
-                const float f = m[rb] == -INFINITY ? 0.0f : exp_from(m[rb], mx, c[rb]);
-                m[rb] = mx;
+                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+                const float nb = raised(mx, b[rb], c[rb]), f = rescale_of(b[rb], nb);
+                b[rb] = nb;
+                huge = huge || __any(fabsf(nb) > kHuge && nb != -INFINITY);
                 l[rb] *= f;
 #pragma unroll
                 for (int e = 0; e < E; e++) o[rb][e] *= f;
             }
-            const float base = m[rb] == -INFINITY ? 0.0f : m[rb];
-            float pr[8];
+            const float base = shift_of(b[rb]);
+            float w[8];
+            if (huge) {
 #pragma unroll
-            for (int u = 0; u < 8; u++) {
-                pr[u] = exp_from(x[rb][u >> 2][u & 3], base, c[rb]);
-                l[rb] += pr[u];
+                for (int u = 0; u < 8; u++) w[u] = exp2_of(argument_of_huge(x[rb][u >> 2][u & 3], c[rb], base));
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; u++) w[u] = weight_of(x[rb][u >> 2][u & 3], c[rb], base);
             }
 #pragma unroll
-            for (int u = 0; u < 4; u++) p[rb][u] = pack_out<DT_F16>(pr[2 * u], pr[2 * u + 1]);
+            for (int u = 0; u < 4; u++) {
+                p[rb][u] = pack_out<DT_F16>(w[2 * u], w[2 * u + 1]);
+                l[rb] = add_pair(p[rb][u], l[rb]);
+            }
         }
         const QuadHead h0 = quad_head(r.vh[0]), h1 = quad_head(r.vh[1]);
 #pragma unroll
@@ -311,22 +367,20 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
                 *(f32x4 *)&s_o[wave][n][E * (4 * g + i) + e] =
                     f32x4{o[rb][e][i], o[rb][e + 1][i], o[rb][e + 2][i], o[rb][e + 3][i]};
         if (g == 0) {
-            s_m[wave][n] = m[rb];
+            s_b[wave][n] = b[rb];
             s_l[wave][n] = l[rb];
-            if (wave == 0) s_c[n] = c[rb];
         }
         __syncthreads();
         const int rr = threadIdx.x >> 4, dl = threadIdx.x & 15, r = 16 * rb + rr;
         if (r >= rows) continue;
-        const float cr = s_c[rr];
-        float mx = s_m[0][rr], sum = 0.0f, y[E];
+        float top = s_b[0][rr], sum = 0.0f, y[E];
 #pragma unroll
-        for (int w = 1; w < kFewWaves; w++) mx = fmaxf(mx, s_m[w][rr]);
+        for (int w = 1; w < kFewWaves; w++) top = fmaxf(top, s_b[w][rr]);
 #pragma unroll
         for (int e = 0; e < E; e++) y[e] = 0.0f;
 #pragma unroll
         for (int w = 0; w < kFewWaves; w++) {
-            const float f = s_m[w][rr] == -INFINITY ? 0.0f : exp_from(s_m[w][rr], mx, cr);
+            const float f = rescale_of(s_b[w][rr], top);
             sum += s_l[w][rr] * f;
 #pragma unroll
             for (int e = 0; e < E; e++) y[e] += s_o[w][rr][E * dl + e] * f;
@@ -340,7 +394,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
         } else {
             const long long entry = ((long long)(s * a.v.H + h) * a.few_rows + ra) * a.few_splits + z;
             if (sum != 0.0f) store_out<QGEMM_F32, E>(a.few_sum, entry * D + E * dl, y);
-            if (dl == 0) a.few_stat[entry] = f32x4{mx, sum, cr, 0.0f};
+            if (dl == 0) a.few_stat[entry] = f32x2{top, sum};
         }
     }
 }
@@ -352,70 +406,86 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 64;
 
+// Half of the words of a tile's 16 tokens, keys and values (each wave of eight takes
+// one; of four, both).
 template <int D>
 struct ManyRaw {
-    typename Words<D>::W w;
-    u32x4 head;
-    bool there;
+    static constexpr int N = D / 64;  // words
+    typedef uint32_t W __attribute__((ext_vector_type(N)));
+    W k, v;
+    uint32_t kh;
+    u32x4 vh;
 };
 
-// Job 0..3: the keys of a tile's 16 tokens; 4..7: their values.
 template <int D>
-__device__ __forceinline__ void many_load(const AttnArgs &a, int s, int h, int kt, int job, int lane, ManyRaw<D> &r)
+__device__ __forceinline__ void many_load(const AttnArgs &a, int entry, int h, int kt, int job, int lane, ManyRaw<D> &r)
 {
     using L = KvLay<D>;
-    using W = typename Words<D>::W;
+    using W = typename ManyRaw<D>::W;
     const int n = lane & 15, g = lane >> 4;
-    const uint8_t *p = wave_tile<D>(a.v, s, kt * kKeys + 16 * (job & 3), h, r.there);
-    if (job < 4) {
-        r.w = *(const W *)(p + lane * L::kLane);
-        r.head.x = *(const uint32_t *)(p + L::kKeyHead + (g * (D / 4) / 32 * 16 + n) * 4);
-    } else {
-        r.w = *(const W *)(p + L::kVal + lane * L::kLane);
-        r.head = *(const u32x4 *)(p + L::kValHead + (n * L::E / 32 * 16 + 4 * g) * 4);
-    }
+    const uint8_t *p = tile_at<D>(a.v, entry, kt * kKeys + 16 * (job & 3), h);
+    const int at = lane * L::kLane + (job >> 2) * (L::kLane / 2);
+    r.k = *(const W *)(p + at);
+    r.v = *(const W *)(p + L::kVal + at);
+    r.kh = *(const uint32_t *)(p + L::kKeyHead + (g * (D / 4) / 32 * 16 + n) * 4);
+    r.vh = *(const u32x4 *)(p + L::kValHead + (n * L::E / 32 * 16 + 4 * g) * 4);
 }
 
-// LDS of one tile of keys and values: keys as [32-key half][8-dim piece][key]
-// of 16 bytes; values as [16 tokens][32-dim block][quad parity][dim row] of 16
-// bytes, two quads of four tokens.  Row d of block b is dim E*(d%16) + 2b + d/16:
-// a wave's stores are then contiguous, and a lane ends with E neighbouring dims.
+// LDS of a tile: keys as [32-key half][8-dim piece][key] of 16 bytes; values as
+// [16 tokens][32-dim block][quad parity][dim row] of 16 bytes, two quads of four
+// tokens.  Row d of block b is dim E*(d%16) + 2b + d/16: a wave's stores are then
+// contiguous, and a lane ends with E neighbouring dims.
 template <int D>
-struct ManyLds {
+struct ManyKeys {
     uint4 k[2][D / 8][32];
+};
+template <int D>
+struct ManyValues {
     uint2 v[4][D / 32][2][32][2];
-    int absent[4];
 };
 
+// len: the sequence's, or 0 where the table names no page.
 template <int D>
-__device__ __forceinline__ void many_store(ManyLds<D> &t, const ManyRaw<D> &r, int kt, int job, int len, int lane)
+__device__ __forceinline__ void many_store(ManyKeys<D> &tk, ManyValues<D> &tv, const ManyRaw<D> &r, int kt, int job, int len, int lane)
 {
-    constexpr int E = D / 16;
-    const int n = lane & 15, g = lane >> 4, i = job & 3;
-    if (job < 4) {
-        const float f = head_scale(r.head.x), b = head_min(r.head.x);
+    constexpr int N = ManyRaw<D>::N;
+    const int n = lane & 15, g = lane >> 4, i = job & 3, part = job >> 2;
+    const float f = head_scale(r.kh), b = head_min(r.kh);
 #pragma unroll
-        for (int j = 0; j < D / 32; j++) {
-            const u32x4 kv = key_values(r.w[j], f, b);
-            *(u32x4 *)&t.k[i >> 1][(D / 32) * g + j][16 * (i & 1) + n] = kv;
-        }
-        if (lane == 0) t.absent[i] = !r.there;
-    } else {
-        u32x4 hd = r.head;
-        const int at = kt * kKeys + 16 * i;
-        if (!r.there || at + 16 > len) hd = live_heads(hd, at + 4 * g, r.there ? len : 0);
-        const QuadHead q = quad_head(hd);
+    for (int j = 0; j < N; j++)
+        *(u32x4 *)&tk.k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = key_values(r.k[j], f, b);
+    const QuadHead q = quad_head(live_heads(r.vh, kt * kKeys + 16 * i + 4 * g, len));
 #pragma unroll
-        for (int e = 0; e < E; e++)
-            *(u32x2 *)&t.v[i][e >> 1][g & 1][n + 16 * (e & 1)][g >> 1] = quad_values(r.w[e >> 1] >> (8 * (e & 1)), q);
+    for (int j = 0; j < N; j++)
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+            *(u32x2 *)&tv.v[i][N * part + j][g & 1][n + 16 * e][g >> 1] = quad_values(r.v[j] >> (8 * e), q);
+}
+
+// One tile of 64 keys in a wave's registers: products of its 32 rows.
+template <int D>
+__device__ __forceinline__ void many_products(const ManyKeys<D> &t, const u32x4 (&qf)[D / 16], int n, int g, f32x16 (&x)[2])
+{
+#pragma unroll
+    for (int b = 0; b < 2; b++) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) x[b][i] = 0.0f;
+#pragma unroll
+        for (int p = 0; p < D / 16; p++) x[b] = mma32<DT_F16>(*(const u32x4 *)&t.k[b][2 * p + g][n], qf[p], x[b]);
     }
 }
 
+// The loop is a pipeline over the tiles of 64 keys: while a tile's products become
+// probabilities (VALU), the next tile's products run (MFMA), and while its
+// probabilities meet its values (MFMA), the tile after that is unpacked into LDS
+// (VALU); the raw bytes of one more are in flight.  Keys have two LDS
+// buffers, values three, and one barrier per tile orders all of it.
 template <int DT, int D, int NW>
-__global__ void __launch_bounds__(64 * NW) k_attn_many(AttnArgs a)
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) k_attn_many(AttnArgs a)
 {
     constexpr int E = D / 16, B = D / 32, P = D / 16, JOBS = 8 / NW;
-    __shared__ __align__(16) ManyLds<D> lds[2];
+    __shared__ __align__(16) ManyKeys<D> s_k[2];
+    __shared__ __align__(16) ManyValues<D> s_v[3];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, g = lane >> 5;
     // key heads side by side, so that with a multiple of eight of them each XCD's
@@ -429,12 +499,14 @@ __global__ void __launch_bounds__(64 * NW) k_attn_many(AttnArgs a)
     const int rows = min(all - row0, a.tile_tokens * a.group);
     const Range keys = seen(a, q, row0, rows);
     const int from = max(keys.lo, z * a.many_chunk), to = z + 1 < a.many_splits ? min(keys.hi, (z + 1) * a.many_chunk) : keys.hi;
+    const int kt0 = from / kKeys, kt1 = to > from ? (to + kKeys - 1) / kKeys : kt0;
 
     const int w0 = 32 * wave, r = row0 + w0 + n, token = r / a.group;
     const bool live = w0 + n < rows;
     const int place = live ? q.first + token : -1;
+    // tiles in which some row of the wave sees a key, and keys that all its rows see
     const Range mine = w0 < rows ? seen(a, q, row0 + w0, min(rows - w0, 32)) : Range{0, 0};
-    // keys that every row of the wave sees: [clear_lo, clear_hi]
+    const int mt0 = mine.lo / kKeys, mt1 = (mine.hi + kKeys - 1) / kKeys;
     const int clear_hi = q.first + (row0 + w0) / a.group;
     const int clear_lo = a.window ? q.first + (row0 + min(rows, w0 + 32) - 1) / a.group - a.window + 1 : 0;
 
@@ -442,104 +514,133 @@ __global__ void __launch_bounds__(64 * NW) k_attn_many(AttnArgs a)
     const float c = load_query<DT, P, 32>(a.q + (long long)(q.row + (live ? token : 0)) * a.q_stride +
                                               (h * a.group + r - token * a.group) * D + 8 * g,
                                           live, 16, a.scale, qf);
-    float m = -INFINITY, l = 0.0f;
+    // pages that the table does not name: looked for once, since there are none as a rule
+    bool gaps = false;
+    for (int i = (kt0 * kKeys >> a.v.page_shift) + lane; i <= (max(to, 1) - 1) >> a.v.page_shift; i += 64)
+        gaps |= i >= a.v.width || (unsigned)a.v.tables[(long long)s * a.v.width + i] >= (unsigned)a.v.pages;
+    gaps = __any(gaps);
+
+    float b = -INFINITY, l = 0.0f;
+    bool huge = false;
     f32x16 o[B];
 #pragma unroll
-    for (int b = 0; b < B; b++)
+    for (int d = 0; d < B; d++)
 #pragma unroll
-        for (int i = 0; i < 16; i++) o[b][i] = 0.0f;
+        for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
 
-    const int kt0 = from / kKeys, kt1 = to > from ? (to + kKeys - 1) / kKeys : kt0;
     ManyRaw<D> raw[JOBS];
+    int entry[JOBS], ahead[JOBS];  // of the raw tile, and of the one after it
+    // past the last tile, the last once more
+    auto place_in = [&](int kt, int j) { return min(kt, kt1 - 1) * kKeys + 16 * ((wave + j * NW) & 3); };
+    auto look = [&](int kt, int(&e)[JOBS]) {
+#pragma unroll
+        for (int j = 0; j < JOBS; j++) e[j] = entry_of(a.v, s, place_in(kt, j));
+    };
+    auto load = [&](int kt) {
+#pragma unroll
+        for (int j = 0; j < JOBS; j++) many_load<D>(a, entry[j], h, min(kt, kt1 - 1), wave + j * NW, lane, raw[j]);
+    };
+    auto store = [&](int kt) {
+#pragma unroll
+        for (int j = 0; j < JOBS; j++)
+            many_store<D>(s_k[(kt - kt0) & 1], s_v[(kt - kt0) % 3], raw[j], min(kt, kt1 - 1), wave + j * NW,
+                          names_page(a.v, entry[j], place_in(kt, j)) ? q.len : 0, lane);
+    };
+    auto advance = [&](int kt) {  // tile kt out of the registers, kt+1 into them
+        store(kt);
+#pragma unroll
+        for (int j = 0; j < JOBS; j++) entry[j] = ahead[j];
+        load(kt + 1);
+        look(kt + 2, ahead);
+    };
+    f32x16 x[2];
     if (kt0 < kt1) {
-#pragma unroll
-        for (int j = 0; j < JOBS; j++) many_load<D>(a, s, h, kt0, wave + j * NW, lane, raw[j]);
-#pragma unroll
-        for (int j = 0; j < JOBS; j++) many_store<D>(lds[0], raw[j], kt0, wave + j * NW, q.len, lane);
-        if (kt0 + 1 < kt1)
-#pragma unroll
-            for (int j = 0; j < JOBS; j++) many_load<D>(a, s, h, kt0 + 1, wave + j * NW, lane, raw[j]);
+        look(kt0, entry);
+        load(kt0);
+        look(kt0 + 1, ahead);
+        advance(kt0);
+        __syncthreads();
+        many_products<D>(s_k[0], qf, n, g, x);
+        advance(kt0 + 1);
     }
     for (int kt = kt0; kt < kt1; kt++) {
-        __syncthreads();  // this tile is whole, and the other buffer's readers are done
-        const ManyLds<D> &t = lds[(kt - kt0) & 1];
-        if (kt + 1 < kt1) {
-#pragma unroll
-            for (int j = 0; j < JOBS; j++) many_store<D>(lds[(kt - kt0 + 1) & 1], raw[j], kt + 1, wave + j * NW, q.len, lane);
-        }
-        if (kt + 2 < kt1) {
-#pragma unroll
-            for (int j = 0; j < JOBS; j++) many_load<D>(a, s, h, kt + 2, wave + j * NW, lane, raw[j]);
-        }
+        __syncthreads();  // tile kt+1 is whole; the buffers of kt-1 and of kt's keys are free
         const int k0 = kt * kKeys;
-        if (k0 >= min(mine.hi, to) || k0 + kKeys <= mine.lo) continue;
-        f32x16 x[2];
-#pragma unroll
-        for (int b = 0; b < 2; b++) {
-#pragma unroll
-            for (int i = 0; i < 16; i++) x[b][i] = 0.0f;
-#pragma unroll
-            for (int p = 0; p < P; p++) x[b] = mma32<DT_F16>(*(const u32x4 *)&t.k[b][2 * p + g][n], qf[p], x[b]);
+        const ManyKeys<D> &tk = s_k[(kt + 1 - kt0) & 1];
+        const ManyValues<D> &tv = s_v[(kt - kt0) % 3];
+        if (kt < mt0 || kt >= mt1) {  // nothing for this wave
+            if (kt + 1 == mt0) many_products<D>(tk, qf, n, g, x);
+            advance(kt + 2);
+            continue;
         }
-        const int4 gone = *(const int4 *)t.absent;
-        const bool some_gone = __builtin_amdgcn_readfirstlane(gone.x | gone.y | gone.z | gone.w) != 0;
-        if (some_gone || k0 + kKeys - 1 > clear_hi || k0 < clear_lo) {
-            const int ab[4] = {gone.x, gone.y, gone.z, gone.w};
+        if (gaps || k0 + kKeys - 1 > clear_hi || k0 < clear_lo) {
 #pragma unroll
-            for (int b = 0; b < 2; b++)
+            for (int u = 0; u < 4; u++) {
+                const bool there = !gaps || names_page(a.v, entry_of(a.v, s, k0 + 16 * u), k0 + 16 * u);
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int at = k0 + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3);
-                    const bool ok = at <= place && (!a.window || at > place - a.window) && !ab[2 * b + (i >> 3)];
-                    x[b][i] = ok ? x[b][i] : -INFINITY;
+                for (int i = 0; i < 8; i++) {
+                    const int at = k0 + 16 * u + 8 * (i >> 2) + 4 * g + (i & 3);
+                    const bool ok = there && at <= place && (!a.window || at > place - a.window);
+                    x[u >> 1][8 * (u & 1) + i] = ok ? x[u >> 1][8 * (u & 1) + i] : -INFINITY;
                 }
+            }
         }
         float mx = x[0][0];
 #pragma unroll
-        for (int b = 0; b < 2; b++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) mx = fmaxf(mx, x[b][i]);
-        if (__any((mx - m) * c > kLift)) {
-            mx = raised(fmaxf(mx, __shfl_xor(mx, 32, 64)), m, c);
-            const float f = m == -INFINITY ? 0.0f : exp_from(m, mx, c);
-            m = mx;
+        for (int i = 0; i < 16; i++) mx = fmaxf(fmaxf(mx, x[0][i]), x[1][i]);
+        if (__any(mx * c - b > kLift)) {
+            const float nb = raised(fmaxf(mx, __shfl_xor(mx, 32, 64)), b, c), f = rescale_of(b, nb);
+            b = nb;
+            huge = huge || __any(fabsf(nb) > kHuge && nb != -INFINITY);
             l *= f;
 #pragma unroll
-            for (int b = 0; b < B; b++) o[b] *= f;
+            for (int d = 0; d < B; d++) o[d] *= f;
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = shift_of(b);
+        if (huge) {  // the arguments as they are to be: what follows then adds and multiplies nothing
 #pragma unroll
-        for (int u = 0; u < 4; u++) {  // 16 tokens: registers 8*(u%2) .. +7 of half u/2
-            float pr[8];
+            for (int u = 0; u < 2; u++)
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                pr[i] = exp_from(x[u >> 1][8 * (u & 1) + i], base, c);
-                l += pr[i];
+                for (int i = 0; i < 16; i++) x[u][i] = argument_of_huge(x[u][i], c, base);
+        }
+        const float cc = huge ? 1.0f : c, bb = huge ? 0.0f : base;
+        f32x16 y[2];
+        u32x4 p[4];  // 16 tokens each: registers 8*(u%2) .. +7 of half u/2
+        many_products<D>(tk, qf, n, g, y);
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int k = 8 * (u & 1) + 2 * i;
+                p[u][i] = pack_out<DT_F16>(weight_of(x[u >> 1][k], cc, bb), weight_of(x[u >> 1][k + 1], cc, bb));
+                l = add_pair(p[u][i], l);
             }
-            const u32x4 p = {pack_out<DT_F16>(pr[0], pr[1]), pack_out<DT_F16>(pr[2], pr[3]), pack_out<DT_F16>(pr[4], pr[5]),
-                             pack_out<DT_F16>(pr[6], pr[7])};
 #pragma unroll
-            for (int b = 0; b < B; b++) o[b] = mma32<DT_F16>(*(const u32x4 *)&t.v[u][b][g][n][0], p, o[b]);
-        }
+        for (int u = 0; u < 4; u++)
+#pragma unroll
+            for (int d = 0; d < B; d++) o[d] = mma32<DT_F16>(*(const u32x4 *)&tv.v[u][d][g][n][0], p[u], o[d]);
+        advance(kt + 2);
+#pragma unroll
+        for (int i = 0; i < 2; i++) x[i] = y[i];
     }
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
     const long long row = (long long)(q.row + token) * a.heads + h * a.group + r - token * a.group;
-    const long long entry = row * a.many_splits + z;
+    const long long part = row * a.many_splits + z;
     const float inv = a.many_splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        float y[E];
+        float v[E];
 #pragma unroll
-        for (int b = 0; b < B; b++) {
-            y[2 * b] = o[b][i] * inv;
-            y[2 * b + 1] = o[b][i + 8] * inv;
+        for (int d = 0; d < B; d++) {
+            v[2 * d] = o[d][i] * inv;
+            v[2 * d + 1] = o[d][i + 8] * inv;
         }
         const int d = E * (8 * (i >> 2) + 4 * g + (i & 3));
-        if (a.many_splits == 1) store_out<DT, E>(a.y, row * D + d, y);
-        else if (l != 0.0f) store_out<QGEMM_F32, E>(a.many_sum, entry * D + d, y);
+        if (a.many_splits == 1) store_out<DT, E>(a.y, row * D + d, v);
+        else if (l != 0.0f) store_out<QGEMM_F32, E>(a.many_sum, part * D + d, v);
     }
-    if (a.many_splits > 1 && g == 0) a.many_stat[entry] = f32x4{m, l, c, 0.0f};
+    if (a.many_splits > 1 && g == 0) a.many_stat[part] = f32x2{b, l};
 }
 
 // The parts of a row's keys joined: 16 lanes per row and query head.
@@ -559,19 +660,19 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a)
     const int h = head / a.group, ra = (row - q.row) * a.group + head - h * a.group;
     const long long entry = few ? ((long long)(s * a.v.H + h) * a.few_rows + ra) * splits
                                 : ((long long)row * a.heads + head) * splits;
-    const f32x4 *stat = (few ? a.few_stat : a.many_stat) + entry;
+    const f32x2 *stat = (few ? a.few_stat : a.many_stat) + entry;
     const float *sums = (few ? a.few_sum : a.many_sum) + entry * D + E * dl;
-    float mx = -INFINITY;
-    for (int z = dl; z < splits; z += 16) mx = fmaxf(mx, stat[z].x);
+    float top = -INFINITY;
+    for (int z = dl; z < splits; z += 16) top = fmaxf(top, stat[z].x);
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 16));
+    for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 16));
     float y[E], sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; e++) y[e] = 0.0f;
     for (int z = 0; z < splits; z++) {
-        const f32x4 st = stat[z];
+        const f32x2 st = stat[z];
         if (st.y == 0.0f) continue;  // no keys, and no sums written
-        const float f = exp_from(st.x, mx, st.z);
+        const float f = rescale_of(st.x, top);
         sum += st.y * f;
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
@@ -646,7 +747,9 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     p.many_splits = 1;
     p.many_chunk = INT32_MAX / 2;
     p.many_entries = 0;
-    p.bytes = (size_t)(p.few_entries + p.many_entries) * (size_t)(D + 4) * 4;
+    p.few_entries += p.few_entries & 1;  // the sums behind the statistics stay 16-byte aligned
+    p.many_entries += p.many_entries & 1;
+    p.bytes = (size_t)(p.few_entries + p.many_entries) * (size_t)(D + 2) * 4;
     return p;
 }
 
@@ -661,7 +764,7 @@ hipError_t launch_kv_attention(int dtype, int D, const AttnPlan &pl, AttnArgs a,
     a.tile_tokens = pl.tile_tokens;
     a.slots = (int)pl.slots;
     float *w = (float *)workspace;
-    a.few_stat = (f32x4 *)w;
+    a.few_stat = (f32x2 *)w;
     a.many_stat = a.few_stat + pl.few_entries;
     a.few_sum = (float *)(a.many_stat + pl.many_entries);
     a.many_sum = a.few_sum + pl.few_entries * D;

@@ -89,7 +89,7 @@ __device__ __forceinline__ int find_seq(const KvView &v, int x, int per, int ext
     while (span > 1) {
         const int step = (span + W - 1) / W, s = lo + lane * step;
         const bool before = s < min(lo + span, v.S) && row_end(v, s) / per + extra * s <= x;
-        const unsigned long long b = (__ballot(before) >> shift) & (W == 64 ? ~0ull : (1ull << W) - 1ull);
+        const unsigned long long b = (__ballot(before) >> shift) & (~0ull >> (64 - W));
         lo += max(__popcll(b) - 1, 0) * step;
         span = step;
     }
@@ -177,7 +177,7 @@ struct AttnArgs {
     int window;             // 0: none
     float scale;
     int few_rows;           // sequences of at most so many rows (tokens * group) are k_attn_few's
-    int few_tiles;          // k_attn_few: row tiles of a sequence
+    int few_tiles, few_tile_rows;  // k_attn_few: row tiles of a sequence, rows of each
     int few_splits, few_chunk;    // k_attn_few: workgroups along the keys, keys of each
     int many_splits, many_chunk;  // k_attn_many's
     int tile_tokens, slots;       // k_attn_many: tokens of a row tile, row tiles of all sequences (a bound)

@@ -183,6 +183,15 @@ struct Range {
     int lo, hi;
 };
 
+// The part, of `splits` parts of `chunk` keys (the last one open), that holds all the
+// keys of a range, or -1: rows of one part need no join, whatever the splits.
+__device__ __forceinline__ int only_part(Range keys, int splits, int chunk)
+{
+    if (keys.hi <= keys.lo) return 0;
+    const int first = min(keys.lo / chunk, splits - 1);
+    return first == min((keys.hi - 1) / chunk, splits - 1) ? first : -1;
+}
+
 __device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0, int rows)
 {
     const int cap = a.v.width << a.v.page_shift;
@@ -231,7 +240,7 @@ __device__ __forceinline__ void few_load(const AttnArgs &a, const int (&entry)[2
 }
 
 template <int DT, int D, int RB>
-__global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
+__global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(RB == 1 ? 4 : 2))) k_attn_few(AttnArgs a)
 {
     using L = KvLay<D>;
     constexpr int E = L::E, J = D / 32, LD = D + 4;
@@ -245,6 +254,8 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
     if ((a.v.offs && all > a.few_rows) || row0 >= all) return;
     const int rows = min(all - row0, 16 * RB);
     const Range keys = seen(a, q, row0, rows);
+    const int only = only_part(keys, a.few_splits, a.few_chunk);
+    if (only >= 0 && only != z) return;
     const int from = max(keys.lo & ~(kStep - 1), z * a.few_chunk), to = z + 1 < a.few_splits ? min(keys.hi, (z + 1) * a.few_chunk) : keys.hi;
 
     u32x4 qf[RB][J];
@@ -265,7 +276,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
         for (int e = 0; e < E; e++) o[rb][e] = f32x4{0, 0, 0, 0};
     }
 
-    const int stride = kStep * kFewWaves;
+    const int stride = kStep * kFewWaves, window = a.window ? a.window : INT_MAX;
     const int pmin = q.first + row0 / a.group, pmax_lo = a.window ? q.first + (row0 + rows - 1) / a.group - a.window + 1 : 0;
     int t = from + wave * kStep;
     FewRaw<D> next;
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
                         const int at = t + 16 * i + 4 * g + u;
-                        const bool ok = there[i] && at <= place[rb] && (!a.window || at > place[rb] - a.window);
+                        const bool ok = there[i] & (at <= place[rb]) & (at > place[rb] - window);
                         x[rb][i][u] = ok ? x[rb][i][u] : -INFINITY;
                     }
         }
@@ -386,7 +397,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_attn_few(AttnArgs a)
             for (int e = 0; e < E; e++) y[e] += s_o[w][rr][E * dl + e] * f;
         }
         const int ra = row0 + r, token = ra / a.group;
-        if (a.few_splits == 1) {
+        if (only >= 0) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
             for (int e = 0; e < E; e++) y[e] *= inv;
@@ -498,27 +509,19 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     if (tile < 0 || row0 >= all || all <= a.few_rows) return;
     const int rows = min(all - row0, a.tile_tokens * a.group);
     const Range keys = seen(a, q, row0, rows);
+    const int only = only_part(keys, a.many_splits, a.many_chunk);
+    if (only >= 0 && only != z) return;
     const int from = max(keys.lo, z * a.many_chunk), to = z + 1 < a.many_splits ? min(keys.hi, (z + 1) * a.many_chunk) : keys.hi;
     const int kt0 = from / kKeys, kt1 = to > from ? (to + kKeys - 1) / kKeys : kt0;
 
     const int w0 = 32 * wave, r = row0 + w0 + n, token = r / a.group;
     const bool live = w0 + n < rows;
-    const int place = live ? q.first + token : -1;
+    const int place = live ? q.first + token : -1, window = a.window ? a.window : INT_MAX;
     // tiles in which some row of the wave sees a key, and keys that all its rows see
     const Range mine = w0 < rows ? seen(a, q, row0 + w0, min(rows - w0, 32)) : Range{0, 0};
     const int mt0 = mine.lo / kKeys, mt1 = (mine.hi + kKeys - 1) / kKeys;
     const int clear_hi = q.first + (row0 + w0) / a.group;
     const int clear_lo = a.window ? q.first + (row0 + min(rows, w0 + 32) - 1) / a.group - a.window + 1 : 0;
-
-    u32x4 qf[P];
-    const float c = load_query<DT, P, 32>(a.q + (long long)(q.row + (live ? token : 0)) * a.q_stride +
-                                              (h * a.group + r - token * a.group) * D + 8 * g,
-                                          live, 16, a.scale, qf);
-    // pages that the table does not name: looked for once, since there are none as a rule
-    bool gaps = false;
-    for (int i = (kt0 * kKeys >> a.v.page_shift) + lane; i <= (max(to, 1) - 1) >> a.v.page_shift; i += 64)
-        gaps |= i >= a.v.width || (unsigned)a.v.tables[(long long)s * a.v.width + i] >= (unsigned)a.v.pages;
-    gaps = __any(gaps);
 
     float b = -INFINITY, l = 0.0f;
     bool huge = false;
@@ -536,32 +539,45 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
         for (int j = 0; j < JOBS; j++) e[j] = entry_of(a.v, s, place_in(kt, j));
     };
-    auto load = [&](int kt) {
+    auto load = [&](int kt, const int(&e)[JOBS], ManyRaw<D>(&to_raw)[JOBS]) {
 #pragma unroll
-        for (int j = 0; j < JOBS; j++) many_load<D>(a, entry[j], h, min(kt, kt1 - 1), wave + j * NW, lane, raw[j]);
+        for (int j = 0; j < JOBS; j++) many_load<D>(a, e[j], h, min(kt, kt1 - 1), wave + j * NW, lane, to_raw[j]);
     };
-    auto store = [&](int kt) {
+    auto store = [&](int kt, const int(&e)[JOBS], const ManyRaw<D>(&of_raw)[JOBS]) {
 #pragma unroll
         for (int j = 0; j < JOBS; j++)
-            many_store<D>(s_k[(kt - kt0) & 1], s_v[(kt - kt0) % 3], raw[j], min(kt, kt1 - 1), wave + j * NW,
-                          names_page(a.v, entry[j], place_in(kt, j)) ? q.len : 0, lane);
+            many_store<D>(s_k[(kt - kt0) & 1], s_v[(kt - kt0) % 3], of_raw[j], min(kt, kt1 - 1), wave + j * NW,
+                          names_page(a.v, e[j], place_in(kt, j)) ? q.len : 0, lane);
     };
     auto advance = [&](int kt) {  // tile kt out of the registers, kt+1 into them
-        store(kt);
+        store(kt, entry, raw);
 #pragma unroll
         for (int j = 0; j < JOBS; j++) entry[j] = ahead[j];
-        load(kt + 1);
+        load(kt + 1, entry, raw);
         look(kt + 2, ahead);
     };
     f32x16 x[2];
-    if (kt0 < kt1) {
-        look(kt0, entry);
-        load(kt0);
-        look(kt0 + 1, ahead);
-        advance(kt0);
+    u32x4 qf[P];
+    float c = 0.0f;
+    bool gaps = false;  // pages that the table does not name: looked for once, since there are none as a rule
+    if (kt0 < kt1) {    // every load that the first products wait for at once
+        ManyRaw<D> first[JOBS];
+        int first_entry[JOBS];
+        look(kt0, first_entry);
+        look(kt0 + 1, entry);
+        look(kt0 + 2, ahead);
+        load(kt0, first_entry, first);
+        load(kt0 + 1, entry, raw);
+        c = load_query<DT, P, 32>(a.q + (long long)(q.row + (live ? token : 0)) * a.q_stride +
+                                      (h * a.group + r - token * a.group) * D + 8 * g,
+                                  live, 16, a.scale, qf);
+        for (int i = (kt0 * kKeys >> a.v.page_shift) + lane; i <= (to - 1) >> a.v.page_shift; i += 64)
+            gaps |= i >= a.v.width || (unsigned)a.v.tables[(long long)s * a.v.width + i] >= (unsigned)a.v.pages;
+        store(kt0, first_entry, first);
         __syncthreads();
         many_products<D>(s_k[0], qf, n, g, x);
         advance(kt0 + 1);
+        gaps = __any(gaps);
     }
     for (int kt = kt0; kt < kt1; kt++) {
         __syncthreads();  // tile kt+1 is whole; the buffers of kt-1 and of kt's keys are free
@@ -580,7 +596,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     const int at = k0 + 16 * u + 8 * (i >> 2) + 4 * g + (i & 3);
-                    const bool ok = there && at <= place && (!a.window || at > place - a.window);
+                    const bool ok = there & (at <= place) & (at > place - window);
                     x[u >> 1][8 * (u & 1) + i] = ok ? x[u >> 1][8 * (u & 1) + i] : -INFINITY;
                 }
             }
@@ -627,7 +643,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     if (!live) return;
     const long long row = (long long)(q.row + token) * a.heads + h * a.group + r - token * a.group;
     const long long part = row * a.many_splits + z;
-    const float inv = a.many_splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = only < 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         float v[E];
@@ -637,41 +653,47 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
             v[2 * d + 1] = o[d][i + 8] * inv;
         }
         const int d = E * (8 * (i >> 2) + 4 * g + (i & 3));
-        if (a.many_splits == 1) store_out<DT, E>(a.y, row * D + d, v);
+        if (only >= 0) store_out<DT, E>(a.y, row * D + d, v);
         else if (l != 0.0f) store_out<QGEMM_F32, E>(a.many_sum, part * D + d, v);
     }
-    if (a.many_splits > 1 && g == 0) a.many_stat[part] = f32x2{b, l};
+    if (only < 0 && g == 0) a.many_stat[part] = f32x2{b, l};
 }
 
-// The parts of a row's keys joined: 16 lanes per row and query head.
-template <int DT, int D>
+// The parts of a row's keys joined, a row and query head at a time by G groups of
+// 16 lanes: group i takes every G-th part, and the groups' results meet in LDS.
+template <int DT, int D, int G>
 __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a)
 {
     constexpr int E = D / 16;
-    const int item = (int)(blockIdx.x * 16 + (threadIdx.x >> 4)), dl = threadIdx.x & 15;
+    __shared__ __align__(16) float s_y[G > 1 ? G : 1][D + 4];
+    const int item = (int)(blockIdx.x * (16 / G) + (threadIdx.x >> 4) / G), dl = threadIdx.x & 15, gi = (threadIdx.x >> 4) % G;
     const int row = item / a.heads, head = item - row * a.heads;
     if (row >= a.v.T) return;
     const int s = a.v.offs ? find_seq<16>(a.v, row, 1, 0) : row;
     const Seq q = seq_of(a.v, s);
     if (row < q.row || row >= q.row + q.n) return;
     const bool few = !a.v.offs || q.n * a.group <= a.few_rows;
-    const int splits = few ? a.few_splits : a.many_splits;
-    if (splits == 1) return;  // written where it was computed
+    const int splits = few ? a.few_splits : a.many_splits, chunk = few ? a.few_chunk : a.many_chunk;
     const int h = head / a.group, ra = (row - q.row) * a.group + head - h * a.group;
+    // the row tile it was computed in: rows of one part are written already
+    const int tile_rows = few ? a.few_tile_rows : a.tile_tokens * a.group, row0 = ra / tile_rows * tile_rows;
+    const Range keys = seen(a, q, row0, min(q.n * a.group - row0, tile_rows));
+    if (only_part(keys, splits, chunk) >= 0) return;
+    const int z0 = min(keys.lo / chunk, splits - 1), z1 = min((keys.hi - 1) / chunk, splits - 1);
     const long long entry = few ? ((long long)(s * a.v.H + h) * a.few_rows + ra) * splits
                                 : ((long long)row * a.heads + head) * splits;
     const f32x2 *stat = (few ? a.few_stat : a.many_stat) + entry;
     const float *sums = (few ? a.few_sum : a.many_sum) + entry * D + E * dl;
     float top = -INFINITY;
-    for (int z = dl; z < splits; z += 16) top = fmaxf(top, stat[z].x);
+    for (int z = z0 + dl; z <= z1; z += 16) top = fmaxf(top, stat[z].x);
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 16));
     float y[E], sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; e++) y[e] = 0.0f;
-    for (int z = 0; z < splits; z++) {
+    for (int z = z0 + gi; z <= z1; z += G) {
         const f32x2 st = stat[z];
-        if (st.y == 0.0f) continue;  // no keys, and no sums written
+        if (st.y == 0.0f) continue;  // it saw no key, and wrote no sums
         const float f = rescale_of(st.x, top);
         sum += st.y * f;
 #pragma unroll
@@ -679,6 +701,22 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a)
             const f32x4 v = *(const f32x4 *)(sums + (long long)z * D + e);
 #pragma unroll
             for (int i = 0; i < 4; i++) y[e + i] += v[i] * f;
+        }
+    }
+    if constexpr (G > 1) {
+        static_assert(G == 16, "one row and head to a workgroup");
+#pragma unroll
+        for (int e = 0; e < E; e++) s_y[gi][E * dl + e] = y[e];
+        if (dl == 0) s_y[gi][D] = sum;
+        __syncthreads();
+        if (gi) return;
+        sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; e++) y[e] = 0.0f;
+        for (int i = 0; i < G; i++) {
+            sum += s_y[i][D];
+#pragma unroll
+            for (int e = 0; e < E; e++) y[e] += s_y[i][E * dl + e];
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -716,8 +754,12 @@ hipError_t run_attention(const AttnPlan &pl, const AttnArgs &a, hipStream_t s)
         const hipError_t e = pl.many_waves == 8 ? run_many<DT, D, 8>(a, s) : run_many<DT, D, 4>(a, s);
         if (e != hipSuccess) return e;
     }
-    if ((pl.few && pl.few_splits > 1) || (pl.many && pl.many_splits > 1))
-        hipLaunchKernelGGL((k_attn_join<DT, D>), dim3((unsigned)ceil_of((long long)a.v.T * a.heads, 16)), dim3(256), 0, s, a);
+    const int splits = pl.few && pl.few_splits > 1 ? pl.few_splits : pl.many ? pl.many_splits : 1;
+    if (splits > 1) {
+        const long long items = (long long)a.v.T * a.heads;
+        if (splits > 4 && items <= 4096) hipLaunchKernelGGL((k_attn_join<DT, D, 16>), dim3((unsigned)items), dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_attn_join<DT, D, 1>), dim3((unsigned)ceil_of(items, 16)), dim3(256), 0, s, a);
+    }
     return hipGetLastError();
 }
 
@@ -736,7 +778,7 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     if (max_len < 1) max_len = 1;
     // chunks of whole steps for every wave; enough workgroups to fill the CUs
     const long long step = kStep * kFewWaves, units = S * kv_heads * p.few_tiles;
-    long long chunk = ceil_of(ceil_of(units * max_len, 1536), step) * step;
+    long long chunk = ceil_of(ceil_of(units * max_len, 768), step) * step;
     if (ceil_of(max_len, chunk) > 128) chunk = ceil_of(ceil_of(max_len, 128), step) * step;
     p.few_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
     p.few_splits = (int)ceil_of(max_len, p.few_chunk);
@@ -744,9 +786,14 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     p.many_waves = 8;
     p.tile_tokens = 32 * p.many_waves / group;
     p.slots = T / p.tile_tokens + S;
-    p.many_splits = 1;
-    p.many_chunk = INT32_MAX / 2;
-    p.many_entries = 0;
+    // few row tiles over long caches: split the keys, down to 1024
+    const long long tiles = p.slots * kv_heads;
+    chunk = tiles >= 256 ? max_len : ceil_of(ceil_of(tiles * max_len, 640), kKeys) * kKeys;
+    if (chunk < 1024) chunk = 1024;
+    if (ceil_of(max_len, chunk) > 64) chunk = ceil_of(ceil_of(max_len, 64), kKeys) * kKeys;
+    p.many_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
+    p.many_splits = (int)ceil_of(max_len, p.many_chunk);
+    p.many_entries = p.many && p.many_splits > 1 ? T * heads * (long long)p.many_splits : 0;
     p.few_entries += p.few_entries & 1;  // the sums behind the statistics stay 16-byte aligned
     p.many_entries += p.many_entries & 1;
     p.bytes = (size_t)(p.few_entries + p.many_entries) * (size_t)(D + 2) * 4;
@@ -757,6 +804,7 @@ hipError_t launch_kv_attention(int dtype, int D, const AttnPlan &pl, AttnArgs a,
 {
     a.few_rows = pl.few_rows;
     a.few_tiles = pl.few_tiles;
+    a.few_tile_rows = 16 * pl.few_rb;
     a.few_splits = pl.few_splits;
     a.few_chunk = pl.few_chunk;
     a.many_splits = pl.many_splits;

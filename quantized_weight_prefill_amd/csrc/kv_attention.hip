@@ -417,27 +417,29 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 64;
 
-// Half of the words of a tile's 16 tokens, keys and values (each wave of eight takes
-// one; of four, both).
-template <int D>
+// A wave's share of a tile's raw bytes: N words a lane of 16 tokens' keys and values,
+// all of them where four waves share a tile, half where eight do.
+template <int D, int PARTS>
 struct ManyRaw {
-    static constexpr int N = D / 64;  // words
+    static constexpr int N = D / 32 / PARTS;
     typedef uint32_t W __attribute__((ext_vector_type(N)));
     W k, v;
     uint32_t kh;
     u32x4 vh;
+    int entry;  // of the table
 };
 
-template <int D>
-__device__ __forceinline__ void many_load(const AttnArgs &a, int entry, int h, int kt, int job, int lane, ManyRaw<D> &r)
+template <int D, int PARTS>
+__device__ __forceinline__ void many_load(const AttnArgs &a, int entry, int h, int at, int part, int lane, ManyRaw<D, PARTS> &r)
 {
     using L = KvLay<D>;
-    using W = typename ManyRaw<D>::W;
+    using W = typename ManyRaw<D, PARTS>::W;
     const int n = lane & 15, g = lane >> 4;
-    const uint8_t *p = tile_at<D>(a.v, entry, kt * kKeys + 16 * (job & 3), h);
-    const int at = lane * L::kLane + (job >> 2) * (L::kLane / 2);
-    r.k = *(const W *)(p + at);
-    r.v = *(const W *)(p + L::kVal + at);
+    const uint8_t *p = tile_at<D>(a.v, entry, at, h);
+    const int mine = lane * L::kLane + part * (L::kLane / PARTS);
+    r.entry = entry;
+    r.k = *(const W *)(p + mine);
+    r.v = *(const W *)(p + L::kVal + mine);
     r.kh = *(const uint32_t *)(p + L::kKeyHead + (g * (D / 4) / 32 * 16 + n) * 4);
     r.vh = *(const u32x4 *)(p + L::kValHead + (n * L::E / 32 * 16 + 4 * g) * 4);
 }
@@ -447,56 +449,37 @@ __device__ __forceinline__ void many_load(const AttnArgs &a, int entry, int h, i
 // tokens.  Row d of block b is dim E*(d%16) + 2b + d/16: a wave's stores are then
 // contiguous, and a lane ends with E neighbouring dims.
 template <int D>
-struct ManyKeys {
+struct ManyTile {
     uint4 k[2][D / 8][32];
-};
-template <int D>
-struct ManyValues {
     uint2 v[4][D / 32][2][32][2];
 };
 
-// len: the sequence's, or 0 where the table names no page.
-template <int D>
-__device__ __forceinline__ void many_store(ManyKeys<D> &tk, ManyValues<D> &tv, const ManyRaw<D> &r, int kt, int job, int len, int lane)
+// i: which 16 tokens of the tile, from place `at` on; len: the sequence's, or 0 where
+// the table names no page.
+template <int D, int PARTS>
+__device__ __forceinline__ void many_store(ManyTile<D> &t, const ManyRaw<D, PARTS> &r, int i, int part, int at, int len, int lane)
 {
-    constexpr int N = ManyRaw<D>::N;
-    const int n = lane & 15, g = lane >> 4, i = job & 3, part = job >> 2;
+    constexpr int N = ManyRaw<D, PARTS>::N;
+    const int n = lane & 15, g = lane >> 4;
     const float f = head_scale(r.kh), b = head_min(r.kh);
 #pragma unroll
     for (int j = 0; j < N; j++)
-        *(u32x4 *)&tk.k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = key_values(r.k[j], f, b);
-    const QuadHead q = quad_head(live_heads(r.vh, kt * kKeys + 16 * i + 4 * g, len));
+        *(u32x4 *)&t.k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = key_values(r.k[j], f, b);
+    const QuadHead q = quad_head(live_heads(r.vh, at + 4 * g, len));
 #pragma unroll
     for (int j = 0; j < N; j++)
 #pragma unroll
         for (int e = 0; e < 2; e++)
-            *(u32x2 *)&tv.v[i][N * part + j][g & 1][n + 16 * e][g >> 1] = quad_values(r.v[j] >> (8 * e), q);
+            *(u32x2 *)&t.v[i][N * part + j][g & 1][n + 16 * e][g >> 1] = quad_values(r.v[j] >> (8 * e), q);
 }
 
-// One tile of 64 keys in a wave's registers: products of its 32 rows.
-template <int D>
-__device__ __forceinline__ void many_products(const ManyKeys<D> &t, const u32x4 (&qf)[D / 16], int n, int g, f32x16 (&x)[2])
-{
-#pragma unroll
-    for (int b = 0; b < 2; b++) {
-#pragma unroll
-        for (int i = 0; i < 16; i++) x[b][i] = 0.0f;
-#pragma unroll
-        for (int p = 0; p < D / 16; p++) x[b] = mma32<DT_F16>(*(const u32x4 *)&t.k[b][2 * p + g][n], qf[p], x[b]);
-    }
-}
-
-// The loop is a pipeline over the tiles of 64 keys: while a tile's products become
-// probabilities (VALU), the next tile's products run (MFMA), and while its
-// probabilities meet its values (MFMA), the tile after that is unpacked into LDS
-// (VALU); the raw bytes of one more are in flight.  Keys have two LDS
-// buffers, values three, and one barrier per tile orders all of it.
+// While a tile is multiplied, the next one is unpacked into the other LDS buffer
+// and the two after it are on their way from memory; one barrier per tile.
 template <int DT, int D, int NW>
 __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) k_attn_many(AttnArgs a)
 {
-    constexpr int E = D / 16, B = D / 32, P = D / 16, JOBS = 8 / NW;
-    __shared__ __align__(16) ManyKeys<D> s_k[2];
-    __shared__ __align__(16) ManyValues<D> s_v[3];
+    constexpr int E = D / 16, B = D / 32, P = D / 16, PARTS = NW / 4;
+    __shared__ __align__(16) ManyTile<D> s_tile[2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, g = lane >> 5;
     // key heads side by side, so that with a multiple of eight of them each XCD's
@@ -523,121 +506,101 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     const int clear_hi = q.first + (row0 + w0) / a.group;
     const int clear_lo = a.window ? q.first + (row0 + min(rows, w0 + 32) - 1) / a.group - a.window + 1 : 0;
 
-    float b = -INFINITY, l = 0.0f;
-    bool huge = false;
+    // this wave's 16 tokens of a tile; past the last tile, of the last once more
+    auto place_in = [&](int kt) { return min(kt, kt1 - 1) * kKeys + 16 * (wave & 3); };
+    auto load = [&](int kt, int entry, ManyRaw<D, PARTS> &to_raw) {
+        many_load<D, PARTS>(a, entry, h, place_in(kt), wave >> 2, lane, to_raw);
+    };
+    auto store = [&](int kt, const ManyRaw<D, PARTS> &of_raw) {
+        many_store<D, PARTS>(s_tile[(kt - kt0) & 1], of_raw, wave & 3, wave >> 2, place_in(kt),
+                             names_page(a.v, of_raw.entry, place_in(kt)) ? q.len : 0, lane);
+    };
+    ManyRaw<D, PARTS> raw, later;  // the next tile's bytes, and those of the one after it
+    int ahead = 0;                 // the table's entry for the one after that
+    u32x4 qf[P];
+    float c = 0.0f, b = -INFINITY, l = 0.0f;
+    bool gaps = false, huge = false;  // gaps: pages that the table does not name, looked for once
     f32x16 o[B];
 #pragma unroll
     for (int d = 0; d < B; d++)
 #pragma unroll
         for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
-
-    ManyRaw<D> raw[JOBS];
-    int entry[JOBS], ahead[JOBS];  // of the raw tile, and of the one after it
-    // past the last tile, the last once more
-    auto place_in = [&](int kt, int j) { return min(kt, kt1 - 1) * kKeys + 16 * ((wave + j * NW) & 3); };
-    auto look = [&](int kt, int(&e)[JOBS]) {
-#pragma unroll
-        for (int j = 0; j < JOBS; j++) e[j] = entry_of(a.v, s, place_in(kt, j));
-    };
-    auto load = [&](int kt, const int(&e)[JOBS], ManyRaw<D>(&to_raw)[JOBS]) {
-#pragma unroll
-        for (int j = 0; j < JOBS; j++) many_load<D>(a, e[j], h, min(kt, kt1 - 1), wave + j * NW, lane, to_raw[j]);
-    };
-    auto store = [&](int kt, const int(&e)[JOBS], const ManyRaw<D>(&of_raw)[JOBS]) {
-#pragma unroll
-        for (int j = 0; j < JOBS; j++)
-            many_store<D>(s_k[(kt - kt0) & 1], s_v[(kt - kt0) % 3], of_raw[j], min(kt, kt1 - 1), wave + j * NW,
-                          names_page(a.v, e[j], place_in(kt, j)) ? q.len : 0, lane);
-    };
-    auto advance = [&](int kt) {  // tile kt out of the registers, kt+1 into them
-        store(kt, entry, raw);
-#pragma unroll
-        for (int j = 0; j < JOBS; j++) entry[j] = ahead[j];
-        load(kt + 1, entry, raw);
-        look(kt + 2, ahead);
-    };
-    f32x16 x[2];
-    u32x4 qf[P];
-    float c = 0.0f;
-    bool gaps = false;  // pages that the table does not name: looked for once, since there are none as a rule
-    if (kt0 < kt1) {    // every load that the first products wait for at once
-        ManyRaw<D> first[JOBS];
-        int first_entry[JOBS];
-        look(kt0, first_entry);
-        look(kt0 + 1, entry);
-        look(kt0 + 2, ahead);
-        load(kt0, first_entry, first);
-        load(kt0 + 1, entry, raw);
+    if (kt0 < kt1) {  // everything that the first products wait for at once
+        const int e0 = entry_of(a.v, s, place_in(kt0)), e1 = entry_of(a.v, s, place_in(kt0 + 1)), e2 = entry_of(a.v, s, place_in(kt0 + 2));
+        ahead = entry_of(a.v, s, place_in(kt0 + 3));
+        ManyRaw<D, PARTS> first;
+        load(kt0, e0, first);
         c = load_query<DT, P, 32>(a.q + (long long)(q.row + (live ? token : 0)) * a.q_stride +
                                       (h * a.group + r - token * a.group) * D + 8 * g,
                                   live, 16, a.scale, qf);
         for (int i = (kt0 * kKeys >> a.v.page_shift) + lane; i <= (to - 1) >> a.v.page_shift; i += 64)
             gaps |= i >= a.v.width || (unsigned)a.v.tables[(long long)s * a.v.width + i] >= (unsigned)a.v.pages;
-        store(kt0, first_entry, first);
-        __syncthreads();
-        many_products<D>(s_k[0], qf, n, g, x);
-        advance(kt0 + 1);
+        load(kt0 + 1, e1, raw);
+        load(kt0 + 2, e2, later);
+        store(kt0, first);
         gaps = __any(gaps);
     }
     for (int kt = kt0; kt < kt1; kt++) {
-        __syncthreads();  // tile kt+1 is whole; the buffers of kt-1 and of kt's keys are free
+        __syncthreads();  // this tile is whole, and the other buffer's readers are done
         const int k0 = kt * kKeys;
-        const ManyKeys<D> &tk = s_k[(kt + 1 - kt0) & 1];
-        const ManyValues<D> &tv = s_v[(kt - kt0) % 3];
-        if (kt < mt0 || kt >= mt1) {  // nothing for this wave
-            if (kt + 1 == mt0) many_products<D>(tk, qf, n, g, x);
-            advance(kt + 2);
-            continue;
-        }
-        if (gaps || k0 + kKeys - 1 > clear_hi || k0 < clear_lo) {
+        const ManyTile<D> &t = s_tile[(kt - kt0) & 1];
+        if (kt >= mt0 && kt < mt1) {
+            f32x16 x[2];
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const bool there = !gaps || names_page(a.v, entry_of(a.v, s, k0 + 16 * u), k0 + 16 * u);
+            for (int i = 0; i < 2; i++) {
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int at = k0 + 16 * u + 8 * (i >> 2) + 4 * g + (i & 3);
-                    const bool ok = there & (at <= place) & (at > place - window);
-                    x[u >> 1][8 * (u & 1) + i] = ok ? x[u >> 1][8 * (u & 1) + i] : -INFINITY;
+                for (int j = 0; j < 16; j++) x[i][j] = 0.0f;
+#pragma unroll
+                for (int p = 0; p < P; p++) x[i] = mma32<DT_F16>(*(const u32x4 *)&t.k[i][2 * p + g][n], qf[p], x[i]);
+            }
+            if (gaps || k0 + kKeys - 1 > clear_hi || k0 < clear_lo) {
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    const bool there = !gaps || names_page(a.v, entry_of(a.v, s, k0 + 16 * u), k0 + 16 * u);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const int at = k0 + 16 * u + 8 * (i >> 2) + 4 * g + (i & 3);
+                        const bool ok = there & (at <= place) & (at > place - window);
+                        x[u >> 1][8 * (u & 1) + i] = ok ? x[u >> 1][8 * (u & 1) + i] : -INFINITY;
+                    }
                 }
             }
-        }
-        float mx = x[0][0];
+            float mx = x[0][0];
 #pragma unroll
-        for (int i = 0; i < 16; i++) mx = fmaxf(fmaxf(mx, x[0][i]), x[1][i]);
-        if (__any(mx * c - b > kLift)) {
-            const float nb = raised(fmaxf(mx, __shfl_xor(mx, 32, 64)), b, c), f = rescale_of(b, nb);
-            b = nb;
-            huge = huge || __any(fabsf(nb) > kHuge && nb != -INFINITY);
-            l *= f;
+            for (int i = 0; i < 16; i++) mx = fmaxf(fmaxf(mx, x[0][i]), x[1][i]);
+            if (__any(mx * c - b > kLift)) {
+                const float nb = raised(fmaxf(mx, __shfl_xor(mx, 32, 64)), b, c), f = rescale_of(b, nb);
+                b = nb;
+                huge = huge || __any(fabsf(nb) > kHuge && nb != -INFINITY);
+                l *= f;
 #pragma unroll
-            for (int d = 0; d < B; d++) o[d] *= f;
-        }
-        const float base = shift_of(b);
-        if (huge) {  // the arguments as they are to be: what follows then adds and multiplies nothing
-#pragma unroll
-            for (int u = 0; u < 2; u++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) x[u][i] = argument_of_huge(x[u][i], c, base);
-        }
-        const float cc = huge ? 1.0f : c, bb = huge ? 0.0f : base;
-        f32x16 y[2];
-        u32x4 p[4];  // 16 tokens each: registers 8*(u%2) .. +7 of half u/2
-        many_products<D>(tk, qf, n, g, y);
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int k = 8 * (u & 1) + 2 * i;
-                p[u][i] = pack_out<DT_F16>(weight_of(x[u >> 1][k], cc, bb), weight_of(x[u >> 1][k + 1], cc, bb));
-                l = add_pair(p[u][i], l);
+                for (int d = 0; d < B; d++) o[d] *= f;
             }
+            const float base = shift_of(b);
+            if (huge) {  // the arguments as they are to be: what follows then adds and multiplies nothing
 #pragma unroll
-        for (int u = 0; u < 4; u++)
+                for (int u = 0; u < 2; u++)
 #pragma unroll
-            for (int d = 0; d < B; d++) o[d] = mma32<DT_F16>(*(const u32x4 *)&tv.v[u][d][g][n][0], p[u], o[d]);
-        advance(kt + 2);
+                    for (int i = 0; i < 16; i++) x[u][i] = argument_of_huge(x[u][i], c, base);
+            }
+            const float cc = huge ? 1.0f : c, bb = huge ? 0.0f : base;
 #pragma unroll
-        for (int i = 0; i < 2; i++) x[i] = y[i];
+            for (int u = 0; u < 4; u++) {  // 16 tokens: registers 8*(u%2) .. +7 of half u/2
+                u32x4 p;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int k = 8 * (u & 1) + 2 * i;
+                    p[i] = pack_out<DT_F16>(weight_of(x[u >> 1][k], cc, bb), weight_of(x[u >> 1][k + 1], cc, bb));
+                    l = add_pair(p[i], l);
+                }
+#pragma unroll
+                for (int d = 0; d < B; d++) o[d] = mma32<DT_F16>(*(const u32x4 *)&t.v[u][d][g][n][0], p, o[d]);
+            }
+        }
+        store(kt + 1, raw);
+        raw = later;
+        load(kt + 3, ahead, later);
+        ahead = entry_of(a.v, s, place_in(kt + 4));
     }
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
@@ -783,13 +746,15 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     p.few_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
     p.few_splits = (int)ceil_of(max_len, p.few_chunk);
     p.few_entries = p.few && p.few_splits > 1 ? S * kv_heads * (long long)p.few_rows * p.few_splits : 0;
-    p.many_waves = 8;
+    // row tiles of 128 rows until tiles of 256 fill the CUs
+    p.many_waves = (T / (256 / group) + S) * kv_heads > 256 ? 8 : 4;
     p.tile_tokens = 32 * p.many_waves / group;
     p.slots = T / p.tile_tokens + S;
-    // few row tiles over long caches: split the keys, down to 1024
-    const long long tiles = p.slots * kv_heads;
-    chunk = tiles >= 256 ? max_len : ceil_of(ceil_of(tiles * max_len, 640), kKeys) * kKeys;
-    if (chunk < 1024) chunk = 1024;
+    // few row tiles over long caches: split the keys
+    const long long tiles = p.slots * kv_heads, least = tiles < 256 ? 1024 : 3072;
+    chunk = ceil_of(ceil_of(tiles * max_len, 640), kKeys) * kKeys;
+    if (chunk < least) chunk = least;
+    if (tiles >= 512) chunk = max_len;
     if (ceil_of(max_len, chunk) > 64) chunk = ceil_of(ceil_of(max_len, 64), kKeys) * kKeys;
     p.many_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
     p.many_splits = (int)ceil_of(max_len, p.many_chunk);

@@ -563,7 +563,8 @@ size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64
  * Cache.  `cache` is `pages` pages of qgemm_kv_page_bytes(kv_heads, head_dim,
  *   page) bytes (device, 16-byte aligned); page is 16, 32, 64, 128 or 256 tokens.
  *   tables [S][table_width] (int32, device): the pages of each sequence in order,
- *   so that its token at place p is in page tables[s][p / page].  Values are held
+ *   so that its token at place p is in page tables[s][p / page]; table_width * page
+ *   is at most 2^30.  Values are held
  *   in groups of 32 dims of one token's head: minimum = fp16(min), scale =
  *   fp16((max - minimum) / 15), both rounded to binary32 first, code = the nearest of
  *   0..15 to (x - minimum) / scale, ties to even (0 where scale is 0); a value reads as code * scale +

@@ -63,7 +63,7 @@ int view_of(const void *cache, long long pages, long long page, const int32_t *t
     const int shift = page_shift(page);
     if (shift < 0) return QGEMM_ERR_FORMAT;
     if (S < 0 || T < 0 || T > INT32_MAX / 2 || S > INT32_MAX / 8 || (!offsets && S != T)) return QGEMM_ERR_SHAPE;
-    if (pages < 1 || pages > INT32_MAX || width < 1 || width > (INT32_MAX >> shift)) return QGEMM_ERR_SHAPE;
+    if (pages < 1 || pages > INT32_MAX || width < 1 || width > ((1 << 30) >> shift)) return QGEMM_ERR_SHAPE;
     if (T == 0 || S == 0) return QGEMM_OK;
     if (!cache || !tables || !lens) return QGEMM_ERR_NULL;
     if (!aligned(cache, 16) || !aligned(tables, 4) || !aligned(lens, 4) || !aligned(offsets, 4)) return QGEMM_ERR_ALIGN;

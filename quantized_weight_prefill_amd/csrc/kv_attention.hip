@@ -240,7 +240,7 @@ __device__ __forceinline__ void few_load(const AttnArgs &a, const int (&entry)[2
 }
 
 template <int DT, int D, int RB>
-__global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(RB == 1 ? 4 : 2))) k_attn_few(AttnArgs a)
+__global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(RB == 2 ? 2 : D == 64 ? 4 : 3))) k_attn_few(AttnArgs a)
 {
     using L = KvLay<D>;
     constexpr int E = L::E, J = D / 32, LD = D + 4;
@@ -258,6 +258,16 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
     if (only >= 0 && only != z) return;
     const int from = max(keys.lo & ~(kStep - 1), z * a.few_chunk), to = z + 1 < a.few_splits ? min(keys.hi, (z + 1) * a.few_chunk) : keys.hi;
 
+    const int stride = kStep * kFewWaves, window = a.window ? a.window : INT_MAX;
+    const int pmin = q.first + row0 / a.group, pmax_lo = a.window ? q.first + (row0 + rows - 1) / a.group - a.window + 1 : 0;
+    int t = from + wave * kStep, ahead[2];
+    FewRaw<D> even, odd;  // this step's bytes and the next one's
+    bool huge = false;
+    if (t < to) {
+        few_entries(a, s, t, ahead);
+        few_load<D>(a, ahead, h, t, lane, even);
+        few_entries(a, s, t + stride, ahead);
+    }
     u32x4 qf[RB][J];
     float c[RB], b[RB], l[RB];
     int place[RB];
@@ -276,19 +286,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
         for (int e = 0; e < E; e++) o[rb][e] = f32x4{0, 0, 0, 0};
     }
 
-    const int stride = kStep * kFewWaves, window = a.window ? a.window : INT_MAX;
-    const int pmin = q.first + row0 / a.group, pmax_lo = a.window ? q.first + (row0 + rows - 1) / a.group - a.window + 1 : 0;
-    int t = from + wave * kStep;
-    FewRaw<D> next;
-    int ahead[2];
-    bool huge = false;
-    if (t < to) {
-        few_entries(a, s, t, ahead);
-        few_load<D>(a, ahead, h, t, lane, next);
-        few_entries(a, s, t + stride, ahead);
-    }
-    for (; t < to; t += stride) {
-        FewRaw<D> r = next;
+    auto turn = [&](int t, FewRaw<D> &r, FewRaw<D> &next) {
         if (t + stride < to) {
             few_load<D>(a, ahead, h, t + stride, lane, next);
             few_entries(a, s, t + 2 * stride, ahead);
@@ -362,6 +360,10 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
 #pragma unroll
             for (int rb = 0; rb < RB; rb++) o[rb][e] = mma<DT_F16>(v, p[rb], o[rb][e]);
         }
+    };
+    for (; t < to; t += 2 * stride) {
+        turn(t, even, odd);
+        if (t + stride < to) turn(t + stride, odd, even);
     }
 
 #pragma unroll
@@ -739,9 +741,9 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     p.few_rb = p.few_rows <= 16 ? 1 : 2;
     p.few_tiles = (int)ceil_of(p.few_rows > 0 ? p.few_rows : 1, 16 * p.few_rb);
     if (max_len < 1) max_len = 1;
-    // chunks of whole steps for every wave; enough workgroups to fill the CUs
+    // chunks of whole steps for every wave; as many workgroups as the CUs hold at once: three or four
     const long long step = kStep * kFewWaves, units = S * kv_heads * p.few_tiles;
-    long long chunk = ceil_of(ceil_of(units * max_len, 768), step) * step;
+    long long chunk = ceil_of(ceil_of(units * max_len, D == 64 ? 1024 : 768), step) * step;
     if (ceil_of(max_len, chunk) > 128) chunk = ceil_of(ceil_of(max_len, 128), step) * step;
     p.few_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
     p.few_splits = (int)ceil_of(max_len, p.few_chunk);

@@ -204,6 +204,13 @@ __device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0,
 // workgroup takes one key head of one sequence, 16*RB rows and a chunk of the
 // keys; its four waves take steps of 32 keys in turn, straight from memory into
 // MFMA registers, and add their results through LDS.
+//
+// Bound by the cache's bytes where it is long: 64 sequences of up to 8192 tokens,
+// 432 MB of codes and headers, take 101 us with the join, 4.3 TB/s.  The 16x16x32
+// product leaves the fewest rows idle; 64 keys in flight a wave (two steps' registers in turn)
+// and three workgroups a CU cover the loads, where a fourth would spill (149 us).  Short ones are a
+// chain of dependent loads (lengths, table, cache), a merge and a second launch to
+// join: one sequence of 658 tokens 8.3 us, of 300 in one part 7.1 us.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 4;
 constexpr int kStep = 32;
@@ -416,6 +423,14 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
 // Many rows (prompts): a workgroup takes one key head and 32 rows per wave,
 // row r being token r/group, head r%group of the key head's; tiles of 64 keys are
 // unpacked once into LDS, in fragment order, for all its waves.
+//
+// Bound by the exponentials and the unpacking beside the products, and by the power
+// limit: 4096 tokens of 32 query heads of 128 (137 GFLOP under the mask) take 165 us, 0.83
+// PFLOP/s, where the matrix units alone, on random operands, sustain 1.35.  The 32x32x16
+// product reads the fewest LDS bytes a flop; a 64-key tile takes a CU's 8 waves 4160 cycles,
+// half of them products.  Eight waves share a tile's unpacking (189 us with four) where that
+// still fills the CUs; short prompts are a chain of one tile after the other (658 tokens
+// 22.6 us), which two waves to 32 rows shorten.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 64;
 
@@ -477,12 +492,14 @@ __device__ __forceinline__ void many_store(ManyTile<D> &t, const ManyRaw<D, PART
 
 // While a tile is multiplied, the next one is unpacked into the other LDS buffer
 // and the two after it are on their way from memory; one barrier per tile.
-template <int DT, int D, int NW>
-__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) k_attn_many(AttnArgs a)
+// KS = 2: two waves share 32 rows, each with half of every tile's keys, and are joined at the end.
+template <int DT, int D, int NW, int KS>
+__global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_eu(2, 2))) k_attn_many(AttnArgs a)
 {
-    constexpr int E = D / 16, B = D / 32, P = D / 16, PARTS = NW / 4;
+    constexpr int E = D / 16, B = D / 32, P = D / 16, PARTS = NW * KS / 4, HALVES = 2 / KS;
     __shared__ __align__(16) ManyTile<D> s_tile[2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = KS == 2 ? wave / NW : 0;  // the first of the tile's halves of 32 keys that it takes
     const int n = lane & 31, g = lane >> 5;
     // key heads side by side, so that with a multiple of eight of them each XCD's
     // L2 holds its own; later row tiles, which see more keys, first
@@ -499,7 +516,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
     const int from = max(keys.lo, z * a.many_chunk), to = z + 1 < a.many_splits ? min(keys.hi, (z + 1) * a.many_chunk) : keys.hi;
     const int kt0 = from / kKeys, kt1 = to > from ? (to + kKeys - 1) / kKeys : kt0;
 
-    const int w0 = 32 * wave, r = row0 + w0 + n, token = r / a.group;
+    const int w0 = 32 * (wave % NW), r = row0 + w0 + n, token = r / a.group;
     const bool live = w0 + n < rows;
     const int place = live ? q.first + token : -1, window = a.window ? a.window : INT_MAX;
     // tiles in which some row of the wave sees a key, and keys that all its rows see
@@ -547,21 +564,22 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
         const int k0 = kt * kKeys;
         const ManyTile<D> &t = s_tile[(kt - kt0) & 1];
         if (kt >= mt0 && kt < mt1) {
-            f32x16 x[2];
+            f32x16 x[HALVES];
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
+            for (int i = 0; i < HALVES; i++) {
 #pragma unroll
                 for (int j = 0; j < 16; j++) x[i][j] = 0.0f;
 #pragma unroll
-                for (int p = 0; p < P; p++) x[i] = mma32<DT_F16>(*(const u32x4 *)&t.k[i][2 * p + g][n], qf[p], x[i]);
+                for (int p = 0; p < P; p++) x[i] = mma32<DT_F16>(*(const u32x4 *)&t.k[half + i][2 * p + g][n], qf[p], x[i]);
             }
             if (gaps || k0 + kKeys - 1 > clear_hi || k0 < clear_lo) {
 #pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const bool there = !gaps || names_page(a.v, entry_of(a.v, s, k0 + 16 * u), k0 + 16 * u);
+                for (int u = 0; u < 2 * HALVES; u++) {
+                    const int k = k0 + 32 * half + 16 * u;
+                    const bool there = !gaps || names_page(a.v, entry_of(a.v, s, k), k);
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
-                        const int at = k0 + 16 * u + 8 * (i >> 2) + 4 * g + (i & 3);
+                        const int at = k + 8 * (i >> 2) + 4 * g + (i & 3);
                         const bool ok = there & (at <= place) & (at > place - window);
                         x[u >> 1][8 * (u & 1) + i] = ok ? x[u >> 1][8 * (u & 1) + i] : -INFINITY;
                     }
@@ -569,7 +587,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
             }
             float mx = x[0][0];
 #pragma unroll
-            for (int i = 0; i < 16; i++) mx = fmaxf(fmaxf(mx, x[0][i]), x[1][i]);
+            for (int i = 0; i < 16; i++) mx = fmaxf(fmaxf(mx, x[0][i]), x[HALVES - 1][i]);
             if (__any(mx * c - b > kLift)) {
                 const float nb = raised(fmaxf(mx, __shfl_xor(mx, 32, 64)), b, c), f = rescale_of(b, nb);
                 b = nb;
@@ -581,13 +599,13 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
             const float base = shift_of(b);
             if (huge) {  // the arguments as they are to be: what follows then adds and multiplies nothing
 #pragma unroll
-                for (int u = 0; u < 2; u++)
+                for (int u = 0; u < HALVES; u++)
 #pragma unroll
                     for (int i = 0; i < 16; i++) x[u][i] = argument_of_huge(x[u][i], c, base);
             }
             const float cc = huge ? 1.0f : c, bb = huge ? 0.0f : base;
 #pragma unroll
-            for (int u = 0; u < 4; u++) {  // 16 tokens: registers 8*(u%2) .. +7 of half u/2
+            for (int u = 0; u < 2 * HALVES; u++) {  // 16 tokens: registers 8*(u%2) .. +7 of half u/2
                 u32x4 p;
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -596,7 +614,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
                     l = add_pair(p[i], l);
                 }
 #pragma unroll
-                for (int d = 0; d < B; d++) o[d] = mma32<DT_F16>(*(const u32x4 *)&t.v[u][d][g][n][0], p, o[d]);
+                for (int d = 0; d < B; d++) o[d] = mma32<DT_F16>(*(const u32x4 *)&t.v[2 * half + u][d][g][n][0], p, o[d]);
             }
         }
         store(kt + 1, raw);
@@ -605,6 +623,29 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
         ahead = entry_of(a.v, s, place_in(kt + 4));
     }
     l += __shfl_xor(l, 32, 64);
+    if constexpr (KS == 2) {  // through the LDS of the tiles
+        __shared__ f32x2 s_stat[NW][64];
+        static_assert(sizeof(s_tile) == sizeof(float) * NW * B * 16 * 64, "the tiles' LDS holds half of the waves' sums");
+        float *sums = (float *)s_tile + (wave % NW) * B * 16 * 64 + lane;
+        __syncthreads();
+        if (half == 1) {
+#pragma unroll
+            for (int d = 0; d < B; d++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) sums[(d * 16 + i) * 64] = o[d][i];
+            s_stat[wave % NW][lane] = f32x2{b, l};
+        }
+        __syncthreads();
+        if (half == 1) return;
+        const f32x2 st = s_stat[wave][lane];
+        const float top = fmaxf(b, st.x), f = l == 0.0f ? 0.0f : rescale_of(b, top), f1 = st.y == 0.0f ? 0.0f : rescale_of(st.x, top);
+        b = top;
+        l = l * f + st.y * f1;
+#pragma unroll
+        for (int d = 0; d < B; d++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) o[d][i] = o[d][i] * f + sums[(d * 16 + i) * 64] * f1;
+    }
     if (!live) return;
     const long long row = (long long)(q.row + token) * a.heads + h * a.group + r - token * a.group;
     const long long part = row * a.many_splits + z;
@@ -699,10 +740,10 @@ void run_few(const AttnArgs &a, hipStream_t s)
                        dim3(64 * kFewWaves), 0, s, a);
 }
 
-template <int DT, int D, int NW>
+template <int DT, int D, int NW, int KS>
 hipError_t run_many(const AttnArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_attn_many<DT, D, NW>), dim3((unsigned)(a.slots * a.v.H), (unsigned)a.many_splits), dim3(64 * NW), 0, s, a);
+    hipLaunchKernelGGL((k_attn_many<DT, D, NW, KS>), dim3((unsigned)(a.slots * a.v.H), (unsigned)a.many_splits), dim3(64 * NW * KS), 0, s, a);
     return hipGetLastError();
 }
 
@@ -716,7 +757,9 @@ hipError_t run_attention(const AttnPlan &pl, const AttnArgs &a, hipStream_t s)
         if (e != hipSuccess) return e;
     }
     if (pl.many) {
-        const hipError_t e = pl.many_waves == 8 ? run_many<DT, D, 8>(a, s) : run_many<DT, D, 4>(a, s);
+        const hipError_t e = pl.many_waves == 8 ? run_many<DT, D, 8, 1>(a, s)
+                             : pl.many_halves ? run_many<DT, D, 4, 2>(a, s)
+                                              : run_many<DT, D, 4, 1>(a, s);
         if (e != hipSuccess) return e;
     }
     const int splits = pl.few && pl.few_splits > 1 ? pl.few_splits : pl.many ? pl.many_splits : 1;
@@ -744,19 +787,42 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     // chunks of whole steps for every wave; as many workgroups as the CUs hold at once: three or four
     const long long step = kStep * kFewWaves, units = S * kv_heads * p.few_tiles;
     long long chunk = ceil_of(ceil_of(units * max_len, D == 64 ? 1024 : 768), step) * step;
+    // one part up to 384 keys (one sequence of 300: 7.1 us against 8.8 in three parts), parts of 128 up to 4096 (of 2000: 8.6
+    // against 9.7 in parts of 256) and of 256 at least from there on (of 8192: 11.5 against 13.5)
+    const long long least_few = max_len <= 384 ? 384 : max_len <= 4096 ? step : 256;
+    if (chunk < least_few) chunk = least_few;
     if (ceil_of(max_len, chunk) > 128) chunk = ceil_of(ceil_of(max_len, 128), step) * step;
     p.few_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
     p.few_splits = (int)ceil_of(max_len, p.few_chunk);
     p.few_entries = p.few && p.few_splits > 1 ? S * kv_heads * (long long)p.few_rows * p.few_splits : 0;
-    // row tiles of 128 rows until tiles of 256 fill the CUs
-    p.many_waves = (T / (256 / group) + S) * kv_heads > 256 ? 8 : 4;
+    // row tiles of 128 rows until tiles of 256 more than fill the CUs; a sequence's last one counts half
+    const long long each = (T + S - 1) / S, wide = 256 / group;
+    auto count = [&](long long tokens) { return ceil_of(T + (S - 1) * tokens / 2, tokens) * kv_heads; };
+    p.many_waves = count(wide) > 256 ? 8 : 4;
     p.tile_tokens = 32 * p.many_waves / group;
     p.slots = T / p.tile_tokens + S;
-    // few row tiles over long caches: split the keys
-    const long long tiles = p.slots * kv_heads, least = tiles < 256 ? 1024 : 3072;
-    chunk = ceil_of(ceil_of(tiles * max_len, 640), kKeys) * kKeys;
-    if (chunk < least) chunk = least;
-    if (tiles >= 512) chunk = max_len;
+    // Keys are split where tiles of 128 rows do not fill the CUs, of a prompt's own triangle only where they leave
+    // half of them idle: joining costs more than it gains else.  Eight waves of two halves make a workgroup
+    // to a CU; where whole parts leave too many idle that way, two workgroups of four waves.
+    // In us, 32 query and 8 key heads of 128.  One wave and two to 32 rows: 1300 tokens 45 and 39, 658 tokens
+    // 23.9 and 22.6, 256 tokens behind 4000 57 and 47; but 2000 tokens of heads of 64 (500 tiles) 44 and 47.
+    // Whole and in parts: 64 tokens behind 8000 170 and 39, 512 behind 7600 172 and 112, 1100 of three sequences
+    // behind up to 8000 (288 tiles) 189 and 145; 1024 behind 7000 (256 tiles) 182 and 179.
+    const long long tiles = count(p.tile_tokens);
+    const bool behind = max_len > 2 * each;
+    long long least = 512;
+    chunk = max_len;
+    p.many_halves = p.many_waves == 4 && max_len > 256 && tiles <= (behind ? 256 : 384);
+    if (p.many_waves == 4 && tiles <= (behind ? 256 : 128)) {
+        const bool pairs = behind && 256 / tiles * tiles < 176;
+        if (pairs) p.many_halves = false;
+        if (!behind) least = 1024;
+        chunk = ceil_of(max_len, (pairs ? 512 : 256) / tiles);
+    } else if (p.many_waves == 4 && behind && tiles < 512) {
+        chunk = ceil_of(tiles * max_len, 640);
+        least = 2048;
+    }
+    chunk = chunk < least ? least : ceil_of(chunk, kKeys) * kKeys;
     if (ceil_of(max_len, chunk) > 64) chunk = ceil_of(ceil_of(max_len, 64), kKeys) * kKeys;
     p.many_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
     p.many_splits = (int)ceil_of(max_len, p.many_chunk);

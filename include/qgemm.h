@@ -614,10 +614,10 @@ size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64
  *   row that sees none gets zeros.  The new tokens' keys must be in the cache.
  *   Statistics and sums in 32 bits; the result does not depend on timing.  max_len (0:
  *   the table's width) is a bound on the lengths that the split of the work over a
- *   long cache goes by; longer ones are read all the same.  `workspace`
+ *   long cache goes by (one above table_width * page counts as that); longer ones are read all the same.  `workspace`
  *   (device, 16-byte aligned, of any contents) has at least
  *   qgemm_kv_attention_workspace_bytes(T, S, heads, kv_heads, head_dim, max_len,
- *   offsets != NULL) bytes, max_len 0 counted as table_width * page; calls that may run
+ *   offsets != NULL) bytes, with the max_len that counts; calls that may run
  *   at the same time need one each.
  * T = 0 or S = 0 is a no-op.  Errors of the device calls: QGEMM_ERR_SHAPE,
  * _DTYPE, _FORMAT (page), _NULL, _ALIGN, _SIZE (workspace), _HIP; all but the

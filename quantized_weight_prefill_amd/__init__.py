@@ -1281,7 +1281,8 @@ def kv_read(cache, tables, lens, T: int, kv_heads: int, head_dim: int, offsets=N
         raise ValueError("cache must be a device tensor")
     page = _kv_page(cache, kv_heads, head_dim)
     tp, width, lp, op, S = _kv_sequences(tables, lens, offsets, T, index)
-    k, v = _allocate(stream, index, lambda: tuple(torch.empty((T, kv_heads, head_dim), dtype=dtype, device=cache.device) for _ in "kv"))
+    new = torch.empty if S else torch.zeros  # no sequence: the call does nothing
+    k, v = _allocate(stream, index, lambda: tuple(new((T, kv_heads, head_dim), dtype=dtype, device=cache.device) for _ in "kv"))
     _call("qgemm_kv_read", index, stream, cache.data_ptr(), cache.shape[0], page, tp, width, lp, op, S, k.data_ptr(),
           v.data_ptr(), T, kv_heads, head_dim, codes[dtype])
     return k, v

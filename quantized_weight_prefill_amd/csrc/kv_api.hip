@@ -18,8 +18,8 @@ int status_of(hipError_t e, const char *what)
     return QGEMM_ERR_HIP;
 }
 
-// Items of 16 lanes, 16 to a workgroup, in one launch; counts stay below 2^28 so
-// that a kernel's item index is an int.
+// Items of at most 16 lanes in one launch; counts stay below 2^28 so that a kernel's item index is an
+// int.
 bool items_fit(long long n) { return n >= 0 && n < (1LL << 28); }
 
 int page_shift(long long page)
@@ -80,8 +80,9 @@ int attention_shape(long long T, long long S, long long heads, long long kv_head
     if (heads < 1 || heads % kv_heads != 0 || heads / kv_heads > 128 || T > INT32_MAX / 2 || S > INT32_MAX / 8 ||
         max_len < 0 || max_len > INT32_MAX)
         return QGEMM_ERR_SHAPE;
-    // every launch's work-items along x below 2^32: 16 lanes per row and head, 512 threads per sequence and head
-    return items_fit(T * heads) && items_fit(32 * S * heads) ? QGEMM_OK : QGEMM_ERR_SHAPE;
+    // every launch's work-items along x below 2^32: 16 lanes a row and head, 512 threads for each sequence's key head
+    // and for each 128 of its rows
+    return items_fit(T * heads) && items_fit(64 * S * heads) ? QGEMM_OK : QGEMM_ERR_SHAPE;
 }
 
 }  // namespace

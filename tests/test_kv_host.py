@@ -140,3 +140,28 @@ def test_rows_apart():
         with pytest.raises(ValueError, match="shares memory"):
             qg._rows_apart("out", other, [("q", q)])
     qg._rows_apart("out", q, [("later", torch.zeros((6, 8, 128), dtype=torch.float16))])
+
+
+def test_workspace_bytes():
+    """None for one part or sizes that no call takes; a multiple of 16; the bound on the lengths only splits."""
+    f = qg.kv_attention_workspace_bytes
+    assert f(1, 1, 32, 8, 128, 384, False) == 0 and f(1, 1, 32, 8, 128, 4096, False) > 0
+    assert f(658, 1, 32, 8, 128, 658, True) == 0 and f(64, 1, 32, 8, 128, 8000, True) > 0
+    assert f(4096, 1, 32, 8, 128, 4096, True) == 0
+    for bad in ((0, 1, 32, 8, 128, 99), (1, 0, 32, 8, 128, 99), (1, 1, 32, 7, 128, 99), (1, 1, 32, 8, 96, 99), (1, 1, 32, 8, 128, -1),
+                (1 << 31, 1, 32, 8, 128, 99), (1, 1 << 30, 32, 8, 128, 99), (1 << 22, 1 << 22, 1, 1, 64, 99)):
+        assert f(*bad, True) == 0
+    for T, S, heads, kv in ((1, 1, 1, 1), (3, 3, 5, 1), (700, 2, 16, 2), (9, 4, 40, 1), (2000, 7, 7, 7)):
+        for n in (0, 1, 385, 5000, 1 << 30):
+            for D in (64, 128):
+                b = f(T, S, heads, kv, D, n, True)
+                assert b % 16 == 0 and b <= (T * heads + S * kv * 32) * 128 * (D + 2) * 4 + 4096, (T, S, heads, kv, n, D)
+
+
+@pytest.mark.parametrize("kw", [dict(page=256, width=(1 << 22) + 1), dict(page=16, width=(1 << 26) + 1), dict(S=1 << 23, T=1 << 23),
+                                dict(S=1 << 22, T=4, heads=1, kv=1)])
+def test_sizes_beyond_the_kernels(kw):
+    """Places from 2^30 on, and more sequences and heads than a launch holds."""
+    assert attn_call(**kw) == -2
+    if "width" in kw:
+        assert append_call(**kw) == -2 and read_call(**kw) == -2

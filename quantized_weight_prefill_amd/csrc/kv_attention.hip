@@ -16,6 +16,13 @@
 // fp16 (v_fma_mix, as the weights of the fp16 GEMMs), probabilities likewise.
 // Products, maxima, sums and O are binary32.
 //
+// Of an fp16 result, whose own rounding is no larger than these, the keys' is the one that
+// shows: over few keys the errors of their products do not average out. Rows that see at most
+// kFewKeys of them therefore take the keys in two fp16 parts, about 22 bits (few_keys). The error
+// is then at most 1.4 times that of binary32 arithmetic with the result rounded, where it was
+// 1.8 over 20 keys, 1.65 over 100, 1.4 over 330 and 1.3 over 658. It costs 658 tokens 24.0 -> 25.2 us; two parts
+// everywhere would cost a third (4096 tokens 177 -> 229, 64 single tokens over up to 8192 104 -> 156).
+//
 // With x the product and c the scale in log2 units, p = 2^(x*c - b): one FMA and one
 // exponential.  b is an integer, so that a raised b rescales O by an exact power
 // of two; it is raised only when some product passes it by more than kLift, to
@@ -43,6 +50,23 @@ __device__ __forceinline__ u32x4 key_values(uint32_t w, float f, float b)
     const uint32_t h = w >> 8;
     return u32x4{dq_pair<DT_F16>(w & 0x000F000Fu, f, b), dq_pair<DT_F16>(w & 0x00F000F0u, f16, b),
                  dq_pair<DT_F16>(h & 0x000F000Fu, f, b), dq_pair<DT_F16>(h & 0x00F000F0u, f16, b)};
+}
+
+// What key_values' roundings left off, rounded in turn.
+__device__ __forceinline__ uint32_t rest_pair(uint32_t t, float f, float b, uint32_t rounded)
+{
+    const f16x2 c = __builtin_bit_cast(f16x2, t), v = __builtin_bit_cast(f16x2, rounded);
+    const float x = __builtin_fmaf((float)c.x, f, b), y = __builtin_fmaf((float)c.y, f, b);
+    const f16x2 r = {(_Float16)__builtin_fmaf((float)v.x, -1.0f, x), (_Float16)__builtin_fmaf((float)v.y, -1.0f, y)};
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ u32x4 key_rests(uint32_t w, float f, float b, u32x4 v)
+{
+    const float f16 = f * 0.0625f;
+    const uint32_t h = w >> 8;
+    return u32x4{rest_pair(w & 0x000F000Fu, f, b, v.x), rest_pair(w & 0x00F000F0u, f16, b, v.y),
+                 rest_pair(h & 0x000F000Fu, f, b, v.z), rest_pair(h & 0x00F000F0u, f16, b, v.w)};
 }
 
 // Two codes of two tokens.
@@ -192,6 +216,14 @@ __device__ __forceinline__ int only_part(Range keys, int splits, int chunk)
     return first == min((keys.hi - 1) / chunk, splits - 1) ? first : -1;
 }
 
+// Whether rows that see these keys take them in two parts.
+constexpr int kFewKeys = 512;
+template <int DT>
+__device__ __forceinline__ bool few_keys(Range keys)
+{
+    return DT == DT_F16 && keys.hi - keys.lo <= kFewKeys;
+}
+
 __device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0, int rows)
 {
     const int cap = a.v.width << a.v.page_shift;
@@ -261,6 +293,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
     if ((a.v.offs && all > a.few_rows) || row0 >= all) return;
     const int rows = min(all - row0, 16 * RB);
     const Range keys = seen(a, q, row0, rows);
+    const bool rests = few_keys<DT>(keys);
     const int only = only_part(keys, a.few_splits, a.few_chunk);
     if (only >= 0 && only != z) return;
     const int from = max(keys.lo & ~(kStep - 1), z * a.few_chunk), to = z + 1 < a.few_splits ? min(keys.hi, (z + 1) * a.few_chunk) : keys.hi;
@@ -309,6 +342,10 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
                 const u32x4 kv = key_values(r.k[i][j], f, bm);
 #pragma unroll
                 for (int rb = 0; rb < RB; rb++) x[rb][i] = mma<DT_F16>(kv, qf[rb][j], x[rb][i]);
+                if (!rests) continue;
+                const u32x4 kr = key_rests(r.k[i][j], f, bm, kv);
+#pragma unroll
+                for (int rb = 0; rb < RB; rb++) x[rb][i] = mma<DT_F16>(kr, qf[rb][j], x[rb][i]);
             }
         }
         const bool there[2] = {names_page(a.v, r.entry[0], t), names_page(a.v, r.entry[1], t + 16)}, whole = there[0] && there[1];
@@ -472,16 +509,19 @@ struct ManyTile {
 };
 
 // i: which 16 tokens of the tile, from place `at` on; len: the sequence's, or 0 where
-// the table names no page.
+// the table names no page; rests: where the keys' second parts go, or null.
 template <int D, int PARTS>
-__device__ __forceinline__ void many_store(ManyTile<D> &t, const ManyRaw<D, PARTS> &r, int i, int part, int at, int len, int lane)
+__device__ __forceinline__ void many_store(ManyTile<D> &t, ManyTile<D> *rests, const ManyRaw<D, PARTS> &r, int i, int part, int at, int len, int lane)
 {
     constexpr int N = ManyRaw<D, PARTS>::N;
     const int n = lane & 15, g = lane >> 4;
     const float f = head_scale(r.kh), b = head_min(r.kh);
 #pragma unroll
-    for (int j = 0; j < N; j++)
-        *(u32x4 *)&t.k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = key_values(r.k[j], f, b);
+    for (int j = 0; j < N; j++) {
+        const u32x4 v = key_values(r.k[j], f, b);
+        *(u32x4 *)&t.k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = v;
+        if (rests) *(u32x4 *)&rests->k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = key_rests(r.k[j], f, b, v);
+    }
     const QuadHead q = quad_head(live_heads(r.vh, at + 4 * g, len));
 #pragma unroll
     for (int j = 0; j < N; j++)
@@ -511,6 +551,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
     if (tile < 0 || row0 >= all || all <= a.few_rows) return;
     const int rows = min(all - row0, a.tile_tokens * a.group);
     const Range keys = seen(a, q, row0, rows);
+    const bool rests = few_keys<DT>(keys);  // then one tile at a time, its second parts in the other's place
     const int only = only_part(keys, a.many_splits, a.many_chunk);
     if (only >= 0 && only != z) return;
     const int from = max(keys.lo, z * a.many_chunk), to = z + 1 < a.many_splits ? min(keys.hi, (z + 1) * a.many_chunk) : keys.hi;
@@ -531,7 +572,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
         many_load<D, PARTS>(a, entry, h, place_in(kt), wave >> 2, lane, to_raw);
     };
     auto store = [&](int kt, const ManyRaw<D, PARTS> &of_raw) {
-        many_store<D, PARTS>(s_tile[(kt - kt0) & 1], of_raw, wave & 3, wave >> 2, place_in(kt),
+        many_store<D, PARTS>(s_tile[rests ? 0 : (kt - kt0) & 1], rests ? &s_tile[1] : nullptr, of_raw, wave & 3, wave >> 2, place_in(kt),
                              names_page(a.v, of_raw.entry, place_in(kt)) ? q.len : 0, lane);
     };
     ManyRaw<D, PARTS> raw, later;  // the next tile's bytes, and those of the one after it
@@ -562,7 +603,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
     for (int kt = kt0; kt < kt1; kt++) {
         __syncthreads();  // this tile is whole, and the other buffer's readers are done
         const int k0 = kt * kKeys;
-        const ManyTile<D> &t = s_tile[(kt - kt0) & 1];
+        const ManyTile<D> &t = s_tile[rests ? 0 : (kt - kt0) & 1];
         if (kt >= mt0 && kt < mt1) {
             f32x16 x[HALVES];
 #pragma unroll
@@ -571,6 +612,9 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
                 for (int j = 0; j < 16; j++) x[i][j] = 0.0f;
 #pragma unroll
                 for (int p = 0; p < P; p++) x[i] = mma32<DT_F16>(*(const u32x4 *)&t.k[half + i][2 * p + g][n], qf[p], x[i]);
+                if (!rests) continue;
+#pragma unroll
+                for (int p = 0; p < P; p++) x[i] = mma32<DT_F16>(*(const u32x4 *)&s_tile[1].k[half + i][2 * p + g][n], qf[p], x[i]);
             }
             if (gaps || k0 + kKeys - 1 > clear_hi || k0 < clear_lo) {
 #pragma unroll
@@ -617,6 +661,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
                 for (int d = 0; d < B; d++) o[d] = mma32<DT_F16>(*(const u32x4 *)&t.v[2 * half + u][d][g][n][0], p, o[d]);
             }
         }
+        if (rests) __syncthreads();  // all have read this one
         store(kt + 1, raw);
         raw = later;
         load(kt + 3, ahead, later);

@@ -207,3 +207,21 @@ def test_cache_beyond_32_bit_offsets():
                     qg.kv_attention(q[:2], c, t, ln, kv)))
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert_within(got[0][1], R.held64(v), R.store_err(R.held64(v), 0.0 * R.held64(v), torch.float32), "values")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 40])
+def test_few_keys_keep_fp16_precision(D, new):
+    """Large queries at right angles to the differences of the keys: all weights alike, while one fp16
+    rounding of the keys would move the products by 12 times what the result's own rounding leaves.  What else is
+    rounded, values and weights, is off by at most the relative half step that the result's rounding has
+    at worst, twice the least that it has: the error is below sqrt(1 + 4 + 4) of the result's rounding."""
+    L, heads = 48, 4
+    b = Batch([new], [L], heads, 1, D, 32, F16, seed=61)
+    basis = torch.linalg.svd(b.k64[1:, 0] - b.k64[:1, 0])[2][L - 1:]
+    g = torch.Generator().manual_seed(62)
+    b.q = (12 * torch.randn((new, heads, len(basis)), generator=g, dtype=torch.float64) @ basis).to(F16).cuda()
+    y = b.run().double().cpu()
+    want, _ = R.attention64(b.q, b.k64, b.v64, [L - new + i for i in range(new)], D ** -0.5, 0, F16)
+    own = (want.to(F16).double() - want).norm()
+    assert (y - want).norm() < 3 * own

@@ -13,14 +13,14 @@
 // Operands are fp16 for both activation types.  Queries in bfloat16 are scaled
 // by a power of two per row, which fp16 then holds exactly but for elements 2^-22
 // of the row's largest; keys and values are code*scale + minimum rounded once to
-// fp16 (v_fma_mix, as the weights of the fp16 GEMMs), probabilities likewise.
+// fp16, probabilities likewise.
 // Products, maxima, sums and O are binary32.
 //
 // Of an fp16 result, whose own rounding is no larger than these, the keys' is the one that
 // shows: over few keys the errors of their products do not average out. Rows that see at most
 // kFewKeys of them therefore take the keys in two fp16 parts, about 22 bits (few_keys). The error
 // is then at most 1.4 times that of binary32 arithmetic with the result rounded, where it was
-// 1.8 over 20 keys, 1.65 over 100, 1.4 over 330 and 1.3 over 658. It costs 658 tokens 24.0 -> 25.2 us; two parts
+// 1.8 over 20 keys, 1.65 over 100, 1.4 over 330 and 1.3 over 658. It costs 658 tokens 5%; two parts
 // everywhere would cost a third (4096 tokens 177 -> 229, 64 single tokens over up to 8192 104 -> 156).
 //
 // With x the product and c the scale in log2 units, p = 2^(x*c - b): one FMA and one
@@ -43,64 +43,88 @@ struct Words {
     typedef uint32_t W __attribute__((ext_vector_type(D / 32)));  // a lane's codes of 16 tokens
 };
 
-// Eight codes of one key -> eight fp16 values; f is scale*2^24, b the minimum.
-__device__ __forceinline__ u32x4 key_values(uint32_t w, float f, float b)
+// Two codes of a word, exactly: or'ed into the low bits of 1024 (four bits up, of 64), where a step is
+// one, and the 1024 taken off.
+template <uint32_t MASK, uint32_t BIAS>
+__device__ __forceinline__ f16x2 biased_codes(uint32_t w)
 {
-    const float f16 = f * 0.0625f;
-    const uint32_t h = w >> 8;
-    return u32x4{dq_pair<DT_F16>(w & 0x000F000Fu, f, b), dq_pair<DT_F16>(w & 0x00F000F0u, f16, b),
-                 dq_pair<DT_F16>(h & 0x000F000Fu, f, b), dq_pair<DT_F16>(h & 0x00F000F0u, f16, b)};
+    uint32_t mask = MASK, bias = BIAS;
+    asm("" : "+s"(mask));  // constants in registers, for one v_and_or_b32, which takes no literals
+    asm("" : "+v"(bias));
+    return __builtin_bit_cast(f16x2, (w & mask) | bias) - __builtin_bit_cast(f16x2, BIAS);
+}
+
+__device__ __forceinline__ f16x2 low_codes(uint32_t w) { return biased_codes<0x000F000Fu, 0x64006400u>(w); }
+__device__ __forceinline__ f16x2 high_codes(uint32_t w) { return biased_codes<0x00F000F0u, 0x54005400u>(w); }
+
+// code * scale + minimum, all fp16, with one rounding: a packed FMA. (v_fma_mix, which the GEMMs' products of a
+// code and a binary32 factor need, takes two issue slots for each value.)
+__device__ __forceinline__ uint32_t values(f16x2 code, f16x2 scale, f16x2 min)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(code, scale, min));
+}
+
+// A key's header, both fields twice.
+struct KeyHead {
+    f16x2 s, m;
+};
+
+__device__ __forceinline__ KeyHead key_head(uint32_t h)
+{
+    return KeyHead{__builtin_bit_cast(f16x2, __builtin_amdgcn_perm(h, h, 0x01000100u)),
+                   __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(h, h, 0x03020302u))};
+}
+
+// Eight codes of one key -> eight fp16 values.
+struct Codes {
+    f16x2 c[4];
+};
+
+__device__ __forceinline__ Codes codes_of(uint32_t w)
+{
+    return Codes{{low_codes(w), high_codes(w), low_codes(w >> 8), high_codes(w >> 8)}};
+}
+
+__device__ __forceinline__ u32x4 key_values(const Codes &c, const KeyHead &k)
+{
+    return u32x4{values(c.c[0], k.s, k.m), values(c.c[1], k.s, k.m), values(c.c[2], k.s, k.m), values(c.c[3], k.s, k.m)};
 }
 
 // What key_values' roundings left off, rounded in turn.
-__device__ __forceinline__ uint32_t rest_pair(uint32_t t, float f, float b, uint32_t rounded)
+__device__ __forceinline__ u32x4 key_rests(const Codes &c, const KeyHead &k, u32x4 v)
 {
-    const f16x2 c = __builtin_bit_cast(f16x2, t), v = __builtin_bit_cast(f16x2, rounded);
-    const float x = __builtin_fmaf((float)c.x, f, b), y = __builtin_fmaf((float)c.y, f, b);
-    const f16x2 r = {(_Float16)__builtin_fmaf((float)v.x, -1.0f, x), (_Float16)__builtin_fmaf((float)v.y, -1.0f, y)};
-    return __builtin_bit_cast(uint32_t, r);
+    const float s = (float)k.s.x, m = (float)k.m.x;
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t rounded = v[i];  // by value: of a vector's element, the cast would read the first
+        const f16x2 h = __builtin_bit_cast(f16x2, rounded);
+        r[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)__builtin_fmaf((float)h.x, -1.0f, __builtin_fmaf((float)c.c[i].x, s, m)),
+                                                  (_Float16)__builtin_fmaf((float)h.y, -1.0f, __builtin_fmaf((float)c.c[i].y, s, m))});
+    }
+    return r;
 }
 
-__device__ __forceinline__ u32x4 key_rests(uint32_t w, float f, float b, u32x4 v)
-{
-    const float f16 = f * 0.0625f;
-    const uint32_t h = w >> 8;
-    return u32x4{rest_pair(w & 0x000F000Fu, f, b, v.x), rest_pair(w & 0x00F000F0u, f16, b, v.y),
-                 rest_pair(h & 0x000F000Fu, f, b, v.z), rest_pair(h & 0x00F000F0u, f16, b, v.w)};
-}
-
-// Two codes of two tokens.
-__device__ __forceinline__ uint32_t two_values(uint32_t t, float f0, float b0, float f1, float b1)
-{
-    const f16x2 h = __builtin_bit_cast(f16x2, t);
-    const f16x2 r = {(_Float16)__builtin_fmaf((float)h.x, f0, b0), (_Float16)__builtin_fmaf((float)h.y, f1, b1)};
-    return __builtin_bit_cast(uint32_t, r);
-}
-
-__device__ __forceinline__ float head_scale(uint32_t h) { return f16_to_f32(h & 0xFFFFu) * kTwo24; }
-__device__ __forceinline__ float head_min(uint32_t h) { return f16_to_f32(h >> 16); }
-
-// A quad's values: word w of a lane, dims 2w and 2w+1 of four tokens, as two dims
-// of two fp16 pairs.
+// A quad's headers, tokens 0 and 1, then 2 and 3; word w of a lane, dims 2w and 2w+1 of its four
+// tokens, as two dims of two fp16 pairs.
 struct QuadHead {
-    float f[4], b[4];  // tokens 2 and 3 with their codes four bits up
+    f16x2 s[2], m[2];
 };
 
 __device__ __forceinline__ QuadHead quad_head(u32x4 h)
 {
     QuadHead q;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        q.f[i] = head_scale(h[i]) * (i < 2 ? 1.0f : 0.0625f);
-        q.b[i] = head_min(h[i]);
+    for (int i = 0; i < 2; i++) {
+        q.s[i] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(h[2 * i + 1], h[2 * i], 0x05040100u));
+        q.m[i] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(h[2 * i + 1], h[2 * i], 0x07060302u));
     }
     return q;
 }
 
 __device__ __forceinline__ u32x2 quad_values(uint32_t w, const QuadHead &q)
 {
-    return u32x2{two_values(w & 0x000F000Fu, q.f[0], q.b[0], q.f[1], q.b[1]),
-                 two_values(w & 0x00F000F0u, q.f[2], q.b[2], q.f[3], q.b[3])};
+    return u32x2{values(low_codes(w), q.s[0], q.m[0]), values(high_codes(w), q.s[1], q.m[1])};
 }
 
 // Headers of tokens that the sequence does not have are cleared: their
@@ -238,11 +262,13 @@ __device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0,
 // MFMA registers, and add their results through LDS.
 //
 // Bound by the cache's bytes where it is long: 64 sequences of up to 8192 tokens,
-// 432 MB of codes and headers, take 101 us with the join, 4.3 TB/s.  The 16x16x32
+// 432 MB of codes and headers, take 94 us with the join, 4.6 TB/s, where four instructions for two codes
+// (and the arithmetic beside them) still fill half of the time.  The 16x16x32
 // product leaves the fewest rows idle; 64 keys in flight a wave (two steps' registers in turn)
-// and three workgroups a CU cover the loads, where a fourth would spill (149 us).  Short ones are a
+// and three workgroups a CU cover the loads: a third step in flight gained nothing, a fourth workgroup would
+// spill (149 us).  Short ones are a
 // chain of dependent loads (lengths, table, cache), a merge and a second launch to
-// join: one sequence of 658 tokens 8.3 us, of 300 in one part 7.1 us.
+// join: one sequence of 658 tokens 8.3 us, of 300 in one part 6.5 us.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 4;
 constexpr int kStep = 32;
@@ -334,16 +360,17 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
         f32x4 x[RB][2];
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const float f = head_scale(r.kh[i]), bm = head_min(r.kh[i]);
+            const KeyHead head = key_head(r.kh[i]);
 #pragma unroll
             for (int rb = 0; rb < RB; rb++) x[rb][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < J; j++) {
-                const u32x4 kv = key_values(r.k[i][j], f, bm);
+                const Codes codes = codes_of(r.k[i][j]);
+                const u32x4 kv = key_values(codes, head);
 #pragma unroll
                 for (int rb = 0; rb < RB; rb++) x[rb][i] = mma<DT_F16>(kv, qf[rb][j], x[rb][i]);
                 if (!rests) continue;
-                const u32x4 kr = key_rests(r.k[i][j], f, bm, kv);
+                const u32x4 kr = key_rests(codes, head, kv);
 #pragma unroll
                 for (int rb = 0; rb < RB; rb++) x[rb][i] = mma<DT_F16>(kr, qf[rb][j], x[rb][i]);
             }
@@ -515,12 +542,13 @@ __device__ __forceinline__ void many_store(ManyTile<D> &t, ManyTile<D> *rests, c
 {
     constexpr int N = ManyRaw<D, PARTS>::N;
     const int n = lane & 15, g = lane >> 4;
-    const float f = head_scale(r.kh), b = head_min(r.kh);
+    const KeyHead head = key_head(r.kh);
 #pragma unroll
     for (int j = 0; j < N; j++) {
-        const u32x4 v = key_values(r.k[j], f, b);
+        const Codes codes = codes_of(r.k[j]);
+        const u32x4 v = key_values(codes, head);
         *(u32x4 *)&t.k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = v;
-        if (rests) *(u32x4 *)&rests->k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = key_rests(r.k[j], f, b, v);
+        if (rests) *(u32x4 *)&rests->k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = key_rests(codes, head, v);
     }
     const QuadHead q = quad_head(live_heads(r.vh, at + 4 * g, len));
 #pragma unroll

@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
 // unpacked once into LDS, in fragment order, for all its waves.
 //
 // Bound by the exponentials and the unpacking beside the products, and by the power
-// limit: 4096 tokens of 32 query heads of 128 (137 GFLOP under the mask) take 165 us, 0.83
+// limit: 4096 tokens of 32 query heads of 128 (137 GFLOP under the mask) take 160 us, 0.86
 // PFLOP/s, where the matrix units alone, on random operands, sustain 1.35.  The 32x32x16
 // product reads the fewest LDS bytes a flop; a 64-key tile takes a CU's 8 waves 4160 cycles,
 // half of them products.  Eight waves share a tile's unpacking (189 us with four) where that
@@ -559,7 +559,8 @@ __device__ __forceinline__ void many_store(ManyTile<D> &t, ManyTile<D> *rests, c
 }
 
 // While a tile is multiplied, the next one is unpacked into the other LDS buffer
-// and the two after it are on their way from memory; one barrier per tile.
+// and the two after it are on their way from memory; one barrier per tile (two where the
+// keys have second parts).
 // KS = 2: two waves share 32 rows, each with half of every tile's keys, and are joined at the end.
 template <int DT, int D, int NW, int KS>
 __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_eu(2, 2))) k_attn_many(AttnArgs a)
@@ -605,6 +606,16 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
     };
     ManyRaw<D, PARTS> raw, later;  // the next tile's bytes, and those of the one after it
     int ahead = 0;                 // the table's entry for the one after that
+    auto next = [&](int kt) {
+        store(kt + 1, raw);
+        raw = later;
+        load(kt + 3, ahead, later);
+        ahead = entry_of(a.v, s, place_in(kt + 4));
+    };
+    // The next tile is unpacked between this one's products, beside the first ones, by waves that have the keys to
+    // themselves (2048 tokens behind 6000 284 -> 276 us); by those that halve them, after (658 tokens of 64 dims 16.1, else
+    // 16.9).
+    const bool early = KS == 1 && !rests;
     u32x4 qf[P];
     float c = 0.0f, b = -INFINITY, l = 0.0f;
     bool gaps = false, huge = false;  // gaps: pages that the table does not name, looked for once
@@ -644,6 +655,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
 #pragma unroll
                 for (int p = 0; p < P; p++) x[i] = mma32<DT_F16>(*(const u32x4 *)&s_tile[1].k[half + i][2 * p + g][n], qf[p], x[i]);
             }
+            if (early) next(kt);
             if (gaps || k0 + kKeys - 1 > clear_hi || k0 < clear_lo) {
 #pragma unroll
                 for (int u = 0; u < 2 * HALVES; u++) {
@@ -689,11 +701,10 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
                 for (int d = 0; d < B; d++) o[d] = mma32<DT_F16>(*(const u32x4 *)&t.v[2 * half + u][d][g][n][0], p, o[d]);
             }
         }
-        if (rests) __syncthreads();  // all have read this one
-        store(kt + 1, raw);
-        raw = later;
-        load(kt + 3, ahead, later);
-        ahead = entry_of(a.v, s, place_in(kt + 4));
+        if (!early || !(kt >= mt0 && kt < mt1)) {
+            if (rests) __syncthreads();  // all have read this one
+            next(kt);
+        }
     }
     l += __shfl_xor(l, 32, 64);
     if constexpr (KS == 2) {  // through the LDS of the tiles

@@ -49,7 +49,7 @@ struct KvView {
 
 // A sequence's rows [row, row + n) and the place of the first of them.  Any
 // contents of offs and lens give rows inside [0, T); places outside the
-// table are for page_of and the callers' range checks.
+// table are for tile_of and the callers' range checks.
 struct Seq {
     int row, n, first, len;
 };

@@ -310,7 +310,7 @@ __device__ __forceinline__ uint32_t quantize(F (&x)[E], uint32_t (&code)[E])
     return (uint32_t)__builtin_bit_cast(uint16_t, s) | ((uint32_t)__builtin_bit_cast(uint16_t, m) << 16);
 }
 
-// Row t's sequence and place, for LANES lanes of equal t; place -1 for a row of no
+// Row t's sequence and place, for LANES lanes of equal t; INT_MIN for a row of no
 // sequence.
 template <int LANES>
 __device__ __forceinline__ int place_of(const KvView &v, int t, int &s)
@@ -404,8 +404,8 @@ __device__ __forceinline__ void append_values(const AppendArgs &a, int slot, int
 // Workgroups of values (quads, the longest chains, first), of keys and of queries.  Bound by the
 // 64-bit arithmetic of the codes, about 30 instructions a dim, next to the loads: 4096 tokens of
 // 32 query and 8 key heads of 128 take 24 us (89 MB, 3.7 TB/s), 8192 of 8 key heads of 64
-// 13 us; one token takes 3.4 us, a chain of look-up, load and reduction.  A lane of 8 dims
-// in place of 4 for heads of 64 took the 8192 tokens from 14.5 us to 13.
+// 14 us; one token takes 3.4 us, a chain of look-up, load and reduction.  A lane of 8 dims
+// in place of 4 for heads of 64 took the 8192 tokens from 15.5 us to 14.
 template <int DT, int D, int HC>
 __global__ void __launch_bounds__(256) k_kv_append(AppendArgs a)
 {

@@ -188,7 +188,7 @@ struct AttnArgs {
 // The parts of a call's workspace and its launches (kv_attention.hip).
 struct AttnPlan {
     bool few, many, many_halves;  // halves: two waves to 32 rows, each with half of the keys
-    int few_rows, few_tiles, few_rb;
+    int few_rows, few_tiles, few_rb, few_waves;
     int few_splits, few_chunk, many_splits, many_chunk, tile_tokens, many_waves;
     long long slots, few_entries, many_entries;  // entries: rows * heads * splits kept
     size_t bytes;

@@ -258,7 +258,7 @@ __device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0,
 // ---------------------------------------------------------------------------
 // A few rows of each sequence (single tokens): a stream of the cache.  A
 // workgroup takes one key head of one sequence, 16*RB rows and a chunk of the
-// keys; its four waves take steps of 32 keys in turn, straight from memory into
+// keys; its four or eight waves take steps of 32 keys in turn, straight from memory into
 // MFMA registers, and add their results through LDS.
 //
 // Bound by the cache's bytes where it is long: 64 sequences of up to 8192 tokens,
@@ -268,9 +268,8 @@ __device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0,
 // and three workgroups a CU cover the loads: a third step in flight gained nothing, a fourth workgroup would
 // spill (149 us).  Short ones are a
 // chain of dependent loads (lengths, table, cache), a merge and a second launch to
-// join: one sequence of 658 tokens 8.3 us, of 300 in one part 6.5 us.
+// join: one sequence of 658 tokens 8.3 us, of 500 in one part 7.1 us.
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 4;
 constexpr int kStep = 32;
 
 template <int D>
@@ -304,13 +303,13 @@ __device__ __forceinline__ void few_load(const AttnArgs &a, const int (&entry)[2
     }
 }
 
-template <int DT, int D, int RB>
-__global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(RB == 2 ? 2 : D == 64 ? 4 : 3))) k_attn_few(AttnArgs a)
+template <int DT, int D, int RB, int NW>
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW == 8 || RB == 2 ? 2 : D == 64 ? 4 : 3))) k_attn_few(AttnArgs a)
 {
     using L = KvLay<D>;
     constexpr int E = L::E, J = D / 32, LD = D + 4;
-    __shared__ __align__(16) float s_o[kFewWaves][16][LD];
-    __shared__ float s_b[kFewWaves][16], s_l[kFewWaves][16];
+    __shared__ __align__(16) float s_o[NW][16][LD];
+    __shared__ float s_b[NW][16], s_l[NW][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int rt = blockIdx.x % a.few_tiles, sh = blockIdx.x / a.few_tiles, h = sh % a.v.H, s = sh / a.v.H, z = blockIdx.y;
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
     if (only >= 0 && only != z) return;
     const int from = max(keys.lo & ~(kStep - 1), z * a.few_chunk), to = z + 1 < a.few_splits ? min(keys.hi, (z + 1) * a.few_chunk) : keys.hi;
 
-    const int stride = kStep * kFewWaves, window = a.window ? a.window : INT_MAX;
+    const int stride = kStep * NW, window = a.window ? a.window : INT_MAX;
     const int pmin = q.first + row0 / a.group, pmax_lo = a.window ? q.first + (row0 + rows - 1) / a.group - a.window + 1 : 0;
     int t = from + wave * kStep, ahead[2];
     FewRaw<D> even, odd;  // this step's bytes and the next one's
@@ -456,14 +455,14 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
         }
         __syncthreads();
         const int rr = threadIdx.x >> 4, dl = threadIdx.x & 15, r = 16 * rb + rr;
-        if (r >= rows) continue;
+        if (rr >= 16 || r >= rows) continue;
         float top = s_b[0][rr], sum = 0.0f, y[E];
 #pragma unroll
-        for (int w = 1; w < kFewWaves; w++) top = fmaxf(top, s_b[w][rr]);
+        for (int w = 1; w < NW; w++) top = fmaxf(top, s_b[w][rr]);
 #pragma unroll
         for (int e = 0; e < E; e++) y[e] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFewWaves; w++) {
+        for (int w = 0; w < NW; w++) {
             const float f = rescale_of(s_b[w][rr], top);
             sum += s_l[w][rr] * f;
 #pragma unroll
@@ -819,11 +818,11 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a)
 
 long long ceil_of(long long a, long long b) { return (a + b - 1) / b; }
 
-template <int DT, int D, int RB>
+template <int DT, int D, int RB, int NW>
 void run_few(const AttnArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_attn_few<DT, D, RB>), dim3((unsigned)(a.v.S * a.v.H * a.few_tiles), (unsigned)a.few_splits),
-                       dim3(64 * kFewWaves), 0, s, a);
+    hipLaunchKernelGGL((k_attn_few<DT, D, RB, NW>), dim3((unsigned)(a.v.S * a.v.H * a.few_tiles), (unsigned)a.few_splits),
+                       dim3(64 * NW), 0, s, a);
 }
 
 template <int DT, int D, int NW, int KS>
@@ -837,8 +836,9 @@ template <int DT, int D>
 hipError_t run_attention(const AttnPlan &pl, const AttnArgs &a, hipStream_t s)
 {
     if (pl.few) {
-        if (pl.few_rb == 1) run_few<DT, D, 1>(a, s);
-        else run_few<DT, D, 2>(a, s);
+        if (pl.few_rb == 2) run_few<DT, D, 2, 4>(a, s);
+        else if (pl.few_waves == 8) run_few<DT, D, 1, 8>(a, s);
+        else run_few<DT, D, 1, 4>(a, s);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -873,11 +873,19 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     p.few_tiles = (int)ceil_of(p.few_rows > 0 ? p.few_rows : 1, 16 * p.few_rb);
     if (max_len < 1) max_len = 1;
     // chunks of whole steps for every wave; as many workgroups as the CUs hold at once: three or four
-    const long long step = kStep * kFewWaves, units = S * kv_heads * p.few_tiles;
+    const long long step = kStep * 4, units = S * kv_heads * p.few_tiles;
     long long chunk = ceil_of(ceil_of(units * max_len, D == 64 ? 1024 : 768), step) * step;
-    // one part up to 384 keys (one sequence of 300: 7.1 us against 8.8 in three parts), parts of 128 up to 4096 (of 2000: 8.6
-    // against 9.7 in parts of 256) and of 256 at least from there on (of 8192: 11.5 against 13.5)
-    const long long least_few = max_len <= 384 ? 384 : max_len <= 4096 ? step : 256;
+    // One part where a second launch costs more than it gains.  Of eight waves up to 1024 keys, while a workgroup (or, with
+    // heads of 64, two) to a CU holds them: always up to 512 (768), above where parts would be more workgroups than
+    // CUs.  In us, 32 query and 8 key heads of 128, parts and one part: one sequence of 500 9.3 and 7.1, of 658 8.3 and
+    // 8.6, 8 of 658 9.8 and 8.6, 16 of 1000 13.0 and 10.8, 4 of 1000 8.6 and 9.9, 64 of 1000 19.7 and 20.6.  Of four
+    // waves up to 384 keys else: one of 200 5.5 (eight waves 5.7), 128 of 300 15.7 (21.8).
+    const bool one = p.few_rb == 1 && max_len > 256 && max_len <= 1024 && units <= (D == 64 ? 512 : 256) &&
+                     (max_len <= (D == 64 ? 768 : 512) || units * ceil_of(max_len, step) > 256);
+    p.few_waves = one ? 8 : 4;
+    // Parts of 128 up to 4096 keys (one sequence of 2000: 8.6, and 9.7 in parts of 256) and of 256 at least from
+    // there on (of 8192: 13.5 and 11.5).
+    const long long least_few = one ? 1024 : max_len <= 384 ? 384 : max_len <= 4096 ? step : 256;
     if (chunk < least_few) chunk = least_few;
     if (ceil_of(max_len, chunk) > 128) chunk = ceil_of(ceil_of(max_len, 128), step) * step;
     p.few_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);

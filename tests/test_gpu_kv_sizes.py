@@ -225,3 +225,17 @@ def test_few_keys_keep_fp16_precision(D, new):
     want, _ = R.attention64(b.q, b.k64, b.v64, [L - new + i for i in range(new)], D ** -0.5, 0, F16)
     own = (want.to(F16).double() - want).norm()
     assert (y - want).norm() < 3 * own
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, F16), (128, BF16)])
+@pytest.mark.parametrize("heads", [4, 16])
+def test_decode_in_one_part(D, dtype, heads):
+    """Enough sequences that lengths up to 1024 stay in one part, of eight waves; few that do up to 512."""
+    lens = [1000, 1, 500, 777, 33, 257, 0, 999, 640, 255]
+    b = Batch([1] * len(lens), lens, heads, 4, D, 16, dtype, seed=71)
+    assert qg.kv_attention_workspace_bytes(10, 10, heads, 4, D, 1008, False) == 0
+    b.check(b.run())
+    b.check(b.run(window=300), window=300)
+    few = Batch([1, 1], [511, 300], heads, 4, D, 256, dtype, seed=72)
+    assert qg.kv_attention_workspace_bytes(2, 2, heads, 4, D, 512, False) == 0
+    few.check(few.run())

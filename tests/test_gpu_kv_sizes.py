@@ -239,3 +239,16 @@ def test_decode_in_one_part(D, dtype, heads):
     few = Batch([1, 1], [511, 300], heads, 4, D, 256, dtype, seed=72)
     assert qg.kv_attention_workspace_bytes(2, 2, heads, 4, D, 512, False) == 0
     few.check(few.run())
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 3]])
+@pytest.mark.parametrize("ks,vs", [(1e-5, 1e-6), (1.0, 3e-5), (200.0, 5000.0)])
+def test_small_and_large_cache_values(new, ks, vs):
+    """Scales and minima that are subnormal in fp16, and values near the largest that the cache holds."""
+    b = Batch(new, [130, 60], 4, 2, 64, 16, BF16, seed=73)
+    b.k, b.v = (b.k.float() * ks).to(BF16), (b.v.float() * vs).to(BF16)
+    qg.kv_append(b.pool.cache, b.k, b.v, b.pool.tables, i32(b.lens), offsets=i32(b.start))
+    b.k64, b.v64 = R.held64(b.k), R.held64(b.v)
+    y = b.run()
+    assert y.abs().max() > vs * 0.05
+    b.check(y)

@@ -252,3 +252,14 @@ def test_small_and_large_cache_values(new, ks, vs):
     y = b.run()
     assert y.abs().max() > vs * 0.05
     b.check(y)
+
+
+@pytest.mark.parametrize("new", [[5, 8, 6], [1, 8, 1, 1, 0, 5], [1] * 6, [8] * 4])
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+def test_a_few_tokens_of_each_sequence(new, D, dtype):
+    """Up to 32 rows of a key head in one block of rows or two."""
+    lens = [2000, 8, 700, 90, 33, 1500][:len(new)]
+    b = Batch(new, lens, 8, 2, D, 32, dtype, seed=75)
+    b.offsets = i32(np.cumsum([0] + new).tolist())
+    b.check(b.run())
+    b.check(b.run(window=64, max_len=2000), window=64)

@@ -892,7 +892,7 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     // there on (of 8192: 13.5 and 11.5).
     const long long least_few = one ? 1024 : max_len <= 384 ? 384 : max_len <= 4096 ? step : 256;
     if (chunk < least_few) chunk = least_few;
-    if (ceil_of(max_len, chunk) > 128) chunk = ceil_of(ceil_of(max_len, 128), step) * step;
+    if (ceil_of(max_len, chunk) > 128) chunk = ceil_of(ceil_of(max_len, 128), step) * step;  // what the workspace holds
     p.few_chunk = (int)(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
     p.few_splits = (int)ceil_of(max_len, p.few_chunk);
     p.few_entries = p.few && p.few_splits > 1 ? S * kv_heads * (long long)p.few_rows * p.few_splits : 0;

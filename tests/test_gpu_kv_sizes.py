@@ -263,3 +263,16 @@ def test_a_few_tokens_of_each_sequence(new, D, dtype):
     b.offsets = i32(np.cumsum([0] + new).tolist())
     b.check(b.run())
     b.check(b.run(window=64, max_len=2000), window=64)
+
+
+@pytest.mark.parametrize("heads", [4, 16])
+def test_offsets_of_any_contents(heads):
+    """Offsets that are none give rows inside the batch or none at all; rows of no sequence stay as they were."""
+    b = Batch([20, 20], [600, 40], heads, 2, 128, 32, BF16, seed=77)
+    args = (b.pool.cache, b.pool.tables, i32(b.lens), 2)
+    for offsets, outside in (([5, 5, 5], range(40)), ([2 ** 31 - 1, 40, -7], range(40)), ([0, -2 ** 31, 3], range(3, 40)),
+                             ([30, 3, 40], range(3)), ([-7, 2 ** 31 - 1, -2 ** 31], ())):
+        out = torch.full_like(b.q, 9.0)
+        qg.kv_attention(b.q, *args, offsets=i32(offsets), out=out)
+        assert (out[list(outside)] == 9).all(), offsets
+    b.check(b.run())

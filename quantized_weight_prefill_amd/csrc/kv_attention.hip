@@ -592,7 +592,10 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
     // tiles in which some row of the wave sees a key, and keys that all its rows see
     const Range mine = w0 < rows ? seen(a, q, row0 + w0, min(rows - w0, 32)) : Range{0, 0};
     const int mt0 = mine.lo / kKeys, mt1 = (mine.hi + kKeys - 1) / kKeys;
-    const int clear_hi = q.first + (row0 + w0) / a.group;
+    // places from `cap` on lie behind the table, also those of a last tile that it ends inside of (capacities that are
+    // no multiple of 64), whatever the length
+    const int cap = a.v.width << a.v.page_shift, last = min(place, cap - 1);
+    const int clear_hi = min(q.first + (row0 + w0) / a.group, cap - 1);
     const int clear_lo = a.window ? q.first + (row0 + min(rows, w0 + 32) - 1) / a.group - a.window + 1 : 0;
 
     // this wave's 16 tokens of a tile; past the last tile, of the last once more
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
                                       (h * a.group + r - token * a.group) * D + 8 * g,
                                   live, 16, a.scale, qf);
         for (int i = (kt0 * kKeys >> a.v.page_shift) + lane; i <= (to - 1) >> a.v.page_shift; i += 64)
-            gaps |= i >= a.v.width || (unsigned)a.v.tables[(long long)s * a.v.width + i] >= (unsigned)a.v.pages;
+            gaps |= (unsigned)a.v.tables[(long long)s * a.v.width + i] >= (unsigned)a.v.pages;
         load(kt0 + 1, e1, raw);
         load(kt0 + 2, e2, later);
         store(kt0, first);
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
                         const int at = k + 8 * (i >> 2) + 4 * g + (i & 3);
-                        const bool ok = there & (at <= place) & (at > place - window);
+                        const bool ok = there & (at <= last) & (at > place - window);
                         x[u >> 1][8 * (u & 1) + i] = ok ? x[u >> 1][8 * (u & 1) + i] : -INFINITY;
                     }
                 }

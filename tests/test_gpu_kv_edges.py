@@ -1,0 +1,49 @@
+"""Attention over the 4-bit cache, its append and their binding at the ends of tables, windows, batches and number
+ranges, against the 64-bit forms of tests/kv_ref.py."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import quantized_weight_prefill_amd as qg
+from tests import kv_ref as R
+from tests.test_gpu_kv import BF16, F16, Pool, assert_within, i32, randn, table
+from tests.test_gpu_kv_attention import Batch
+
+pytestmark = pytest.mark.gpu
+
+
+def check_behind_table(q, y, k64, v64, cap, length, window, dtype, rows, what):
+    """Rows of one sequence of `length` tokens, of which the table has places for `cap`."""
+    n = q.shape[0]
+    for i in rows:
+        p = length - n + i
+        lo = max(0, p - window + 1) if window else 0
+        if p < 0 or lo >= min(p + 1, cap):
+            assert (y[i] == 0).all(), f"{what} row {i}"
+            continue
+        want, err = R.attention64(q[i:i + 1], k64[:cap], v64[:cap], [p], q.shape[2] ** -0.5, window, dtype)
+        assert_within(y[i:i + 1], want, err, f"{what} row {i}")
+
+
+@pytest.mark.parametrize("page,width,n,heads,kv", [
+    (16, 5, 40, 8, 2), (32, 3, 40, 8, 2), (16, 3, 300, 4, 2), (32, 1, 40, 4, 1),  # four waves of 32 rows
+    (16, 21, 40, 8, 2), (32, 27, 300, 8, 2),                                      # two waves to 32 rows
+    (16, 189, 70, 8, 2),                                                          # and parts of the keys
+    (16, 45, 700, 96, 12),                                                        # eight waves
+    (16, 5, 6, 8, 2), (32, 3, 1, 8, 2),                                           # a few rows
+])
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+def test_lengths_past_the_table(page, width, n, heads, kv, D, dtype):
+    """Places behind the table are not seen, wherever a tile of keys ends; a single token of the same place agrees."""
+    cap = page * width
+    b = Batch([n], [cap], heads, kv, D, page, dtype, seed=81)
+    assert b.pool.tables.shape == (1, width)
+    b.q = randn((n, heads, D), 82, dtype, 1.5)
+    off = i32([0, n])
+    rows = sorted({0, 1, n // 3, n // 2, n - 2, n - 1} & set(range(n)))
+    for length in (cap - 1, cap, cap + 1, cap + 17, cap + n // 2, cap + n + 9, cap + 63, cap + 5000):
+        for window in (0, n + 30):
+            call = lambda q, o: qg.kv_attention(q, b.pool.cache, b.pool.tables, i32([length]), kv, offsets=o, window=window)
+            check_behind_table(b.q, call(b.q, off), b.k64, b.v64, cap, length, window, dtype, rows, f"length {length}, window {window}")
+            check_behind_table(b.q[-1:], call(b.q[-1:], None), b.k64, b.v64, cap, length, window, dtype, [0], f"single token, length {length}")

@@ -354,7 +354,8 @@ Cache cache_of(PyObject *cache, PyObject *tables, PyObject *lens, PyObject *offs
                int index)
 {
     const at::Tensor &c = tensor(cache), &tb = tensor(tables);
-    if (c.dim() != 2 || c.scalar_type() != at::kByte || tb.dim() != 2 || lens == Py_None || kv_heads < 1) throw Bad{};
+    if (c.dim() != 2 || c.scalar_type() != at::kByte || tb.dim() != 2 || lens == Py_None) throw Bad{};
+    if (kv_heads < 1 || kv_heads > 65536 || (D != 64 && D != 128)) throw Bad{};  // their product divides below: never 0
     Cache r;
     r.p = (uint8_t *)data(cache, index);
     r.bytes = c.nbytes();

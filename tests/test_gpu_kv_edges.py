@@ -47,3 +47,18 @@ def test_lengths_past_the_table(page, width, n, heads, kv, D, dtype):
             call = lambda q, o: qg.kv_attention(q, b.pool.cache, b.pool.tables, i32([length]), kv, offsets=o, window=window)
             check_behind_table(b.q, call(b.q, off), b.k64, b.v64, cap, length, window, dtype, rows, f"length {length}, window {window}")
             check_behind_table(b.q[-1:], call(b.q[-1:], None), b.k64, b.v64, cap, length, window, dtype, [0], f"single token, length {length}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kv_heads", [2 ** 58, 2 ** 60, 2 ** 61, 2 ** 62, 2 ** 63 - 1, 65537, 0, -1, -2 ** 61])
+def test_numbers_of_key_heads_that_wrap_around(kv_heads, D):
+    """Refused, whatever their product with the bytes of a head comes to in 64 bits."""
+    pool = Pool(1, [5], 2, D, 16)
+    q = randn((1, 4, D), 83, F16)
+    with pytest.raises(ValueError, match="page"):
+        qg.kv_read(pool.cache, pool.tables, i32([5]), 1, kv_heads, D)
+    with pytest.raises(ValueError, match="page"):
+        qg.kv_attention(q, pool.cache, pool.tables, i32([5]), kv_heads)
+    for head_dim in (2 ** 62, 2 ** 59, 0, -D):
+        with pytest.raises((ValueError, qg.QGemmError)):
+            qg.kv_read(pool.cache, pool.tables, i32([5]), 1, 2, head_dim)

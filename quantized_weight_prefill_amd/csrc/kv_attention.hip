@@ -248,11 +248,15 @@ __device__ __forceinline__ bool few_keys(Range keys)
     return DT == DT_F16 && keys.hi - keys.lo <= kFewKeys;
 }
 
+// The place in front of the window of a row at `place`; rows without a place, whose places are negative, count as at 0,
+// so that no window takes it out of an int's range.
+__device__ __forceinline__ int before_window(int place, int window) { return max(place, 0) - window; }
+
 __device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0, int rows)
 {
     const int cap = a.v.width << a.v.page_shift;
     const int pmin = q.first + row0 / a.group, pmax = q.first + (row0 + rows - 1) / a.group;
-    return Range{a.window ? max(pmin - a.window + 1, 0) : 0, min(pmax + 1, cap)};
+    return Range{a.window ? max(before_window(pmin, a.window) + 1, 0) : 0, min(pmax + 1, cap)};
 }
 
 // ---------------------------------------------------------------------------
@@ -325,7 +329,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     const int from = max(keys.lo & ~(kStep - 1), z * a.few_chunk), to = z + 1 < a.few_splits ? min(keys.hi, (z + 1) * a.few_chunk) : keys.hi;
 
     const int stride = kStep * NW, window = a.window ? a.window : INT_MAX;
-    const int pmin = q.first + row0 / a.group, pmax_lo = a.window ? q.first + (row0 + rows - 1) / a.group - a.window + 1 : 0;
+    const int pmin = q.first + row0 / a.group, pmax_lo = a.window ? before_window(q.first + (row0 + rows - 1) / a.group, a.window) + 1 : 0;
     int t = from + wave * kStep, ahead[2];
     FewRaw<D> even, odd;  // this step's bytes and the next one's
     bool huge = false;
@@ -336,13 +340,14 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     }
     u32x4 qf[RB][J];
     float c[RB], b[RB], l[RB];
-    int place[RB];
+    int place[RB], low[RB];  // a row sees the places above low, up to its own
     f32x4 o[RB][E];
 #pragma unroll
     for (int rb = 0; rb < RB; rb++) {
         const int r = row0 + 16 * rb + n, token = r / a.group;
         const bool live = r < all;
         place[rb] = live ? q.first + token : -1;
+        low[rb] = before_window(place[rb], window);
         c[rb] = load_query<DT, J, 16>(a.q + (long long)(q.row + (live ? token : 0)) * a.q_stride +
                                           (h * a.group + r - token * a.group) * D + g * (D / 4),
                                       live, 8, a.scale, qf[rb]);
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
                         const int at = t + 16 * i + 4 * g + u;
-                        const bool ok = there[i] & (at <= place[rb]) & (at > place[rb] - window);
+                        const bool ok = there[i] & (at <= place[rb]) & (at > low[rb]);
                         x[rb][i][u] = ok ? x[rb][i][u] : -INFINITY;
                     }
         }
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
 
     const int w0 = 32 * (wave % NW), r = row0 + w0 + n, token = r / a.group;
     const bool live = w0 + n < rows;
-    const int place = live ? q.first + token : -1, window = a.window ? a.window : INT_MAX;
+    const int place = live ? q.first + token : -1, low = before_window(place, a.window ? a.window : INT_MAX);
     // tiles in which some row of the wave sees a key, and keys that all its rows see
     const Range mine = w0 < rows ? seen(a, q, row0 + w0, min(rows - w0, 32)) : Range{0, 0};
     const int mt0 = mine.lo / kKeys, mt1 = (mine.hi + kKeys - 1) / kKeys;
@@ -596,7 +601,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
     // no multiple of 64), whatever the length
     const int cap = a.v.width << a.v.page_shift, last = min(place, cap - 1);
     const int clear_hi = min(q.first + (row0 + w0) / a.group, cap - 1);
-    const int clear_lo = a.window ? q.first + (row0 + min(rows, w0 + 32) - 1) / a.group - a.window + 1 : 0;
+    const int clear_lo = a.window ? before_window(q.first + (row0 + min(rows, w0 + 32) - 1) / a.group, a.window) + 1 : 0;
 
     // this wave's 16 tokens of a tile; past the last tile, of the last once more
     auto place_in = [&](int kt) { return min(kt, kt1 - 1) * kKeys + 16 * (wave & 3); };
@@ -667,7 +672,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
                         const int at = k + 8 * (i >> 2) + 4 * g + (i & 3);
-                        const bool ok = there & (at <= last) & (at > place - window);
+                        const bool ok = there & (at <= last) & (at > low);
                         x[u >> 1][8 * (u & 1) + i] = ok ? x[u >> 1][8 * (u & 1) + i] : -INFINITY;
                     }
                 }

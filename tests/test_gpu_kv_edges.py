@@ -62,3 +62,16 @@ def test_numbers_of_key_heads_that_wrap_around(kv_heads, D):
     for head_dim in (2 ** 62, 2 ** 59, 0, -D):
         with pytest.raises((ValueError, qg.QGemmError)):
             qg.kv_read(pool.cache, pool.tables, i32([5]), 1, 2, head_dim)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 31 - 30, 2 ** 40])
+@pytest.mark.parametrize("n,heads", [(8, 4), (40, 4), (300, 8)])
+def test_windows_wider_than_any_length(n, heads, window):
+    """Also behind rows that have no place in their sequence: what no window gives."""
+    b = Batch([n], [n], heads, 2, 128, 16, BF16, seed=84)
+    b.offsets = i32([0, n])
+    for length in (5, n - 1, n):
+        call = lambda **kw: qg.kv_attention(b.q, b.pool.cache, b.pool.tables, i32([length]), 2, offsets=b.offsets, **kw)
+        want = call()
+        assert (want[n - 1] != 0).any() and (want[:n - length] == 0).all()
+        assert torch.equal(call(window=window), want), length

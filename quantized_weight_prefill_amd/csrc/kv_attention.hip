@@ -127,12 +127,18 @@ __device__ __forceinline__ u32x2 quad_values(uint32_t w, const QuadHead &q)
     return u32x2{values(low_codes(w), q.s[0], q.m[0]), values(high_codes(w), q.s[1], q.m[1])};
 }
 
-// Headers of tokens that the sequence does not have are cleared: their
-// probability is 0, and 0 times what lies there could be NaN.
-__device__ __forceinline__ u32x4 live_heads(u32x4 h, int from, int len)
+// Keys that a range of rows sees.
+struct Range {
+    int lo, hi;
+};
+
+// Headers of four tokens, the first of them `from` places behind the first of the `n` that some row of a tile sees:
+// those that none does (behind the last row's place, or in front of the first one's window) are cleared.  Their
+// probability is 0, what lies there need not have been written, and 0 times it could be NaN.
+__device__ __forceinline__ u32x4 live_heads(u32x4 h, int from, int n)
 {
 #pragma unroll
-    for (int i = 0; i < 4; i++) h[i] = from + i < len ? h[i] : 0u;
+    for (int i = 0; i < 4; i++) h[i] = (unsigned)(from + i) < (unsigned)n ? h[i] : 0u;
     return h;
 }
 
@@ -225,11 +231,6 @@ __device__ __forceinline__ float add_pair(uint32_t pair, float l)
 {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), f16x2{(_Float16)1.0f, (_Float16)1.0f}, l, false);
 }
-
-// Keys that a range of rows sees.
-struct Range {
-    int lo, hi;
-};
 
 // The part, of `splits` parts of `chunk` keys (the last one open), that holds all the
 // keys of a range, or -1: rows of one part need no join, whatever the splits.
@@ -393,9 +394,9 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
                         x[rb][i][u] = ok ? x[rb][i][u] : -INFINITY;
                     }
         }
-        if (!whole || t + kStep > q.len) {
+        if (!(whole && t >= keys.lo && t + kStep <= keys.hi)) {
 #pragma unroll
-            for (int i = 0; i < 2; i++) r.vh[i] = live_heads(r.vh[i], t + 16 * i + 4 * g, there[i] ? q.len : 0);
+            for (int i = 0; i < 2; i++) r.vh[i] = live_heads(r.vh[i], t + 16 * i - keys.lo + 4 * g, there[i] ? keys.hi - keys.lo : 0);
         }
         u32x4 p[RB];
 #pragma unroll
@@ -540,10 +541,10 @@ struct ManyTile {
     uint2 v[4][D / 32][2][32][2];
 };
 
-// i: which 16 tokens of the tile, from place `at` on; len: the sequence's, or 0 where
-// the table names no page; rests: where the keys' second parts go, or null.
+// i: which 16 tokens of the tile, from place `at` behind the first of the n_seen keys that the row tile sees (0 where the
+// table names no page); rests: where the keys' second parts go, or null.
 template <int D, int PARTS>
-__device__ __forceinline__ void many_store(ManyTile<D> &t, ManyTile<D> *rests, const ManyRaw<D, PARTS> &r, int i, int part, int at, int len, int lane)
+__device__ __forceinline__ void many_store(ManyTile<D> &t, ManyTile<D> *rests, const ManyRaw<D, PARTS> &r, int i, int part, int at, int n_seen, int lane)
 {
     constexpr int N = ManyRaw<D, PARTS>::N;
     const int n = lane & 15, g = lane >> 4;
@@ -555,7 +556,7 @@ __device__ __forceinline__ void many_store(ManyTile<D> &t, ManyTile<D> *rests, c
         *(u32x4 *)&t.k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = v;
         if (rests) *(u32x4 *)&rests->k[i >> 1][(D / 32) * g + N * part + j][16 * (i & 1) + n] = key_rests(codes, head, v);
     }
-    const QuadHead q = quad_head(live_heads(r.vh, at + 4 * g, len));
+    const QuadHead q = quad_head(live_heads(r.vh, at + 4 * g, n_seen));
 #pragma unroll
     for (int j = 0; j < N; j++)
 #pragma unroll
@@ -609,8 +610,8 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
         many_load<D, PARTS>(a, entry, h, place_in(kt), wave >> 2, lane, to_raw);
     };
     auto store = [&](int kt, const ManyRaw<D, PARTS> &of_raw) {
-        many_store<D, PARTS>(s_tile[rests ? 0 : (kt - kt0) & 1], rests ? &s_tile[1] : nullptr, of_raw, wave & 3, wave >> 2, place_in(kt),
-                             names_page(a.v, of_raw.entry, place_in(kt)) ? q.len : 0, lane);
+        many_store<D, PARTS>(s_tile[rests ? 0 : (kt - kt0) & 1], rests ? &s_tile[1] : nullptr, of_raw, wave & 3, wave >> 2,
+                             place_in(kt) - keys.lo, names_page(a.v, of_raw.entry, place_in(kt)) ? keys.hi - keys.lo : 0, lane);
     };
     ManyRaw<D, PARTS> raw, later;  // the next tile's bytes, and those of the one after it
     int ahead = 0;                 // the table's entry for the one after that

@@ -75,3 +75,18 @@ def test_windows_wider_than_any_length(n, heads, window):
         want = call()
         assert (want[n - 1] != 0).any() and (want[:n - length] == 0).all()
         assert torch.equal(call(window=window), want), length
+
+
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+@pytest.mark.parametrize("new,window,length", [(1, 20, 100), (1, 500, 3000), (6, 30, 133), (40, 20, 150), (40, 100, 3050), (300, 77, 700)])
+def test_places_before_the_window_need_not_be_written(D, dtype, new, window, length):
+    """A sequence of which only what some window sees was appended, in a cache of bytes that read as NaN."""
+    whole = Batch([new], [length], 8, 2, D, 64, dtype, seed=85)
+    first = length - new - window + 1  # the first place that a row sees
+    part = Pool(1, [length], 2, D, 64, 85, fill=0xFF)
+    qg.kv_append(part.cache, whole.k[first:], whole.v[first:], part.tables, i32([length]), offsets=i32([0, length - first]))
+    whole.offsets = None if new == 1 else i32([0, new])
+    want = whole.run(window=window)
+    whole.check(want, window=window, rows={0, new // 2, new - 1})
+    y = qg.kv_attention(whole.q, part.cache, part.tables, i32([length]), 2, offsets=whole.offsets, window=window)
+    assert torch.equal(y, want)

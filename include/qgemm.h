@@ -611,9 +611,10 @@ size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64
  *   times it; query heads g*j .. g*j+g-1 read key head j), Y [T][heads][head_dim]
  *   contiguous.  Row t at place p of its sequence sees the places 0 .. p, with
  *   window > 0 those above p - window; keys without a place are not seen, and a
- *   row that sees none gets zeros.  What some row sees must have been appended, the new
- *   tokens included (the append leaves a padded row's place as it was: no later row
- *   may see it); what none sees, in front of a window, need not.
+ *   row that sees none gets zeros.  What a sequence's rows see must have been appended, the
+ *   new tokens included, or that sequence's results have no meaning: a padded row, whose
+ *   place the append leaves as it was, belongs behind offsets[S] or to a sequence of
+ *   length 0.  What none of them sees, in front of a window, need not be in the cache.
  *   Statistics and sums in 32 bits; the result does not depend on timing.  max_len (0:
  *   the table's width) is a bound on the lengths that the split of the work over a
  *   long cache goes by (one above table_width * page counts as that); longer ones are read all the same.  `workspace`

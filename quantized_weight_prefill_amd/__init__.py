@@ -1301,8 +1301,9 @@ def kv_attention(q, cache, tables, lens, kv_heads: int, offsets=None, scale=None
     p of its sequence, sees the places up to p (with ``window``, the last `window` of
     them); [T, heads, D], zeros for a row that sees nothing.
 
-    tables, lens and offsets as in :func:`kv_append`; what some row sees, the new
-    tokens included, must have been appended, what none sees need not; query heads j*g .. j*g+g-1 read key head j, g =
+    tables, lens and offsets as in :func:`kv_append`; what a sequence's rows see, the
+    new tokens included, must have been appended (padded rows, which are not, belong
+    behind offsets[S] or to a sequence of length 0); query heads j*g .. j*g+g-1 read key head j, g =
     heads / kv_heads.  ``scale`` defaults to D**-0.5.  ``max_len``, a bound on the
     lengths (0: the width of the tables), only decides how the work is split.
     Rows of ``out`` behind offsets[S] stay as they were."""

@@ -88,6 +88,7 @@ const char *qgemm_status_str(int status);
 #define QGEMM_F16 0
 #define QGEMM_BF16 1
 #define QGEMM_F32 2 /* routing logits and qgemm_kv_read only */
+#define QGEMM_ZERO_REST 16 /* or'ed to the dtype of qgemm_kv_append and qgemm_kv_attention: see there */
 
 #define QGEMM_FMT_Q4K 0
 #define QGEMM_FMT_Q6K 1
@@ -583,8 +584,9 @@ size_t qgemm_moe_workspace_bytes(int64_t T, int64_t top_k, int64_t hidden, int64
  * Sequences.  lens [S] (int32, device) are their lengths, the new tokens
  *   included.  offsets [S+1] (int32, device) say which rows are whose: rows
  *   offsets[s] .. offsets[s+1]-1 are the last places of sequence s, in order; NULL means
- *   one row each (T = S).  Rows from offsets[S] on belong to no sequence: they
- *   are not read, and their results stay as they were (qgemm_kv_read: zeros).  A row whose place is
+ *   one row each (T = S).  Rows in front of offsets[0] and from offsets[S] on belong to no
+ *   sequence: they are not read, and their results stay as they were, or are zeros where dtype
+ *   has QGEMM_ZERO_REST (for results in new memory; qgemm_kv_read: always zeros).  A row whose place is
  *   negative, beyond the table or in a page that is not in [0, pages) has no
  *   place in the cache.  The kernels clamp all of these, so any contents stay
  *   inside the buffers (bad ones only give wrong values); a page must not be

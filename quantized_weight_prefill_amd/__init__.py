@@ -1045,6 +1045,8 @@ def moe(fmt_up, fmt_down, x, w_up, w_down, weights, offsets, rows, inter: int, g
 
 # ---- attention ----------------------------------------------------------------
 
+_ZERO_REST = 16  # QGEMM_ZERO_REST
+
 #: tokens of a cache page
 KV_PAGES = (16, 32, 64, 128, 256)
 
@@ -1215,7 +1217,8 @@ def kv_append(cache, k, v, tables, lens, offsets=None, rope=None, positions=None
     tables [S, pages of a sequence], lens [S] (lengths with the new tokens),
     offsets [S+1] (rows offsets[s] .. offsets[s+1]-1 are the last places of
     sequence s; None: one row each), all int32.  ``positions`` None takes a row's
-    place in its sequence.  Rows behind offsets[S] stay as they were."""
+    place in its sequence.  Rows behind offsets[S] stay as they were in ``q_out``, and are
+    zeros in a new result."""
     if stream is None and q_out is None:
         y = _common("qgemm_kv_append", "kv_append", (cache, k, v, tables, lens, offsets, rope, positions, k_weight, eps,
                                                      interleaved, q, q_weight))
@@ -1235,7 +1238,7 @@ def kv_append(cache, k, v, tables, lens, offsets=None, rope=None, positions=None
     inputs = [("k", k, _span(k)), ("v", v, _span(v)), ("tables", tables, 4 * S * width),
               ("lens", lens, 4 * S), ("offsets", offsets, 4 * (S + 1)), ("rope", rope, 4 * rl * rot),
               ("positions", positions, 4 * T), ("k_weight", k_weight, 4 * D), ("q_weight", q_weight, 4 * D)]
-    qp, qs, heads, yp, ys = None, 0, 0, None, 0
+    qp, qs, heads, yp, ys, rest = None, 0, 0, None, 0, 0
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
@@ -1244,8 +1247,9 @@ def kv_append(cache, k, v, tables, lens, offsets=None, rope=None, positions=None
         if dq != D or q.shape[0] != T:
             raise ValueError("q must have k's rows and head size")
         if q_out is None:
-            (q_out,) = _allocate(stream, index, lambda: (torch.empty((T, heads, D), dtype=q.dtype, device=q.device),))
-            ys = heads * D
+            new = torch.empty if S else torch.zeros  # no sequence: the call does nothing
+            (q_out,) = _allocate(stream, index, lambda: (new((T, heads, D), dtype=q.dtype, device=q.device),))
+            ys, rest = heads * D, _ZERO_REST
         else:
             if q_out.shape != q.shape or q_out.dtype != q.dtype:
                 raise ValueError("q_out must have q's shape and dtype")
@@ -1258,7 +1262,7 @@ def kv_append(cache, k, v, tables, lens, offsets=None, rope=None, positions=None
         yp = q_out.data_ptr()
     _apart("cache", cache, cache.numel(), inputs)
     _call("qgemm_kv_append", index, stream, cache.data_ptr(), cache.shape[0], page, tp, width, lp, op, S, kp, ks, vp, vs, wk,
-          rp, rl, rot, int(bool(interleaved)), pp, -1.0 if eps is None else eps, qp, qs, wq, yp, ys, T, heads, H, D, code)
+          rp, rl, rot, int(bool(interleaved)), pp, -1.0 if eps is None else eps, qp, qs, wq, yp, ys, T, heads, H, D, code | rest)
     return q_out
 
 
@@ -1306,7 +1310,7 @@ def kv_attention(q, cache, tables, lens, kv_heads: int, offsets=None, scale=None
     behind offsets[S] or to a sequence of length 0); query heads j*g .. j*g+g-1 read key head j, g =
     heads / kv_heads.  ``scale`` defaults to D**-0.5.  ``max_len``, a bound on the
     lengths (0: the width of the tables), only decides how the work is split.
-    Rows of ``out`` behind offsets[S] stay as they were."""
+    Rows of ``out`` behind offsets[S] stay as they were; they are zeros in a new result."""
     if stream is None and workspace is None:
         y = _common("qgemm_kv_attention", "kv_attention", (q, cache, tables, lens, kv_heads, offsets, scale, window, max_len, out))
         if y is not None:
@@ -1327,11 +1331,13 @@ def kv_attention(q, cache, tables, lens, kv_heads: int, offsets=None, scale=None
                   ("lens", lens, 4 * S), ("offsets", offsets, 4 * (S + 1)))
         _apart("out", out, 2 * T * heads * D, inputs)
         _apart("workspace", workspace, need, (*inputs, ("out", out, 2 * T * heads * D)))
+    rest = 0
     if out is None:
-        (out,) = _allocate(stream, index, lambda: (torch.empty((T, heads, D), dtype=q.dtype, device=q.device),))
+        new, rest = torch.empty if S else torch.zeros, _ZERO_REST  # no sequence: the call does nothing
+        (out,) = _allocate(stream, index, lambda: (new((T, heads, D), dtype=q.dtype, device=q.device),))
     ws, wsb, _keep = _scratch(need, workspace, q, stream)
     _call("qgemm_kv_attention", index, stream, qp, qs, cache.data_ptr(), cache.shape[0], page, tp, width, lp, op, S,
-          out.data_ptr(), T, heads, kv_heads, D, window, D ** -0.5 if scale is None else scale, max_len, code, ws, wsb)
+          out.data_ptr(), T, heads, kv_heads, D, window, D ** -0.5 if scale is None else scale, max_len, code | rest, ws, wsb)
     return out
 
 

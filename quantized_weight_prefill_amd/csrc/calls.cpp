@@ -442,7 +442,7 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
         Py_BEGIN_ALLOW_THREADS
         st = qgemm_kv_append(c.p, c.pages, c.page, c.tables, c.width, c.lens, c.offsets, c.S, k.p, k.stride, v.p, v.stride, wk,
                              t.rope, t.lines, t.rot, t.interleaved, t.positions, t.eps, q.p, q.stride, wq,
-                             q.p ? y.data_ptr() : nullptr, q.heads * q.D, k.T, q.heads, k.heads, k.D, dtype, s);
+                             q.p ? y.data_ptr() : nullptr, q.heads * q.D, k.T, q.heads, k.heads, k.D, dtype | QGEMM_ZERO_REST, s);
         Py_END_ALLOW_THREADS
         if (st != QGEMM_OK) return PyLong_FromLong(st);
         if (q.p) return THPVariable_Wrap(y);
@@ -504,7 +504,8 @@ PyObject *kv_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         int st;
         Py_BEGIN_ALLOW_THREADS
         st = qgemm_kv_attention(q.p, q.stride, c.p, c.pages, c.page, c.tables, c.width, c.lens, c.offsets, c.S, y.data_ptr(), q.T,
-                                q.heads, H, q.D, window, scale, max_len, dtype, need ? ws.data_ptr() : nullptr, need, s);
+                                q.heads, H, q.D, window, scale, max_len, yp ? dtype : dtype | QGEMM_ZERO_REST, need ? ws.data_ptr() : nullptr,
+                                need, s);
         Py_END_ALLOW_THREADS
         return wrap_or_status(st, y);
     });

@@ -162,6 +162,7 @@ struct AppendArgs {
     const uint16_t *val;
     long long val_stride;
     int value_blocks, key_blocks;  // workgroups of values and of keys; the rest are the queries'
+    bool zero_rest;         // zeros to the queries of no sequence
 };
 
 // Partial results of the attention, of one row and query head from one part of
@@ -181,6 +182,7 @@ struct AttnArgs {
     int few_splits, few_chunk;    // k_attn_few: workgroups along the keys, keys of each
     int many_splits, many_chunk;  // k_attn_many's
     int tile_tokens, slots;       // k_attn_many: tokens of a row tile, row tiles of all sequences (a bound)
+    int work_blocks, rest_blocks;  // a launch's workgroups along x, and those behind them that write zeros to the rows of no sequence
     float *few_sum, *many_sum;    // partial results (null: one split)
     f32x2 *few_stat, *many_stat;
 };
@@ -199,6 +201,7 @@ hipError_t launch_norm_rope(int dtype, int D, const NormRopeArgs &a, hipStream_t
 hipError_t launch_kv_append(int dtype, int D, const AppendArgs &a, hipStream_t s);
 // out_type: QGEMM_F16, QGEMM_BF16 or QGEMM_F32
 hipError_t launch_kv_read(int out_type, int D, const KvView &v, void *k, void *val, hipStream_t s);
-hipError_t launch_kv_attention(int dtype, int D, const AttnPlan &pl, AttnArgs a, void *workspace, hipStream_t s);
+// zero_rest: zeros to the rows of no sequence
+hipError_t launch_kv_attention(int dtype, int D, const AttnPlan &pl, AttnArgs a, bool zero_rest, void *workspace, hipStream_t s);
 
 }  // namespace qg

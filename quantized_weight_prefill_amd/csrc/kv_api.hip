@@ -154,6 +154,8 @@ int qgemm_kv_append(void *cache, int64_t pages, int64_t page, const int32_t *tab
                     int64_t head_dim, int dtype, void *stream)
 {
     AppendArgs a{};
+    a.zero_rest = (dtype & QGEMM_ZERO_REST) != 0;
+    dtype &= ~QGEMM_ZERO_REST;
     if (dtype != DT_F16 && dtype != DT_BF16) return QGEMM_ERR_DTYPE;
     int st = head_shape(heads, kv_heads, head_dim);
     if (st != QGEMM_OK) return st;
@@ -206,6 +208,8 @@ int qgemm_kv_attention(const void *Q, int64_t q_stride, const void *cache, int64
                        int64_t max_len, int dtype, void *workspace, size_t workspace_bytes, void *stream)
 {
     AttnArgs a{};
+    const bool zero_rest = (dtype & QGEMM_ZERO_REST) != 0;
+    dtype &= ~QGEMM_ZERO_REST;
     if (dtype != DT_F16 && dtype != DT_BF16) return QGEMM_ERR_DTYPE;
     int st = head_shape(heads, kv_heads, head_dim);
     if (st != QGEMM_OK) return st;
@@ -228,7 +232,7 @@ int qgemm_kv_attention(const void *Q, int64_t q_stride, const void *cache, int64
     a.group = (int)(heads / kv_heads);
     a.window = (int)(window > INT32_MAX ? 0 : window);
     a.scale = scale;
-    return status_of(launch_kv_attention(dtype, (int)head_dim, pl, a, workspace, (hipStream_t)stream), "cache attention");
+    return status_of(launch_kv_attention(dtype, (int)head_dim, pl, a, zero_rest, workspace, (hipStream_t)stream), "cache attention");
 }
 
 }  // extern "C"

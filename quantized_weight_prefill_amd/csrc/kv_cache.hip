@@ -197,15 +197,17 @@ __device__ __forceinline__ void turn_head(const TurnArgs &t, const RowTurn<F> &r
 }
 
 // HC heads of one row from `head` on to y, in binary32 with one rounding at the end; zeros
-// for a position outside the table.  pos_of: the row's position; false: leave it.
+// for a position outside the table.  pos_of: the row's position; false: it belongs to no sequence,
+// and is left or, with zero_rest, zeros.
 template <typename By, int DT, int D, int HC, typename PosOf>
-__device__ __forceinline__ void turn_store(const TurnArgs &t, const Heads &h, int row, int head, int l, PosOf pos_of)
+__device__ __forceinline__ void turn_store(const TurnArgs &t, const Heads &h, int row, int head, int l, bool zero_rest, PosOf pos_of)
 {
     uint32_t own[HC][E / 2], part[HC][E / 2];
     load_heads<By, D, HC>(t, h, row, head, l, own, part);
     int pos;
-    if (!pos_of(pos)) return;
-    const bool inside = By::mode == kPlain || (unsigned)pos < (unsigned)t.rope_len;
+    const bool owned = pos_of(pos);
+    if (!owned && !zero_rest) return;
+    const bool inside = owned && (By::mode == kPlain || (unsigned)pos < (unsigned)t.rope_len);
     RowTurn<float> r;
     row_turn<By>(t, h.weight, inside ? pos : 0, l, r);
     uint16_t *o = h.y + (long long)row * h.y_stride + head * D + E * l;
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(256) k_norm_rope(NormRopeArgs a)
     if (row >= a.T) return;
     const bool key = i >= qc;
     turn_by(a.t, [&](auto by) {
-        turn_store<decltype(by), DT, D, HC>(a.t, key ? a.k : a.q, row, HC * (key ? i - qc : i), l, [&](int &p) {
+        turn_store<decltype(by), DT, D, HC>(a.t, key ? a.k : a.q, row, HC * (key ? i - qc : i), l, false, [&](int &p) {
             p = a.t.positions ? a.t.positions[row] : 0;
             return true;
         });
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(256) k_kv_append(AppendArgs a)
     const int qc = chunks(a.q.heads, HC), item = (b - a.key_blocks) * kItems<D> + sub, row = item / qc;
     if (row >= a.v.T) return;
     turn_by(a.t, [&](auto by) {
-        turn_store<decltype(by), DT, D, HC>(a.t, a.q, row, HC * (item - row * qc), l, [&](int &p) {
+        turn_store<decltype(by), DT, D, HC>(a.t, a.q, row, HC * (item - row * qc), l, a.zero_rest, [&](int &p) {
             int s;
             const int at = place_of<D / E>(a.v, row, s);
             p = a.t.positions ? a.t.positions[row] : at;

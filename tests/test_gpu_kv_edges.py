@@ -90,3 +90,100 @@ def test_places_before_the_window_need_not_be_written(D, dtype, new, window, len
     whole.check(want, window=window, rows={0, new // 2, new - 1})
     y = qg.kv_attention(whole.q, part.cache, part.tables, i32([length]), 2, offsets=whole.offsets, window=window)
     assert torch.equal(y, want)
+
+
+def poison(shape, dtype):
+    """Free memory of a result's size that reads as NaN, for the allocator to hand out next."""
+    x = torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+    del x
+
+
+# rows before the first sequence, of each, and behind the last; lengths
+RESTS = [
+    (0, [1], 3, [20]), (2, [1, 2], 3, [30, 20]),       # a few rows
+    (0, [40], 9, [40]), (5, [40, 1, 0], 70, [90, 30, 9]),  # prompts and single tokens
+    (0, [700], 324, [700]), (300, [1], 20, [50]),
+    (3, [70], 90, [3000]), (1, [1, 1], 62, [5000, 700]),   # parts of the keys
+]
+
+
+@pytest.mark.parametrize("before,new,behind,lens", RESTS)
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+def test_rows_of_no_sequence_are_zeros_in_new_results(before, new, behind, lens, D, dtype):
+    """What the library allocates is written whole; a result that the caller brings keeps those rows."""
+    b = Batch(new, lens, 8, 2, D, 32, dtype, seed=86)
+    T = before + sum(new) + behind
+    off = [before]
+    for m in new:
+        off.append(off[-1] + m)
+    b.offsets, b.q = i32(off), randn((T, 8, D), 87, dtype)
+    own = slice(before, T - behind)
+    marked = torch.full_like(b.q, 9.0)
+    b.run(out=marked)
+    assert (marked[:before] == 9).all() and (marked[own] != 9).any() and (marked[T - behind:] == 9).all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for kw in ({}, dict(stream=side.cuda_stream)):
+        poison(b.q.shape, dtype)
+        y = b.run(**kw)
+        side.synchronize()
+        assert torch.equal(y[own], marked[own]) and (y[:before] == 0).all() and (y[T - behind:] == 0).all()
+    k, v = randn((T, 2, D), 88, dtype), randn((T, 2, D), 89, dtype)
+    rope = table(6000, D)
+    call = lambda **kw: qg.kv_append(b.pool.cache, k, v, b.pool.tables, i32(lens), offsets=b.offsets, rope=rope, eps=1e-6, q=b.q, **kw)
+    marked = torch.full_like(b.q, 9.0)
+    call(q_out=marked)
+    assert (marked[:before] == 9).all() and (marked[own] != 9).any() and (marked[T - behind:] == 9).all()
+    for kw in ({}, dict(stream=side.cuda_stream)):
+        poison(b.q.shape, dtype)
+        y = call(**kw)
+        side.synchronize()
+        assert torch.equal(y[own], marked[own]) and (y[:before] == 0).all() and (y[T - behind:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+def test_no_sequence_at_all_gives_zeros(dtype):
+    pool = Pool(1, [20], 2, 64, 16)
+    none = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    x = randn((37, 2, 64), 90, dtype)
+    for o in (i32([0]), i32([37])):
+        poison(x.shape, dtype)
+        assert (qg.kv_attention(x, pool.cache, none, none[:, 0], 2, offsets=o) == 0).all()
+        poison(x.shape, dtype)
+        assert (qg.kv_append(pool.cache, x, x, none, none[:, 0], offsets=o, q=x) == 0).all()
+    empty = i32([0, 0])  # a sequence without new rows
+    poison(x.shape, dtype)
+    assert (qg.kv_attention(x, pool.cache, pool.tables, i32([20]), 2, offsets=empty) == 0).all()
+    poison(x.shape, dtype)
+    assert (qg.kv_append(pool.cache, x, x, pool.tables, i32([20]), offsets=empty, q=x) == 0).all()
+
+
+def test_captured_batches_that_shrink():
+    """A padded step in a graph, replayed with fewer rows each time: no row of an earlier replay is left."""
+    D, T = 128, 96
+    b = Batch([60, 30], [600, 300], 8, 2, D, 32, BF16, seed=91)
+    b.q = randn((T, 8, D), 92, BF16)
+    k, v = randn((T, 2, D), 93, BF16), randn((T, 2, D), 94, BF16)
+    off, lens = i32([0, 60, 90]), i32([600, 300])
+
+    def step():
+        q = qg.kv_append(b.pool.cache, k, v, b.pool.tables, lens, offsets=off, eps=1e-6, q=b.q)
+        return q, qg.kv_attention(q, b.pool.cache, b.pool.tables, lens, 2, offsets=off)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for o in ([0, 60, 90], [0, 50, 51], [4, 5, 6], [0, 0, 0], [0, 1, 96]):
+        off.copy_(i32(o))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = step()
+        torch.cuda.synchronize()
+        for x, w in zip(got, want):
+            assert torch.equal(x, w) and (x[o[2]:] == 0).all() and (x[:o[0]] == 0).all(), o

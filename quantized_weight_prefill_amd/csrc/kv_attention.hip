@@ -18,9 +18,10 @@
 //
 // Of an fp16 result, whose own rounding is no larger than these, the keys' is the one that
 // shows: over few keys the errors of their products do not average out. Rows that see at most
-// kFewKeys of them therefore take the keys in two fp16 parts, about 22 bits (few_keys). The error
+// kFewKeys of them therefore take the keys in two fp16 parts, about 22 bits, and with them the other rows of their tile (few_keys). The error
 // is then at most 1.4 times that of binary32 arithmetic with the result rounded, where it was
-// 1.8 over 20 keys, 1.65 over 100, 1.4 over 330 and 1.3 over 658. It costs 658 tokens 5%; two parts
+// 1.8 over 20 keys, 1.65 over 100, 1.4 over 330 and 1.3 over 658. It costs 658 tokens 5%, 3000 with
+// a window of 512 20% (62 -> 75 us); two parts
 // everywhere would cost a third (4096 tokens 177 -> 229, 64 single tokens over up to 8192 104 -> 156).
 //
 // With x the product and c the scale in log2 units, p = 2^(x*c - b): one FMA and one
@@ -243,14 +244,6 @@ __device__ __forceinline__ int only_part(Range keys, int splits, int chunk)
     return first == min((keys.hi - 1) / chunk, splits - 1) ? first : -1;
 }
 
-// Whether rows that see these keys take them in two parts.
-constexpr int kFewKeys = 512;
-template <int DT>
-__device__ __forceinline__ bool few_keys(Range keys)
-{
-    return DT == DT_F16 && keys.hi - keys.lo <= kFewKeys;
-}
-
 // The place in front of the window of a row at `place`; rows without a place, whose places are negative, count as at 0,
 // so that no window takes it out of an int's range.
 __device__ __forceinline__ int before_window(int place, int window) { return max(place, 0) - window; }
@@ -260,6 +253,17 @@ __device__ __forceinline__ Range seen(const AttnArgs &a, const Seq &q, int row0,
     const int cap = a.v.width << a.v.page_shift;
     const int pmin = q.first + row0 / a.group, pmax = q.first + (row0 + rows - 1) / a.group;
     return Range{a.window ? max(before_window(pmin, a.window) + 1, 0) : 0, min(pmax + 1, cap)};
+}
+
+// Whether some row of a tile sees at most kFewKeys keys, and the tile takes them in two parts.  With a row's place the number
+// of its keys rises, stays (at the window) and falls (behind the table), so that it is least for the first row or the last.
+constexpr int kFewKeys = 512;
+template <int DT>
+__device__ __forceinline__ bool few_keys(const AttnArgs &a, const Seq &q, int row0, int rows)
+{
+    if (DT != DT_F16) return false;
+    const Range first = seen(a, q, row0, 1), last = seen(a, q, row0 + rows - 1, 1);
+    return min(first.hi - first.lo, last.hi - last.lo) <= kFewKeys;
 }
 
 // Zeros to the rows of no sequence, in front of the first one and behind the last, by
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     if ((a.v.offs && all > a.few_rows) || row0 >= all) return;
     const int rows = min(all - row0, 16 * RB);
     const Range keys = seen(a, q, row0, rows);
-    const bool rests = few_keys<DT>(keys);
+    const bool rests = few_keys<DT>(a, q, row0, rows);
     const int only = only_part(keys, a.few_splits, a.few_chunk);
     if (only >= 0 && only != z) return;
     const int from = max(keys.lo & ~(kStep - 1), z * a.few_chunk), to = z + 1 < a.few_splits ? min(keys.hi, (z + 1) * a.few_chunk) : keys.hi;
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
     if (tile < 0 || row0 >= all || all <= a.few_rows) return;
     const int rows = min(all - row0, a.tile_tokens * a.group);
     const Range keys = seen(a, q, row0, rows);
-    const bool rests = few_keys<DT>(keys);  // then one tile at a time, its second parts in the other's place
+    const bool rests = few_keys<DT>(a, q, row0, rows);  // then one tile at a time, its second parts in the other's place
     const int only = only_part(keys, a.many_splits, a.many_chunk);
     if (only >= 0 && only != z) return;
     const int from = max(keys.lo, z * a.many_chunk), to = z + 1 < a.many_splits ? min(keys.hi, (z + 1) * a.many_chunk) : keys.hi;

@@ -187,3 +187,37 @@ def test_captured_batches_that_shrink():
         torch.cuda.synchronize()
         for x, w in zip(got, want):
             assert torch.equal(x, w) and (x[o[2]:] == 0).all() and (x[:o[0]] == 0).all(), o
+
+
+def equal_weights(L, n, heads, D, seed):
+    """A sequence whose keys are 48 vectors in turn, and queries at right angles to all their differences: every key that a
+    row sees weighs the same, while one fp16 rounding of the keys would move the products by many times what the result's own
+    rounding leaves."""
+    b = Batch([n], [L], heads, 1, D, 32, F16, seed=seed)
+    b.k = b.k[:48][torch.arange(L, device="cuda") % 48].contiguous()
+    qg.kv_append(b.pool.cache, b.k, b.v, b.pool.tables, i32([L]), offsets=i32([0, L]))
+    b.k64 = R.held64(b.k)
+    basis = torch.linalg.svd(b.k64[1:48, 0] - b.k64[:1, 0])[2][47:]
+    g = torch.Generator().manual_seed(seed + 1)
+    b.q = (12 * torch.randn((n, heads, len(basis)), generator=g, dtype=torch.float64) @ basis).to(F16).cuda()
+    return b
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L,n,window,rows", [
+    (900, 300, 512, range(0, 300, 7)),    # every row sees 512 keys, a tile of rows more
+    (900, 300, 500, range(0, 300, 7)),
+    (900, 9, 510, range(9)),
+    (530, 40, 0, range(0, 22)),           # a tile of rows that see up to 512 keys, and of others
+    (516, 9, 0, range(0, 5)),
+])
+def test_rows_of_few_keys_keep_fp16_precision_beside_any_others(D, L, n, window, rows):
+    """What a row sees decides, not what its tile's other rows see: the bound of 512 keys is the row's own. Values and
+    weights are each off by at most the relative half step that the result's rounding has at worst, twice the least that it
+    has: the error is below sqrt(1 + 4 + 4) of the result's own rounding."""
+    b = equal_weights(L, n, 4, D, 95)
+    y = b.run(window=window).double().cpu()
+    rows = list(rows)
+    want, _ = R.attention64(b.q[rows], b.k64, b.v64, [L - n + i for i in rows], D ** -0.5, window, F16)
+    own = (want.to(F16).double() - want).norm()
+    assert (y[rows] - want).norm() < 3 * own

@@ -1147,7 +1147,7 @@ def _rows_apart(what, t, others):
         b, wb, sb, n = _rows(o)
         if not (a < b + (n - 1) * sb + wb and b < a + (T - 1) * sa + wa):
             continue
-        if sa == sb and (b - a) % sa >= wa and (a - b) % sa >= wb:
+        if sa == sb > 0 and (b - a) % sa >= wa and (a - b) % sa >= wb:
             continue
         raise ValueError(f"{what} shares memory with {name}")
 

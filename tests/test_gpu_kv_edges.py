@@ -221,3 +221,16 @@ def test_rows_of_few_keys_keep_fp16_precision_beside_any_others(D, L, n, window,
     want, _ = R.attention64(b.q[rows], b.k64, b.v64, [L - n + i for i in rows], D ** -0.5, window, F16)
     own = (want.to(F16).double() - want).norm()
     assert (y[rows] - want).norm() < 3 * own
+
+
+def test_one_result_for_every_row_is_refused():
+    """Rows that share one place cannot be written."""
+    q, k = randn((3, 4, 64), 96, F16), randn((3, 2, 64), 97, F16)
+    one = torch.empty((1, 4, 64), dtype=F16, device="cuda").expand(3, 4, 64)
+    for x in (q, q[:1].expand(3, 4, 64), one):
+        with pytest.raises((ValueError, qg.QGemmError)):
+            qg.qk_norm_rope(x, k, q_out=one)
+    pool = Pool(3, [1] * 3, 2, 64, 16)
+    for x in (q, q[:1].expand(3, 4, 64), one):
+        with pytest.raises((ValueError, qg.QGemmError)):
+            qg.kv_append(pool.cache, k, k, pool.tables, i32([1] * 3), q=x, q_out=one)

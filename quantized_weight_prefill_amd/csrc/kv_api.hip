@@ -18,9 +18,9 @@ int status_of(hipError_t e, const char *what)
     return QGEMM_ERR_HIP;
 }
 
-// Items of at most 16 lanes in one launch; counts stay below 2^28 so that a kernel's item index is an
-// int.
-bool items_fit(long long n) { return n >= 0 && n < (1LL << 28); }
+// Items of at most 16 lanes in one launch, whose lanes, those of a last workgroup that is not full among them, stay below
+// 2^32; a kernel's item index is an int.
+bool items_fit(long long n) { return n >= 0 && n <= (1LL << 28) - 16; }
 
 int page_shift(long long page)
 {

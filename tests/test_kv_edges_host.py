@@ -16,3 +16,16 @@ def test_rows_that_lie_on_one_another():
             qg._rows_apart("out", one(0, 4), [("other", other)])
     for other in (one(4, 4), one(48, 2)):
         qg._rows_apart("out", one(0, 4), [("other", other)])
+
+
+@pytest.mark.parametrize("beyond,status", [(15, -2), (1, -2), (16, -1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_heads_that_one_launch_holds(D, beyond, status):
+    """16 lanes to a head of 128, fewer than 2^32 lanes: up to 2^28 - 16 heads get as far as the missing pointer."""
+    from tests.test_kv_host import P, attn_call, read_call, rope_call
+
+    T = (1 << 28) - beyond
+    missing = None if status == -1 else P  # sizes are refused first
+    assert rope_call(Q=missing, qs=D, qos=D, K=None, Ko=None, T=T, heads=1, kv=0, D=D, rot=D) == status
+    assert read_call(K=missing, T=T, kv=1, D=D) == status
+    assert attn_call(Q=missing, qs=D, T=T, heads=1, kv=1, D=D) == status

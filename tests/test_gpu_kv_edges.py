@@ -234,3 +234,60 @@ def test_one_result_for_every_row_is_refused():
     for x in (q, q[:1].expand(3, 4, 64), one):
         with pytest.raises((ValueError, qg.QGemmError)):
             qg.kv_append(pool.cache, k, k, pool.tables, i32([1] * 3), q=x, q_out=one)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 6, 90])
+@pytest.mark.parametrize("scale", [2.0 ** 12, 2.0 ** 18, 2.0 ** 40])
+def test_products_far_beyond_the_exponential(dtype, D, n, scale):
+    """Keys of +-1 and queries that are one of them, with products from 2^21 to 2^50 in log2 units: every other key's weight is 0
+    in any arithmetic, so the result is the picked key's value, or where two keys are alike the mean of their values, each
+    rounded once. Values are off by 2^-11 of each and half a subnormal step, the sum and its quotient by 2^-22."""
+    kv, heads, L = 2, 4, 300
+    g = torch.Generator().manual_seed(98)
+    k = torch.where(torch.rand((L, kv, D), generator=g) < 0.5, -1.0, 1.0)
+    twins = {L - 1: 17, 40: 3}
+    for a, b in twins.items():
+        k[a] = k[b]
+    twins.update({b: a for a, b in list(twins.items())})
+    v = torch.randn((L, kv, D), generator=g)
+    pool = Pool(1, [L], kv, D, 32)
+    qg.kv_append(pool.cache, k.to(dtype).cuda(), v.to(dtype).cuda(), pool.tables, i32([L]), offsets=i32([0, L]))
+    held = R.held64(v.to(dtype))
+    place = [L - n + i for i in range(n)]
+    pick = [[(7 * i + 31 * h) % (p + 1) for h in range(heads)] for i, p in enumerate(place)]
+    pick[-1] = [L - 1, 40, 3, 17]
+    for sign in (1.0, -1.0):  # a negative scale turns the order around: the same result of negated queries
+        q = torch.stack([torch.stack([sign * 8 * k[pick[i][h], h // 2] for h in range(heads)]) for i in range(n)])
+        y = qg.kv_attention(q.to(dtype).cuda(), pool.cache, pool.tables, i32([L]), kv, offsets=None if n == 1 else i32([0, n]),
+                            scale=sign * scale)
+        want, mag = torch.zeros((n, heads, D), dtype=torch.float64), torch.zeros((n, heads, D), dtype=torch.float64)
+        for i in range(n):
+            for h in range(heads):
+                a = pick[i][h]
+                both = [a] + ([twins[a]] if twins.get(a, L) <= place[i] else [])
+                want[i, h] = held[both, h // 2].mean(0)
+                mag[i, h] = held[both, h // 2].abs().mean(0)
+        assert_within(y, want, R.store_err(want, (2.0 ** -11 + 2.0 ** -22) * mag + 2.0 ** -25, dtype), f"sign {sign}")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("n", [1, 6, 90])
+def test_products_far_below_zero(dtype, n):
+    """Every product is the same, from -2^21 to -2^50 in log2 units: all keys weigh the same. A weight is the same number for all
+    keys of a row, so the result is off by the values' roundings, 2^-23 for each key's sums and the store's."""
+    D, kv, heads, L = 128, 2, 4, 150
+    pool = Pool(1, [L], kv, D, 32)
+    k = torch.ones((L, kv, D), dtype=dtype, device="cuda")
+    v = randn((L, kv, D), 99, dtype)
+    qg.kv_append(pool.cache, k, v, pool.tables, i32([L]), offsets=i32([0, L]))
+    held = R.held64(v)
+    q = torch.full((n, heads, D), -1.0, dtype=dtype, device="cuda")
+    for scale in (2.0 ** 14, 2.0 ** 21, 2.0 ** 43):
+        y = qg.kv_attention(q, pool.cache, pool.tables, i32([L]), kv, offsets=None if n == 1 else i32([0, n]), scale=scale)
+        for i in range(n):
+            m = L - n + i + 1
+            want, mag = (x[:m].mean(0).repeat_interleave(heads // kv, 0)[None] for x in (held, held.abs()))
+            bound = R.store_err(want, (2.0 ** -11 + m * 2.0 ** -23) * mag + 2.0 ** -25, dtype)
+            assert_within(y[i:i + 1], want, bound, f"scale {scale} row {i}")

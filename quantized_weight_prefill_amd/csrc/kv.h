@@ -182,7 +182,8 @@ struct AttnArgs {
     int few_splits, few_chunk;    // k_attn_few: workgroups along the keys, keys of each
     int many_splits, many_chunk;  // k_attn_many's
     int tile_tokens, slots;       // k_attn_many: tokens of a row tile, row tiles of all sequences (a bound)
-    int work_blocks, rest_blocks;  // a launch's workgroups along x, and those behind them that write zeros to the rows of no sequence
+    bool zero_rest;               // zeros to the rows of no sequence: by k_attn_join or, without it, by
+    int work_blocks, rest_blocks;  // rest_blocks workgroups behind the work_blocks of the last launch
     float *few_sum, *many_sum;    // partial results (null: one split)
     f32x2 *few_stat, *many_stat;
 };

@@ -266,12 +266,12 @@ __device__ __forceinline__ bool few_keys(const AttnArgs &a, const Seq &q, int ro
     return min(first.hi - first.lo, last.hi - last.lo) <= kFewKeys;
 }
 
-// Zeros to the rows of no sequence, in front of the first one and behind the last, by
-// workgroups behind those of a launch: beside the others' work, which they do not touch (658 tokens 23.6 us with and without
-// them, 4096 159).
+// Zeros to the rows of no sequence, in front of the first one and behind the last, by workgroups behind those of a launch
+// that no join follows: beside the others' work, which they do not touch (658 tokens 23.6 us with and without them, 4096
+// 159).  The join comes by every row anyway; workgroups behind those of a launch in parts, which are as many as the CUs hold,
+// took 64 tokens behind 8000 from 49.9 us to 52.2.
 __device__ __forceinline__ void zero_rest(const AttnArgs &a, int D)
 {
-    if (blockIdx.y != 0) return;
     const long long per = (long long)a.heads * D / 8;  // pieces of 16 bytes in a row
     const long long front = row_end(a.v, 0) * per, back = row_end(a.v, a.v.S) * per, n = front + a.v.T * per - back;
     const long long step = (long long)a.rest_blocks * blockDim.x;
@@ -793,7 +793,11 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a)
     if (row >= a.v.T) return;
     const int s = a.v.offs ? find_seq<16>(a.v, row, 1, 0) : row;
     const Seq q = seq_of(a.v, s);
-    if (row < q.row || row >= q.row + q.n) return;
+    if (row < q.row || row >= q.row + q.n) {
+        const float zeros[E] = {};
+        if (a.zero_rest && gi == 0) store_out<DT, E>(a.y, ((long long)row * a.heads + head) * D + E * dl, zeros);
+        return;
+    }
     const bool few = !a.v.offs || q.n * a.group <= a.few_rows;
     const int splits = few ? a.few_splits : a.many_splits, chunk = few ? a.few_chunk : a.many_chunk;
     const int h = head / a.group, ra = (row - q.row) * a.group + head - h * a.group;
@@ -866,10 +870,11 @@ hipError_t run_many(AttnArgs a, hipStream_t s)
 }
 
 template <int DT, int D>
-hipError_t run_attention(const AttnPlan &pl, AttnArgs a, bool zero_rest, hipStream_t s)
+hipError_t run_attention(const AttnPlan &pl, AttnArgs a, hipStream_t s)
 {
-    // workgroups of the last launch with one for every 32 KB of results, up to one to a CU
-    const int rest = !zero_rest ? 0 : (int)std::min(ceil_of((long long)a.v.T * a.heads * D, 16384), 256LL);
+    const int splits = pl.few && pl.few_splits > 1 ? pl.few_splits : pl.many ? pl.many_splits : 1;
+    // a workgroup for every 32 KB of results, up to one to a CU
+    const int rest = !a.zero_rest || splits > 1 ? 0 : (int)std::min(ceil_of((long long)a.v.T * a.heads * D, 16384), 256LL);
     if (pl.few) {
         a.rest_blocks = pl.many ? 0 : rest;
         if (pl.few_rb == 2) run_few<DT, D, 2, 4>(a, s);
@@ -885,7 +890,6 @@ hipError_t run_attention(const AttnPlan &pl, AttnArgs a, bool zero_rest, hipStre
                                               : run_many<DT, D, 4, 1>(a, s);
         if (e != hipSuccess) return e;
     }
-    const int splits = pl.few && pl.few_splits > 1 ? pl.few_splits : pl.many ? pl.many_splits : 1;
     if (splits > 1) {
         const long long items = (long long)a.v.T * a.heads;
         // a workgroup to a row and head where 16 lanes would walk through many parts and there are few of
@@ -987,9 +991,9 @@ hipError_t launch_kv_attention(int dtype, int D, const AttnPlan &pl, AttnArgs a,
     a.many_stat = a.few_stat + pl.few_entries;
     a.few_sum = (float *)(a.many_stat + pl.many_entries);
     a.many_sum = a.few_sum + pl.few_entries * D;
-    zero_rest = zero_rest && a.v.offs;  // without offsets every row is a sequence's
-    if (dtype == DT_F16) return D == 64 ? run_attention<DT_F16, 64>(pl, a, zero_rest, s) : run_attention<DT_F16, 128>(pl, a, zero_rest, s);
-    return D == 64 ? run_attention<DT_BF16, 64>(pl, a, zero_rest, s) : run_attention<DT_BF16, 128>(pl, a, zero_rest, s);
+    a.zero_rest = zero_rest && a.v.offs;  // without offsets every row is a sequence's
+    if (dtype == DT_F16) return D == 64 ? run_attention<DT_F16, 64>(pl, a, s) : run_attention<DT_F16, 128>(pl, a, s);
+    return D == 64 ? run_attention<DT_BF16, 64>(pl, a, s) : run_attention<DT_BF16, 128>(pl, a, s);
 }
 
 }  // namespace qg

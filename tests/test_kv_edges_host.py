@@ -29,3 +29,14 @@ def test_heads_that_one_launch_holds(D, beyond, status):
     assert rope_call(Q=missing, qs=D, qos=D, K=None, Ko=None, T=T, heads=1, kv=0, D=D, rot=D) == status
     assert read_call(K=missing, T=T, kv=1, D=D) == status
     assert attn_call(Q=missing, qs=D, T=T, heads=1, kv=1, D=D) == status
+
+
+def test_zero_rest_is_a_flag_of_two_calls():
+    from tests.test_kv_host import append_call, attn_call, read_call, rope_call
+
+    for dtype in (16, 17):  # QGEMM_ZERO_REST with float16 and bfloat16
+        assert append_call(dtype=dtype, T=0, K=None) == 0 and attn_call(dtype=dtype, T=0, Q=None) == 0
+        assert append_call(dtype=dtype, K=None) == -1 and attn_call(dtype=dtype, Q=None) == -1
+        assert rope_call(dtype=dtype) == -3 and read_call(ot=dtype) == -3
+    for dtype in (18, 32, -1):
+        assert append_call(dtype=dtype) == -3 and attn_call(dtype=dtype) == -3

@@ -18,11 +18,12 @@
 //
 // Of an fp16 result, whose own rounding is no larger than these, the keys' is the one that
 // shows: over few keys the errors of their products do not average out. Rows that see at most
-// kFewKeys of them therefore take the keys in two fp16 parts, about 22 bits, and with them the other rows of their tile (few_keys). The error
-// is then at most 1.4 times that of binary32 arithmetic with the result rounded, where it was
-// 1.8 over 20 keys, 1.65 over 100, 1.4 over 330 and 1.3 over 658. It costs 658 tokens 5%, 3000 with
-// a window of 512 20% (62 -> 75 us); two parts
-// everywhere would cost a third (4096 tokens 177 -> 229, 64 single tokens over up to 8192 104 -> 156).
+// kFewKeys of them therefore take the keys in two fp16 parts, about 22 bits, and with them the
+// other rows of their tile (few_keys). The error is then at most 1.4 times that of binary32
+// arithmetic with the result rounded, where it was 1.8 over 20 keys, 1.65 over 100, 1.4 over 330 and 1.3
+// over 658. In us, with one part and as it is: 658 tokens 22.2 and 23.7, 4096 165 and 170, 3000 with a
+// window of 512, which all take two, 60 and 75. Two parts everywhere would cost 30% (4096 tokens 222, 64 single
+// tokens over up to 8192 95 -> 121).
 //
 // With x the product and c the scale in log2 units, p = 2^(x*c - b): one FMA and one
 // exponential.  b is an integer, so that a raised b rescales O by an exact power
@@ -292,7 +293,7 @@ __device__ __forceinline__ void zero_rest(const AttnArgs &a, int D)
 // and three workgroups a CU cover the loads: a third step in flight gained nothing, a fourth workgroup would
 // spill (149 us).  Short ones are a
 // chain of dependent loads (lengths, table, cache), a merge and a second launch to
-// join: one sequence of 658 tokens 8.3 us, of 500 in one part 7.1 us.
+// join: one sequence of 658 tokens 8.3 us, of 500 in one part 7.2 us.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 32;
 
@@ -515,12 +516,12 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
 // unpacked once into LDS, in fragment order, for all its waves.
 //
 // Bound by the exponentials and the unpacking beside the products, and by the power
-// limit: 4096 tokens of 32 query heads of 128 (137 GFLOP under the mask) take 160 us, 0.86
+// limit: 4096 tokens of 32 query heads of 128 (137 GFLOP under the mask) take 156 to 163 us, 0.84 to 0.88
 // PFLOP/s, where the matrix units alone, on random operands, sustain 1.35.  The 32x32x16
 // product reads the fewest LDS bytes a flop; a 64-key tile takes a CU's 8 waves 4160 cycles,
-// half of them products.  Eight waves share a tile's unpacking (189 us with four) where that
+// half of them products.  Eight waves share a tile's unpacking (179 us with four) where that
 // still fills the CUs; short prompts are a chain of one tile after the other (658 tokens
-// 22.6 us), which two waves to 32 rows shorten.
+// of fp16 23.7 us), which two waves to 32 rows shorten.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 64;
 
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
         ahead = entry_of(a.v, s, place_in(kt + 4));
     };
     // The next tile is unpacked between this one's products, beside the first ones, by waves that have the keys to
-    // themselves (2048 tokens behind 6000 284 -> 276 us); by those that halve them, after (658 tokens of 64 dims 16.1, else
+    // themselves (2048 tokens behind 6000 282 -> 276 us); by those that halve them, after (658 tokens of 64 dims 16.1, else
     // 16.9).
     const bool early = KS == 1 && !rests;
     u32x4 qf[P];
@@ -781,8 +782,8 @@ __global__ void __launch_bounds__(64 * NW * KS) __attribute__((amdgpu_waves_per_
 
 // The parts of a row's keys joined, a row and query head at a time by G groups of
 // 16 lanes: group i takes every G-th part, and the groups' results meet in LDS.  Its time is a
-// launch and a chain of loads (4.3 us for one token in six parts, 5.0 for 64 in two) until rows
-// are many (1100 rows of 32 heads in three parts: 17 us, 3.2 TB/s).
+// launch and a chain of loads (4.3 us for one token in six parts, 4.9 for 64 in two) until rows
+// are many (1100 rows of 32 heads in three parts: 16 us, 3.4 TB/s).
 template <int DT, int D, int G>
 __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a)
 {
@@ -912,7 +913,7 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     p.few_rows = !p.few ? 0 : ragged ? 32 : group;
     // Blocks of 16 rows that share the unpacked keys and values: two where rows, evenly shared out, would need them. A
     // ragged batch of single tokens (or of those and prompts) takes one, and a second workgroup for what has more: 64
-    // single tokens over up to 1000 24.0 us against 28.5, 64 sequences of 3 over up to 4000 53 against 63; 5 and 8 of each are the same.
+    // single tokens over up to 1000 24.8 us against 30.4, 64 sequences of 3 over up to 4000 54 against 68; 5 and 8 of each are the same.
     const bool two = ragged ? T * group > 16 * S && T * group <= 32 * S : p.few_rows > 16;
     p.few_rb = two ? 2 : 1;
     p.few_tiles = (int)ceil_of(p.few_rows > 0 ? p.few_rows : 1, 16 * p.few_rb);
@@ -922,9 +923,9 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     long long chunk = ceil_of(ceil_of(units * max_len, D == 64 ? 1024 : 768), step) * step;
     // One part where a second launch costs more than it gains.  Of eight waves up to 1024 keys, while a workgroup (or, with
     // heads of 64, two) to a CU holds them: always up to 512 (768), above where parts would be more workgroups than
-    // CUs.  In us, 32 query and 8 key heads of 128, parts and one part: one sequence of 500 9.3 and 7.1, of 658 8.3 and
-    // 8.6, 8 of 658 9.8 and 8.6, 16 of 1000 13.0 and 10.8, 4 of 1000 8.6 and 9.9, 64 of 1000 19.7 and 20.6.  Of four
-    // waves up to 384 keys else: one of 200 5.5 (eight waves 5.7), 128 of 300 15.7 (21.8).
+    // CUs.  In us, 32 query and 8 key heads of 128, parts and one part: one sequence of 500 9.4 and 7.2, of 658 8.4 and
+    // 8.6, 8 of 658 9.7 and 7.6, 16 of 1000 12.3 and 10.3, 4 of 1000 8.7 and 10.0, 64 of 1000 20.1 and 20.5.  Of four
+    // waves up to 384 keys else: one of 200 5.6 (eight waves 6.0), 128 of 300 15.7 (21.8).
     const bool one = p.few_rb == 1 && max_len > 256 && max_len <= 1024 && units <= (D == 64 ? 512 : 256) &&
                      (max_len <= (D == 64 ? 768 : 512) || units * ceil_of(max_len, step) > 256);
     p.few_waves = one ? 8 : 4;
@@ -946,10 +947,13 @@ AttnPlan plan_attention(long long T, long long S, int heads, int kv_heads, int D
     // Keys are split where tiles of 128 rows do not fill the CUs, of a prompt's own triangle only where they leave
     // half of them idle: joining costs more than it gains else.  Eight waves of two halves make a workgroup
     // to a CU; where whole parts leave too many idle that way, two workgroups of four waves.
-    // In us, 32 query and 8 key heads of 128.  One wave and two to 32 rows: 1300 tokens 45 and 39, 658 tokens
-    // 23.9 and 22.6, 256 tokens behind 4000 57 and 47; but 2000 tokens of heads of 64 (500 tiles) 44 and 47.
-    // Whole and in parts: 64 tokens behind 8000 170 and 39, 512 behind 7600 172 and 112, 1100 of three sequences
-    // behind up to 8000 (288 tiles) 189 and 145; 1024 behind 7000 (256 tiles) 182 and 179.
+    // In us, 32 query and 8 key heads of 128.  One wave and two to 32 rows: 1300 tokens 42 and 35, 658 tokens
+    // of fp16 26.8 and 23.7, 256 tokens behind 4000 60 and 45; but 2000 tokens of heads of 64 (500 tiles) 44 and 47.
+    // Whole and in parts: 64 tokens behind 8000 162 and 50, 512 behind 7600 166 and 102, 1100 of three sequences
+    // behind up to 8000 (288 tiles) 185 and 132; 1024 behind 7000 (256 tiles) 182 and 179.
+    // max_len is what the caller bounds the lengths by: where it is many times the lengths (the default, in tables of
+    // 32768), parts are too long and prompts are taken for chunks behind a context: 16 single tokens over 4096 36 us for
+    // 21, 8 over 2000 20.3 for 11.4, 658 tokens 28.8 for 23.7, 512 behind 7600 168 for 102, 4096 tokens the same.
     const long long tiles = count(p.tile_tokens);
     const bool behind = max_len > 2 * each;
     long long least = 512;

@@ -225,8 +225,8 @@ __device__ __forceinline__ void turn_store(const TurnArgs &t, const Heads &h, in
 __host__ __device__ inline int chunks(int heads, int hc) { return (heads + hc - 1) / hc; }
 
 // One read and one write of each head; bound by memory once the heads fill the CUs (4099 tokens of 36
-// heads of 128 in 14.6 us, 75 MB at 5.2 TB/s out of and into the last-level cache) and by
-// the launch and one chain of loads below (one token 2.6 us).
+// heads of 128 in 14.9 us, 75 MB at 5.0 TB/s out of and into the last-level cache) and by
+// the launch and one chain of loads below (one token 2.5 us).
 template <int DT, int D, int HC>
 __global__ void __launch_bounds__(256) k_norm_rope(NormRopeArgs a)
 {
@@ -406,7 +406,7 @@ __device__ __forceinline__ void append_values(const AppendArgs &a, int slot, int
 // Workgroups of values (quads, the longest chains, first), of keys and of queries.  Bound by the
 // 64-bit arithmetic of the codes, about 30 instructions a dim, next to the loads: 4096 tokens of
 // 32 query and 8 key heads of 128 take 24 us (89 MB, 3.7 TB/s), 8192 of 8 key heads of 64
-// 14 us; one token takes 3.4 us, a chain of look-up, load and reduction.  A lane of 8 dims
+// 14 us; one token takes 3.3 us, a chain of look-up, load and reduction.  A lane of 8 dims
 // in place of 4 for heads of 64 took the 8192 tokens from 15.5 us to 14.
 template <int DT, int D, int HC>
 __global__ void __launch_bounds__(256) k_kv_append(AppendArgs a)

@@ -291,3 +291,21 @@ def test_products_far_below_zero(dtype, n):
             want, mag = (x[:m].mean(0).repeat_interleave(heads // kv, 0)[None] for x in (held, held.abs()))
             bound = R.store_err(want, (2.0 ** -11 + m * 2.0 ** -23) * mag + 2.0 ** -25, dtype)
             assert_within(y[i:i + 1], want, bound, f"scale {scale} row {i}")
+
+
+@pytest.mark.parametrize("new,lens,heads", [([1] * 4, [300, 1, 700, 2100], 8), ([40], [40], 8), ([300, 1, 5], [300, 90, 1200], 8),
+                                            ([658], [700], 32), ([600], [2600], 64)])
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+def test_tables_wider_than_the_lengths(new, lens, heads, D, dtype):
+    """Entries behind a sequence's pages are not followed, whatever they name; the split that their number leads to, and the
+    one that max_len gives, keep the result within its bound."""
+    kv = heads // 4
+    b = Batch(new, lens, heads, kv, D, 64, dtype, seed=111)
+    rows = set(range(0, sum(new), 1 + sum(new) // 24)) | {sum(new) - 1}
+    narrow = b.pool.tables
+    for entry in (-1, 0, 2 ** 31 - 1):
+        b.pool.tables = torch.cat([narrow, torch.full((len(lens), 512 - narrow.shape[1]), entry, dtype=torch.int32, device="cuda")], 1)
+        for s, n in enumerate(lens):
+            b.pool.tables[s, (n + 63) // 64:] = entry
+        for kw in ({}, dict(max_len=max(lens)), dict(window=70)):
+            b.check(b.run(**kw), window=kw.get("window", 0), what=f"entries {entry}, {kw}", rows=rows)
